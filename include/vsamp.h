@@ -326,6 +326,93 @@ vsamp_status vsamp_shard_merge(const vsamp_piece_rec* recs, const vsamp_shard_wi
                                int32_t* token, float* logprob, float* target_logprob, int32_t* row_status,
                                void* stream);
 
+/* ---------------------------------------------------------------------------------------------------
+ * The vocabulary's tables on either side of the logits: scoring of given tokens and its gradient, the output
+ * head with 4-bit weights, the embedding lookup and its gradient. Streams, ownership and errors are as above.
+ * --------------------------------------------------------------------------------------------------- */
+
+/* A token that is not scored, looked up as a row of zeros, and given no gradient (a prompt position of a
+ * training batch, padding). */
+#define VSAMP_TOKEN_IGNORE (-100)
+
+/* Scores of given tokens: with s_v = (x_v - m) / T, m = max x, S = sum exp(s_v), p_v = exp(s_v) / S
+ * (T <= 0 read as 1):
+ *   logprob[r]    min(s_t - log S, 0) for t = token[r]
+ *   entropy[r]    -sum p_v log p_v = log S - sum s_v exp(s_v) / S
+ *   rank[r]       tokens before t in the order (logit descending, index ascending); 0 is the most probable
+ *   alt_idx, alt_lp [B, N]  the first N tokens of that order and their log-probabilities
+ *   row_max[r] = m, row_logsum[r] = log S   what vsamp_score_tokens_backward reads again
+ * Any output may be NULL; alt_idx and alt_lp are required when N > 0 (0 <= N <= VSAMP_SCORE_ALT_MAX).
+ * Masked tokens: a logit of -inf has probability 0, is never an alternative, and as the given token has the
+ *   log-probability -inf. Alternatives past the unmasked tokens hold -1 and NaN.
+ * token[r] = VSAMP_TOKEN_IGNORE: the row is not read; log-probability, entropy, row_max and row_logsum are 0,
+ *   the rank is -1, alternatives hold -1 and NaN, the status is VSAMP_OK.
+ * Row errors (every output NaN or -1): NaN or +inf in the row, or a row whose tokens are all masked
+ *   (VSAMP_ERR_NONFINITE); another token outside [0, V), a NaN or infinite temperature (VSAMP_ERR_INVALID_ARG).
+ *   workspace  vsamp_score_workspace_size bytes, 16-byte aligned; needs no initialisation, not shared by calls
+ *              that may overlap.
+ * Every row is read once, in pieces of 4 KB that depend on V alone: the results of a row do not depend on B, the
+ * stride or the launch. Two launches on `stream`. */
+#define VSAMP_SCORE_ALT_MAX 128
+size_t vsamp_score_workspace_size(vsamp_dtype dt, int64_t B, int64_t V, int32_t N);
+vsamp_status vsamp_score_tokens(const void* logits, vsamp_dtype dt, int64_t B, int64_t V, int64_t ld,
+                                const float* temperature, const int32_t* token, int32_t N, float* logprob,
+                                float* entropy, int32_t* rank, int32_t* alt_idx, float* alt_lp, float* row_max,
+                                float* row_logsum, int32_t* row_status, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Gradient of vsamp_score_tokens with respect to the logits:
+ *   dlogits[r, v] = (g (v == t) - p_v (g + h (log p_v + H))) / T,  g = dlogprob[r], h = dentropy[r], H = entropy[r]
+ *   dlogprob, dentropy  [B], one of them may be NULL (0); entropy is required with dentropy.
+ *   row_max, row_logsum, entropy  as vsamp_score_tokens wrote them for the same logits, tokens and temperature.
+ *   dlogits   [B, ldd] of the logits' type, rounded once; it may be the logits' own buffer with the same stride
+ *             (the logits are then replaced).
+ * Masked tokens have p = 0. An ignored row's gradient is 0. A row that vsamp_score_tokens refused gets NaN and its
+ * status. One launch on `stream`. */
+vsamp_status vsamp_score_tokens_backward(const void* logits, vsamp_dtype dt, int64_t B, int64_t V, int64_t ld,
+                                         const float* temperature, const int32_t* token, const float* dlogprob,
+                                         const float* dentropy, const float* row_max, const float* row_logsum,
+                                         const float* entropy, void* dlogits, int64_t ldd, int32_t* row_status,
+                                         void* stream);
+
+/* The output head with 4-bit weights in groups along the inner dimension:
+ *   logits[m, v] = sum over groups g of scale[v, g] * sum over k in g of (code[v, k] - zero[v, g]) * hidden[m, k]
+ *   codes   [V, D / 2] bytes, element k in the low nibble for even k, in the high nibble for odd k
+ *   scales  [V, D / group] fp32 or bf16
+ *   zeros   [V, D / group] bytes, values 0..15, or NULL: every zero point is 8
+ *   group   32, 64 or 128; D a multiple of it
+ * vsamp_head_pack lays the weights out once (vsamp_head_packed_size bytes, 16-byte aligned) for any number of
+ * vsamp_head_logits calls. hidden is [M, ldh], fp32 or bf16, logits [M, ld], fp32 or bf16 (the sampler's input);
+ * scale_dt, has_zeros, V, D and group are those of the pack. Products are exact, sums fp32, one rounding at the end.
+ * The weights are read once per 64 hidden rows: the call is meant for the few rows of a decode step. */
+size_t vsamp_head_packed_size(vsamp_dtype scale_dt, int32_t has_zeros, int64_t V, int64_t D, int32_t group);
+vsamp_status vsamp_head_pack(const uint8_t* codes, const void* scales, vsamp_dtype scale_dt, const uint8_t* zeros,
+                             int64_t V, int64_t D, int32_t group, void* packed, size_t packed_bytes, void* stream);
+vsamp_status vsamp_head_logits(const void* hidden, vsamp_dtype dt, int64_t M, int64_t ldh, const void* packed,
+                               size_t packed_bytes, vsamp_dtype scale_dt, int32_t has_zeros, int64_t V, int64_t D,
+                               int32_t group, void* logits, vsamp_dtype out_dt, int64_t ld, void* stream);
+
+/* Embedding lookup with scaling: out[n, :] = scale * table[token[n], :], formed in fp32, rounded once.
+ *   table [V, ldt], out [N, ldo], D columns, each fp32 or bf16.
+ *   token[n] = VSAMP_TOKEN_IGNORE gives zeros; another token outside [0, V) a row of NaN and
+ *   row_status[n] = VSAMP_ERR_INVALID_ARG (vsamp_sample's -1 among them). row_status may be NULL. */
+vsamp_status vsamp_embed(const int32_t* token, int64_t N, const void* table, vsamp_dtype dt, int64_t V, int64_t D,
+                         int64_t ldt, float scale, void* out, vsamp_dtype out_dt, int64_t ldo, int32_t* row_status,
+                         void* stream);
+
+/* Gradient of vsamp_embed with respect to the table, by sorted tokens:
+ *   dtable[v, :] = scale * sum over n with token[n] = v of dout[n, :]      (accumulate = 0: every row is written)
+ *   dtable[v, :] += the same                                               (accumulate != 0: only rows of tokens)
+ *   dout [N, ldd], dtable [V, ldt], each fp32 or bf16; sums in fp32, one rounding. Ignored tokens and tokens outside
+ *   [0, V) add nothing. Positions of a token are added in a fixed order: the result is the same on every call.
+ *   workspace  vsamp_embed_workspace_size(N, D) bytes, 16-byte aligned; needs no initialisation, not shared by
+ *              calls that may overlap. */
+size_t vsamp_embed_workspace_size(int64_t N, int64_t D);
+vsamp_status vsamp_embed_backward(const int32_t* token, int64_t N, const void* dout, vsamp_dtype dt, int64_t D,
+                                  int64_t ldd, float scale, int64_t V, void* dtable, vsamp_dtype table_dt,
+                                  int64_t ldt, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
 /* Static description of a status code. */
 const char* vsamp_status_string(vsamp_status s);
 

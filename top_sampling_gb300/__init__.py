@@ -27,11 +27,16 @@ VSAMP_ERR_SCRATCH_LIMIT = 6
 VSAMP_STATIC_SCRATCH_BYTES = 1 << 22   # the fixed scratch array of vsamp_sample_static
 VSAMP_F32 = 0
 VSAMP_BF16 = 1
+VSAMP_TOKEN_IGNORE = -100              # a token that is not scored and gets no gradient
+VSAMP_SCORE_ALT_MAX = 128              # most alternatives of vsamp_score_tokens
 
 EXPORTED = ("vsamp_softmax_lse", "vsamp_topk_select", "vsamp_topp_minp_mask", "vsamp_sample",
             "vsamp_sample_ws", "vsamp_sample_workspace_size", "vsamp_sample_static", "vsamp_logprob", "vsamp_topn_logprobs", "vsamp_kept_logprob",
             "vsamp_shard_pieces", "vsamp_shard_workspace_size", "vsamp_shard_partial", "vsamp_shard_merge",
             "vsamp_sample_rejection",
+            "vsamp_score_workspace_size", "vsamp_score_tokens", "vsamp_score_tokens_backward",
+            "vsamp_head_packed_size", "vsamp_head_pack", "vsamp_head_logits",
+            "vsamp_embed", "vsamp_embed_workspace_size", "vsamp_embed_backward",
             "vsamp_status_string",
             "vsamp_device_info", "vsamp_version")
 
@@ -91,6 +96,23 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.vsamp_sample_workspace_size.restype = ctypes.c_size_t
     for f in ("vsamp_softmax_lse", "vsamp_topk_select", "vsamp_topp_minp_mask", "vsamp_sample", "vsamp_logprob",
               "vsamp_sample_ws", "vsamp_sample_static", "vsamp_topn_logprobs", "vsamp_kept_logprob"):
+        getattr(lib, f).restype = st
+    sz = ctypes.c_size_t
+    f32 = ctypes.c_float
+    lib.vsamp_score_workspace_size.argtypes = [st, i64, i64, i32]
+    lib.vsamp_score_workspace_size.restype = sz
+    lib.vsamp_score_tokens.argtypes = [vp, st, i64, i64, i64, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.vsamp_score_tokens_backward.argtypes = [vp, st, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp]
+    lib.vsamp_head_packed_size.argtypes = [st, i32, i64, i64, i32]
+    lib.vsamp_head_packed_size.restype = sz
+    lib.vsamp_head_pack.argtypes = [vp, vp, st, vp, i64, i64, i32, vp, sz, vp]
+    lib.vsamp_head_logits.argtypes = [vp, st, i64, i64, vp, sz, st, i32, i64, i64, i32, vp, st, i64, vp]
+    lib.vsamp_embed.argtypes = [vp, i64, vp, st, i64, i64, i64, f32, vp, st, i64, vp, vp]
+    lib.vsamp_embed_workspace_size.argtypes = [i64, i64]
+    lib.vsamp_embed_workspace_size.restype = sz
+    lib.vsamp_embed_backward.argtypes = [vp, i64, vp, st, i64, i64, f32, i64, vp, st, i64, i32, vp, sz, vp]
+    for f in ("vsamp_score_tokens", "vsamp_score_tokens_backward", "vsamp_head_pack", "vsamp_head_logits",
+              "vsamp_embed", "vsamp_embed_backward"):
         getattr(lib, f).restype = st
     lib.vsamp_status_string.argtypes = [st]
     lib.vsamp_status_string.restype = ctypes.c_char_p
@@ -568,3 +590,254 @@ def vsamp_sample_sharded(logits, R: int, temperature=None, seed=None, step=None,
                             row_id=row_id, target=target, recs=recs[r], win=wins[r], stream=stream)
     return vsamp_shard_merge(recs, wins, V, temperature=temperature, seed=seed, step=step, row_id=row_id,
                              want_target=target is not None, stream=stream)
+
+
+# ------------------------------------------------------------------------------------------------
+# the vocabulary's tables: token scores and their gradient, the 4-bit head, the embedding and its gradient
+# ------------------------------------------------------------------------------------------------
+def _elsewhere(t: torch.Tensor, stream):
+    """The context a call on tensor t and `stream` has to run in, or None when the current device and stream are it.
+
+    Everything a call allocates or converts then belongs to the stream its kernels run on."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+
+
+def _current(dev) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _token_ids(v, B: int, dev):
+    """Token ids as a contiguous int32 device tensor; wider ids outside its range stay outside every vocabulary."""
+    if isinstance(v, torch.Tensor):
+        if v.dtype == torch.int32 and v.device == dev and v.is_contiguous():
+            return v
+        if v.is_floating_point():
+            raise TypeError(f"token must hold whole numbers, got {v.dtype}")
+        if v.dtype == torch.int64:
+            v = v.clamp(-(1 << 31), (1 << 31) - 1)
+        return v.to(device=dev, dtype=torch.int32).contiguous()
+    return torch.full((B,), int(v), dtype=torch.int32, device=dev)
+
+
+def _row_values(v, B: int, dev, name):
+    """A per-row fp32 parameter: None, a scalar (broadcast) or a [B] tensor."""
+    if v is None or (isinstance(v, torch.Tensor) and v.dtype == torch.float32 and v.device == dev and v.is_contiguous()):
+        return v
+    return _param(v, B, torch.float32, dev, name)
+
+
+def _matrix(t: torch.Tensor, name: str, dev, rows=None, cols=None):
+    """Checks a row-major matrix (rows may be padded); returns its row stride in elements."""
+    if t.dim() != 2 or t.device != dev or t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must be a 2-D tensor on {dev} with contiguous rows")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _logits_matrix(x: torch.Tensor, V):
+    B, V, ld = _rows(x, V)
+    if not 0 < V <= x.shape[1]:
+        raise ValueError(f"V = {V} is outside the rows of {x.shape[1]} logits")
+    return B, V, ld
+
+
+def _f32_out(t, n: int, dev):
+    return torch.empty(n, dtype=torch.float32, device=dev) if t is None else t
+
+
+def vsamp_score_tokens(logits, token, temperature=None, n_alt=0, V=None, logprob=None, entropy=None, rank=None,
+                       alt_idx=None, alt_lp=None, row_max=None, row_logsum=None, row_status=None, workspace=None,
+                       stream=None):
+    """Log-probability, entropy and rank of given tokens, with the n_alt most probable alternatives, in one pass over
+    the logits. -inf logits are masked tokens; VSAMP_TOKEN_IGNORE as a token skips the row. Returns (logprob [B],
+    entropy [B], rank [B] int32, alt_idx [B, n_alt] int32 or None, alt_lp [B, n_alt] or None, row_max [B],
+    row_logsum [B], row_status [B])."""
+    where = _elsewhere(logits, stream)
+    if where is not None:
+        with where:
+            return vsamp_score_tokens(logits, token, temperature, n_alt, V, logprob, entropy, rank, alt_idx, alt_lp,
+                                      row_max, row_logsum, row_status, workspace)
+    B, V, ld = _logits_matrix(logits, V)
+    dev, dt, n_alt = logits.device, _dtype_code(logits), int(n_alt)
+    if not 0 <= n_alt <= VSAMP_SCORE_ALT_MAX:
+        raise ValueError(f"n_alt must be in [0, {VSAMP_SCORE_ALT_MAX}]")
+    token = _token_ids(token, B, dev)
+    temperature = _row_values(temperature, B, dev, "temperature")
+    logprob, entropy = _f32_out(logprob, B, dev), _f32_out(entropy, B, dev)
+    row_max, row_logsum = _f32_out(row_max, B, dev), _f32_out(row_logsum, B, dev)
+    rank = torch.empty(B, dtype=torch.int32, device=dev) if rank is None else rank
+    row_status = torch.empty(B, dtype=torch.int32, device=dev) if row_status is None else row_status
+    if n_alt:
+        alt_idx = torch.empty((B, n_alt), dtype=torch.int32, device=dev) if alt_idx is None else alt_idx
+        alt_lp = torch.empty((B, n_alt), dtype=torch.float32, device=dev) if alt_lp is None else alt_lp
+    else:
+        alt_idx = alt_lp = None
+    lib = load()
+    if workspace is None:
+        need = lib.vsamp_score_workspace_size(dt, B, V, n_alt)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    f32, i32 = torch.float32, torch.int32
+    st = lib.vsamp_score_tokens(
+        logits.data_ptr(), dt, B, V, ld, _ptr(temperature, f32, dev, B, "temperature"),
+        _ptr(token, i32, dev, B, "token"), n_alt, _ptr(logprob, f32, dev, B, "logprob"),
+        _ptr(entropy, f32, dev, B, "entropy"), _ptr(rank, i32, dev, B, "rank"),
+        _ptr(alt_idx, i32, dev, B * n_alt, "alt_idx"), _ptr(alt_lp, f32, dev, B * n_alt, "alt_lp"),
+        _ptr(row_max, f32, dev, B, "row_max"), _ptr(row_logsum, f32, dev, B, "row_logsum"),
+        _ptr(row_status, i32, dev, B, "row_status"), _ptr(workspace, torch.uint8, dev, 0, "workspace"),
+        workspace.numel(), _current(dev))
+    _check(st, "vsamp_score_tokens")
+    return logprob, entropy, rank, alt_idx, alt_lp, row_max, row_logsum, row_status
+
+
+def vsamp_score_tokens_backward(logits, token, dlogprob, row_max, row_logsum, entropy=None, dentropy=None,
+                                temperature=None, V=None, dlogits=None, row_status=None, stream=None):
+    """Gradient of vsamp_score_tokens with respect to the logits from the gradients of the log-probabilities and of
+    the entropies (either may be None) and the statistics of the forward call. dlogits may be the logits' own
+    buffer. Returns (dlogits [B, V] of the logits' type, row_status [B])."""
+    where = _elsewhere(logits, stream)
+    if where is not None:
+        with where:
+            return vsamp_score_tokens_backward(logits, token, dlogprob, row_max, row_logsum, entropy, dentropy,
+                                               temperature, V, dlogits, row_status)
+    B, V, ld = _logits_matrix(logits, V)
+    dev = logits.device
+    token = _token_ids(token, B, dev)
+    temperature = _row_values(temperature, B, dev, "temperature")
+    dlogprob, dentropy = _row_values(dlogprob, B, dev, "dlogprob"), _row_values(dentropy, B, dev, "dentropy")
+    if dlogits is None:
+        dlogits = torch.empty((B, V), dtype=logits.dtype, device=dev)
+    elif dlogits.dtype != logits.dtype or dlogits.dim() != 2 or dlogits.shape[1] < V:
+        raise ValueError(f"dlogits must be [{B}, >= {V}] of {logits.dtype}")
+    ldd = _matrix(dlogits, "dlogits", dev, B)
+    row_status = torch.empty(B, dtype=torch.int32, device=dev) if row_status is None else row_status
+    f32, i32 = torch.float32, torch.int32
+    st = load().vsamp_score_tokens_backward(
+        logits.data_ptr(), _dtype_code(logits), B, V, ld, _ptr(temperature, f32, dev, B, "temperature"),
+        _ptr(token, i32, dev, B, "token"), _ptr(dlogprob, f32, dev, B, "dlogprob"),
+        _ptr(dentropy, f32, dev, B, "dentropy"), _ptr(row_max, f32, dev, B, "row_max"),
+        _ptr(row_logsum, f32, dev, B, "row_logsum"), _ptr(entropy, f32, dev, B, "entropy"), dlogits.data_ptr(), ldd,
+        _ptr(row_status, i32, dev, B, "row_status"), _current(dev))
+    _check(st, "vsamp_score_tokens_backward")
+    return dlogits, row_status
+
+
+class HeadWeights:
+    """4-bit head weights as vsamp_head_pack laid them out: the buffer and the shape it was packed for."""
+
+    __slots__ = ("data", "V", "D", "group", "scale_dt", "has_zeros")
+
+    def __init__(self, data: torch.Tensor, V: int, D: int, group: int, scale_dt: int, has_zeros: bool):
+        self.data, self.V, self.D, self.group = data, V, D, group
+        self.scale_dt, self.has_zeros = scale_dt, has_zeros
+
+
+def vsamp_head_pack(codes, scales, zeros=None, group=64, stream=None) -> HeadWeights:
+    """Lays out 4-bit weights for vsamp_head_logits: codes [V, D / 2] uint8 (even elements in the low nibble), scales
+    [V, D / group] fp32 or bf16, zeros [V, D / group] uint8 in 0..15 or None (8 everywhere); group 32, 64 or 128."""
+    where = _elsewhere(codes, stream)
+    if where is not None:
+        with where:
+            return vsamp_head_pack(codes, scales, zeros, group)
+    dev, group = codes.device, int(group)
+    if codes.dim() != 2 or codes.dtype != torch.uint8:
+        raise ValueError("codes must be a 2-D uint8 tensor [V, D / 2]")
+    V, D = int(codes.shape[0]), 2 * int(codes.shape[1])
+    if group not in (32, 64, 128) or V == 0 or D == 0 or D % group:
+        raise ValueError(f"group must be 32, 64 or 128 and divide D (group {group}, V {V}, D {D})")
+    for t, name in ((scales, "scales"), (zeros, "zeros")):
+        if t is not None and tuple(t.shape) != (V, D // group):
+            raise ValueError(f"{name} must be [{V}, {D // group}], got {tuple(t.shape)}")
+    lib = load()
+    dt = _dtype_code(scales)
+    need = lib.vsamp_head_packed_size(dt, zeros is not None, V, D, group)
+    data = torch.empty(need, dtype=torch.uint8, device=dev)
+    st = lib.vsamp_head_pack(_ptr(codes, torch.uint8, dev, V * D // 2, "codes"),
+                             _ptr(scales, None, dev, V * D // group, "scales"), dt,
+                             _ptr(zeros, torch.uint8, dev, V * D // group, "zeros"), V, D, group, data.data_ptr(), need,
+                             _current(dev))
+    _check(st, "vsamp_head_pack")
+    return HeadWeights(data, V, D, group, dt, zeros is not None)
+
+
+def vsamp_head_logits(hidden, head: HeadWeights, out=None, out_dtype=torch.float32, stream=None):
+    """Logits [M, V] of hidden states [M, D] (fp32 or bf16) under 4-bit head weights, for the few rows of a decode
+    step. `out` (fp32 or bf16, rows may be padded) or a new tensor of out_dtype is returned."""
+    where = _elsewhere(hidden, stream)
+    if where is not None:
+        with where:
+            return vsamp_head_logits(hidden, head, out, out_dtype)
+    dev = hidden.device
+    ldh = _matrix(hidden, "hidden", dev, None, head.D)
+    M = hidden.shape[0]
+    if out is None:
+        out = torch.empty((M, head.V), dtype=out_dtype, device=dev)
+    ld = _matrix(out, "out", dev, M, head.V)
+    data = head.data
+    if data.device != dev:
+        raise ValueError(f"head weights are on {data.device}, hidden states on {dev}")
+    st = load().vsamp_head_logits(hidden.data_ptr(), _dtype_code(hidden), M, ldh, data.data_ptr(), data.numel(),
+                                  head.scale_dt, head.has_zeros, head.V, head.D, head.group, out.data_ptr(),
+                                  _dtype_code(out), ld, _current(dev))
+    _check(st, "vsamp_head_logits")
+    return out
+
+
+def vsamp_embed(token, table, scale=1.0, out=None, out_dtype=None, row_status=None, stream=None):
+    """scale * table[token] (token [N], table [V, D] fp32 or bf16). VSAMP_TOKEN_IGNORE gives zeros, another token
+    outside the table NaN and a row status. Returns (out [N, D] of out_dtype or the table's type, row_status [N])."""
+    where = _elsewhere(table, stream)
+    if where is not None:
+        with where:
+            return vsamp_embed(token, table, scale, out, out_dtype, row_status)
+    dev = table.device
+    ldt = _matrix(table, "table", dev)
+    V, D = table.shape
+    N = token.numel() if isinstance(token, torch.Tensor) else 1
+    token = _token_ids(token, N, dev)
+    if out is None:
+        out = torch.empty((N, D), dtype=out_dtype or table.dtype, device=dev)
+    ldo = _matrix(out, "out", dev, N, D)
+    row_status = torch.empty(N, dtype=torch.int32, device=dev) if row_status is None else row_status
+    st = load().vsamp_embed(_ptr(token, torch.int32, dev, N, "token"), N, table.data_ptr(), _dtype_code(table), V, D, ldt,
+                            float(scale), out.data_ptr(), _dtype_code(out), ldo,
+                            _ptr(row_status, torch.int32, dev, N, "row_status"), _current(dev))
+    _check(st, "vsamp_embed")
+    return out, row_status
+
+
+def vsamp_embed_backward(token, dout, V, scale=1.0, dtable=None, dtype=None, accumulate=False, workspace=None,
+                         stream=None):
+    """Gradient of vsamp_embed with respect to the table: scale * the sum of dout's rows (dout [N, D]) of every token.
+    accumulate adds it to dtable's rows of those tokens, otherwise every row of dtable is written. Returns dtable
+    [V, D] (a new one of `dtype` or dout's type if not given)."""
+    where = _elsewhere(dout, stream)
+    if where is not None:
+        with where:
+            return vsamp_embed_backward(token, dout, V, scale, dtable, dtype, accumulate, workspace)
+    dev, V = dout.device, int(V)
+    ldd = _matrix(dout, "dout", dev)
+    N, D = dout.shape
+    token = _token_ids(token, N, dev)
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate needs the table gradient to add to")
+        dtable = torch.empty((V, D), dtype=dtype or dout.dtype, device=dev)
+    ldt = _matrix(dtable, "dtable", dev, V, D)
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(lib.vsamp_embed_workspace_size(N, D), dtype=torch.uint8, device=dev)
+    st = lib.vsamp_embed_backward(_ptr(token, torch.int32, dev, N, "token"), N, dout.data_ptr(), _dtype_code(dout), D,
+                                  ldd, float(scale), V, dtable.data_ptr(), _dtype_code(dtable), ldt, int(accumulate),
+                                  _ptr(workspace, torch.uint8, dev, 0, "workspace"), workspace.numel(), _current(dev))
+    _check(st, "vsamp_embed_backward")
+    return dtable

@@ -1,0 +1,36 @@
+// Host helpers of the one-dimensional launches (scoring, head, embedding).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "vsamp.h"
+
+namespace vsamp {
+
+// CTAs of a launch over n blocks of work; the kernels stride over what is beyond it.
+inline unsigned grid_of(int64_t n) { return (unsigned)(n < 0x3FFFFFFFLL ? n : 0x3FFFFFFFLL); }
+
+// `overlap`: the launch may begin while the stream's previous kernel drains (the kernel itself waits for that
+// kernel's writes with cudaGridDependencySynchronize before it touches memory).
+template <typename... KArgs, typename... Args>
+vsamp_status launch_1d(void (*kern)(KArgs...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                       bool overlap, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return VSAMP_ERR_CUDA;
+  }
+  return VSAMP_OK;
+}
+
+}  // namespace vsamp

@@ -1,0 +1,506 @@
+// Scoring of given tokens (vsamp_score_tokens) and its gradient (vsamp_score_tokens_backward).
+//
+// Forward. With s_v = (x_v - m) / T, S = sum e^s_v and A = sum s_v e^s_v a row needs
+//   log-probability of t   min(s_t - log S, 0)
+//   entropy                log S - A / S
+//   rank of t              #{v : x_v > x_t, or x_v = x_t and v < t}
+//   the N alternatives     the first N tokens in the order (value descending, index ascending)
+// Rows are cut into fixed 4 KB pieces, one warp each; a piece is read once into registers, its maximum m_p is found
+// and S_p, A_p are formed relative to it, so no pass waits for the row maximum and the sums of a row depend on V
+// alone. A second launch folds the pieces of every row:
+//   S = sum 2^((m_p - m) c) S_p,   A = sum 2^((m_p - m) c) (A_p + (m_p - m) c S_p),   c = log2(e) / T.
+// -inf marks a masked token (probability 0); NaN and +inf are row errors.
+//
+// Alternatives. A piece also records the maxima of its eight 512-byte chunks. The first N tokens of the order lie in
+// the first N chunks in the order (chunk maximum descending, chunk index ascending): a token of any later chunk is
+// preceded by the maxima of N chunks. So the finish re-reads N chunks, whatever the data.
+#pragma once
+
+#include "vsamp.h"
+#include "vsamp_device.cuh"
+
+namespace vsamp {
+
+constexpr int kScorePiece = 4096;      // bytes of a row per warp
+constexpr int kScoreChunks = 8;        // 512-byte chunks per piece: one 16-byte vector per lane each
+constexpr int kScoreWarps = 8;
+constexpr int kScoreFinishThreads = 128;
+constexpr int kScoreList = 512;        // alternatives' candidates kept on chip; more of them take the radix path
+
+struct ScoreParams {
+  const unsigned char* x;
+  int64_t B, V, ld;
+  const float* temperature;
+  const int32_t* token;
+  int N;                 // alternatives per row
+  int vec;               // rows are 16-byte aligned
+  int64_t np;            // pieces per row
+  float4* rec;           // [B, np] {m_p, S_p, A_p, tokens before the given one}
+  float* chunk_max;      // [B, np, 8] (N > 0)
+  float* logprob;
+  float* entropy;
+  int32_t* rank;
+  int32_t* alt_idx;
+  float* alt_lp;
+  float* row_max;
+  float* row_logsum;
+  int32_t* row_status;
+};
+
+struct ScoreGradParams {
+  const unsigned char* x;
+  int64_t B, V, ld, ldo;
+  const float* temperature;
+  const int32_t* token;
+  const float* dlogprob;
+  const float* dentropy;
+  const float* row_max;
+  const float* row_logsum;
+  const float* entropy;
+  unsigned char* dx;
+  int32_t* row_status;
+  int64_t spans;         // CTAs per row
+};
+
+template <typename T>
+struct ScoreType;
+template <>
+struct ScoreType<float> {
+  static constexpr int ES = 4, VE = 4;
+  static constexpr uint32_t kMasked = 0xFF800000u;   // a 32-bit word of -inf
+  static __device__ __forceinline__ float load(const unsigned char* p, int64_t i) {
+    return reinterpret_cast<const float*>(p)[i];
+  }
+  // element j of a 16-byte vector
+  static __device__ __forceinline__ float at(const uint32_t (&w)[4], int j) { return __uint_as_float(w[j]); }
+  static __device__ __forceinline__ void put(uint32_t (&w)[4], int j, float f) { w[j] = __float_as_uint(f); }
+  static __device__ __forceinline__ void store(unsigned char* p, int64_t i, float f) {
+    reinterpret_cast<float*>(p)[i] = f;
+  }
+};
+template <>
+struct ScoreType<__nv_bfloat16> {
+  static constexpr int ES = 2, VE = 8;
+  static constexpr uint32_t kMasked = 0xFF80FF80u;
+  static __device__ __forceinline__ float load(const unsigned char* p, int64_t i) {
+    return __uint_as_float((uint32_t) reinterpret_cast<const unsigned short*>(p)[i] << 16);
+  }
+  static __device__ __forceinline__ float at(const uint32_t (&w)[4], int j) {
+    return __uint_as_float((j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
+  }
+  // bits of a value that is exactly a bf16
+  static __device__ __forceinline__ void put(uint32_t (&w)[4], int j, float f) {
+    const uint32_t b = __float_as_uint(f);
+    w[j >> 1] = (j & 1) ? ((w[j >> 1] & 0xFFFFu) | (b & 0xFFFF0000u)) : ((w[j >> 1] & 0xFFFF0000u) | (b >> 16));
+  }
+  static __device__ __forceinline__ void store(unsigned char* p, int64_t i, float f) {
+    reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(f);
+  }
+};
+
+// max that returns NaN when either operand is NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_sum_f(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+  return v;
+}
+__device__ __forceinline__ double warp_sum_d(double v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+  return v;
+}
+
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// The vector of elements [e, e + VE) of a row; elements at or beyond V read as -inf.
+template <typename T>
+__device__ __forceinline__ void score_load(const unsigned char* xr, int64_t e, int64_t V, int vec, uint32_t (&w)[4]) {
+  using Ty = ScoreType<T>;
+  if (vec && e + Ty::VE <= V) {
+    const uint4 v = ldg_stream(xr + e * Ty::ES);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = Ty::kMasked;
+#pragma unroll
+  for (int j = 0; j < Ty::VE; ++j)
+    if (e + j < V) Ty::put(w, j, Ty::load(xr, e + j));
+}
+
+// One warp per piece.
+template <typename T, bool ALT>
+__global__ void __launch_bounds__(kScoreWarps * 32) score_piece_kernel(const ScoreParams p) {
+  using Ty = ScoreType<T>;
+  constexpr int PE = kScorePiece / Ty::ES;      // elements per piece
+  constexpr int CE = PE / kScoreChunks;         // elements per chunk
+  const int lane = threadIdx.x & 31;
+  const int64_t total = p.B * p.np;
+  for (int64_t id = (int64_t)blockIdx.x * kScoreWarps + (threadIdx.x >> 5); id < total;
+       id += (int64_t)gridDim.x * kScoreWarps) {
+    const int64_t row = id / p.np;
+    const int64_t e0 = (id - row * p.np) * PE;
+    const int32_t t = p.token[row];
+    if (t == VSAMP_TOKEN_IGNORE) continue;
+    const unsigned char* xr = p.x + row * p.ld * Ty::ES;
+    uint32_t w[kScoreChunks][4];
+#pragma unroll
+    for (int i = 0; i < kScoreChunks; ++i) score_load<T>(xr, e0 + i * CE + lane * Ty::VE, p.V, p.vec, w[i]);
+    const float temp = p.temperature ? p.temperature[row] : 1.f;
+    const float c = kLog2e / (temp > 0.f ? temp : 1.f);
+    const bool known = t >= 0 && t < p.V;
+    const float xt = known ? Ty::load(xr, t) : INFINITY;
+
+    // maximum of every lane's vectors, of the chunks and of the piece
+    float m = -INFINITY;
+    float mine = -INFINITY;    // lane i < 8: maximum of chunk i
+#pragma unroll
+    for (int i = 0; i < kScoreChunks; ++i) {
+      float cm = Ty::at(w[i], 0);
+#pragma unroll
+      for (int j = 1; j < Ty::VE; ++j) cm = max_nan(cm, Ty::at(w[i], j));
+      if (ALT) {
+        cm = warp_max_nan(cm);
+        if (lane == i) mine = cm;
+      }
+      m = max_nan(m, cm);
+    }
+    if (!ALT) m = warp_max_nan(m);
+    if (ALT && lane < kScoreChunks) p.chunk_max[id * kScoreChunks + lane] = mine;
+
+    float S = 0.f, A = 0.f;
+    uint32_t before = 0;
+    if (m > -INFINITY && m < INFINITY) {   // false for NaN too
+#pragma unroll
+      for (int i = 0; i < kScoreChunks; ++i) {
+#pragma unroll
+        for (int j = 0; j < Ty::VE; ++j) {
+          const float x = Ty::at(w[i], j);
+          // 2^-150 is 0 in the flushed exponential: a masked token adds 0 to both sums
+          const float s = fmaxf((x - m) * c, -150.f);
+          const float e = ex2_approx(s);
+          S += e;
+          A = fmaf(s, e, A);
+          const int64_t v = e0 + i * CE + lane * Ty::VE + j;
+          before += (x > xt || (x == xt && v < t)) ? 1u : 0u;
+        }
+      }
+    } else if (m == -INFINITY && known && xt == -INFINITY) {
+      // a masked piece before a masked given token: all of its tokens come first
+#pragma unroll
+      for (int i = 0; i < kScoreChunks; ++i)
+#pragma unroll
+        for (int j = 0; j < Ty::VE; ++j) before += e0 + i * CE + lane * Ty::VE + j < t ? 1u : 0u;
+    }
+    S = warp_sum_f(S);
+    A = warp_sum_f(A);
+    before = warp_sum_u32(before);
+    if (lane == 0) p.rec[id] = make_float4(m, S, A, __uint_as_float(before));
+  }
+}
+
+struct ScoreRow {
+  int status;
+  float m, logsum, entropy;
+  uint32_t before;
+  float invT;
+};
+
+// A warp folds the piece records of a row (every lane returns the same values).
+template <typename T>
+__device__ __forceinline__ ScoreRow score_fold(const ScoreParams& p, int64_t row, int32_t t) {
+  const int lane = threadIdx.x & 31;
+  const float4* rec = p.rec + row * p.np;
+  const float temp = p.temperature ? p.temperature[row] : 1.f;
+  ScoreRow r;
+  r.invT = 1.f / (temp > 0.f ? temp : 1.f);
+  const float c = kLog2e / (temp > 0.f ? temp : 1.f);
+  float m = -INFINITY;
+  for (int64_t i = lane; i < p.np; i += 32) m = max_nan(m, rec[i].x);
+  m = warp_max_nan(m);
+  double S = 0.0, A = 0.0;
+  uint32_t before = 0;
+  const bool finite = m > -INFINITY && m < INFINITY;
+  if (finite) {
+    for (int64_t i = lane; i < p.np; i += 32) {
+      const float4 q = rec[i];
+      before += __float_as_uint(q.w);
+      if (q.x > -INFINITY) {
+        const float d = fmaxf((q.x - m) * c, -150.f);
+        const float f = ex2_approx(d);
+        S += (double)(f * q.y);
+        A += (double)(f * fmaf(d, q.y, q.z));
+      }
+    }
+  }
+  S = warp_sum_d(S);
+  A = warp_sum_d(A);
+  r.before = warp_sum_u32(before);
+  r.m = m;
+  // S >= 1: log1p keeps the digits of a sum close to 1
+  r.logsum = log1pf((float)(S - 1.0));
+  r.entropy = fmaxf(r.logsum - 0.69314718056f * (float)(A / S), 0.f);
+  r.status = VSAMP_OK;
+  if (!finite) r.status = VSAMP_ERR_NONFINITE;
+  else if (isnan(temp) || isinf(temp) || t < 0 || (int64_t)t >= p.V) r.status = VSAMP_ERR_INVALID_ARG;
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void score_write(const ScoreParams& p, int64_t row, int32_t t, const ScoreRow& r) {
+  const float qnan = __int_as_float(0x7FC00000);
+  const bool skip = t == VSAMP_TOKEN_IGNORE;
+  const bool ok = r.status == VSAMP_OK;
+  const float none = skip ? 0.f : qnan;
+  if (p.logprob) {
+    float lp = none;
+    if (ok && !skip) {
+      const float xt = ScoreType<T>::load(p.x + row * p.ld * ScoreType<T>::ES, t);
+      const float temp = p.temperature ? p.temperature[row] : 1.f;
+      lp = fminf((float)((double)(xt - r.m) / (temp > 0.f ? temp : 1.f) - (double)r.logsum), 0.f);
+    }
+    p.logprob[row] = lp;
+  }
+  if (p.entropy) p.entropy[row] = ok && !skip ? r.entropy : none;
+  if (p.rank) p.rank[row] = ok && !skip ? (int32_t)r.before : -1;
+  if (p.row_max) p.row_max[row] = ok && !skip ? r.m : none;
+  if (p.row_logsum) p.row_logsum[row] = ok && !skip ? r.logsum : none;
+  if (p.row_status) p.row_status[row] = r.status;
+}
+
+// No alternatives: one warp per row.
+template <typename T>
+__global__ void __launch_bounds__(128) score_finish_kernel(const ScoreParams p) {
+  for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); row < p.B; row += (int64_t)gridDim.x * 4) {
+    const int32_t t = p.token[row];
+    ScoreRow r{};
+    if (t != VSAMP_TOKEN_IGNORE) r = score_fold<T>(p, row, t);
+    if ((threadIdx.x & 31) == 0) score_write<T>(p, row, t, r);
+  }
+}
+
+// Threshold of the `want` largest of the 64-bit keys that for_each visits (all different, at least `want` of them,
+// want > 0): exactly `want` keys are >= the value returned. Byte-wise radix search; it stops when a whole group of
+// equal leading bytes is taken. Called by all threads of the CTA.
+template <typename F>
+__device__ uint64_t score_radix_select(F for_each, uint32_t want, uint32_t* hist, uint32_t* bc) {
+  uint64_t prefix = 0, mask = 0;
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < 256; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    for_each([&](uint64_t k) {
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1u);
+    });
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      // lane l holds bins 255 - 8 l down to 248 - 8 l
+      const int top = 255 - 8 * (int)threadIdx.x;
+      uint32_t n[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n[i] = hist[top - i];
+        sum += n[i];
+      }
+      uint32_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(kFullMask, incl, o);
+        if (threadIdx.x >= o) incl += v;
+      }
+      uint32_t above = incl - sum;
+      if (above < want && incl >= want) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (above < want && above + n[i] >= want) {
+            bc[0] = (uint32_t)(top - i);
+            bc[1] = above;
+            bc[2] = n[i];
+          }
+          above += n[i];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= (uint64_t)bc[0] << shift;
+    mask |= 0xFFull << shift;
+    want -= bc[1];
+    const bool whole = bc[2] == want;
+    __syncthreads();
+    if (whole) break;
+  }
+  return prefix;
+}
+
+// One CTA per row: warp 0 folds the records, then all threads find the alternatives.
+template <typename T>
+__global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(const ScoreParams p) {
+  using Ty = ScoreType<T>;
+  constexpr int CE = kScorePiece / Ty::ES / kScoreChunks;
+  constexpr int NW = kScoreFinishThreads / 32;
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t bc[3];
+  __shared__ uint64_t list[kScoreList];
+  __shared__ int32_t chunks[VSAMP_SCORE_ALT_MAX];
+  __shared__ uint32_t n_chunks, n_list, floor_key, n_valid;
+  __shared__ ScoreRow shared_row;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float qnan = __int_as_float(0x7FC00000);
+  constexpr uint32_t kNone = 0x007FFFFFu;   // key of -inf
+  for (int64_t row = blockIdx.x; row < p.B; row += gridDim.x) {
+    const int32_t t = p.token[row];
+    const bool skip = t == VSAMP_TOKEN_IGNORE;
+    if (warp == 0) {
+      ScoreRow r{};
+      if (!skip) r = score_fold<T>(p, row, t);
+      if (lane == 0) {
+        score_write<T>(p, row, t, r);
+        shared_row = r;
+        n_chunks = n_list = n_valid = 0;
+        floor_key = 0xFFFFFFFFu;
+      }
+    }
+    __syncthreads();
+    const ScoreRow r = shared_row;
+    int32_t* oi = p.alt_idx + row * p.N;
+    float* ol = p.alt_lp + row * p.N;
+    uint32_t found = 0;
+    if (!skip && r.status == VSAMP_OK) {
+      const int64_t nch = p.np * kScoreChunks;
+      const float* cm = p.chunk_max + row * nch;
+      const unsigned char* xr = p.x + row * p.ld * Ty::ES;
+      auto each_chunk = [&](auto f) {
+        for (int64_t i = threadIdx.x; i < nch; i += kScoreFinishThreads) {
+          const uint32_t k = key_f32_bits(__float_as_uint(cm[i]));
+          if (k > kNone) f(((uint64_t)k << 32) | (uint32_t)~(uint32_t)i);
+        }
+      };
+      uint32_t mine = 0;
+      each_chunk([&](uint64_t) { ++mine; });
+      if (mine) atomicAdd(&n_valid, mine);
+      __syncthreads();
+      const uint64_t cut = n_valid > (uint32_t)p.N ? score_radix_select(each_chunk, (uint32_t)p.N, hist, bc) : 0;
+      each_chunk([&](uint64_t k) {
+        if (k >= cut) {
+          chunks[atomicAdd(&n_chunks, 1u)] = (int32_t)~(uint32_t)k;
+          atomicMin(&floor_key, (uint32_t)(k >> 32));
+        }
+      });
+      __syncthreads();
+      const uint32_t nc = n_chunks;
+      // every alternative is at least the smallest of these chunks' maxima when there are N of them
+      const uint32_t lowest = n_valid >= (uint32_t)p.N ? floor_key : kNone + 1;
+      auto each_token = [&](auto f) {
+        for (uint32_t i = warp; i < nc; i += NW) {
+          const int64_t e = (int64_t)chunks[i] * CE + lane * Ty::VE;
+          uint32_t w[4];
+          score_load<T>(xr, e, p.V, p.vec, w);
+#pragma unroll
+          for (int j = 0; j < Ty::VE; ++j) {
+            const uint32_t k = key_f32_bits(__float_as_uint(Ty::at(w, j)));
+            if (k >= lowest) f(((uint64_t)k << 32) | (uint32_t)~(uint32_t)(e + j));
+          }
+        }
+      };
+      each_token([&](uint64_t k) {
+        const uint32_t at = atomicAdd(&n_list, 1u);
+        if (at < kScoreList) list[at] = k;
+      });
+      __syncthreads();
+      uint32_t n = n_list;
+      if (n > kScoreList) {
+        // more candidates than the list holds: find the last alternative by radix search, list the N exactly
+        const uint64_t last = score_radix_select(each_token, (uint32_t)p.N, hist, bc);
+        if (threadIdx.x == 0) n_list = 0;
+        __syncthreads();
+        each_token([&](uint64_t k) {
+          if (k >= last) list[atomicAdd(&n_list, 1u)] = k;
+        });
+        __syncthreads();
+        n = n_list;
+      }
+      found = n < (uint32_t)p.N ? n : (uint32_t)p.N;
+      for (uint32_t i = threadIdx.x; i < n; i += kScoreFinishThreads) {
+        const uint64_t k = list[i];
+        uint32_t place = 0;
+        for (uint32_t j = 0; j < n; ++j) place += list[j] > k ? 1u : 0u;
+        if (place < (uint32_t)p.N) {
+          oi[place] = (int32_t)~(uint32_t)k;
+          const float s = (value_of_key32((uint32_t)(k >> 32)) - r.m) * r.invT;
+          ol[place] = fminf(s - r.logsum, 0.f);
+        }
+      }
+    }
+    for (uint32_t j = found + threadIdx.x; j < (uint32_t)p.N; j += kScoreFinishThreads) {
+      oi[j] = -1;
+      ol[j] = qnan;
+    }
+    __syncthreads();   // the next row reuses the shared arrays
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Gradient with respect to the logits: with g, h the gradients of the log-probability and the entropy,
+//   dx_v = [g (d_vt - p_v) - h p_v (log p_v + H)] / T,   p_v = e^s_v / S.
+// Elementwise: one read and one write of the row.
+// ------------------------------------------------------------------------------------------------
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 4;   // 16-byte vectors per thread
+
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGradParams p) {
+  using Ty = ScoreType<T>;
+  constexpr int64_t SPAN = (int64_t)kGradThreads * kGradVecs * Ty::VE;
+  const int64_t total = p.B * p.spans;
+  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
+    const int64_t row = id / p.spans;
+    const int64_t e0 = (id - row * p.spans) * SPAN;
+    const unsigned char* xr = p.x + row * p.ld * Ty::ES;
+    unsigned char* dr = p.dx + row * p.ldo * Ty::ES;
+    const int32_t t = p.token[row];
+    const bool skip = t == VSAMP_TOKEN_IGNORE;
+    const float temp = p.temperature ? p.temperature[row] : 1.f;
+    const float m = p.row_max[row], ls = p.row_logsum[row];
+    const float H = p.dentropy ? p.entropy[row] : 0.f;
+    const bool ok = t >= 0 && (int64_t)t < p.V && !isnan(temp) && !isinf(temp) && isfinite(m) && isfinite(ls) && isfinite(H);
+    const float invT = 1.f / (temp > 0.f ? temp : 1.f);
+    const float c = kLog2e / (temp > 0.f ? temp : 1.f);
+    const float invS = expf(-ls);
+    const float g = skip ? 0.f : p.dlogprob ? p.dlogprob[row] : 0.f;
+    const float h = skip || !p.dentropy ? 0.f : p.dentropy[row];
+    // d log p / dx in terms of q = e^s2, s2 = (x - m) c: p (g + h (s2 ln 2 - log S + H)) / T
+    const float k0 = (g + h * (H - ls)) * invT * invS;
+    const float k1 = h * 0.69314718056f * invT * invS;
+    const float gt = g * invT;
+    const float fill = skip ? 0.f : __int_as_float(0x7FC00000);
+    if (p.row_status && e0 == 0 && threadIdx.x == 0)
+      p.row_status[row] = skip || ok ? VSAMP_OK
+                          : (t >= 0 && (int64_t)t < p.V && !isnan(temp) && !isinf(temp)) ? VSAMP_ERR_NONFINITE
+                                                                                       : VSAMP_ERR_INVALID_ARG;
+    auto grad = [&](float x, int64_t v) -> float {
+      const float s = fmaxf((x - m) * c, -150.f);
+      const float q = ex2_approx(s);
+      const float d = -q * fmaf(k1, s, k0);
+      return v == t ? d + gt : d;
+    };
+    for (int64_t e = e0 + threadIdx.x; e < e0 + SPAN && e < p.V; e += kGradThreads)
+      Ty::store(dr, e, ok ? grad(Ty::load(xr, e), e) : fill);
+  }
+}
+
+}  // namespace vsamp
