@@ -1,4 +1,6 @@
 // vsamp_head_pack and vsamp_head_logits: argument checks and launches.
+#include <atomic>
+
 #include "vsamp_grid.h"
 #include "vsamp_head.cuh"
 #include "vsamp_host.h"
@@ -18,47 +20,56 @@ static bool head_shape(vsamp_dtype scale_dt, int32_t has_zeros, int64_t V, int64
   return true;
 }
 
-template <typename T, int NT, int SB, bool ZEROS>
-static vsamp_status launch_head_cfg(HeadParams p, const DeviceInfo& d, cudaStream_t stream) {
-  auto kern = head_kernel<T, NT, SB, ZEROS>;
-  const int64_t steps = p.s.blocks() * (kHeadBlock / 16);
-  const int64_t step_bytes = (int64_t)NT * kHeadTerms<T> * 256;
-  // chunks of a multiple of eight steps (a largest group) within half of an SM's shared memory, or all of it
-  int64_t most = (d.optin / 2) / step_bytes / 8 * 8;
-  if (steps > most && steps <= (int64_t)d.optin / step_bytes) most = steps;
-  if (most < 8) return VSAMP_ERR_UNSUPPORTED;
-  p.chunk = steps < most ? steps : most;
-  const int smem = (int)(p.chunk * step_bytes);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-    cudaGetLastError();
-    return VSAMP_ERR_CUDA;
+template <typename T, int NT, int RT, int GROUP, int PF>
+static vsamp_status launch_head_cfg(HeadParams p, const DeviceInfo& d, int dev, cudaStream_t stream) {
+  auto kern = head_kernel<T, NT, RT, GROUP, PF>;
+  // Warps share a row tile when there are not enough tiles for every warp of the device.
+  const int64_t sets = (p.s.tiles() + RT - 1) / RT;
+  const int64_t warps = (int64_t)d.sm_count * kHeadWarps;
+  p.split = 1;
+  while (p.split < kHeadWarps && sets * p.split * 2 <= warps && p.split * 2 <= p.units) p.split *= 2;
+  const int red = p.split > 1 ? kHeadWarps * RT * NT * 4 * 32 * 4 : 0;
+  const int64_t unit_bytes = (int64_t)kHeadUnitSteps * kHeadTerms<T> * p.rows * 32;
+  const int ring = kHeadWarps * PF * RT * p.s.record();
+  const int64_t most = (d.optin - red - ring) / unit_bytes;
+  if (most < 1) return VSAMP_ERR_UNSUPPORTED;
+  p.chunk = p.units <= most ? p.units : (int)most;
+  p.ring_off = (int)(p.chunk * unit_bytes);
+  p.red_off = p.ring_off + ring;
+  const int smem = p.red_off + red;
+  // the kernel's limit is raised to the device's once, so concurrent callers never lower it under each other
+  static std::atomic<bool> raised[64];
+  if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d.optin) != cudaSuccess) {
+      cudaGetLastError();
+      return VSAMP_ERR_CUDA;
+    }
+    if (dev < 64) raised[dev].store(true, std::memory_order_release);
   }
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kHeadWarps * 32, smem) != cudaSuccess || per_sm < 1) {
-    cudaGetLastError();
-    return VSAMP_ERR_CUDA;
-  }
-  const int64_t ctas = (p.s.tiles() + kHeadWarps - 1) / kHeadWarps;
-  const int64_t resident = (int64_t)per_sm * d.sm_count;
-  return launch_1d(kern, grid_of(ctas < resident ? ctas : resident), kHeadWarps * 32, (size_t)smem, stream, false, p);
+  const int64_t ctas = (sets * p.split + kHeadWarps - 1) / kHeadWarps;
+  return launch_1d(kern, grid_of(ctas < d.sm_count ? ctas : d.sm_count), kHeadWarps * 32, (size_t)smem, stream, false,
+                   p);
 }
 
-template <typename T, int NT>
-static vsamp_status launch_head_nt(const HeadParams& p, const DeviceInfo& d, cudaStream_t s) {
-  if (p.s.scale_bytes == 4)
-    return p.s.has_zeros ? launch_head_cfg<T, NT, 4, true>(p, d, s) : launch_head_cfg<T, NT, 4, false>(p, d, s);
-  return p.s.has_zeros ? launch_head_cfg<T, NT, 2, true>(p, d, s) : launch_head_cfg<T, NT, 2, false>(p, d, s);
+template <typename T, int NT, int RT, int PF>
+static vsamp_status launch_head_nt(const HeadParams& p, const DeviceInfo& d, int dev, cudaStream_t s) {
+  if (p.s.group == 32) return launch_head_cfg<T, NT, RT, 32, PF>(p, d, dev, s);
+  if (p.s.group == 64) return launch_head_cfg<T, NT, RT, 64, PF>(p, d, dev, s);
+  return launch_head_cfg<T, NT, RT, 128, PF>(p, d, dev, s);
 }
 
 template <typename T>
-static vsamp_status launch_head(HeadParams p, const DeviceInfo& d, cudaStream_t s) {
+static vsamp_status launch_head(HeadParams p, const DeviceInfo& d, int dev, cudaStream_t s) {
+  p.units = p.s.units();
+  p.vec = (reinterpret_cast<uintptr_t>(p.hidden) & 15u) == 0 && (p.ldh * sizeof(T)) % 16 == 0;
   for (int64_t m = 0; m < p.M; m += 64) {
     p.m0 = m;
     p.rows = (int)(p.M - m < 64 ? p.M - m : 64);
-    const vsamp_status st = p.rows <= 8    ? launch_head_nt<T, 1>(p, d, s)
-                            : p.rows <= 16 ? launch_head_nt<T, 2>(p, d, s)
-                            : p.rows <= 32 ? launch_head_nt<T, 4>(p, d, s)
-                                           : launch_head_nt<T, 8>(p, d, s);
+    const vsamp_status st = p.rows <= 8    ? launch_head_nt<T, 1, 1, 4>(p, d, dev, s)
+                            : p.rows <= 16 ? launch_head_nt<T, 2, 2, 2>(p, d, dev, s)
+                            : p.rows <= 24 ? launch_head_nt<T, 3, 2, 2>(p, d, dev, s)
+                            : p.rows <= 32 ? launch_head_nt<T, 4, 2, 2>(p, d, dev, s)
+                                           : launch_head_nt<T, 8, 1, 4>(p, d, dev, s);
     if (st != VSAMP_OK) return st;
   }
   return VSAMP_OK;
@@ -88,7 +99,7 @@ vsamp_status vsamp_head_pack(const uint8_t* codes, const void* scales, vsamp_dty
   p.scales = static_cast<const unsigned char*>(scales);
   p.zeros = zeros;
   p.packed = static_cast<unsigned char*>(packed);
-  return launch_1d(head_pack_kernel, grid_of((s.code_bytes() / 4 + 1023) / 1024), 256, 0,
+  return launch_1d(head_pack_kernel, grid_of((s.tiles() * s.blocks() * 128 + 1023) / 1024), 256, 0,
                    static_cast<cudaStream_t>(stream), false, p);
 }
 
@@ -122,7 +133,7 @@ vsamp_status vsamp_head_logits(const void* hidden, vsamp_dtype dt, int64_t M, in
   p.ld = ld;
   p.out_f32 = out_dt == VSAMP_F32;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  return dt == VSAMP_F32 ? launch_head<float>(p, d, cs) : launch_head<__nv_bfloat16>(p, d, cs);
+  return dt == VSAMP_F32 ? launch_head<float>(p, d, dev, cs) : launch_head<__nv_bfloat16>(p, d, dev, cs);
 }
 
 }  // extern "C"
