@@ -66,8 +66,9 @@ def test_head_refusals(lib):
                  (BF16, 0, 100, 128, 16), (BF16, 0, 100, 64, 128)):
         assert size(*args) == 0, args
     need = size(BF16, 1, 100, 128, 64)
-    # seven tiles of 16 rows, two blocks of 512 bytes each, two groups of 16 scales and 16 zero points
-    assert need == 7 * (2 * 512 + 2 * 16 * 2 + 2 * 16)
+    # seven tiles of 16 rows, two blocks of 512 bytes each, two groups of 16 scales and 16 zero points; one
+    # more record at the end
+    assert need == 8 * (2 * 512 + 2 * 16 * 2 + 2 * 16)
     pack = dict(c=P, s=P, sdt=BF16, z=P, V=100, D=128, g=64, out=P, n=need, stream=None)
     for change in (dict(c=None), dict(s=None), dict(out=None), dict(n=need - 1), dict(g=48), dict(D=96), dict(V=0),
                    dict(sdt=9), dict(s=ODD), dict(out=ctypes.c_void_p(4104))):

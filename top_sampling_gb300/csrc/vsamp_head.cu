@@ -29,7 +29,7 @@ static vsamp_status launch_head_cfg(HeadParams p, const DeviceInfo& d, int dev, 
   p.split = 1;
   while (p.split < kHeadWarps && sets * p.split * 2 <= warps && p.split * 2 <= p.units) p.split *= 2;
   const int red = p.split > 1 ? kHeadWarps * RT * NT * 4 * 32 * 4 : 0;
-  const int64_t unit_bytes = (int64_t)kHeadUnitSteps * kHeadTerms<T> * p.rows * 32;
+  const int64_t unit_bytes = (int64_t)kHeadUnitSteps * kHeadTerms<T> * NT * 8 * 32;
   const int ring = kHeadWarps * PF * RT * p.s.record();
   const int64_t most = (d.optin - red - ring) / unit_bytes;
   if (most < 1) return VSAMP_ERR_UNSUPPORTED;

@@ -17,7 +17,7 @@
 // of a word are one operand register:
 //   i = 0: row l/4,     columns 2 (l%4) + {0, 1}        i = 1: row l/4 + 8, the same columns
 //   i = 2: row l/4,     columns 2 (l%4) + 8 + {0, 1}    i = 3: row l/4 + 8, the same columns
-// The last record of a tile has only the blocks and groups that D reaches.
+// The last record of a tile has only the blocks and groups that D reaches. One record of slack ends the buffer.
 #pragma once
 
 #include "vsamp.h"
@@ -43,7 +43,8 @@ struct HeadShape {
   // bytes of a whole record, and of a tile (all of its records)
   __host__ __device__ int record() const { return 1024 + kHeadUnit / group * group_bytes(); }
   __host__ __device__ int64_t tile_bytes() const { return (int64_t)blocks() * 512 + (int64_t)groups() * group_bytes(); }
-  __host__ __device__ int64_t total() const { return tiles() * tile_bytes(); }
+  // one record of slack: a warp fetches whole records, also where a tile's last one is shorter
+  __host__ __device__ int64_t total() const { return tiles() * tile_bytes() + record(); }
 };
 
 struct HeadPackParams {
@@ -138,9 +139,10 @@ template <typename T>
 constexpr int kHeadTerms = sizeof(T) == 4 ? 3 : 1;
 
 // Stages the hidden states of units [u0, u1) as the instruction's second operand. In step k, lane l needs hidden row
-// 8 n + l/4 at inner positions 2 (l%4) + {0, 1} and + 8; they are stored as [step][term][row][l%4], two registers
-// each, so a row's 16 positions of a step are 32 contiguous bytes. Positions beyond D are 0.
-template <typename T>
+// 8 n + l/4 at inner positions 2 (l%4) + {0, 1} and + 8; they are stored as [step][term][8 NT rows][l%4], two registers
+// each, so a row's 16 positions of a step are 32 contiguous bytes and the reads have constant offsets. Positions
+// beyond D are 0; the places of rows beyond p.rows are not written (their columns of the product are not used).
+template <typename T, int NT>
 __device__ __forceinline__ void head_stage(const HeadParams& p, uint4* sh, int u0, int u1) {
   constexpr int TERMS = kHeadTerms<T>;
   const int rows = p.rows, n = (u1 - u0) * kHeadUnitSteps * rows;
@@ -192,7 +194,7 @@ __device__ __forceinline__ void head_stage(const HeadParams& p, uint4* sh, int u
     }
 #pragma unroll
     for (int q = 0; q < TERMS; ++q) {
-      uint4* to = sh + ((int64_t)(ks * TERMS + q) * rows + r) * 2;
+      uint4* to = sh + ((ks * TERMS + q) * (8 * NT) + r) * 2;
       to[0] = make_uint4(w[q][0], w[q][4], w[q][1], w[q][5]);
       to[1] = make_uint4(w[q][2], w[q][6], w[q][3], w[q][7]);
     }
@@ -212,7 +214,6 @@ __device__ __forceinline__ void copy_async_wait() {
 // RT tiles of 16 vocabulary rows per warp, NT tiles of 8 hidden rows. Every warp streams the records of its row tiles
 // through a ring of PF slots in shared memory (PF records of each tile in flight, no registers held by loads), across
 // the ends of tiles. p.split warps of a CTA share a set of row tiles, each with a contiguous part of its units.
-// Columns of hidden rows beyond p.rows repeat the last row and are not written.
 template <typename T, int NT, int RT, int GROUP, int PF>
 __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadParams p) {
   constexpr int TERMS = kHeadTerms<T>;
@@ -233,47 +234,56 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
   unsigned char* ring = head_smem + p.ring_off + (size_t)warp * PF * RT * record;
   const uint32_t ring_a = smem_addr(ring);
   const uint2* sh = reinterpret_cast<const uint2*>(head_smem);
-  uint32_t row_off[NT];                                   // this lane's place in a step of the staged states
-#pragma unroll
-  for (int n = 0; n < NT; ++n) row_off[n] = (uint32_t)(min(8 * n + (lane >> 2), rows - 1) * 4 + (lane & 3));
+  const uint32_t gsel = lane >> 2;
 
   // this warp's units [lo, hi) of the chunk that begins at unit c
   auto lo_of = [&](int c) { return c + min(p.chunk, p.units - c) * part_of / p.split; };
   auto hi_of = [&](int c) { return c + min(p.chunk, p.units - c) * (part_of + 1) / p.split; };
-  // the next record to fetch: tile, chunk, unit
+  // the next record to fetch: its tile and chunk, its address for this lane, the records left in this run of units
   int64_t f_tile = first0;
-  int f_chunk = 0, f_unit = lo_of(0), f_slot = 0;
+  int f_chunk = 0, f_left = 0;
+  const unsigned char* f_src[RT];
+  uint32_t f_dst = ring_a + lane * 16;
+  const uint32_t f_end = f_dst + PF * RT * record;
+  const bool tail_lane = 1024 + lane * 16 < record;       // this lane has 16 of the record's bytes beyond the codes
+  auto seek = [&]() {
+    f_left = hi_of(f_chunk) - lo_of(f_chunk);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      // tiles past the last one repeat it: their rows are not written
+      const int64_t tile = f_tile + mine + t < nt ? f_tile + mine + t : nt - 1;
+      f_src[t] = p.packed + tile * tile_bytes + (int64_t)lo_of(f_chunk) * record + lane * 16;
+    }
+  };
   auto fetch = [&]() {
-    while (f_tile < nt && f_unit >= hi_of(f_chunk)) {     // past this chunk: the next one, or the next tile's first
+    while (f_left == 0 && f_tile < nt) {                  // the next chunk, or the next tile's first
       f_chunk += p.chunk;
       if (f_chunk >= p.units) {
         f_chunk = 0;
         f_tile += stride;
       }
-      f_unit = lo_of(f_chunk);
+      if (f_tile < nt) seek();
     }
-    if (f_tile < nt) {
-      const int blocks = min(nb - 2 * f_unit, 2);
-      const int bytes = blocks * 512 + min(ng - f_unit * NG, NG) * s.group_bytes();
+    if (f_left > 0) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        const int64_t tile = f_tile + mine + t;
-        if (tile < nt) {
-          const unsigned char* src = p.packed + tile * tile_bytes + (int64_t)f_unit * record + lane * 16;
-          const uint32_t dst = ring_a + (uint32_t)((f_slot * RT + t) * record + lane * 16);
-          copy_async_16(dst, src);
-          if (lane * 16 + 512 < bytes) copy_async_16(dst + 512, src + 512);
-          if (lane * 16 + 1024 < bytes) copy_async_16(dst + 1024, src + 1024);
-        }
+        const uint32_t dst = f_dst + t * record;
+        copy_async_16(dst, f_src[t]);
+        copy_async_16(dst + 512, f_src[t] + 512);
+        if (tail_lane) copy_async_16(dst + 1024, f_src[t] + 1024);
+        f_src[t] += record;
       }
-      ++f_unit;
+      --f_left;
     }
     copy_async_commit();
-    f_slot = f_slot + 1 == PF ? 0 : f_slot + 1;
+    f_dst += RT * record;
+    if (f_dst == f_end) f_dst = ring_a + lane * 16;
   };
+  seek();
 #pragma unroll
   for (int i = 0; i < PF; ++i) fetch();
-  int slot = 0;
+  const unsigned char* rec = ring;
+  const unsigned char* const ring_end = ring + (size_t)PF * RT * record;
 
   for (int64_t first = first0; first < nt; first += stride) {
     const int64_t tile = first + mine;
@@ -287,15 +297,14 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
     for (int c0 = 0; c0 < p.units; c0 += p.chunk) {
       if (p.chunk < p.units || first == first0) {
         __syncthreads();   // the last chunk has been read
-        head_stage<T>(p, reinterpret_cast<uint4*>(head_smem), c0, min(c0 + p.chunk, p.units));
+        head_stage<T, NT>(p, reinterpret_cast<uint4*>(head_smem), c0, min(c0 + p.chunk, p.units));
         __syncthreads();
       }
       const int u1 = hi_of(c0);
       for (int u = lo_of(c0); u < u1; ++u) {
         copy_async_wait<PF - 1>();
         __syncwarp();
-        const unsigned char* rec = ring + (size_t)slot * RT * record;
-        const uint2* su = sh + (size_t)(u - c0) * (kHeadUnitSteps * TERMS * 4) * rows;
+        const uint2* su = sh + (u - c0) * (kHeadUnitSteps * TERMS * 32 * NT) + lane;
         const int blocks = min(nb - 2 * u, 2), groups = min(ng - u * NG, NG);
         float part[RT][NT][4];
         uint4 q4[RT];
@@ -308,18 +317,18 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
             for (int t = 0; t < RT; ++t) {
               const unsigned char* sc = rec + t * record + blocks * 512;
               if (s.scale_bytes == 4) {
-                const float2 v = reinterpret_cast<const float2*>(sc + g * gb)[lane >> 2];
+                const float2 v = reinterpret_cast<const float2*>(sc + g * gb)[gsel];
                 slo[t] = v.x;
                 shi[t] = v.y;
               } else {
-                const uint32_t v = reinterpret_cast<const uint32_t*>(sc + g * gb)[lane >> 2];
+                const uint32_t v = reinterpret_cast<const uint32_t*>(sc + g * gb)[gsel];
                 slo[t] = __uint_as_float(v << 16);
                 shi[t] = __uint_as_float(v & 0xFFFF0000u);
               }
               // 128 + zero point as bf16, twice
               zlo[t] = zhi[t] = 0x43084308u;
               if (s.has_zeros) {
-                const uint32_t z = reinterpret_cast<const unsigned short*>(sc + groups * gb + g * 16)[lane >> 2];
+                const uint32_t z = reinterpret_cast<const unsigned short*>(sc + groups * gb + g * 16)[gsel];
                 zlo[t] = 0x43004300u + (z & 0xFFu) * 0x00010001u;
                 zhi[t] = 0x43004300u + (z >> 8) * 0x00010001u;
               }
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
 #pragma unroll
               for (int q = 0; q < TERMS; ++q)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) h[n][q] = su[(uint32_t)((k * TERMS + q) * 4) * rows + row_off[n]];
+                for (int n = 0; n < NT; ++n) h[n][q] = su[((k * TERMS + q) * NT + n) * 32];
 #pragma unroll
               for (int t = 0; t < RT; ++t) {
                 if (k % 4 == 0) q4[t] = reinterpret_cast<const uint4*>(rec + t * record)[(k / 4) * 32 + lane];
@@ -364,7 +373,8 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
         }
         __syncwarp();   // every lane has read the slot
         fetch();
-        slot = slot + 1 == PF ? 0 : slot + 1;
+        rec += RT * record;
+        if (rec == ring_end) rec = ring;
       }
     }
     if (p.split > 1) {
