@@ -134,6 +134,13 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// (w & mask) | base: one instruction when both constants are in registers
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t base) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(base));
+  return r;
+}
+
 // bf16 terms per hidden value: x = hi + mid + lo for fp32, each the bf16 nearest to what is left (24 bits in all).
 template <typename T>
 constexpr int kHeadTerms = sizeof(T) == 4 ? 3 : 1;
@@ -235,6 +242,10 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
   const uint32_t ring_a = smem_addr(ring);
   const uint2* sh = reinterpret_cast<const uint2*>(head_smem);
   const uint32_t gsel = lane >> 2;
+  // two nibbles of a word, and 128 as bf16 twice; opaque, so that both stay in registers
+  uint32_t nibbles, base;
+  asm volatile("mov.b32 %0, 0x000F000F;" : "=r"(nibbles));
+  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(base));
 
   // this warp's units [lo, hi) of the chunk that begins at unit c
   auto lo_of = [&](int c) { return c + min(p.chunk, p.units - c) * part_of / p.split; };
@@ -346,10 +357,10 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
                 if (k % 4 == 0) q4[t] = reinterpret_cast<const uint4*>(rec + t * record)[(k / 4) * 32 + lane];
                 const uint32_t w = k % 4 == 0 ? q4[t].x : k % 4 == 1 ? q4[t].y : k % 4 == 2 ? q4[t].z : q4[t].w;
                 // 128 + q as bf16, minus 128 + zero point: exact
-                const uint32_t a0 = sub_bf16x2((w & 0x000F000Fu) | 0x43004300u, zlo[t]);
-                const uint32_t a1 = sub_bf16x2(((w >> 4) & 0x000F000Fu) | 0x43004300u, zhi[t]);
-                const uint32_t a2 = sub_bf16x2(((w >> 8) & 0x000F000Fu) | 0x43004300u, zlo[t]);
-                const uint32_t a3 = sub_bf16x2(((w >> 12) & 0x000F000Fu) | 0x43004300u, zhi[t]);
+                const uint32_t a0 = sub_bf16x2(and_or(w, nibbles, base), zlo[t]);
+                const uint32_t a1 = sub_bf16x2(and_or(w >> 4, nibbles, base), zhi[t]);
+                const uint32_t a2 = sub_bf16x2(and_or(w >> 8, nibbles, base), zlo[t]);
+                const uint32_t a3 = sub_bf16x2(and_or(w >> 12, nibbles, base), zhi[t]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                   float (&d)[4] = part[t][n];
