@@ -223,6 +223,7 @@ __device__ __forceinline__ void copy_async_wait() {
 // the ends of tiles. p.split warps of a CTA share a set of row tiles, each with a contiguous part of its units.
 template <typename T, int NT, int RT, int GROUP, int PF>
 __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadParams p) {
+  static_assert((PF & (PF - 1)) == 0, "slots are taken in turn by masking");
   constexpr int TERMS = kHeadTerms<T>;
   constexpr int GS = GROUP / 16;          // steps per group
   constexpr int NG = kHeadUnit / GROUP;   // groups per unit
@@ -238,9 +239,10 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
   const int rows = p.rows;
   const int gb = s.scale_bytes * 16;                      // bytes of a group's scales
 
-  unsigned char* ring = head_smem + p.ring_off + (size_t)warp * PF * RT * record;
-  const uint32_t ring_a = smem_addr(ring);
-  const uint2* sh = reinterpret_cast<const uint2*>(head_smem);
+  const uint32_t slot_bytes = (uint32_t)(RT * record);
+  const uint32_t ring = (uint32_t)p.ring_off + (uint32_t)warp * PF * slot_bytes;   // this warp's ring, from head_smem
+  const uint32_t smem0 = smem_addr(head_smem);
+
   const uint32_t gsel = lane >> 2;
   // two nibbles of a word, and 128 as bf16 twice; opaque, so that both stay in registers
   uint32_t nibbles, base;
@@ -254,8 +256,6 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
   int64_t f_tile = first0;
   int f_chunk = 0, f_left = 0;
   const unsigned char* f_src[RT];
-  uint32_t f_dst = ring_a + lane * 16;
-  const uint32_t f_end = f_dst + PF * RT * record;
   const bool tail_lane = 1024 + lane * 16 < record;       // this lane has 16 of the record's bytes beyond the codes
   auto seek = [&]() {
     f_left = hi_of(f_chunk) - lo_of(f_chunk);
@@ -266,35 +266,36 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
       f_src[t] = p.packed + tile * tile_bytes + (int64_t)lo_of(f_chunk) * record + lane * 16;
     }
   };
-  auto fetch = [&]() {
-    while (f_left == 0 && f_tile < nt) {                  // the next chunk, or the next tile's first
+  auto next_run = [&]() {                                 // the next chunk, or the next tile's first
+    while (f_left == 0) {
       f_chunk += p.chunk;
       if (f_chunk >= p.units) {
         f_chunk = 0;
         f_tile += stride;
+        if (f_tile >= nt) return;
       }
-      if (f_tile < nt) seek();
+      seek();
     }
+  };
+  auto fetch = [&](uint32_t slot) {                       // the next record of every row tile into a slot of the ring
     if (f_left > 0) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        const uint32_t dst = f_dst + t * record;
+        const uint32_t dst = smem0 + slot + t * record + lane * 16;
         copy_async_16(dst, f_src[t]);
         copy_async_16(dst + 512, f_src[t] + 512);
         if (tail_lane) copy_async_16(dst + 1024, f_src[t] + 1024);
         f_src[t] += record;
       }
-      --f_left;
+      if (--f_left == 0) next_run();
     }
     copy_async_commit();
-    f_dst += RT * record;
-    if (f_dst == f_end) f_dst = ring_a + lane * 16;
   };
   seek();
+  if (f_left == 0) next_run();
 #pragma unroll
-  for (int i = 0; i < PF; ++i) fetch();
-  const unsigned char* rec = ring;
-  const unsigned char* const ring_end = ring + (size_t)PF * RT * record;
+  for (int i = 0; i < PF; ++i) fetch(ring + i * slot_bytes);
+  uint32_t turn = 0;
 
   for (int64_t first = first0; first < nt; first += stride) {
     const int64_t tile = first + mine;
@@ -315,8 +316,10 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
       for (int u = lo_of(c0); u < u1; ++u) {
         copy_async_wait<PF - 1>();
         __syncwarp();
-        const uint2* su = sh + (u - c0) * (kHeadUnitSteps * TERMS * 32 * NT) + lane;
-        const int blocks = min(nb - 2 * u, 2), groups = min(ng - u * NG, NG);
+        const uint32_t rec = ring + (turn++ & (PF - 1)) * slot_bytes;
+        const uint2* su = reinterpret_cast<const uint2*>(head_smem) + (u - c0) * (kHeadUnitSteps * TERMS * 32 * NT) + lane;
+        // a group of 128 fills a record, smaller ones may leave the last record with fewer blocks and groups
+        const int blocks = NG == 1 ? 2 : min(nb - 2 * u, 2), groups = min(ng - u * NG, NG);
         float part[RT][NT][4];
         uint4 q4[RT];
 #pragma unroll
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
             uint32_t zlo[RT], zhi[RT];
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-              const unsigned char* sc = rec + t * record + blocks * 512;
+              const unsigned char* sc = head_smem + rec + t * record + blocks * 512;
               if (s.scale_bytes == 4) {
                 const float2 v = reinterpret_cast<const float2*>(sc + g * gb)[gsel];
                 slo[t] = v.x;
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
                 for (int n = 0; n < NT; ++n) h[n][q] = su[((k * TERMS + q) * NT + n) * 32];
 #pragma unroll
               for (int t = 0; t < RT; ++t) {
-                if (k % 4 == 0) q4[t] = reinterpret_cast<const uint4*>(rec + t * record)[(k / 4) * 32 + lane];
+                if (k % 4 == 0) q4[t] = reinterpret_cast<const uint4*>(head_smem + rec + t * record)[(k / 4) * 32 + lane];
                 const uint32_t w = k % 4 == 0 ? q4[t].x : k % 4 == 1 ? q4[t].y : k % 4 == 2 ? q4[t].z : q4[t].w;
                 // 128 + q as bf16, minus 128 + zero point: exact
                 const uint32_t a0 = sub_bf16x2(and_or(w, nibbles, base), zlo[t]);
@@ -383,9 +386,7 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
           }
         }
         __syncwarp();   // every lane has read the slot
-        fetch();
-        rec += RT * record;
-        if (rec == ring_end) rec = ring;
+        fetch(rec);
       }
     }
     if (p.split > 1) {
