@@ -1,11 +1,49 @@
 // vsamp_head_pack and vsamp_head_logits: argument checks and launches.
-#include <atomic>
-
 #include "vsamp_grid.h"
-#include "vsamp_head.cuh"
-#include "vsamp_host.h"
+#include "vsamp_head_launch.cuh"
 
 namespace vsamp {
+
+// One thread per 32-bit word of codes, then per scale and zero point.
+__global__ void __launch_bounds__(256) head_pack_kernel(const HeadPackParams p) {
+  const HeadShape s = p.s;
+  const int64_t nb = s.blocks(), ng = s.groups(), per_unit = kHeadUnit / s.group;
+  const int64_t words = s.tiles() * nb * 128, scales = s.tiles() * ng * 16;
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  for (int64_t i = first; i < words; i += stride) {
+    // word i: tile, block, lane, step
+    const int step = (int)(i & 3), lane = (int)((i >> 2) & 31);
+    const int64_t blk = (i >> 7) % nb, tile = (i >> 7) / nb;
+    uint32_t word = 0;
+    for (int n = 0; n < 8; ++n) {
+      const int pair = n & 3, hi = n >> 2;
+      const int64_t row = tile * 16 + (lane >> 2) + (pair & 1) * 8;
+      const int64_t k = blk * kHeadBlock + step * 16 + (lane & 3) * 2 + (pair >> 1) * 8 + hi;
+      uint32_t q = 0;
+      if (row < s.V && k < s.D) q = (p.codes[row * (s.D / 2) + k / 2] >> ((k & 1) * 4)) & 15u;
+      word |= q << (n * 4);
+    }
+    unsigned char* rec = p.packed + tile * s.tile_bytes() + (blk / 2) * s.record();
+    reinterpret_cast<uint32_t*>(rec)[(blk & 1) * 128 + (i & 127)] = word;
+  }
+  for (int64_t i = first; i < scales; i += stride) {
+    // scale i: tile, group, row and row + 8
+    const int64_t tile = i / (ng * 16), g = (i / 16) % ng, unit = g / per_unit;
+    const int64_t row = tile * 16 + ((i >> 1) & 7) + (i & 1) * 8;
+    const bool in = row < s.V;
+    const int64_t rec_blocks = nb - 2 * unit < 2 ? nb - 2 * unit : 2;
+    const int64_t rec_groups = ng - unit * per_unit < per_unit ? ng - unit * per_unit : per_unit;
+    unsigned char* at = p.packed + tile * s.tile_bytes() + unit * s.record() + rec_blocks * 512;
+    const int64_t j = (g - unit * per_unit) * 16 + (i & 15);
+    if (s.scale_bytes == 4)
+      reinterpret_cast<uint32_t*>(at)[j] = in ? reinterpret_cast<const uint32_t*>(p.scales)[row * ng + g] : 0u;
+    else
+      reinterpret_cast<unsigned short*>(at)[j] =
+          in ? reinterpret_cast<const unsigned short*>(p.scales)[row * ng + g] : (unsigned short)0;
+    if (s.has_zeros) at[rec_groups * 16 * s.scale_bytes + j] = in ? (p.zeros[row * ng + g] & 15u) : 0;
+  }
+}
 
 // The shape of packed weights, or false for arguments that have none.
 static bool head_shape(vsamp_dtype scale_dt, int32_t has_zeros, int64_t V, int64_t D, int32_t group, HeadShape& s) {
@@ -20,56 +58,16 @@ static bool head_shape(vsamp_dtype scale_dt, int32_t has_zeros, int64_t V, int64
   return true;
 }
 
-template <typename T, int NT, int RT, int GROUP, int PF>
-static vsamp_status launch_head_cfg(HeadParams p, const DeviceInfo& d, int dev, cudaStream_t stream) {
-  auto kern = head_kernel<T, NT, RT, GROUP, PF>;
-  // Warps share a row tile when there are not enough tiles for every warp of the device.
-  const int64_t sets = (p.s.tiles() + RT - 1) / RT;
-  const int64_t warps = (int64_t)d.sm_count * kHeadWarps;
-  p.split = 1;
-  while (p.split < kHeadWarps && sets * p.split * 2 <= warps && p.split * 2 <= p.units) p.split *= 2;
-  const int red = p.split > 1 ? kHeadWarps * RT * NT * 4 * 32 * 4 : 0;
-  const int64_t unit_bytes = (int64_t)kHeadUnitSteps * kHeadTerms<T> * NT * 8 * 32;
-  const int ring = kHeadWarps * PF * RT * p.s.record();
-  const int64_t most = (d.optin - red - ring) / unit_bytes;
-  if (most < 1) return VSAMP_ERR_UNSUPPORTED;
-  p.chunk = p.units <= most ? p.units : (int)most;
-  p.ring_off = (int)(p.chunk * unit_bytes);
-  p.red_off = p.ring_off + ring;
-  const int smem = p.red_off + red;
-  // the kernel's limit is raised to the device's once, so concurrent callers never lower it under each other
-  static std::atomic<bool> raised[64];
-  if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, d.optin) != cudaSuccess) {
-      cudaGetLastError();
-      return VSAMP_ERR_CUDA;
-    }
-    if (dev < 64) raised[dev].store(true, std::memory_order_release);
-  }
-  const int64_t ctas = (sets * p.split + kHeadWarps - 1) / kHeadWarps;
-  return launch_1d(kern, grid_of(ctas < d.sm_count ? ctas : d.sm_count), kHeadWarps * 32, (size_t)smem, stream, false,
-                   p);
-}
-
-template <typename T, int NT, int RT, int PF>
-static vsamp_status launch_head_nt(const HeadParams& p, const DeviceInfo& d, int dev, cudaStream_t s) {
-  if (p.s.group == 32) return launch_head_cfg<T, NT, RT, 32, PF>(p, d, dev, s);
-  if (p.s.group == 64) return launch_head_cfg<T, NT, RT, 64, PF>(p, d, dev, s);
-  return launch_head_cfg<T, NT, RT, 128, PF>(p, d, dev, s);
-}
-
-template <typename T>
 static vsamp_status launch_head(HeadParams p, const DeviceInfo& d, int dev, cudaStream_t s) {
   p.units = p.s.units();
-  p.vec = (reinterpret_cast<uintptr_t>(p.hidden) & 15u) == 0 && (p.ldh * sizeof(T)) % 16 == 0;
-  for (int64_t m = 0; m < p.M; m += 64) {
+  const int most = p.terms == 3 ? 16 : 64;   // hidden rows per launch: at most 8 column tiles (6 of fp32 terms)
+  for (int64_t m = 0; m < p.M; m += most) {
     p.m0 = m;
-    p.rows = (int)(p.M - m < 64 ? p.M - m : 64);
-    const vsamp_status st = p.rows <= 8    ? launch_head_nt<T, 1, 1, 4>(p, d, dev, s)
-                            : p.rows <= 16 ? launch_head_nt<T, 2, 2, 2>(p, d, dev, s)
-                            : p.rows <= 24 ? launch_head_nt<T, 3, 2, 2>(p, d, dev, s)
-                            : p.rows <= 32 ? launch_head_nt<T, 4, 2, 2>(p, d, dev, s)
-                                           : launch_head_nt<T, 8, 1, 4>(p, d, dev, s);
+    p.rows = (int)(p.M - m < most ? p.M - m : most);
+    p.term_tiles = (p.rows + 7) / 8;
+    const vsamp_status st = p.s.group == 32   ? launch_head_group<32>(p, d, dev, s)
+                            : p.s.group == 64 ? launch_head_group<64>(p, d, dev, s)
+                                              : launch_head_group<128>(p, d, dev, s);
     if (st != VSAMP_OK) return st;
   }
   return VSAMP_OK;
@@ -133,7 +131,9 @@ vsamp_status vsamp_head_logits(const void* hidden, vsamp_dtype dt, int64_t M, in
   p.ld = ld;
   p.out_f32 = out_dt == VSAMP_F32;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  return dt == VSAMP_F32 ? launch_head<float>(p, d, dev, cs) : launch_head<__nv_bfloat16>(p, d, dev, cs);
+  p.terms = dt == VSAMP_F32 ? 3 : 1;
+  p.vec = (reinterpret_cast<uintptr_t>(hidden) & 15u) == 0 && (ldh * 2) % 16 == 0;
+  return launch_head(p, d, dev, cs);
 }
 
 }  // extern "C"

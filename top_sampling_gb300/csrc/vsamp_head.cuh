@@ -25,7 +25,6 @@
 
 namespace vsamp {
 
-constexpr int kHeadWarps = 16;
 constexpr int kHeadBlock = 64;      // inner elements per block of a tile
 constexpr int kHeadUnit = 128;      // inner elements a warp processes at once: two blocks, the largest group
 constexpr int kHeadUnitSteps = kHeadUnit / 16;
@@ -65,6 +64,8 @@ struct HeadParams {
   int out_f32;
   int64_t m0;      // first hidden row of this launch
   int rows;        // hidden rows of this launch
+  int terms;       // bf16 terms of a hidden value (1, or 3 for fp32)
+  int term_tiles;  // column tiles per term: term q of hidden row r is column q * 8 * term_tiles + r
   int vec;         // hidden rows are 16-byte aligned
   int units;       // units of the inner dimension (the last one may be padded)
   int chunk;       // units of hidden states staged at once
@@ -73,51 +74,10 @@ struct HeadParams {
   int split;       // warps that share a row tile, each with its part of the inner dimension
 };
 
-// One thread per 32-bit word of codes, then per scale and zero point.
-__global__ void __launch_bounds__(256) head_pack_kernel(const HeadPackParams p) {
-  const HeadShape s = p.s;
-  const int64_t nb = s.blocks(), ng = s.groups(), per_unit = kHeadUnit / s.group;
-  const int64_t words = s.tiles() * nb * 128, scales = s.tiles() * ng * 16;
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  for (int64_t i = first; i < words; i += stride) {
-    // word i: tile, block, lane, step
-    const int step = (int)(i & 3), lane = (int)((i >> 2) & 31);
-    const int64_t blk = (i >> 7) % nb, tile = (i >> 7) / nb;
-    uint32_t word = 0;
-    for (int n = 0; n < 8; ++n) {
-      const int pair = n & 3, hi = n >> 2;
-      const int64_t row = tile * 16 + (lane >> 2) + (pair & 1) * 8;
-      const int64_t k = blk * kHeadBlock + step * 16 + (lane & 3) * 2 + (pair >> 1) * 8 + hi;
-      uint32_t q = 0;
-      if (row < s.V && k < s.D) q = (p.codes[row * (s.D / 2) + k / 2] >> ((k & 1) * 4)) & 15u;
-      word |= q << (n * 4);
-    }
-    unsigned char* rec = p.packed + tile * s.tile_bytes() + (blk / 2) * s.record();
-    reinterpret_cast<uint32_t*>(rec)[(blk & 1) * 128 + (i & 127)] = word;
-  }
-  for (int64_t i = first; i < scales; i += stride) {
-    // scale i: tile, group, row and row + 8
-    const int64_t tile = i / (ng * 16), g = (i / 16) % ng, unit = g / per_unit;
-    const int64_t row = tile * 16 + ((i >> 1) & 7) + (i & 1) * 8;
-    const bool in = row < s.V;
-    const int64_t rec_blocks = nb - 2 * unit < 2 ? nb - 2 * unit : 2;
-    const int64_t rec_groups = ng - unit * per_unit < per_unit ? ng - unit * per_unit : per_unit;
-    unsigned char* at = p.packed + tile * s.tile_bytes() + unit * s.record() + rec_blocks * 512;
-    const int64_t j = (g - unit * per_unit) * 16 + (i & 15);
-    if (s.scale_bytes == 4)
-      reinterpret_cast<uint32_t*>(at)[j] = in ? reinterpret_cast<const uint32_t*>(p.scales)[row * ng + g] : 0u;
-    else
-      reinterpret_cast<unsigned short*>(at)[j] =
-          in ? reinterpret_cast<const unsigned short*>(p.scales)[row * ng + g] : (unsigned short)0;
-    if (s.has_zeros) at[rec_groups * 16 * s.scale_bytes + j] = in ? (p.zeros[row * ng + g] & 15u) : 0;
-  }
-}
-
 // D = A B + C on 16 x 16 by 16 x 8 bf16 operands, fp32 sums
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b,
                                          float c0, float c1, float c2, float c3) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -141,69 +101,64 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
   return r;
 }
 
-// bf16 terms per hidden value: x = hi + mid + lo for fp32, each the bf16 nearest to what is left (24 bits in all).
-template <typename T>
-constexpr int kHeadTerms = sizeof(T) == 4 ? 3 : 1;
+// (a0, a1) += s * (b0, b1), two fused multiply-adds in one instruction
+__device__ __forceinline__ void fma_pair(float& a0, float& a1, float s, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, s;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
+      "fma.rn.f32x2 a, s, b, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1), "f"(s));
+}
 
-// Stages the hidden states of units [u0, u1) as the instruction's second operand. In step k, lane l needs hidden row
-// 8 n + l/4 at inner positions 2 (l%4) + {0, 1} and + 8; they are stored as [step][term][8 NT rows][l%4], two registers
-// each, so a row's 16 positions of a step are 32 contiguous bytes and the reads have constant offsets. Positions
-// beyond D are 0; the places of rows beyond p.rows are not written (their columns of the product are not used).
-template <typename T, int NT>
+// Stages the hidden states of units [u0, u1) as the instruction's second operand, NT column tiles of 8. In step k, lane
+// l needs column 8 n + l/4 at inner positions 2 (l%4) + {0, 1} and + 8; they are stored as [step][8 NT columns][l%4], two
+// registers each, so a column's 16 positions of a step are 32 contiguous bytes and the reads have constant offsets. A
+// bf16 row is a column; an fp32 row is three (x = hi + mid + lo, each the bf16 nearest to what is left: 24 bits in
+// all), in column tiles of their own, so that one lane holds the sums of all three. Positions beyond D are 0; columns
+// without a row are not written (their part of the product is not used).
+template <int NT>
 __device__ __forceinline__ void head_stage(const HeadParams& p, uint4* sh, int u0, int u1) {
-  constexpr int TERMS = kHeadTerms<T>;
-  const int rows = p.rows, n = (u1 - u0) * kHeadUnitSteps * rows;
+  const int rows = p.rows, steps = (u1 - u0) * kHeadUnitSteps, n = steps * rows;
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     // neighbouring threads take neighbouring steps of a row: its bytes are read in order
-    const int steps = (u1 - u0) * kHeadUnitSteps;
     const int r = i / steps, ks = i - r * steps;
     const int64_t k = (int64_t)u0 * kHeadUnit + ks * 16;
-    const unsigned char* src = p.hidden + ((p.m0 + r) * p.ldh + k) * (int64_t)sizeof(T);
     const bool whole = p.vec && k + 16 <= p.s.D;
-    uint32_t w[TERMS][8];   // pairs of neighbouring positions
-    if constexpr (TERMS == 1) {
+    uint4* to = sh + (ks * (8 * NT) + r) * 2;
+    if (p.terms == 1) {
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(p.hidden) + (p.m0 + r) * p.ldh + k;
+      uint32_t w[8];   // pairs of neighbouring positions
       if (whole) {
-        const uint4 a = reinterpret_cast<const uint4*>(src)[0], b = reinterpret_cast<const uint4*>(src)[1];
-        w[0][0] = a.x; w[0][1] = a.y; w[0][2] = a.z; w[0][3] = a.w;
-        w[0][4] = b.x; w[0][5] = b.y; w[0][6] = b.z; w[0][7] = b.w;
+        const uint4 a = reinterpret_cast<const uint4*>(h)[0], b = reinterpret_cast<const uint4*>(h)[1];
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
       } else {
-        const unsigned short* h = reinterpret_cast<const unsigned short*>(src);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          w[0][e] = (k + 2 * e < p.s.D ? h[2 * e] : 0u) | (uint32_t)(k + 2 * e + 1 < p.s.D ? h[2 * e + 1] : 0u) << 16;
+          w[e] = (k + 2 * e < p.s.D ? h[2 * e] : 0u) | (uint32_t)(k + 2 * e + 1 < p.s.D ? h[2 * e + 1] : 0u) << 16;
       }
+      to[0] = make_uint4(w[0], w[4], w[1], w[5]);
+      to[1] = make_uint4(w[2], w[6], w[3], w[7]);
     } else {
-      const float* h = reinterpret_cast<const float*>(src);
+      const float* h = reinterpret_cast<const float*>(p.hidden) + (p.m0 + r) * p.ldh + k;
+      float x[16];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float x[2];
-        if (whole) {
-          const float2 v = reinterpret_cast<const float2*>(src)[e];
-          x[0] = v.x;
-          x[1] = v.y;
-        } else {
-          x[0] = k + 2 * e < p.s.D ? h[2 * e] : 0.f;
-          x[1] = k + 2 * e + 1 < p.s.D ? h[2 * e + 1] : 0.f;
+      for (int e = 0; e < 16; ++e) x[e] = k + e < p.s.D ? h[e] : 0.f;
+      for (int q = 0; q < 3; ++q) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const __nv_bfloat16 v = __float2bfloat16_rn(x[e]);
+          const uint32_t bits = (uint32_t)__bfloat16_as_ushort(v);
+          if (e & 1) w[e / 2] |= bits << 16;
+          else w[e / 2] = bits;
+          // an infinity has no remainder (inf - inf would turn it into NaN)
+          x[e] = isinf(__bfloat162float(v)) ? 0.f : x[e] - __bfloat162float(v);
         }
-#pragma unroll
-        for (int q = 0; q < TERMS; ++q) {
-          uint32_t bits = 0;
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const __nv_bfloat16 v = __float2bfloat16_rn(x[z]);
-            bits |= (uint32_t)__bfloat16_as_ushort(v) << (16 * z);
-            // an infinity has no remainder (inf - inf would turn it into NaN)
-            x[z] = isinf(__bfloat162float(v)) ? 0.f : x[z] - __bfloat162float(v);
-          }
-          w[q][e] = bits;
-        }
+        to[0] = make_uint4(w[0], w[4], w[1], w[5]);
+        to[1] = make_uint4(w[2], w[6], w[3], w[7]);
+        to += p.term_tiles * 16;
       }
-    }
-#pragma unroll
-    for (int q = 0; q < TERMS; ++q) {
-      uint4* to = sh + ((ks * TERMS + q) * (8 * NT) + r) * 2;
-      to[0] = make_uint4(w[q][0], w[q][4], w[q][1], w[q][5]);
-      to[1] = make_uint4(w[q][2], w[q][6], w[q][3], w[q][7]);
     }
   }
 }
@@ -218,28 +173,29 @@ __device__ __forceinline__ void copy_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// RT tiles of 16 vocabulary rows per warp, NT tiles of 8 hidden rows. Every warp streams the records of its row tiles
+// RT tiles of 16 vocabulary rows per warp, NT tiles of 8 columns (hidden rows, or their terms), groups of GROUP, scales
+// of SB bytes. Every warp streams the records of its row tiles
 // through a ring of PF slots in shared memory (PF records of each tile in flight, no registers held by loads), across
 // the ends of tiles. p.split warps of a CTA share a set of row tiles, each with a contiguous part of its units.
-template <typename T, int NT, int RT, int GROUP, int PF>
-__global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadParams p) {
+template <int NT, int RT, int GROUP, int SB, bool ZEROS, int PF, int MAXW>
+__global__ void __launch_bounds__(MAXW * 32, 1) head_kernel(const HeadParams p) {
   static_assert((PF & (PF - 1)) == 0, "slots are taken in turn by masking");
-  constexpr int TERMS = kHeadTerms<T>;
   constexpr int GS = GROUP / 16;          // steps per group
   constexpr int NG = kHeadUnit / GROUP;   // groups per unit
   extern __shared__ __align__(128) unsigned char head_smem[];
   const HeadShape s = p.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int nb = s.blocks(), ng = s.groups(), record = s.record();
+  constexpr int GB = 16 * (SB + (ZEROS ? 1 : 0));         // bytes of a group's scales and zero points
+  constexpr int record = 1024 + NG * GB;
+  const int nb = s.blocks(), ng = s.groups();
   const int64_t nt = s.tiles(), tile_bytes = s.tile_bytes();
   const int part_of = warp % p.split;                     // this warp's part of the inner dimension
-  const int slots = kHeadWarps / p.split;                 // sets of row tiles per CTA and round
+  const int slots = (int)(blockDim.x >> 5) / p.split;               // sets of row tiles per CTA and round
   const int64_t stride = (int64_t)gridDim.x * slots * RT;
   const int64_t first0 = (int64_t)blockIdx.x * slots * RT, mine = (warp / p.split) * RT;
   const int rows = p.rows;
-  const int gb = s.scale_bytes * 16;                      // bytes of a group's scales
 
-  const uint32_t slot_bytes = (uint32_t)(RT * record);
+  constexpr uint32_t slot_bytes = RT * record;
   const uint32_t ring = (uint32_t)p.ring_off + (uint32_t)warp * PF * slot_bytes;   // this warp's ring, from head_smem
   const uint32_t smem0 = smem_addr(head_smem);
 
@@ -309,7 +265,7 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
     for (int c0 = 0; c0 < p.units; c0 += p.chunk) {
       if (p.chunk < p.units || first == first0) {
         __syncthreads();   // the last chunk has been read
-        head_stage<T, NT>(p, reinterpret_cast<uint4*>(head_smem), c0, min(c0 + p.chunk, p.units));
+        head_stage<NT>(p, reinterpret_cast<uint4*>(head_smem), c0, min(c0 + p.chunk, p.units));
         __syncthreads();
       }
       const int u1 = hi_of(c0);
@@ -317,7 +273,7 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
         copy_async_wait<PF - 1>();
         __syncwarp();
         const uint32_t rec = ring + (turn++ & (PF - 1)) * slot_bytes;
-        const uint2* su = reinterpret_cast<const uint2*>(head_smem) + (u - c0) * (kHeadUnitSteps * TERMS * 32 * NT) + lane;
+        const uint2* su = reinterpret_cast<const uint2*>(head_smem) + (u - c0) * (kHeadUnitSteps * 32 * NT) + lane;
         // a group of 128 fills a record, smaller ones may leave the last record with fewer blocks and groups
         const int blocks = NG == 1 ? 2 : min(nb - 2 * u, 2), groups = min(ng - u * NG, NG);
         float part[RT][NT][4];
@@ -330,31 +286,29 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
               const unsigned char* sc = head_smem + rec + t * record + blocks * 512;
-              if (s.scale_bytes == 4) {
-                const float2 v = reinterpret_cast<const float2*>(sc + g * gb)[gsel];
+              if (SB == 4) {
+                const float2 v = reinterpret_cast<const float2*>(sc + g * 64)[gsel];
                 slo[t] = v.x;
                 shi[t] = v.y;
               } else {
-                const uint32_t v = reinterpret_cast<const uint32_t*>(sc + g * gb)[gsel];
+                const uint32_t v = reinterpret_cast<const uint32_t*>(sc + g * 32)[gsel];
                 slo[t] = __uint_as_float(v << 16);
                 shi[t] = __uint_as_float(v & 0xFFFF0000u);
               }
               // 128 + zero point as bf16, twice
               zlo[t] = zhi[t] = 0x43084308u;
-              if (s.has_zeros) {
-                const uint32_t z = reinterpret_cast<const unsigned short*>(sc + groups * gb + g * 16)[gsel];
-                zlo[t] = 0x43004300u + (z & 0xFFu) * 0x00010001u;
-                zhi[t] = 0x43004300u + (z >> 8) * 0x00010001u;
+              if (ZEROS) {
+                const uint32_t z = reinterpret_cast<const unsigned short*>(sc + groups * (16 * SB) + g * 16)[gsel];
+                zlo[t] = __byte_perm(z, 0x43u, 0x4040);
+                zhi[t] = __byte_perm(z, 0x43u, 0x4141);
               }
             }
 #pragma unroll
             for (int i = 0; i < GS; ++i) {
               const int k = g * GS + i;
-              uint2 h[NT][TERMS];
+              uint2 h[NT];
 #pragma unroll
-              for (int q = 0; q < TERMS; ++q)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) h[n][q] = su[((k * TERMS + q) * NT + n) * 32];
+              for (int n = 0; n < NT; ++n) h[n] = su[(k * NT + n) * 32];
 #pragma unroll
               for (int t = 0; t < RT; ++t) {
                 if (k % 4 == 0) q4[t] = reinterpret_cast<const uint4*>(head_smem + rec + t * record)[(k / 4) * 32 + lane];
@@ -367,10 +321,8 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                   float (&d)[4] = part[t][n];
-                  if (i == 0) mma_bf16(d, a0, a1, a2, a3, h[n][0], 0.f, 0.f, 0.f, 0.f);
-                  else mma_bf16(d, a0, a1, a2, a3, h[n][0], d[0], d[1], d[2], d[3]);
-#pragma unroll
-                  for (int q = 1; q < TERMS; ++q) mma_bf16(d, a0, a1, a2, a3, h[n][q], d[0], d[1], d[2], d[3]);
+                  if (i == 0) mma_bf16(d, a0, a1, a2, a3, h[n], 0.f, 0.f, 0.f, 0.f);
+                  else mma_bf16(d, a0, a1, a2, a3, h[n], d[0], d[1], d[2], d[3]);
                 }
               }
             }
@@ -378,10 +330,8 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
             for (int t = 0; t < RT; ++t)
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                acc[t][n][0] = fmaf(slo[t], part[t][n][0], acc[t][n][0]);
-                acc[t][n][1] = fmaf(slo[t], part[t][n][1], acc[t][n][1]);
-                acc[t][n][2] = fmaf(shi[t], part[t][n][2], acc[t][n][2]);
-                acc[t][n][3] = fmaf(shi[t], part[t][n][3], acc[t][n][3]);
+                fma_pair(acc[t][n][0], acc[t][n][1], slo[t], part[t][n][0], part[t][n][1]);
+                fma_pair(acc[t][n][2], acc[t][n][3], shi[t], part[t][n][2], part[t][n][3]);
               }
           }
         }
@@ -414,19 +364,26 @@ __global__ void __launch_bounds__(kHeadWarps * 32, 1) head_kernel(const HeadPara
       __syncthreads();
       if (part_of > 0) continue;
     }
-    // accumulator j of column tile n: vocabulary row l/4 (+ 8 for j >= 2), hidden row 8 n + 2 (l%4) + (j & 1)
+    // accumulator j of column tile n: vocabulary row l/4 (+ 8 for j >= 2), column 8 n + 2 (l%4) + (j & 1)
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
+        if (n < p.term_tiles) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t v = (tile + t) * 16 + (lane >> 2) + (j >> 1) * 8;
-          const int r = n * 8 + 2 * (lane & 3) + (j & 1);
-          if (r < rows && v < s.V) {
-            const int64_t at = (p.m0 + r) * p.ld + v;
-            if (p.out_f32) reinterpret_cast<float*>(p.logits)[at] = acc[t][n][j];
-            else reinterpret_cast<__nv_bfloat16*>(p.logits)[at] = __float2bfloat16_rn(acc[t][n][j]);
+          for (int j = 0; j < 4; ++j) {
+            const int64_t v = (tile + t) * 16 + (lane >> 2) + (j >> 1) * 8;
+            const int r = n * 8 + 2 * (lane & 3) + (j & 1);
+            float y = acc[t][n][j];
+            if (NT % 3 == 0 && p.terms == 3) {   // smallest terms first
+              constexpr int TT = NT / 3;
+              if (n < TT) y += acc[t][(n + TT) % NT][j] + acc[t][(n + 2 * TT) % NT][j];
+            }
+            if (r < rows && v < s.V) {
+              const int64_t at = (p.m0 + r) * p.ld + v;
+              if (p.out_f32) reinterpret_cast<float*>(p.logits)[at] = y;
+              else reinterpret_cast<__nv_bfloat16*>(p.logits)[at] = __float2bfloat16_rn(y);
+            }
           }
         }
       }
