@@ -1,6 +1,9 @@
 // vsamp_embed and vsamp_embed_backward: argument checks and launches.
+#include <atomic>
+
 #include "vsamp_embed.cuh"
 #include "vsamp_grid.h"
+#include "vsamp_host.h"
 
 namespace vsamp {
 
@@ -11,42 +14,122 @@ static bool elem_aligned(const void* p, vsamp_dtype dt) {
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Radix passes for tokens below V and the marker of positions without a token, which sorts last in each digit
-static int sort_passes(int64_t V) {
+static int bits_of(int64_t n) {   // values 0 .. n fit
   int bits = 1;
-  while (bits < 32 && (V >> bits) != 0) ++bits;   // V itself fits: the marker's low bits are larger than any token's
-  return ceil_div(bits, kSortBits);
+  while (bits < 62 && (n >> bits) != 0) ++bits;
+  return bits;
+}
+
+// Elements that a thread takes at once: 16 bytes of the wider type when every row begins on that boundary.
+static bool rows_aligned(const void* p, int64_t ld, int es, int ve) {
+  return (reinterpret_cast<uintptr_t>(p) % (unsigned)(ve * es)) == 0 && ld % ve == 0;
+}
+
+template <typename TI, typename TO, int VE>
+static vsamp_status launch_embed_ve(const EmbedParams& p, cudaStream_t s) {
+  const int64_t nv = ceil_div(p.D, VE);
+  int tx = 1;   // threads along a row
+  while (tx < kEmbedThreads && tx * kEmbedUnroll < nv) tx *= 2;
+  const int64_t spans = ceil_div(nv, (int64_t)tx * kEmbedUnroll), rows = ceil_div(p.N, kEmbedThreads / tx);
+  return launch_1d(embed_kernel<TI, TO, VE>, grid_of(rows * spans), kEmbedThreads, 0, s, false, p, tx, (int)spans);
 }
 
 template <typename TI, typename TO>
 static vsamp_status launch_embed(const EmbedParams& p, cudaStream_t s) {
-  const int64_t spans = ceil_div(p.D, kEmbedSpan);
-  return launch_1d(embed_kernel<TI, TO>, grid_of(p.N * spans), kEmbedThreads, 0, s, false, p);
+  constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
+  if (p.D % VE == 0 && rows_aligned(p.table, p.ldt, sizeof(TI), VE) && rows_aligned(p.out, p.ldo, sizeof(TO), VE))
+    return launch_embed_ve<TI, TO, VE>(p, s);
+  return launch_embed_ve<TI, TO, 1>(p, s);
+}
+
+template <typename TO>
+static ZeroParams zero_params(const EmbedGradParams& p) {
+  ZeroParams z{};
+  z.base = p.dtable;
+  const int64_t es = sizeof(TO);
+  if (p.ldt == p.D || p.V == 1) {   // one contiguous range in equal pieces
+    const int64_t bytes = p.V * p.D * es;
+    z.row_stride = z.row_bytes = kZeroSpan;
+    z.nrows = ceil_div(bytes, kZeroSpan);
+    z.last_bytes = bytes - (z.nrows - 1) * kZeroSpan;
+  } else {
+    z.row_stride = p.ldt * es;
+    z.row_bytes = z.last_bytes = p.D * es;
+    z.nrows = p.V;
+  }
+  return z;
+}
+
+template <typename TI, typename TO, int VE>
+static vsamp_status launch_embed_sums(const EmbedGradParams& p, int last, cudaStream_t s) {
+  const int64_t spans = ceil_div(ceil_div(p.D, VE), kEmbedThreads);
+  const vsamp_status st = launch_1d(embed_sum_kernel<TI, TO, VE>, grid_of(p.sums * spans), kEmbedThreads, 0, s, false, p,
+                                    last, (int)spans);
+  if (st != VSAMP_OK) return st;
+  const int64_t jspans = ceil_div(p.D, kJoinSpan);
+  return launch_1d(embed_join_kernel<TO>, grid_of(p.sums * jspans), kEmbedThreads, 0, s, false, p, last, (int)jspans);
+}
+
+template <typename TI, typename TO, int VE>
+static vsamp_status launch_embed_few(const EmbedGradParams& p, cudaStream_t s) {
+  const int64_t spans = ceil_div(ceil_div(p.D, VE), kEmbedThreads);
+  return launch_1d(embed_few_kernel<TI, TO, VE>, grid_of(p.N * spans), kEmbedThreads, 0, s, false, p, (int)spans);
 }
 
 template <typename TI, typename TO>
-static vsamp_status launch_embed_grad(const EmbedGradParams& p, cudaStream_t s) {
+static vsamp_status launch_embed_grad(const EmbedGradParams& p, const DeviceInfo& d, int dev, cudaStream_t s) {
+  constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
+  const bool vec = p.D % VE == 0 && rows_aligned(p.dout, p.ldd, sizeof(TI), VE) &&
+                   rows_aligned(p.dtable, p.ldt, sizeof(TO), VE);
   vsamp_status st = VSAMP_OK;
-  if (!p.accumulate) {
-    st = launch_1d(embed_zero_kernel<TO>, grid_of(ceil_div(p.V * p.D, kEmbedThreads * 8)), kEmbedThreads, 0, s, false, p);
-    if (st != VSAMP_OK) return st;
+  ZeroParams z{};
+  if (!p.accumulate) z = zero_params<TO>(p);
+  const int64_t zero_warps = z.nrows < (int64_t)d.sm_count * 64 ? z.nrows : (int64_t)d.sm_count * 64;
+  if (p.N <= kEmbedFew) {
+    if (z.nrows > 0) {
+      st = launch_1d(embed_zero_kernel, grid_of(ceil_div(zero_warps, kEmbedThreads / 32)), kEmbedThreads, 0, s, false, z);
+      if (st != VSAMP_OK) return st;
+    }
+    return vec ? launch_embed_few<TI, TO, VE>(p, s) : launch_embed_few<TI, TO, 1>(p, s);
   }
-  const int passes = sort_passes(p.V);
-  for (int k = 0; k < passes; ++k) {
-    st = launch_1d(embed_hist_kernel, grid_of(p.tiles), kSortThreads, 0, s, false, p, k);
+  int last = 0;
+  const int pos_bits = bits_of(p.N - 1), token_bits = bits_of(p.V);
+  if (p.N <= kSortOne && pos_bits + token_bits <= 32) {
+    static std::atomic<bool> raised[64];
+    const int smem = (int)sizeof(SortOneSmem);
+    if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(embed_sort_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return VSAMP_ERR_CUDA;
+      }
+      if (dev < 64) raised[dev].store(true, std::memory_order_release);
+    }
+    // one CTA fits an SM beside the sort's shared memory: one zeroing CTA on each of the others
+    const int64_t zero_ctas = ceil_div(zero_warps, kSortOneThreads / 32);
+    const int64_t most = d.sm_count - 1;
+    st = launch_1d(embed_sort_one_kernel, grid_of(1 + (zero_ctas < most ? zero_ctas : most)), kSortOneThreads,
+                   (size_t)smem, s, false, p, z, pos_bits, (int)ceil_div(token_bits, kSortBits));
     if (st != VSAMP_OK) return st;
-    st = launch_1d(embed_scatter_kernel, grid_of(p.tiles), kSortThreads, 0, s, false, p, k);
-    if (st != VSAMP_OK) return st;
+  } else {
+    if (z.nrows > 0) {
+      st = launch_1d(embed_zero_kernel, grid_of(ceil_div(zero_warps, kEmbedThreads / 32)), kEmbedThreads, 0, s, false, z);
+      if (st != VSAMP_OK) return st;
+    }
+    // the marker's low bits are larger than any token's: V itself fits token_bits
+    const int passes = (int)ceil_div(token_bits, kSortBits);
+    for (int k = 0; k < passes; ++k) {
+      st = launch_1d(embed_hist_kernel, grid_of(p.tiles), kSortThreads, 0, s, false, p, k);
+      if (st != VSAMP_OK) return st;
+      st = launch_1d(embed_scatter_kernel, grid_of(p.tiles), kSortThreads, 0, s, false, p, k);
+      if (st != VSAMP_OK) return st;
+    }
+    last = (passes - 1) & 1;
   }
-  const int last = (passes - 1) & 1;
-  const unsigned grid = grid_of(p.sums * ceil_div(p.D, kEmbedThreads));
-  st = launch_1d(embed_sum_kernel<TI, TO>, grid, kEmbedThreads, 0, s, false, p, last);
-  if (st != VSAMP_OK) return st;
-  return launch_1d(embed_join_kernel<TO>, grid, kEmbedThreads, 0, s, false, p, last);
+  return vec ? launch_embed_sums<TI, TO, VE>(p, last, s) : launch_embed_sums<TI, TO, 1>(p, last, s);
 }
 
 struct EmbedPlan {
-  int64_t tiles, sums;
+  int64_t tiles, sums, ldp;
   size_t keys, hist, part, total;
 };
 static EmbedPlan embed_plan(int64_t N, int64_t D) {
@@ -54,10 +137,11 @@ static EmbedPlan embed_plan(int64_t N, int64_t D) {
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   e.tiles = ceil_div(N, kSortTile);
   e.sums = ceil_div(N, kEmbedTile);
+  e.ldp = ceil_div(D, 8) * 8;
   e.keys = up((size_t)N * sizeof(uint2));
   e.hist = up((size_t)e.tiles * kSortBins * 4);
-  e.part = up((size_t)e.sums * 2 * (size_t)D * 4);
-  e.total = 2 * e.keys + e.hist + e.part;
+  e.part = up((size_t)e.sums * 2 * (size_t)e.ldp * 4);
+  e.total = N <= kEmbedFew ? 16 : 2 * e.keys + e.hist + e.part;   // few positions need none
   return e;
 }
 
@@ -126,11 +210,21 @@ vsamp_status vsamp_embed_backward(const int32_t* token, int64_t N, const void* d
   p.part = reinterpret_cast<float*>(w + 2 * e.keys + e.hist);
   p.tiles = e.tiles;
   p.sums = e.sums;
+  p.ldp = e.ldp;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return VSAMP_ERR_CUDA;
+  }
+  DeviceInfo d;
+  const vsamp_status st = device_info(dev, d);
+  if (st != VSAMP_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dt == VSAMP_F32)
-    return table_dt == VSAMP_F32 ? launch_embed_grad<float, float>(p, s) : launch_embed_grad<float, __nv_bfloat16>(p, s);
-  return table_dt == VSAMP_F32 ? launch_embed_grad<__nv_bfloat16, float>(p, s)
-                               : launch_embed_grad<__nv_bfloat16, __nv_bfloat16>(p, s);
+    return table_dt == VSAMP_F32 ? launch_embed_grad<float, float>(p, d, dev, s)
+                                 : launch_embed_grad<float, __nv_bfloat16>(p, d, dev, s);
+  return table_dt == VSAMP_F32 ? launch_embed_grad<__nv_bfloat16, float>(p, d, dev, s)
+                               : launch_embed_grad<__nv_bfloat16, __nv_bfloat16>(p, d, dev, s);
 }
 
 }  // extern "C"

@@ -2,11 +2,14 @@
 //
 // Lookup: out[n, :] = scale * table[token[n], :], the product in fp32, rounded once.
 //
-// Gradient: dtable[v, :] = (dtable[v, :] +) scale * sum over n with token[n] = v of dout[n, :]. The positions are
-// sorted by (token, position) with a stable radix sort; the sorted list is cut into fixed tiles, each summed in
-// order in fp32. A run of equal tokens inside a tile is written at once, the first and last run of a tile, which may
-// go on in the neighbours, leave partial sums that the run's first tile joins in tile order. So the result depends
-// on the inputs alone: no atomics on floating values, whatever the launch.
+// Gradient: dtable[v, :] = (dtable[v, :] +) scale * sum over n with token[n] = v of dout[n, :]. The result depends on
+// the inputs alone: no atomics on floating values, every sum in a fixed order.
+//   Few positions: a CTA per position and column span finds the later positions of its token (and leaves if there is
+//   an earlier one) and adds their rows in order.
+//   Many positions: they are sorted by (token, position) with a stable radix sort, in one CTA while the others write
+//   the zeros of the untouched rows, or in several launches for long lists. The sorted list is cut into fixed tiles,
+//   each summed in order. A run of equal tokens inside a tile is written at once; the first and last run of a tile,
+//   which may go on in the neighbours, leave partial sums that the run's first tile joins in tile order.
 #pragma once
 
 #include "vsamp.h"
@@ -20,6 +23,7 @@ constexpr int kSortTile = kSortThreads * kSortPer;       // keys per CTA
 constexpr int kSortBits = 8;
 constexpr int kSortBins = 1 << kSortBits;
 constexpr int kEmbedTile = 16;                           // sorted positions per tile of the sums
+constexpr int kJoinSpan = 256;                           // columns per CTA of the join
 constexpr uint32_t kNoToken = 0xFFFFFFFFu;               // sorts after every token
 
 struct EmbedParams {
@@ -44,7 +48,8 @@ struct EmbedGradParams {
   int accumulate;
   uint2* keys[2];          // {token or kNoToken, position}
   uint32_t* hist;          // [tiles, bins]
-  float* part;             // [2 * sum tiles, D] partial sums of the first and last run of a tile
+  float* part;             // [2 * sum tiles, ldp] partial sums of the first and last run of a tile
+  int64_t ldp;
   int64_t tiles;           // sort tiles
   int64_t sums;            // sum tiles
 };
@@ -61,23 +66,81 @@ __device__ __forceinline__ void elem_store(unsigned char* p, int64_t i, float f)
 }
 
 constexpr int kEmbedThreads = 256;
-constexpr int kEmbedSpan = 1024;     // columns per CTA and step
 
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams p) {
-  const int64_t spans = (p.D + kEmbedSpan - 1) / kEmbedSpan;
-  const int64_t total = p.N * spans;
+// VE neighbouring elements as fp32 (VE = 1, or 16 bytes of the wider type involved)
+template <typename T, int VE>
+struct ElemVec {
+  uint32_t w[sizeof(T) * VE >= 4 ? sizeof(T) * VE / 4 : 1];
+  __device__ __forceinline__ void load(const unsigned char* p, int64_t i) {
+    if constexpr (VE == 1) {
+      w[0] = __float_as_uint(elem_load<T>(p, i));
+    } else if constexpr (sizeof(T) * VE == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + i * (int64_t)sizeof(T));
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p + i * (int64_t)sizeof(T));
+      w[0] = v.x; w[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ float at(int j) const {
+    if constexpr (VE == 1 || sizeof(T) == 4) return __uint_as_float(w[j]);
+    else return __uint_as_float((j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
+  }
+};
+template <typename T, int VE>
+__device__ __forceinline__ void elem_store_vec(unsigned char* p, int64_t i, const float (&f)[VE]) {
+  if constexpr (VE == 1) {
+    elem_store<T>(p, i, f[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < VE; j += 4)
+      *reinterpret_cast<float4*>(p + (i + j) * 4) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+  } else {
+    uint32_t w[VE / 2];
+#pragma unroll
+    for (int j = 0; j < VE / 2; ++j) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+      memcpy(&w[j], &b, 4);
+    }
+    if constexpr (VE == 8) *reinterpret_cast<uint4*>(p + i * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2*>(p + i * 2) = make_uint2(w[0], w[1]);
+  }
+}
+
+// tx threads of a CTA along a row (a power of two), kEmbedThreads / tx rows per CTA, U vectors per thread and row so
+// that their loads are in flight together.
+constexpr int kEmbedUnroll = 2;
+
+template <typename TI, typename TO, int VE>
+__global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams p, int tx, int spans) {
+  constexpr int U = kEmbedUnroll;
+  const int col = threadIdx.x & (tx - 1), per = kEmbedThreads / tx;
+  const int64_t total = (p.N + per - 1) / per * spans;
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const int64_t n = id / spans, c0 = (id - n * spans) * kEmbedSpan;
+    const int64_t group = spans == 1 ? id : id / spans;
+    const int64_t n = group * per + threadIdx.x / tx;
+    const int64_t c0 = ((id - group * spans) * U * tx + col) * VE;
+    if (n >= p.N) continue;
     const int32_t t = p.token[n];
     const bool skip = t == VSAMP_TOKEN_IGNORE;
     const bool ok = t >= 0 && (int64_t)t < p.V;
-    if (p.row_status && c0 == 0 && threadIdx.x == 0) p.row_status[n] = ok || skip ? VSAMP_OK : VSAMP_ERR_INVALID_ARG;
+    if (p.row_status && c0 == 0) p.row_status[n] = ok || skip ? VSAMP_OK : VSAMP_ERR_INVALID_ARG;
     const unsigned char* src = p.table + (ok ? (int64_t)t * p.ldt : 0) * (int64_t)sizeof(TI);
     unsigned char* dst = p.out + n * p.ldo * (int64_t)sizeof(TO);
     const float fill = skip ? 0.f : __int_as_float(0x7FC00000);
-    for (int64_t c = c0 + threadIdx.x; c < c0 + kEmbedSpan && c < p.D; c += kEmbedThreads)
-      elem_store<TO>(dst, c, ok ? elem_load<TI>(src, c) * p.scale : fill);
+    ElemVec<TI, VE> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (ok && c0 + u * tx * VE < p.D) v[u].load(src, c0 + u * tx * VE);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c0 + u * tx * VE < p.D) {
+        float f[VE];
+#pragma unroll
+        for (int j = 0; j < VE; ++j) f[j] = ok ? v[u].at(j) * p.scale : fill;
+        elem_store_vec<TO, VE>(dst, c0 + u * tx * VE, f);
+      }
+    }
   }
 }
 
@@ -179,72 +242,287 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const Embed
   }
 }
 
-template <typename TO>
-__global__ void __launch_bounds__(kEmbedThreads) embed_zero_kernel(const EmbedGradParams p) {
-  const int64_t total = p.V * p.D;
-  for (int64_t i = (int64_t)blockIdx.x * kEmbedThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kEmbedThreads) {
-    const int64_t v = i / p.D;
-    elem_store<TO>(p.dtable, v * p.ldt + (i - v * p.D), 0.f);
+// Zeros over nrows byte ranges of row_bytes (the last one last_bytes) that begin row_stride apart: a warp per range.
+struct ZeroParams {
+  unsigned char* base;
+  int64_t row_stride, row_bytes, last_bytes, nrows;
+};
+constexpr int64_t kZeroSpan = 16384;   // bytes per range of a contiguous table
+
+__device__ __forceinline__ void zero_ranges(const ZeroParams& z, int64_t warp, int64_t nwarps) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t r = warp; r < z.nrows; r += nwarps) {
+    unsigned char* p = z.base + r * z.row_stride;
+    const int64_t bytes = r + 1 == z.nrows ? z.last_bytes : z.row_bytes;
+    // up to the first 16-byte boundary, whole vectors, the rest (elements are 2 or 4 bytes, so steps of 2)
+    int64_t head = (16 - (int64_t)(reinterpret_cast<uintptr_t>(p) & 15)) & 15;
+    if (head > bytes) head = bytes;
+    const int64_t nv = (bytes - head) / 16, tail = head + nv * 16;
+    if (lane * 2 < head) *reinterpret_cast<unsigned short*>(p + lane * 2) = 0;
+    uint4* q = reinterpret_cast<uint4*>(p + head);
+#pragma unroll 4
+    for (int64_t i = lane; i < nv; i += 32) __stcs(q + i, make_uint4(0, 0, 0, 0));
+    if (tail + lane * 2 < bytes) *reinterpret_cast<unsigned short*>(p + tail + lane * 2) = 0;
   }
 }
 
-// Sums of one tile of kEmbedTile sorted positions: block (tile, columns).
-template <typename TI, typename TO>
-__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const EmbedGradParams p, int last) {
+__global__ void __launch_bounds__(kEmbedThreads) embed_zero_kernel(const ZeroParams z) {
+  zero_ranges(z, (int64_t)blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5), (int64_t)gridDim.x * (kEmbedThreads / 32));
+}
+
+// One CTA sorts up to kSortOne positions on chip, the others write zeros (no z: z.nrows = 0 and a grid of one CTA).
+// A key is token << pos_bits | position: 32 bits hold both, the marker token V included. Least significant digit
+// first, stable: a warp takes consecutive keys 32 at a time, equal digits keep their order.
+constexpr int kSortOne = 16384;
+constexpr int kSortOneThreads = 1024;
+struct SortOneSmem {
+  uint32_t key[2][kSortOne];
+  uint16_t count[kSortOneThreads / 32][kSortBins];
+  uint32_t wsum[kSortBins / 32];
+};
+
+__global__ void __launch_bounds__(kSortOneThreads) embed_sort_one_kernel(const EmbedGradParams p, const ZeroParams z,
+                                                                         int pos_bits, int passes) {
+  if (blockIdx.x > 0) {
+    zero_ranges(z, (int64_t)(blockIdx.x - 1) * (kSortOneThreads / 32) + (threadIdx.x >> 5),
+                (int64_t)(gridDim.x - 1) * (kSortOneThreads / 32));
+    return;
+  }
+  extern __shared__ __align__(16) unsigned char sort_smem[];
+  SortOneSmem& S = *reinterpret_cast<SortOneSmem*>(sort_smem);
+  constexpr int NW = kSortOneThreads / 32;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int n = (int)p.N, per = (n + NW * 32 - 1) / (NW * 32);   // 32-key steps per warp
+  for (int i = t; i < n; i += kSortOneThreads) {
+    const int32_t tok = p.token[i];
+    const uint32_t v = tok >= 0 && (int64_t)tok < p.V ? (uint32_t)tok : (uint32_t)p.V;
+    S.key[0][i] = v << pos_bits | (uint32_t)i;
+  }
+  for (int pass = 0; pass < passes; ++pass) {
+    const uint32_t* from = S.key[pass & 1];
+    uint32_t* to = S.key[(pass + 1) & 1];
+    const int shift = pos_bits + pass * kSortBits;
+    for (int i = t; i < NW * kSortBins; i += kSortOneThreads) (&S.count[0][0])[i] = 0;
+    __syncthreads();
+    const int w0 = warp * per * 32;
+    for (int j = 0; j < per; ++j) {
+      const int i = w0 + j * 32 + lane;
+      const uint32_t d = i < n ? (from[i] >> shift) & (kSortBins - 1) : kSortBins;
+      const uint32_t same = __match_any_sync(kFullMask, d);
+      if (i < n && (same & ((1u << lane) - 1u)) == 0) S.count[warp][d] += (uint16_t)__popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    uint32_t all = 0;
+    if (t < kSortBins) {   // this digit's keys, and where they begin
+      for (int w = 0; w < NW; ++w) {
+        const uint32_t c = S.count[w][t];
+        S.count[w][t] = (uint16_t)all;
+        all += c;
+      }
+      uint32_t incl = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(kFullMask, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) S.wsum[warp] = incl;
+      all = incl - all;
+    }
+    __syncthreads();
+    if (t < kSortBins) {
+      for (int w = 0; w < warp; ++w) all += S.wsum[w];
+      for (int w = 0; w < NW; ++w) S.count[w][t] = (uint16_t)(S.count[w][t] + all);
+    }
+    __syncthreads();
+    for (int j = 0; j < per; ++j) {
+      const int i = w0 + j * 32 + lane;
+      const uint32_t key = i < n ? from[i] : 0u;
+      const uint32_t d = i < n ? (key >> shift) & (kSortBins - 1) : kSortBins;
+      const uint32_t same = __match_any_sync(kFullMask, d);
+      const uint32_t before = __popc(same & ((1u << lane) - 1u));
+      uint32_t at = 0;
+      if (i < n) at = S.count[warp][d] + before;
+      __syncwarp();
+      if (i < n) {
+        to[at] = key;
+        if (before == 0) S.count[warp][d] += (uint16_t)__popc(same);
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+  }
+  const uint32_t* from = S.key[passes & 1];
+  for (int i = t; i < n; i += kSortOneThreads) {
+    const uint32_t v = from[i] >> pos_bits;
+    p.keys[0][i] = make_uint2(v < (uint32_t)p.V ? v : kNoToken, from[i] & ((1u << pos_bits) - 1u));
+  }
+}
+
+// Adds `n` rows of dout in order; row i is at position pos(i). Eight rows are in flight at a time.
+template <typename TI, int VE, typename F>
+__device__ __forceinline__ void add_rows(const EmbedGradParams& p, int64_t c, int n, F pos, float (&sum)[VE]) {
+  int i = 0;
+  for (; i + 8 <= n; i += 8) {
+    ElemVec<TI, VE> v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j].load(p.dout, (int64_t)pos(i + j) * p.ldd + c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) sum[e] += v[j].at(e);
+  }
+  for (; i < n; ++i) {
+    ElemVec<TI, VE> v;
+    v.load(p.dout, (int64_t)pos(i) * p.ldd + c);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) sum[e] += v.at(e);
+  }
+}
+
+// One row's span of the table: scale * sum, added or written, one rounding.
+template <typename TO, int VE>
+__device__ __forceinline__ void put_row(const EmbedGradParams& p, uint32_t tok, int64_t c, float (&sum)[VE]) {
+  const int64_t at = (int64_t)tok * p.ldt + c;
+#pragma unroll
+  for (int e = 0; e < VE; ++e) sum[e] *= p.scale;
+  if (p.accumulate) {
+    ElemVec<TO, VE> old;
+    old.load(p.dtable, at);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) sum[e] += old.at(e);
+  }
+  elem_store_vec<TO, VE>(p.dtable, at, sum);
+}
+
+// Few positions (N <= kEmbedFew): a CTA per position and span of columns, no workspace.
+constexpr int kEmbedFew = 1024;
+
+template <typename TI, typename TO, int VE>
+__global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const EmbedGradParams p, int spans) {
+  __shared__ uint32_t bits[kEmbedFew / 32];
+  __shared__ uint16_t list[kEmbedFew];
+  __shared__ int count;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n0 = (int)(blockIdx.x / spans), N = (int)p.N;
+  const int32_t tok = p.token[n0];
+  if (tok < 0 || (int64_t)tok >= p.V) return;
+  for (int i = warp * 32; i < kEmbedFew; i += kEmbedThreads) {
+    const uint32_t b = __ballot_sync(kFullMask, i + lane < N && p.token[i + lane] == tok);
+    if (lane == 0) bits[i / 32] = b;
+  }
+  __syncthreads();
+  if (warp == 0) {   // lane l: positions 32 l .. 32 l + 31
+    uint32_t b = bits[lane];
+    const uint32_t first = __ballot_sync(kFullMask, b != 0);
+    const int low = __shfl_sync(kFullMask, __ffs(b) - 1, __ffs(first) - 1) + 32 * (__ffs(first) - 1);
+    int incl = __popc(b);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFullMask, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int at = incl - __popc(b);
+    for (; b; b &= b - 1) list[at++] = (uint16_t)(lane * 32 + __ffs(b) - 1);
+    if (lane == 31) count = low == n0 ? incl : 0;   // an earlier position of the token has these rows
+  }
+  __syncthreads();
+  const int n = count;
+  const int64_t c = ((int64_t)(blockIdx.x % spans) * kEmbedThreads + threadIdx.x) * VE;
+  if (n == 0 || c >= p.D) return;
+  float sum[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) sum[e] = 0.f;
+  add_rows<TI, VE>(p, c, n, [&](int i) { return (int)list[i]; }, sum);
+  put_row<TO, VE>(p, (uint32_t)tok, c, sum);
+}
+
+// Sums of one tile of kEmbedTile sorted positions: a CTA per tile and span of columns.
+template <typename TI, typename TO, int VE>
+__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const EmbedGradParams p, int last, int spans) {
   const uint2* keys = p.keys[last];
-  const int64_t spans = (p.D + kEmbedThreads - 1) / kEmbedThreads;
   for (int64_t id = blockIdx.x; id < p.sums * spans; id += gridDim.x) {
     const int64_t tile = id / spans;
-    const int64_t c = (id - tile * spans) * kEmbedThreads + threadIdx.x;
-    const int64_t i0 = tile * kEmbedTile, i1 = i0 + kEmbedTile < p.N ? i0 + kEmbedTile : p.N;
+    const int64_t c = ((id - tile * spans) * kEmbedThreads + threadIdx.x) * VE;
     if (c >= p.D) continue;
+    const int64_t i0 = tile * kEmbedTile;
+    const int n = (int)(p.N - i0 < kEmbedTile ? p.N - i0 : kEmbedTile);
     const uint32_t prev = i0 > 0 ? keys[i0 - 1].x : kNoToken;
-    const uint32_t next = i1 < p.N ? keys[i1].x : kNoToken;
-    float sum = 0.f;
-    int64_t start = i0;
-    for (int64_t i = i0; i < i1; ++i) {
-      const uint2 k = keys[i];
-      if (k.x == kNoToken) break;
-      sum += elem_load<TI>(p.dout, (int64_t)k.y * p.ldd + c);
-      const uint32_t after = i + 1 < i1 ? keys[i + 1].x : next;
-      if (after == k.x && i + 1 < i1) continue;
-      // the run ends here, or goes on in the next tile
-      const bool from_before = start == i0 && prev == k.x;
-      const bool goes_on = i + 1 == i1 && after == k.x;
-      if (!from_before && !goes_on) {
-        const int64_t at = (int64_t)k.x * p.ldt + c;
-        float r = sum * p.scale;
-        if (p.accumulate) r += elem_load<TO>(p.dtable, at);
-        elem_store<TO>(p.dtable, at, r);
-      } else {
-        // slot 0: the tile's first run, slot 1: its last (a run that fills the tile has slot 0)
-        p.part[(tile * 2 + (from_before ? 0 : 1)) * p.D + c] = sum;
+    const uint32_t next = i0 + n < p.N ? keys[i0 + n].x : kNoToken;
+    uint2 key[kEmbedTile];
+    ElemVec<TI, VE> v[kEmbedTile];
+#pragma unroll
+    for (int i = 0; i < kEmbedTile; ++i) key[i] = i < n ? keys[i0 + i] : make_uint2(kNoToken, 0);
+#pragma unroll
+    for (int i = 0; i < kEmbedTile; ++i)
+      if (key[i].x != kNoToken) v[i].load(p.dout, (int64_t)key[i].y * p.ldd + c);
+    float sum[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) sum[e] = 0.f;
+    bool from_before = prev == key[0].x;   // the run at hand began in an earlier tile
+#pragma unroll
+    for (int i = 0; i < kEmbedTile; ++i) {
+      if (key[i].x != kNoToken) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) sum[e] += v[i].at(e);
+        const uint32_t after = i + 1 < kEmbedTile ? (i + 1 < n ? key[i + 1 < kEmbedTile ? i + 1 : 0].x : next) : next;
+        if (after != key[i].x || i + 1 == n) {
+          const bool goes_on = after == key[i].x;
+          if (!from_before && !goes_on) {
+            put_row<TO, VE>(p, key[i].x, c, sum);
+          } else {
+            // slot 0: the tile's first run, slot 1: its last (a run that fills the tile from before has slot 0)
+            elem_store_vec<float, VE>(reinterpret_cast<unsigned char*>(p.part), (tile * 2 + (from_before ? 0 : 1)) * p.ldp + c, sum);
+          }
+#pragma unroll
+          for (int e = 0; e < VE; ++e) sum[e] = 0.f;
+          from_before = false;
+        }
       }
-      sum = 0.f;
-      start = i + 1;
     }
   }
 }
 
-// Runs over several tiles: the tile where a run begins adds up its parts in order.
+// Runs over several tiles: the tile where a run begins adds up its parts, in order inside each of eight stretches of
+// tiles, then the stretches in order.
 template <typename TO>
-__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGradParams p, int last) {
+__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGradParams p, int last, int spans) {
+  __shared__ float part[kEmbedThreads / 32][32];
   const uint2* keys = p.keys[last];
-  const int64_t spans = (p.D + kEmbedThreads - 1) / kEmbedThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int NW = kEmbedThreads / 32;
   for (int64_t id = blockIdx.x; id < p.sums * spans; id += gridDim.x) {
     const int64_t tile = id / spans;
-    const int64_t c = (id - tile * spans) * kEmbedThreads + threadIdx.x;
     const int64_t i0 = tile * kEmbedTile, i1 = i0 + kEmbedTile;
-    if (c >= p.D || i1 >= p.N) continue;
+    if (i1 >= p.N) continue;
     const uint32_t tok = keys[i1 - 1].x;
-    if (tok == kNoToken || keys[i1].x != tok) continue;               // no run goes on from this tile
-    if (i0 > 0 && keys[i0].x == tok && keys[i0 - 1].x == tok) continue;   // it began earlier
-    float sum = p.part[(tile * 2 + 1) * p.D + c];
-    for (int64_t k = tile + 1; k < p.sums && keys[k * kEmbedTile].x == tok; ++k) sum += p.part[(k * 2) * p.D + c];
-    const int64_t at = (int64_t)tok * p.ldt + c;
-    float r = sum * p.scale;
-    if (p.accumulate) r += elem_load<TO>(p.dtable, at);
-    elem_store<TO>(p.dtable, at, r);
+    if (tok == kNoToken || keys[i1].x != tok) continue;                  // no run goes on from this tile
+    if (i0 > 0 && keys[i0].x == tok && keys[i0 - 1].x == tok) continue;  // it began earlier
+    // tiles [tile, end) hold the run: the first tile that does not begin with the token
+    int64_t lo = tile + 1, hi = p.sums;
+    while (lo + 1 < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (keys[mid * kEmbedTile].x == tok) lo = mid;
+      else hi = mid;
+    }
+    const int64_t n = lo + 1 - tile;
+    const int64_t k0 = tile + n * warp / NW, k1 = tile + n * (warp + 1) / NW;
+    for (int64_t c0 = (id - tile * spans) * kJoinSpan; c0 < (id - tile * spans + 1) * kJoinSpan && c0 < p.D; c0 += 32) {
+      const int64_t c = c0 + lane;
+      float sum = 0.f;
+      if (c < p.D) {
+#pragma unroll 8
+        for (int64_t k = k0; k < k1; ++k) sum += p.part[(k * 2 + (k == tile ? 1 : 0)) * p.ldp + c];
+      }
+      part[warp][lane] = sum;
+      __syncthreads();
+      if (warp == 0 && c < p.D) {
+        float all[1] = {part[0][lane]};
+        for (int w = 1; w < NW; ++w) all[0] += part[w][lane];
+        put_row<TO, 1>(p, tok, c, all);
+      }
+      __syncthreads();
+    }
   }
 }
 
