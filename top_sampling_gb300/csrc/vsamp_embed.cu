@@ -61,13 +61,16 @@ static ZeroParams zero_params(const EmbedGradParams& p) {
 }
 
 template <typename TI, typename TO, int VE>
-static vsamp_status launch_embed_sums(const EmbedGradParams& p, int last, cudaStream_t s) {
+static vsamp_status launch_embed_sums(const EmbedGradParams& p, int last, const DeviceInfo& d, cudaStream_t s) {
   const int64_t spans = ceil_div(ceil_div(p.D, VE), kEmbedThreads);
   const vsamp_status st = launch_1d(embed_sum_kernel<TI, TO, VE>, grid_of(p.sums * spans), kEmbedThreads, 0, s, false, p,
                                     last, (int)spans);
   if (st != VSAMP_OK) return st;
   const int64_t jspans = ceil_div(p.D, kJoinSpan);
-  return launch_1d(embed_join_kernel<TO>, grid_of(p.sums * jspans), kEmbedThreads, 0, s, false, p, last, (int)jspans);
+  const int64_t most = p.sums * jspans, resident = (int64_t)d.sm_count * 8;   // the list's length is not known here
+  const int vec = VE > 1;   // rows of the table begin on a boundary of four elements
+  return launch_1d(embed_join_kernel<TO>, grid_of(most < resident ? most : resident), kEmbedThreads, 0, s, false, p,
+                   last, (int)jspans, vec);
 }
 
 template <typename TI, typename TO, int VE>
@@ -125,12 +128,12 @@ static vsamp_status launch_embed_grad(const EmbedGradParams& p, const DeviceInfo
     }
     last = (passes - 1) & 1;
   }
-  return vec ? launch_embed_sums<TI, TO, VE>(p, last, s) : launch_embed_sums<TI, TO, 1>(p, last, s);
+  return vec ? launch_embed_sums<TI, TO, VE>(p, last, d, s) : launch_embed_sums<TI, TO, 1>(p, last, d, s);
 }
 
 struct EmbedPlan {
   int64_t tiles, sums, ldp;
-  size_t keys, hist, part, total;
+  size_t keys, hist, part, runs, total;
 };
 static EmbedPlan embed_plan(int64_t N, int64_t D) {
   EmbedPlan e;
@@ -141,7 +144,8 @@ static EmbedPlan embed_plan(int64_t N, int64_t D) {
   e.keys = up((size_t)N * sizeof(uint2));
   e.hist = up((size_t)e.tiles * kSortBins * 4);
   e.part = up((size_t)e.sums * 2 * (size_t)e.ldp * 4);
-  e.total = N <= kEmbedFew ? 16 : 2 * e.keys + e.hist + e.part;   // few positions need none
+  e.runs = up((size_t)e.sums * 4) + 256;
+  e.total = N <= kEmbedFew ? 16 : 2 * e.keys + e.hist + e.part + e.runs;   // few positions need none
   return e;
 }
 
@@ -208,6 +212,8 @@ vsamp_status vsamp_embed_backward(const int32_t* token, int64_t N, const void* d
   p.keys[1] = reinterpret_cast<uint2*>(w + e.keys);
   p.hist = reinterpret_cast<uint32_t*>(w + 2 * e.keys);
   p.part = reinterpret_cast<float*>(w + 2 * e.keys + e.hist);
+  p.runs = reinterpret_cast<uint32_t*>(w + 2 * e.keys + e.hist + e.part);
+  p.n_runs = p.runs + (e.runs - 256) / 4;
   p.tiles = e.tiles;
   p.sums = e.sums;
   p.ldp = e.ldp;

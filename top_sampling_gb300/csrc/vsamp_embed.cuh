@@ -23,7 +23,7 @@ constexpr int kSortTile = kSortThreads * kSortPer;       // keys per CTA
 constexpr int kSortBits = 8;
 constexpr int kSortBins = 1 << kSortBits;
 constexpr int kEmbedTile = 16;                           // sorted positions per tile of the sums
-constexpr int kJoinSpan = 256;                           // columns per CTA of the join
+constexpr int kJoinSpan = 128;                           // columns per CTA of the join
 constexpr uint32_t kNoToken = 0xFFFFFFFFu;               // sorts after every token
 
 struct EmbedParams {
@@ -50,6 +50,8 @@ struct EmbedGradParams {
   uint32_t* hist;          // [tiles, bins]
   float* part;             // [2 * sum tiles, ldp] partial sums of the first and last run of a tile
   int64_t ldp;
+  uint32_t* runs;          // [sum tiles] tiles where a run over several tiles begins, in any order
+  uint32_t* n_runs;
   int64_t tiles;           // sort tiles
   int64_t sums;            // sum tiles
 };
@@ -109,7 +111,7 @@ __device__ __forceinline__ void elem_store_vec(unsigned char* p, int64_t i, cons
 
 // tx threads of a CTA along a row (a power of two), kEmbedThreads / tx rows per CTA, U vectors per thread and row so
 // that their loads are in flight together.
-constexpr int kEmbedUnroll = 2;
+constexpr int kEmbedUnroll = 4;
 
 template <typename TI, typename TO, int VE>
 __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams p, int tx, int spans) {
@@ -155,6 +157,7 @@ __device__ __forceinline__ uint2 embed_key(const EmbedGradParams& p, int pass, i
 
 __global__ void __launch_bounds__(kSortThreads) embed_hist_kernel(const EmbedGradParams p, int pass) {
   __shared__ uint32_t hist[kSortBins];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.n_runs = 0;
   for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
     for (int i = threadIdx.x; i < kSortBins; i += kSortThreads) hist[i] = 0;
     __syncthreads();
@@ -293,6 +296,7 @@ __global__ void __launch_bounds__(kSortOneThreads) embed_sort_one_kernel(const E
   constexpr int NW = kSortOneThreads / 32;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int n = (int)p.N, per = (n + NW * 32 - 1) / (NW * 32);   // 32-key steps per warp
+  if (t == 0) *p.n_runs = 0;
   for (int i = t; i < n; i += kSortOneThreads) {
     const int32_t tok = p.token[i];
     const uint32_t v = tok >= 0 && (int64_t)tok < p.V ? (uint32_t)tok : (uint32_t)p.V;
@@ -437,92 +441,117 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const EmbedGra
   put_row<TO, VE>(p, (uint32_t)tok, c, sum);
 }
 
-// Sums of one tile of kEmbedTile sorted positions: a CTA per tile and span of columns.
+// Sums of one tile of kEmbedTile sorted positions: a CTA per tile and span of columns. A tile is read in two halves:
+// eight rows in flight per thread and three CTAs per SM (all sixteen at once held 174 registers, one CTA per SM, and
+// took twice the time).
+constexpr int kSumBatch = 8;
+
 template <typename TI, typename TO, int VE>
-__global__ void __launch_bounds__(kEmbedThreads) embed_sum_kernel(const EmbedGradParams p, int last, int spans) {
+__global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(const EmbedGradParams p, int last, int spans) {
   const uint2* keys = p.keys[last];
   for (int64_t id = blockIdx.x; id < p.sums * spans; id += gridDim.x) {
-    const int64_t tile = id / spans;
-    const int64_t c = ((id - tile * spans) * kEmbedThreads + threadIdx.x) * VE;
-    if (c >= p.D) continue;
-    const int64_t i0 = tile * kEmbedTile;
-    const int n = (int)(p.N - i0 < kEmbedTile ? p.N - i0 : kEmbedTile);
+    const int64_t tile = spans == 1 ? id : id / spans;
+    const int64_t span = id - tile * spans, c = (span * kEmbedThreads + threadIdx.x) * VE;
+    const int64_t i0 = tile * kEmbedTile, i1 = i0 + kEmbedTile < p.N ? i0 + kEmbedTile : p.N;
     const uint32_t prev = i0 > 0 ? keys[i0 - 1].x : kNoToken;
-    const uint32_t next = i0 + n < p.N ? keys[i0 + n].x : kNoToken;
-    uint2 key[kEmbedTile];
-    ElemVec<TI, VE> v[kEmbedTile];
-#pragma unroll
-    for (int i = 0; i < kEmbedTile; ++i) key[i] = i < n ? keys[i0 + i] : make_uint2(kNoToken, 0);
-#pragma unroll
-    for (int i = 0; i < kEmbedTile; ++i)
-      if (key[i].x != kNoToken) v[i].load(p.dout, (int64_t)key[i].y * p.ldd + c);
+    const uint32_t next = i1 < p.N ? keys[i1].x : kNoToken;
+    const uint32_t head = keys[i0].x, tail = keys[i1 - 1].x;
+    bool from_before = prev == head;   // the run at hand began in an earlier tile
+    // the tile where a run begins that goes on past it puts it on the join's list
+    if (span == 0 && threadIdx.x == 0 && tail == next && tail != kNoToken && !(from_before && head == tail))
+      p.runs[atomicAdd(p.n_runs, 1u)] = (uint32_t)tile;
+    if (c >= p.D) continue;
     float sum[VE];
 #pragma unroll
     for (int e = 0; e < VE; ++e) sum[e] = 0.f;
-    bool from_before = prev == key[0].x;   // the run at hand began in an earlier tile
+    for (int64_t b = i0; b < i1; b += kSumBatch) {
+      uint2 key[kSumBatch];
+      ElemVec<TI, VE> v[kSumBatch];
 #pragma unroll
-    for (int i = 0; i < kEmbedTile; ++i) {
-      if (key[i].x != kNoToken) {
+      for (int i = 0; i < kSumBatch; ++i) key[i] = b + i < i1 ? keys[b + i] : make_uint2(kNoToken, 0);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) sum[e] += v[i].at(e);
-        const uint32_t after = i + 1 < kEmbedTile ? (i + 1 < n ? key[i + 1 < kEmbedTile ? i + 1 : 0].x : next) : next;
-        if (after != key[i].x || i + 1 == n) {
-          const bool goes_on = after == key[i].x;
-          if (!from_before && !goes_on) {
-            put_row<TO, VE>(p, key[i].x, c, sum);
-          } else {
-            // slot 0: the tile's first run, slot 1: its last (a run that fills the tile from before has slot 0)
-            elem_store_vec<float, VE>(reinterpret_cast<unsigned char*>(p.part), (tile * 2 + (from_before ? 0 : 1)) * p.ldp + c, sum);
+      for (int i = 0; i < kSumBatch; ++i)
+        if (key[i].x != kNoToken) v[i].load(p.dout, (int64_t)key[i].y * p.ldd + c);
+      const uint32_t after_batch = b + kSumBatch < i1 ? keys[b + kSumBatch].x : next;
+#pragma unroll
+      for (int i = 0; i < kSumBatch; ++i) {
+        if (key[i].x != kNoToken) {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) sum[e] += v[i].at(e);
+          const bool end = b + i + 1 == i1;   // of the tile
+          const uint32_t after = end ? next : i + 1 < kSumBatch ? key[i + 1 < kSumBatch ? i + 1 : 0].x : after_batch;
+          if (after != key[i].x || end) {
+            if (!from_before && after != key[i].x) {
+              put_row<TO, VE>(p, key[i].x, c, sum);
+            } else {
+              // slot 0: the tile's first run, slot 1: its last (a run that fills the tile from before has slot 0)
+              elem_store_vec<float, VE>(reinterpret_cast<unsigned char*>(p.part), (tile * 2 + (from_before ? 0 : 1)) * p.ldp + c, sum);
+            }
+#pragma unroll
+            for (int e = 0; e < VE; ++e) sum[e] = 0.f;
+            from_before = false;
           }
-#pragma unroll
-          for (int e = 0; e < VE; ++e) sum[e] = 0.f;
-          from_before = false;
         }
       }
     }
   }
 }
 
-// Runs over several tiles: the tile where a run begins adds up its parts, in order inside each of eight stretches of
-// tiles, then the stretches in order.
+// Runs over several tiles, from the list that the sums left: the parts of a run are added in order inside each of
+// eight stretches of tiles, then the stretches in order. A CTA per run and kJoinSpan columns, four per lane.
 template <typename TO>
-__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGradParams p, int last, int spans) {
-  __shared__ float part[kEmbedThreads / 32][32];
+__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGradParams p, int last, int spans, int vec) {
+  constexpr int NW = kEmbedThreads / 32;
+  __shared__ float4 part[NW][32];
   const uint2* keys = p.keys[last];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int NW = kEmbedThreads / 32;
-  for (int64_t id = blockIdx.x; id < p.sums * spans; id += gridDim.x) {
-    const int64_t tile = id / spans;
-    const int64_t i0 = tile * kEmbedTile, i1 = i0 + kEmbedTile;
-    if (i1 >= p.N) continue;
-    const uint32_t tok = keys[i1 - 1].x;
-    if (tok == kNoToken || keys[i1].x != tok) continue;                  // no run goes on from this tile
-    if (i0 > 0 && keys[i0].x == tok && keys[i0 - 1].x == tok) continue;  // it began earlier
-    // tiles [tile, end) hold the run: the first tile that does not begin with the token
+  const int64_t total = (int64_t)*p.n_runs * spans;
+  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
+    const int64_t run = id / spans, tile = p.runs[run];
+    const uint32_t tok = keys[tile * kEmbedTile + kEmbedTile - 1].x;
+    // tiles [tile, lo] hold the run: lo is the last tile that begins with the token
     int64_t lo = tile + 1, hi = p.sums;
     while (lo + 1 < hi) {
       const int64_t mid = (lo + hi) / 2;
       if (keys[mid * kEmbedTile].x == tok) lo = mid;
       else hi = mid;
     }
-    const int64_t n = lo + 1 - tile;
-    const int64_t k0 = tile + n * warp / NW, k1 = tile + n * (warp + 1) / NW;
-    for (int64_t c0 = (id - tile * spans) * kJoinSpan; c0 < (id - tile * spans + 1) * kJoinSpan && c0 < p.D; c0 += 32) {
-      const int64_t c = c0 + lane;
-      float sum = 0.f;
-      if (c < p.D) {
+    const int64_t n = lo + 1 - tile, k0 = tile + n * warp / NW, k1 = tile + n * (warp + 1) / NW;
+    const int64_t c = (id - run * spans) * kJoinSpan + lane * 4;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < p.D) {   // parts are padded to ldp, a multiple of 8, columns
 #pragma unroll 8
-        for (int64_t k = k0; k < k1; ++k) sum += p.part[(k * 2 + (k == tile ? 1 : 0)) * p.ldp + c];
+      for (int64_t k = k0; k < k1; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part + (k * 2 + (k == tile ? 1 : 0)) * p.ldp + c);
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
       }
-      part[warp][lane] = sum;
-      __syncthreads();
-      if (warp == 0 && c < p.D) {
-        float all[1] = {part[0][lane]};
-        for (int w = 1; w < NW; ++w) all[0] += part[w][lane];
-        put_row<TO, 1>(p, tok, c, all);
-      }
-      __syncthreads();
     }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp == 0 && c < p.D) {
+      for (int w = 1; w < NW; ++w) {
+        const float4 v = part[w][lane];
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+      }
+      if (vec) {
+        float all[4] = {sum.x, sum.y, sum.z, sum.w};
+        put_row<TO, 4>(p, tok, c, all);
+      } else {
+        const float all[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float one[1] = {all[e]};
+          if (c + e < p.D) put_row<TO, 1>(p, tok, c + e, one);
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 
