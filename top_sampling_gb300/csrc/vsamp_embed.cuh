@@ -23,7 +23,7 @@ constexpr int kSortTile = kSortThreads * kSortPer;       // keys per CTA
 constexpr int kSortBits = 8;
 constexpr int kSortBins = 1 << kSortBits;
 constexpr int kEmbedTile = 16;                           // sorted positions per tile of the sums
-constexpr int kJoinSpan = 128;                           // columns per CTA of the join
+constexpr int kJoinSpan = 1024;                          // columns per CTA of the join
 constexpr uint32_t kNoToken = 0xFFFFFFFFu;               // sorts after every token
 
 struct EmbedParams {
@@ -497,61 +497,56 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(const Embed
   }
 }
 
-// Runs over several tiles, from the list that the sums left: the parts of a run are added in order inside each of
-// eight stretches of tiles, then the stretches in order. A CTA per run and kJoinSpan columns, four per lane.
+// Tiles after `tile` that begin with tok, for a run that goes on past its tile: called by a whole warp, which looks at
+// 32 tiles at a time, then at 32 points of what is left.
+__device__ __forceinline__ int64_t run_tiles(const uint2* keys, int64_t tile, int64_t tiles, uint32_t tok) {
+  const int lane = threadIdx.x & 31;
+  auto holds = [&](int64_t k) { return k < tiles && keys[k * kEmbedTile].x == tok; };
+  uint32_t b = __ballot_sync(kFullMask, holds(tile + 1 + lane));
+  if (b != kFullMask) return __popc(b);
+  int64_t lo = tile + 32, hi = tiles;   // lo holds the token, hi does not
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 31) / 32;
+    b = __ballot_sync(kFullMask, lo + step * lane < hi && holds(lo + step * lane));
+    lo += step * (__popc(b) - 1);
+    if (lo + step < hi) hi = lo + step;
+  }
+  return lo - tile;
+}
+
+// Runs over several tiles, from the list that the sums left: a CTA per run and kJoinSpan columns, four per thread, adds
+// the run's parts in tile order, eight in flight.
 template <typename TO>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGradParams p, int last, int spans, int vec) {
-  constexpr int NW = kEmbedThreads / 32;
-  __shared__ float4 part[NW][32];
   const uint2* keys = p.keys[last];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t total = (int64_t)*p.n_runs * spans;
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
     const int64_t run = id / spans, tile = p.runs[run];
     const uint32_t tok = keys[tile * kEmbedTile + kEmbedTile - 1].x;
-    // tiles [tile, lo] hold the run: lo is the last tile that begins with the token
-    int64_t lo = tile + 1, hi = p.sums;
-    while (lo + 1 < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (keys[mid * kEmbedTile].x == tok) lo = mid;
-      else hi = mid;
-    }
-    const int64_t n = lo + 1 - tile, k0 = tile + n * warp / NW, k1 = tile + n * (warp + 1) / NW;
-    const int64_t c = (id - run * spans) * kJoinSpan + lane * 4;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < p.D) {   // parts are padded to ldp, a multiple of 8, columns
+    const int64_t end = tile + run_tiles(keys, tile, p.sums, tok);   // the last tile of the run
+    const int64_t c = (id - run * spans) * kJoinSpan + threadIdx.x * 4;
+    if (c >= p.D) continue;
+    // parts are padded to ldp, a multiple of 8, columns; slot 1 of the first tile, slot 0 of the others
+    auto at = [&](int64_t k, int slot) { return *reinterpret_cast<const float4*>(p.part + (k * 2 + slot) * p.ldp + c); };
+    float4 sum = at(tile, 1);
 #pragma unroll 8
-      for (int64_t k = k0; k < k1; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part + (k * 2 + (k == tile ? 1 : 0)) * p.ldp + c);
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
-      }
+    for (int64_t k = tile + 1; k <= end; ++k) {
+      const float4 v = at(k, 0);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
     }
-    part[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && c < p.D) {
-      for (int w = 1; w < NW; ++w) {
-        const float4 v = part[w][lane];
-        sum.x += v.x;
-        sum.y += v.y;
-        sum.z += v.z;
-        sum.w += v.w;
-      }
-      if (vec) {
-        float all[4] = {sum.x, sum.y, sum.z, sum.w};
-        put_row<TO, 4>(p, tok, c, all);
-      } else {
-        const float all[4] = {sum.x, sum.y, sum.z, sum.w};
+    float all[4] = {sum.x, sum.y, sum.z, sum.w};
+    if (vec) {
+      put_row<TO, 4>(p, tok, c, all);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float one[1] = {all[e]};
-          if (c + e < p.D) put_row<TO, 1>(p, tok, c + e, one);
-        }
+      for (int e = 0; e < 4; ++e) {
+        float one[1] = {all[e]};
+        if (c + e < p.D) put_row<TO, 1>(p, tok, c + e, one);
       }
     }
-    __syncthreads();
   }
 }
 
