@@ -23,7 +23,7 @@ static vsamp_status launch_score(const ScoreParams& p, cudaStream_t s) {
 template <typename T>
 static vsamp_status launch_score_grad(ScoreGradParams p, cudaStream_t s) {
   constexpr int64_t SPAN = (int64_t)kGradThreads * kGradVecs * ScoreType<T>::VE;
-  p.spans = (p.V + SPAN - 1) / SPAN;
+  p.spans = (p.V + SPAN - 1) / SPAN;   // covers the whole vectors wherever they begin
   return launch_1d(score_grad_kernel<T>, grid_of(p.B * p.spans), kGradThreads, 0, s, false, p);
 }
 

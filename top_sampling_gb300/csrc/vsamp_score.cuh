@@ -462,44 +462,154 @@ __global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(c
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;   // 16-byte vectors per thread
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// One row's constants. With q = 2^s2, s2 = (x - m) log2(e) / T, the gradient off the given token is
+//   -p (g + h (log p + H)) / T = q (k0 + k1 s2)
+struct GradRow {
+  float m, c, k0, k1;
+  __device__ __forceinline__ float at(float x) const {
+    const float s = fmaxf((x - m) * c, -150.f);   // a masked token: 2^-150 is 0 in the flushed exponential
+    return ex2_approx(s) * fmaf(k1, s, k0);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void grad_vector(const GradRow& r, uint32_t (&w)[4]) {
+  using Ty = ScoreType<T>;
+  const uint64_t m2 = pack2(-r.m, -r.m), c2 = pack2(r.c, r.c), k02 = pack2(r.k0, r.k0), k12 = pack2(r.k1, r.k1);
+  uint32_t out[4];
+#pragma unroll
+  for (int j = 0; j < Ty::VE; j += 2) {
+    float a, b;
+    unpack2(mul2(add2(pack2(Ty::at(w, j), Ty::at(w, j + 1)), m2), c2), a, b);
+    a = fmaxf(a, -150.f);
+    b = fmaxf(b, -150.f);
+    const uint64_t d = mul2(pack2(ex2_approx(a), ex2_approx(b)), fma2(k12, pack2(a, b), k02));
+    unpack2(d, a, b);
+    if constexpr (Ty::ES == 4) {
+      out[j] = __float_as_uint(a);
+      out[j + 1] = __float_as_uint(b);
+    } else {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+      memcpy(&out[j / 2], &v, 4);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = out[j];
+}
+
+// One CTA per row and span of kGradThreads * kGradVecs vectors. Vectors begin at the row's first 16-byte boundary when
+// the logits' and the gradient's rows have the same one; the elements before and after the whole vectors belong to
+// the row's first CTA. Otherwise the span is taken element by element. Streaming loads and stores: nothing is reused.
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGradParams p) {
   using Ty = ScoreType<T>;
-  constexpr int64_t SPAN = (int64_t)kGradThreads * kGradVecs * Ty::VE;
+  constexpr int VE = Ty::VE;
+  constexpr int64_t SPAN = (int64_t)kGradThreads * kGradVecs;   // vectors
   const int64_t total = p.B * p.spans;
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const int64_t row = id / p.spans;
-    const int64_t e0 = (id - row * p.spans) * SPAN;
+    const int64_t row = id / p.spans, span = id - row * p.spans;
     const unsigned char* xr = p.x + row * p.ld * Ty::ES;
     unsigned char* dr = p.dx + row * p.ldo * Ty::ES;
     const int32_t t = p.token[row];
     const bool skip = t == VSAMP_TOKEN_IGNORE;
+    const int xa = (int)((16 - (reinterpret_cast<uintptr_t>(xr) & 15)) & 15) / Ty::ES;
+    const int da = (int)((16 - (reinterpret_cast<uintptr_t>(dr) & 15)) & 15) / Ty::ES;
+    const bool vec = xa == da;
+    const int64_t head = xa < p.V ? xa : p.V, nv = (p.V - head) / VE;
+    const int64_t v0 = span * SPAN + threadIdx.x;
+    uint32_t w[kGradVecs][4];
+    if (vec && !skip) {
+#pragma unroll
+      for (int i = 0; i < kGradVecs; ++i) {
+        const int64_t v = v0 + i * kGradThreads;
+        if (v < nv) {
+          const uint4 q = ldg_stream(xr + (head + v * VE) * Ty::ES);
+          w[i][0] = q.x; w[i][1] = q.y; w[i][2] = q.z; w[i][3] = q.w;
+        }
+      }
+    }
     const float temp = p.temperature ? p.temperature[row] : 1.f;
     const float m = p.row_max[row], ls = p.row_logsum[row];
     const float H = p.dentropy ? p.entropy[row] : 0.f;
-    const bool ok = t >= 0 && (int64_t)t < p.V && !isnan(temp) && !isinf(temp) && isfinite(m) && isfinite(ls) && isfinite(H);
-    const float invT = 1.f / (temp > 0.f ? temp : 1.f);
-    const float c = kLog2e / (temp > 0.f ? temp : 1.f);
-    const float invS = expf(-ls);
-    const float g = skip ? 0.f : p.dlogprob ? p.dlogprob[row] : 0.f;
-    const float h = skip || !p.dentropy ? 0.f : p.dentropy[row];
-    // d log p / dx in terms of q = e^s2, s2 = (x - m) c: p (g + h (s2 ln 2 - log S + H)) / T
-    const float k0 = (g + h * (H - ls)) * invT * invS;
-    const float k1 = h * 0.69314718056f * invT * invS;
-    const float gt = g * invT;
+    const bool args = t >= 0 && (int64_t)t < p.V && !isnan(temp) && !isinf(temp);
+    const bool ok = args && isfinite(m) && isfinite(ls) && isfinite(H);
+    const float T1 = temp > 0.f ? temp : 1.f, invT = 1.f / T1;
+    const float scale = -expf(-ls) * invT;
+    const float g = !skip && p.dlogprob ? p.dlogprob[row] : 0.f;
+    const float h = !skip && p.dentropy ? p.dentropy[row] : 0.f;
+    GradRow r;
+    r.m = m;
+    r.c = kLog2e / T1;
+    r.k0 = (g + h * (H - ls)) * scale;
+    r.k1 = h * 0.69314718056f * scale;
     const float fill = skip ? 0.f : __int_as_float(0x7FC00000);
-    if (p.row_status && e0 == 0 && threadIdx.x == 0)
-      p.row_status[row] = skip || ok ? VSAMP_OK
-                          : (t >= 0 && (int64_t)t < p.V && !isnan(temp) && !isinf(temp)) ? VSAMP_ERR_NONFINITE
-                                                                                       : VSAMP_ERR_INVALID_ARG;
-    auto grad = [&](float x, int64_t v) -> float {
-      const float s = fmaxf((x - m) * c, -150.f);
-      const float q = ex2_approx(s);
-      const float d = -q * fmaf(k1, s, k0);
-      return v == t ? d + gt : d;
+    if (p.row_status && span == 0 && threadIdx.x == 0)
+      p.row_status[row] = skip || ok ? VSAMP_OK : args ? VSAMP_ERR_NONFINITE : VSAMP_ERR_INVALID_ARG;
+    auto one = [&](int64_t v) {
+      float d = fill;
+      if (ok) d = r.at(Ty::load(xr, v)) + (v == t ? g * invT : 0.f);
+      Ty::store(dr, v, d);
     };
-    for (int64_t e = e0 + threadIdx.x; e < e0 + SPAN && e < p.V; e += kGradThreads)
-      Ty::store(dr, e, ok ? grad(Ty::load(xr, e), e) : fill);
+    if (!vec) {
+      const int64_t e1 = (span + 1) * SPAN * VE < p.V ? (span + 1) * SPAN * VE : p.V;
+#pragma unroll 4
+      for (int64_t e = span * SPAN * VE + threadIdx.x; e < e1; e += kGradThreads) one(e);
+      continue;
+    }
+    const int64_t tv = ok ? (t - head) / VE : -1;   // the vector that holds the given token
+#pragma unroll
+    for (int i = 0; i < kGradVecs; ++i) {
+      const int64_t v = v0 + i * kGradThreads;
+      if (v < nv) {
+        if (!ok) {
+          const uint32_t b = skip ? 0u : Ty::ES == 4 ? 0x7FC00000u : 0x7FC07FC0u;
+          w[i][0] = w[i][1] = w[i][2] = w[i][3] = b;
+        } else if (v != tv || t < head) {
+          grad_vector<T>(r, w[i]);
+        } else {
+          const int at = (int)(t - head - v * VE);
+          float f[VE];
+#pragma unroll
+          for (int j = 0; j < VE; ++j) f[j] = r.at(Ty::at(w[i], j)) + (j == at ? g * invT : 0.f);
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            if constexpr (Ty::ES == 4) w[i][j] = __float_as_uint(f[j]);
+            else Ty::put(w[i], j, __bfloat162float(__float2bfloat16_rn(f[j])));
+          }
+        }
+        __stcs(reinterpret_cast<uint4*>(dr + (head + v * VE) * Ty::ES), make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]));
+      }
+    }
+    if (span == 0) {
+      if ((int64_t)threadIdx.x < head) one(threadIdx.x);
+      const int64_t e = head + nv * VE + threadIdx.x;
+      if (threadIdx.x < VE && e < p.V) one(e);
+    }
   }
 }
 
