@@ -120,6 +120,31 @@ __device__ __forceinline__ double warp_sum_d(double v) {
   return v;
 }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -144,9 +169,69 @@ __device__ __forceinline__ void score_load(const unsigned char* xr, int64_t e, i
     if (e + j < V) Ty::put(w, j, Ty::load(xr, e + j));
 }
 
-// One warp per piece.
+// Maximum of two registers of a vector's type; NaN if either holds one.
+template <typename T>
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (sizeof(T) == 4) asm("max.NaN.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The maximum that a register of partial maxima holds.
+template <typename T>
+__device__ __forceinline__ float max_of_word(uint32_t a) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(a);
+  else return max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+}
+
+// Elements of a lane's vectors that are larger than xt (or_equal: or equal to it).
+template <typename T>
+__device__ __forceinline__ uint32_t count_larger(const uint32_t (&w)[kScoreChunks][4], float xt, bool or_equal) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t n = 0;
+    if (or_equal) {
+#pragma unroll
+      for (int i = 0; i < kScoreChunks; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n += __uint_as_float(w[i][j]) >= xt ? 1u : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kScoreChunks; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n += __uint_as_float(w[i][j]) > xt ? 1u : 0u;
+    }
+    return n;
+  } else {
+    // pairs: 1.0 per true comparison, at most 32 per half: exact in bf16
+    const __nv_bfloat162 t = __float2bfloat162_rn(xt);
+    __nv_bfloat162 n = __float2bfloat162_rn(0.f);
+    if (or_equal) {
+#pragma unroll
+      for (int i = 0; i < kScoreChunks; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          __nv_bfloat162 x;
+          memcpy(&x, &w[i][j], 4);
+          n = __hadd2(n, __hge2(x, t));
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kScoreChunks; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          __nv_bfloat162 x;
+          memcpy(&x, &w[i][j], 4);
+          n = __hadd2(n, __hgt2(x, t));
+        }
+    }
+    return (uint32_t)(__low2float(n) + __high2float(n));
+  }
+}
+
+// One warp per piece. What it costs per bf16 element is about six instructions beside the exponential, whose unit
+// (a sixteenth of a warp per cycle and quarter SM) is the nearest bound after the memory.
 template <typename T, bool ALT>
-__global__ void __launch_bounds__(kScoreWarps * 32) score_piece_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const ScoreParams p) {
   using Ty = ScoreType<T>;
   constexpr int PE = kScorePiece / Ty::ES;      // elements per piece
   constexpr int CE = PE / kScoreChunks;         // elements per chunk
@@ -154,63 +239,96 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_piece_kernel(const Sco
   const int64_t total = p.B * p.np;
   for (int64_t id = (int64_t)blockIdx.x * kScoreWarps + (threadIdx.x >> 5); id < total;
        id += (int64_t)gridDim.x * kScoreWarps) {
-    const int64_t row = id / p.np;
+    const int64_t row = total <= 0xFFFFFFFFLL ? (int64_t)((uint32_t)id / (uint32_t)p.np) : id / p.np;
     const int64_t e0 = (id - row * p.np) * PE;
     const int32_t t = p.token[row];
     if (t == VSAMP_TOKEN_IGNORE) continue;
     const unsigned char* xr = p.x + row * p.ld * Ty::ES;
     uint32_t w[kScoreChunks][4];
+    if (p.vec && e0 + PE <= p.V) {
 #pragma unroll
-    for (int i = 0; i < kScoreChunks; ++i) score_load<T>(xr, e0 + i * CE + lane * Ty::VE, p.V, p.vec, w[i]);
+      for (int i = 0; i < kScoreChunks; ++i) {
+        const uint4 v = ldg_stream(xr + e0 * Ty::ES + i * 512 + lane * 16);
+        w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kScoreChunks; ++i) score_load<T>(xr, e0 + i * CE + lane * Ty::VE, p.V, p.vec, w[i]);
+    }
     const float temp = p.temperature ? p.temperature[row] : 1.f;
     const float c = kLog2e / (temp > 0.f ? temp : 1.f);
     const bool known = t >= 0 && t < p.V;
     const float xt = known ? Ty::load(xr, t) : INFINITY;
 
-    // maximum of every lane's vectors, of the chunks and of the piece
+    // maximum of the lane's vectors, of the chunks and of the piece
     float m = -INFINITY;
-    float mine = -INFINITY;    // lane i < 8: maximum of chunk i
+    if (ALT) {
+      float mine = 0.f;    // lane i < 8: maximum of chunk i
 #pragma unroll
-    for (int i = 0; i < kScoreChunks; ++i) {
-      float cm = Ty::at(w[i], 0);
-#pragma unroll
-      for (int j = 1; j < Ty::VE; ++j) cm = max_nan(cm, Ty::at(w[i], j));
-      if (ALT) {
-        cm = warp_max_nan(cm);
+      for (int i = 0; i < kScoreChunks; ++i) {
+        const float cm = warp_max_nan(
+            max_of_word<T>(max_word<T>(max_word<T>(w[i][0], w[i][1]), max_word<T>(w[i][2], w[i][3]))));
         if (lane == i) mine = cm;
+        m = max_nan(m, cm);
       }
-      m = max_nan(m, cm);
+      if (lane < kScoreChunks) p.chunk_max[id * kScoreChunks + lane] = mine;
+    } else {
+      uint32_t a = max_word<T>(w[0][0], w[0][1]), b = max_word<T>(w[0][2], w[0][3]);
+#pragma unroll
+      for (int i = 1; i < kScoreChunks; ++i) {
+        a = max_word<T>(a, max_word<T>(w[i][0], w[i][1]));
+        b = max_word<T>(b, max_word<T>(w[i][2], w[i][3]));
+      }
+      m = warp_max_nan(max_of_word<T>(max_word<T>(a, b)));
     }
-    if (!ALT) m = warp_max_nan(m);
-    if (ALT && lane < kScoreChunks) p.chunk_max[id * kScoreChunks + lane] = mine;
+
+    // tokens before the given one: ties count in the pieces before its own, up to its place in its own
+    uint32_t before = 0;
+    if (known && !isnan(m)) {
+      if (t >= e0 + PE) {
+        before = count_larger<T>(w, xt, true);
+      } else if (t < e0) {
+        before = count_larger<T>(w, xt, false);
+      } else {
+        const int at = (int)(t - e0);
+#pragma unroll
+        for (int i = 0; i < kScoreChunks; ++i)
+#pragma unroll
+          for (int j = 0; j < Ty::VE; ++j) {
+            const float x = Ty::at(w[i], j);
+            before += x > xt || (x == xt && i * CE + lane * Ty::VE + j < at) ? 1u : 0u;
+          }
+      }
+    }
+    before = warp_sum_u32(before);
 
     float S = 0.f, A = 0.f;
-    uint32_t before = 0;
     if (m > -INFINITY && m < INFINITY) {   // false for NaN too
+      const uint64_t m2 = pack2(-m, -m), c2 = pack2(c, c);
+      uint64_t S2[2] = {0, 0}, A2[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < kScoreChunks; ++i) {
 #pragma unroll
-        for (int j = 0; j < Ty::VE; ++j) {
-          const float x = Ty::at(w[i], j);
+        for (int j = 0; j < Ty::VE; j += 2) {
+          float a, b;
+          unpack2(mul2(add2(pack2(Ty::at(w[i], j), Ty::at(w[i], j + 1)), m2), c2), a, b);
           // 2^-150 is 0 in the flushed exponential: a masked token adds 0 to both sums
-          const float s = fmaxf((x - m) * c, -150.f);
-          const float e = ex2_approx(s);
-          S += e;
-          A = fmaf(s, e, A);
-          const int64_t v = e0 + i * CE + lane * Ty::VE + j;
-          before += (x > xt || (x == xt && v < t)) ? 1u : 0u;
+          a = fmaxf(a, -150.f);
+          b = fmaxf(b, -150.f);
+          const uint64_t e = pack2(ex2_approx(a), ex2_approx(b));
+          const int k = (j >> 1) & 1;
+          S2[k] = add2(S2[k], e);
+          A2[k] = fma2(pack2(a, b), e, A2[k]);
         }
       }
-    } else if (m == -INFINITY && known && xt == -INFINITY) {
-      // a masked piece before a masked given token: all of its tokens come first
-#pragma unroll
-      for (int i = 0; i < kScoreChunks; ++i)
-#pragma unroll
-        for (int j = 0; j < Ty::VE; ++j) before += e0 + i * CE + lane * Ty::VE + j < t ? 1u : 0u;
+      float a, b;
+      unpack2(add2(S2[0], S2[1]), a, b);
+      S = a + b;
+      unpack2(add2(A2[0], A2[1]), a, b);
+      A = a + b;
     }
     S = warp_sum_f(S);
     A = warp_sum_f(A);
-    before = warp_sum_u32(before);
     if (lane == 0) p.rec[id] = make_float4(m, S, A, __uint_as_float(before));
   }
 }
@@ -461,31 +579,6 @@ __global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(c
 // ------------------------------------------------------------------------------------------------
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;   // 16-byte vectors per thread
-
-// two fp32 operations in one instruction
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 // One row's constants. With q = 2^s2, s2 = (x - m) log2(e) / T, the gradient off the given token is
 //   -p (g + h (log p + H)) / T = q (k0 + k1 s2)
