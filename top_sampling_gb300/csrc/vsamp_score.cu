@@ -16,8 +16,8 @@ static vsamp_status launch_score(const ScoreParams& p, cudaStream_t s) {
       launch_1d(p.N > 0 ? score_piece_kernel<T, true> : score_piece_kernel<T, false>, grid, kScoreWarps * 32, 0, s,
                 false, p);
   if (st != VSAMP_OK) return st;
-  if (p.N > 0) return launch_1d(score_finish_alt_kernel<T>, grid_of(p.B), kScoreFinishThreads, 0, s, false, p);
-  return launch_1d(score_finish_kernel<T>, grid_of((p.B + 3) / 4), 128, 0, s, false, p);
+  if (p.N > 0) return launch_1d(score_finish_alt_kernel<T>, grid_of(p.B), kScoreFinishThreads, 0, s, true, p);
+  return launch_1d(score_finish_kernel<T>, grid_of((p.B + 3) / 4), 128, 0, s, true, p);
 }
 
 template <typename T>

@@ -24,7 +24,8 @@ namespace vsamp {
 constexpr int kScorePiece = 4096;      // bytes of a row per warp
 constexpr int kScoreChunks = 8;        // 512-byte chunks per piece: one 16-byte vector per lane each
 constexpr int kScoreWarps = 8;
-constexpr int kScoreFinishThreads = 128;
+constexpr int kScoreFinishThreads = 256;
+constexpr int kScoreChunkList = 2 * VSAMP_SCORE_ALT_MAX + 64;   // chunks read again per row
 constexpr int kScoreList = 512;        // alternatives' candidates kept on chip; more of them take the radix path
 
 struct ScoreParams {
@@ -114,12 +115,6 @@ __device__ __forceinline__ float warp_sum_f(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
   return v;
 }
-__device__ __forceinline__ double warp_sum_d(double v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
-  return v;
-}
-
 // two fp32 operations in one instruction
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
@@ -228,6 +223,49 @@ __device__ __forceinline__ uint32_t count_larger(const uint32_t (&w)[kScoreChunk
   }
 }
 
+// A lane's sums of 2^s2 and s2 2^s2, s2 = (x - m) c, over its vectors.
+template <typename T, bool PACKED>
+__device__ __forceinline__ void score_sums(const uint32_t (&w)[kScoreChunks][4], float m, float c, float lowest, float& S,
+                                           float& A) {
+  using Ty = ScoreType<T>;
+  const uint64_t m2 = pack2(-m, -m), c2 = pack2(c, c);
+  uint64_t S2[2] = {0, 0}, A2[2] = {0, 0};
+  __nv_bfloat162 low;
+  low.x = low.y = __float2bfloat16_rd(lowest);
+#pragma unroll
+  for (int i = 0; i < kScoreChunks; ++i) {
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = w[i][j];
+      if (PACKED) {
+        __nv_bfloat162 x;
+        memcpy(&x, &v[j], 4);
+        x = __hmax2(x, low);
+        memcpy(&v[j], &x, 4);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < Ty::VE; j += 2) {
+      float a, b;
+      unpack2(mul2(add2(pack2(Ty::at(v, j), Ty::at(v, j + 1)), m2), c2), a, b);
+      if (!PACKED) {
+        a = fmaxf(a, -150.f);
+        b = fmaxf(b, -150.f);
+      }
+      const uint64_t e = pack2(ex2_approx(a), ex2_approx(b));
+      const int k = (j >> 1) & 1;
+      S2[k] = add2(S2[k], e);
+      A2[k] = fma2(pack2(a, b), e, A2[k]);
+    }
+  }
+  float a, b;
+  unpack2(add2(S2[0], S2[1]), a, b);
+  S = a + b;
+  unpack2(add2(A2[0], A2[1]), a, b);
+  A = a + b;
+}
+
 // One warp per piece. What it costs per bf16 element is about six instructions beside the exponential, whose unit
 // (a sixteenth of a warp per cycle and quarter SM) is the nearest bound after the memory.
 template <typename T, bool ALT>
@@ -237,6 +275,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const 
   constexpr int CE = PE / kScoreChunks;         // elements per chunk
   const int lane = threadIdx.x & 31;
   const int64_t total = p.B * p.np;
+  cudaTriggerProgrammaticLaunchCompletion();   // the finish may be set up while the last pieces run
   for (int64_t id = (int64_t)blockIdx.x * kScoreWarps + (threadIdx.x >> 5); id < total;
        id += (int64_t)gridDim.x * kScoreWarps) {
     const int64_t row = total <= 0xFFFFFFFFLL ? (int64_t)((uint32_t)id / (uint32_t)p.np) : id / p.np;
@@ -284,7 +323,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const 
 
     // tokens before the given one: ties count in the pieces before its own, up to its place in its own
     uint32_t before = 0;
-    if (known && !isnan(m)) {
+    if (known && m >= xt) {   // a piece below the given token has none (false for NaN too)
       if (t >= e0 + PE) {
         before = count_larger<T>(w, xt, true);
       } else if (t < e0) {
@@ -304,28 +343,12 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const 
 
     float S = 0.f, A = 0.f;
     if (m > -INFINITY && m < INFINITY) {   // false for NaN too
-      const uint64_t m2 = pack2(-m, -m), c2 = pack2(c, c);
-      uint64_t S2[2] = {0, 0}, A2[2] = {0, 0};
-#pragma unroll
-      for (int i = 0; i < kScoreChunks; ++i) {
-#pragma unroll
-        for (int j = 0; j < Ty::VE; j += 2) {
-          float a, b;
-          unpack2(mul2(add2(pack2(Ty::at(w[i], j), Ty::at(w[i], j + 1)), m2), c2), a, b);
-          // 2^-150 is 0 in the flushed exponential: a masked token adds 0 to both sums
-          a = fmaxf(a, -150.f);
-          b = fmaxf(b, -150.f);
-          const uint64_t e = pack2(ex2_approx(a), ex2_approx(b));
-          const int k = (j >> 1) & 1;
-          S2[k] = add2(S2[k], e);
-          A2[k] = fma2(pack2(a, b), e, A2[k]);
-        }
-      }
-      float a, b;
-      unpack2(add2(S2[0], S2[1]), a, b);
-      S = a + b;
-      unpack2(add2(A2[0], A2[1]), a, b);
-      A = a + b;
+      // A masked token must add 0 to both sums, and e^s s is NaN at s = -inf: elements are raised to a value so far
+      // below the maximum that its exponential, at 2^-150 or less, is flushed to 0. For bf16 two elements at once, unless
+      // the temperature is so large that no finite bf16 is that low.
+      const float lowest = m - 150.f / c;
+      if (sizeof(T) == 2 && lowest > -3.3e38f) score_sums<T, true>(w, m, c, lowest, S, A);
+      else score_sums<T, false>(w, m, c, lowest, S, A);
     }
     S = warp_sum_f(S);
     A = warp_sum_f(A);
@@ -352,7 +375,7 @@ __device__ __forceinline__ ScoreRow score_fold(const ScoreParams& p, int64_t row
   float m = -INFINITY;
   for (int64_t i = lane; i < p.np; i += 32) m = max_nan(m, rec[i].x);
   m = warp_max_nan(m);
-  double S = 0.0, A = 0.0;
+  float S = 0.f, A = 0.f;
   uint32_t before = 0;
   const bool finite = m > -INFINITY && m < INFINITY;
   if (finite) {
@@ -362,18 +385,18 @@ __device__ __forceinline__ ScoreRow score_fold(const ScoreParams& p, int64_t row
       if (q.x > -INFINITY) {
         const float d = fmaxf((q.x - m) * c, -150.f);
         const float f = ex2_approx(d);
-        S += (double)(f * q.y);
-        A += (double)(f * fmaf(d, q.y, q.z));
+        S = fmaf(f, q.y, S);
+        A = fmaf(f, fmaf(d, q.y, q.z), A);
       }
     }
   }
-  S = warp_sum_d(S);
-  A = warp_sum_d(A);
+  S = warp_sum_f(S);
+  A = warp_sum_f(A);
   r.before = warp_sum_u32(before);
   r.m = m;
   // S >= 1: log1p keeps the digits of a sum close to 1
-  r.logsum = log1pf((float)(S - 1.0));
-  r.entropy = fmaxf(r.logsum - 0.69314718056f * (float)(A / S), 0.f);
+  r.logsum = log1pf(S - 1.f);
+  r.entropy = fmaxf(r.logsum - 0.69314718056f * (A / S), 0.f);
   r.status = VSAMP_OK;
   if (!finite) r.status = VSAMP_ERR_NONFINITE;
   else if (isnan(temp) || isinf(temp) || t < 0 || (int64_t)t >= p.V) r.status = VSAMP_ERR_INVALID_ARG;
@@ -391,7 +414,7 @@ __device__ __forceinline__ void score_write(const ScoreParams& p, int64_t row, i
     if (ok && !skip) {
       const float xt = ScoreType<T>::load(p.x + row * p.ld * ScoreType<T>::ES, t);
       const float temp = p.temperature ? p.temperature[row] : 1.f;
-      lp = fminf((float)((double)(xt - r.m) / (temp > 0.f ? temp : 1.f) - (double)r.logsum), 0.f);
+      lp = fminf((xt - r.m) / (temp > 0.f ? temp : 1.f) - r.logsum, 0.f);
     }
     p.logprob[row] = lp;
   }
@@ -405,6 +428,7 @@ __device__ __forceinline__ void score_write(const ScoreParams& p, int64_t row, i
 // No alternatives: one warp per row.
 template <typename T>
 __global__ void __launch_bounds__(128) score_finish_kernel(const ScoreParams p) {
+  cudaGridDependencySynchronize();   // every piece record is written
   for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); row < p.B; row += (int64_t)gridDim.x * 4) {
     const int32_t t = p.token[row];
     ScoreRow r{};
@@ -465,106 +489,153 @@ __device__ uint64_t score_radix_select(F for_each, uint32_t want, uint32_t* hist
   return prefix;
 }
 
-// One CTA per row: warp 0 folds the records, then all threads find the alternatives.
+// One CTA per row. The last warp folds the records while the others look for the alternatives:
+//   1. every group of threads takes the largest of its chunks; the N-th largest of these is a bound that at least N
+//      chunks reach, so every alternative does;
+//   2. the chunks at or above the bound are listed (their number is close to N; an arrangement that lists many more
+//      is cut to the N that the lemma above needs by a radix search);
+//   3. the tokens of the listed chunks at or above the bound are listed, again close to N of them (more than the list
+//      holds: the last alternative is found by radix search), and each one's place is the number of larger ones.
+// Keys are (value, index) pairs in the order's sense, all different.
 template <typename T>
 __global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(const ScoreParams p) {
   using Ty = ScoreType<T>;
   constexpr int CE = kScorePiece / Ty::ES / kScoreChunks;
-  constexpr int NW = kScoreFinishThreads / 32;
+  constexpr int NT = kScoreFinishThreads, NW = NT / 32;
   __shared__ uint32_t hist[256];
   __shared__ uint32_t bc[3];
-  __shared__ uint64_t list[kScoreList];
-  __shared__ int32_t chunks[VSAMP_SCORE_ALT_MAX];
-  __shared__ uint32_t n_chunks, n_list, floor_key, n_valid;
+  __shared__ __align__(16) uint64_t list[kScoreList];
+  __shared__ __align__(16) uint64_t best[NT];
+  __shared__ int32_t chunks[kScoreChunkList];
+  __shared__ uint32_t n_chunks, n_list;
+  __shared__ uint64_t bound;
   __shared__ ScoreRow shared_row;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float qnan = __int_as_float(0x7FC00000);
   constexpr uint32_t kNone = 0x007FFFFFu;   // key of -inf
+  // threads per group: a few groups for every alternative
+  const int gs = p.N <= NT / 16 ? 8 : p.N <= NT / 8 ? 4 : p.N <= NT / 4 ? 2 : 1;
+  const int groups = NT / gs;
+  cudaGridDependencySynchronize();   // every piece record is written
   for (int64_t row = blockIdx.x; row < p.B; row += gridDim.x) {
     const int32_t t = p.token[row];
     const bool skip = t == VSAMP_TOKEN_IGNORE;
-    if (warp == 0) {
-      ScoreRow r{};
-      if (!skip) r = score_fold<T>(p, row, t);
-      if (lane == 0) {
-        score_write<T>(p, row, t, r);
-        shared_row = r;
-        n_chunks = n_list = n_valid = 0;
-        floor_key = 0xFFFFFFFFu;
-      }
-    }
-    __syncthreads();
-    const ScoreRow r = shared_row;
     int32_t* oi = p.alt_idx + row * p.N;
     float* ol = p.alt_lp + row * p.N;
     uint32_t found = 0;
-    if (!skip && r.status == VSAMP_OK) {
+    if (skip) {
+      if (tid == 0) score_write<T>(p, row, t, ScoreRow{});
+    } else {
       const int64_t nch = p.np * kScoreChunks;
       const float* cm = p.chunk_max + row * nch;
       const unsigned char* xr = p.x + row * p.ld * Ty::ES;
       auto each_chunk = [&](auto f) {
-        for (int64_t i = threadIdx.x; i < nch; i += kScoreFinishThreads) {
+#pragma unroll 4
+        for (int64_t i = tid; i < nch; i += NT) {
           const uint32_t k = key_f32_bits(__float_as_uint(cm[i]));
           if (k > kNone) f(((uint64_t)k << 32) | (uint32_t)~(uint32_t)i);
         }
       };
-      uint32_t mine = 0;
-      each_chunk([&](uint64_t) { ++mine; });
-      if (mine) atomicAdd(&n_valid, mine);
+      uint64_t mine = 0;
+      each_chunk([&](uint64_t k) { mine = k > mine ? k : mine; });
+      for (int o = 1; o < gs; o <<= 1) {
+        const uint64_t v = __shfl_xor_sync(kFullMask, mine, o);
+        mine = v > mine ? v : mine;
+      }
+      if (tid % gs == 0) best[tid / gs] = mine;
+      if (tid == 0) {
+        n_chunks = n_list = 0;
+        bound = 0;
+      }
       __syncthreads();
-      const uint64_t cut = n_valid > (uint32_t)p.N ? score_radix_select(each_chunk, (uint32_t)p.N, hist, bc) : 0;
-      each_chunk([&](uint64_t k) {
-        if (k >= cut) {
-          chunks[atomicAdd(&n_chunks, 1u)] = (int32_t)~(uint32_t)k;
-          atomicMin(&floor_key, (uint32_t)(k >> 32));
+      if (warp == NW - 1) {
+        const ScoreRow r = score_fold<T>(p, row, t);
+        if (lane == 0) {
+          score_write<T>(p, row, t, r);
+          shared_row = r;
         }
-      });
+      }
+      for (int g = tid; g < groups; g += NT - 32) {   // the first warps: the fold is the last one's
+        if (warp == NW - 1) break;
+        const uint64_t k = best[g];
+        int larger = 0;
+#pragma unroll 8
+        for (int i = 0; i < groups; ++i) larger += best[i] > k ? 1 : 0;
+        if (larger == p.N - 1 && k > 0) bound = k;     // one group, if that many groups have a token
+      }
       __syncthreads();
-      const uint32_t nc = n_chunks;
-      // every alternative is at least the smallest of these chunks' maxima when there are N of them
-      const uint32_t lowest = n_valid >= (uint32_t)p.N ? floor_key : kNone + 1;
-      auto each_token = [&](auto f) {
-        for (uint32_t i = warp; i < nc; i += NW) {
-          const int64_t e = (int64_t)chunks[i] * CE + lane * Ty::VE;
-          uint32_t w[4];
-          score_load<T>(xr, e, p.V, p.vec, w);
+      uint64_t cut = bound;
+      const ScoreRow r = shared_row;
+      if (r.status == VSAMP_OK) {
+        auto list_chunks = [&]() {
+          each_chunk([&](uint64_t k) {
+            if (k >= cut) {
+              const uint32_t at = atomicAdd(&n_chunks, 1u);
+              if (at < kScoreChunkList) chunks[at] = (int32_t)~(uint32_t)k;
+            }
+          });
+          __syncthreads();
+        };
+        list_chunks();
+        if (n_chunks > 2 * (uint32_t)p.N + 64) {   // far more than N: at least N of them, so the search finds its N-th
+          cut = score_radix_select(each_chunk, (uint32_t)p.N, hist, bc);
+          if (tid == 0) n_chunks = 0;
+          __syncthreads();
+          list_chunks();
+        }
+        const uint32_t nc = n_chunks;
+        const uint32_t lowest = max((uint32_t)(cut >> 32), kNone + 1);
+        auto each_token = [&](auto f) {
+          for (uint32_t i = warp; i < nc; i += 2 * NW) {   // two chunks in flight
+            uint32_t w[2][4];
+            int64_t e[2];
 #pragma unroll
-          for (int j = 0; j < Ty::VE; ++j) {
-            const uint32_t k = key_f32_bits(__float_as_uint(Ty::at(w, j)));
-            if (k >= lowest) f(((uint64_t)k << 32) | (uint32_t)~(uint32_t)(e + j));
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t at = i + u * NW;
+              e[u] = at < nc ? (int64_t)chunks[at] * CE + lane * Ty::VE : p.V;
+              score_load<T>(xr, e[u], p.V, p.vec, w[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int j = 0; j < Ty::VE; ++j) {
+                const uint32_t k = key_f32_bits(__float_as_uint(Ty::at(w[u], j)));
+                if (k >= lowest) f(((uint64_t)k << 32) | (uint32_t)~(uint32_t)(e[u] + j));
+              }
           }
-        }
-      };
-      each_token([&](uint64_t k) {
-        const uint32_t at = atomicAdd(&n_list, 1u);
-        if (at < kScoreList) list[at] = k;
-      });
-      __syncthreads();
-      uint32_t n = n_list;
-      if (n > kScoreList) {
-        // more candidates than the list holds: find the last alternative by radix search, list the N exactly
-        const uint64_t last = score_radix_select(each_token, (uint32_t)p.N, hist, bc);
-        if (threadIdx.x == 0) n_list = 0;
-        __syncthreads();
+        };
         each_token([&](uint64_t k) {
-          if (k >= last) list[atomicAdd(&n_list, 1u)] = k;
+          const uint32_t at = atomicAdd(&n_list, 1u);
+          if (at < kScoreList) list[at] = k;
         });
         __syncthreads();
-        n = n_list;
-      }
-      found = n < (uint32_t)p.N ? n : (uint32_t)p.N;
-      for (uint32_t i = threadIdx.x; i < n; i += kScoreFinishThreads) {
-        const uint64_t k = list[i];
-        uint32_t place = 0;
-        for (uint32_t j = 0; j < n; ++j) place += list[j] > k ? 1u : 0u;
-        if (place < (uint32_t)p.N) {
-          oi[place] = (int32_t)~(uint32_t)k;
-          const float s = (value_of_key32((uint32_t)(k >> 32)) - r.m) * r.invT;
-          ol[place] = fminf(s - r.logsum, 0.f);
+        uint32_t n = n_list;
+        if (n > kScoreList) {
+          // more candidates than the list holds: find the last alternative by radix search, list the N exactly
+          const uint64_t last = score_radix_select(each_token, (uint32_t)p.N, hist, bc);
+          if (tid == 0) n_list = 0;
+          __syncthreads();
+          each_token([&](uint64_t k) {
+            if (k >= last) list[atomicAdd(&n_list, 1u)] = k;
+          });
+          __syncthreads();
+          n = n_list;
+        }
+        found = n < (uint32_t)p.N ? n : (uint32_t)p.N;
+        for (uint32_t i = tid; i < n; i += NT) {
+          const uint64_t k = list[i];
+          uint32_t place = 0;
+#pragma unroll 4
+          for (uint32_t j = 0; j < n; ++j) place += list[j] > k ? 1u : 0u;
+          if (place < (uint32_t)p.N) {
+            oi[place] = (int32_t)~(uint32_t)k;
+            const float s = (value_of_key32((uint32_t)(k >> 32)) - r.m) * r.invT;
+            ol[place] = fminf(s - r.logsum, 0.f);
+          }
         }
       }
     }
-    for (uint32_t j = found + threadIdx.x; j < (uint32_t)p.N; j += kScoreFinishThreads) {
+    for (uint32_t j = found + tid; j < (uint32_t)p.N; j += NT) {
       oi[j] = -1;
       ol[j] = qnan;
     }
