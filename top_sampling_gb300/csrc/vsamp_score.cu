@@ -72,9 +72,16 @@ vsamp_status vsamp_score_tokens(const void* logits, vsamp_dtype dt, int64_t B, i
   p.N = N;
   const int64_t es = dt == VSAMP_F32 ? 4 : 2;
   p.vec = (reinterpret_cast<uintptr_t>(logits) & 15u) == 0 && (B == 1 || (ld * es) % 16 == 0);
-  p.np = score_pieces(dt, V);
+  const int64_t np = score_pieces(dt, V);
+  if (np * B > 0x7FFFFFFFLL) return VSAMP_ERR_UNSUPPORTED;
+  p.np = (int)np;
+  // id / np for id < 2^31: with l = ceil(log2 np), ceil(2^(31 + l) / np) is exact to 31 bits
+  int l = 0;
+  while ((1LL << l) < np) ++l;
+  p.np_mul = (uint32_t)(((1ULL << (31 + l)) + (uint64_t)np - 1) / (uint64_t)np);
+  p.np_shift = l - 1;
   p.rec = static_cast<float4*>(workspace);
-  p.chunk_max = N > 0 ? reinterpret_cast<float*>(p.rec + B * p.np) : nullptr;
+  p.chunk_max = N > 0 ? reinterpret_cast<float*>(p.rec + B * np) : nullptr;
   p.logprob = logprob;
   p.entropy = entropy;
   p.rank = rank;

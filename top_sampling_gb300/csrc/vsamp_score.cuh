@@ -35,7 +35,9 @@ struct ScoreParams {
   const int32_t* token;
   int N;                 // alternatives per row
   int vec;               // rows are 16-byte aligned
-  int64_t np;            // pieces per row
+  int np;                // pieces per row; B * np < 2^31
+  uint32_t np_mul;       // id / np = umulhi(id, np_mul) >> np_shift for np > 1
+  int np_shift;
   float4* rec;           // [B, np] {m_p, S_p, A_p, tokens before the given one}
   float* chunk_max;      // [B, np, 8] (N > 0)
   float* logprob;
@@ -115,31 +117,6 @@ __device__ __forceinline__ float warp_sum_f(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
   return v;
 }
-// two fp32 operations in one instruction
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -159,6 +136,7 @@ __device__ __forceinline__ void score_load(const unsigned char* xr, int64_t e, i
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = Ty::kMasked;
+  if (e >= V) return;
 #pragma unroll
   for (int j = 0; j < Ty::VE; ++j)
     if (e + j < V) Ty::put(w, j, Ty::load(xr, e + j));
@@ -223,47 +201,37 @@ __device__ __forceinline__ uint32_t count_larger(const uint32_t (&w)[kScoreChunk
   }
 }
 
-// A lane's sums of 2^s2 and s2 2^s2, s2 = (x - m) c, over its vectors.
-template <typename T, bool PACKED>
+// A lane's sums of 2^s2 and s2 2^s2, s2 = (x - m) c, over its vectors. A masked token must add 0 to both, and s2 2^s2
+// is NaN at s2 = -inf: elements are raised to `lowest`, whose exponential is flushed to 0 (2^-150), two bf16 at once
+// (RAISE), or, at a temperature so large that no finite value is that low, the products are.
+// (One fused multiply-add x c - m c instead of the difference and the product is 8% fewer instructions, but then the
+// maximum's own exponential is not exactly 1, and a row with one likely token loses the digits of its log-probability.)
+template <typename T, bool RAISE>
 __device__ __forceinline__ void score_sums(const uint32_t (&w)[kScoreChunks][4], float m, float c, float lowest, float& S,
                                            float& A) {
   using Ty = ScoreType<T>;
-  const uint64_t m2 = pack2(-m, -m), c2 = pack2(c, c);
-  uint64_t S2[2] = {0, 0}, A2[2] = {0, 0};
-  __nv_bfloat162 low;
-  low.x = low.y = __float2bfloat16_rd(lowest);
+  const float2 m2 = make_float2(-m, -m), c2 = make_float2(c, c);
+  float2 S2[2] = {{0.f, 0.f}, {0.f, 0.f}}, A2[2] = {{0.f, 0.f}, {0.f, 0.f}};
+  uint32_t low = __float_as_uint(lowest);
+  if (sizeof(T) == 2) low = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rd(lowest)) * 0x10001u;
 #pragma unroll
   for (int i = 0; i < kScoreChunks; ++i) {
     uint32_t v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = w[i][j];
-      if (PACKED) {
-        __nv_bfloat162 x;
-        memcpy(&x, &v[j], 4);
-        x = __hmax2(x, low);
-        memcpy(&v[j], &x, 4);
-      }
-    }
+    for (int j = 0; j < 4; ++j) v[j] = RAISE ? max_word<T>(w[i][j], low) : w[i][j];
 #pragma unroll
     for (int j = 0; j < Ty::VE; j += 2) {
-      float a, b;
-      unpack2(mul2(add2(pack2(Ty::at(v, j), Ty::at(v, j + 1)), m2), c2), a, b);
-      if (!PACKED) {
-        a = fmaxf(a, -150.f);
-        b = fmaxf(b, -150.f);
-      }
-      const uint64_t e = pack2(ex2_approx(a), ex2_approx(b));
+      const float2 x = make_float2(Ty::at(v, j), Ty::at(v, j + 1));
+      float2 s = __fmul2_rn(__fadd2_rn(x, m2), c2);
+      if (!RAISE) s = make_float2(fmaxf(s.x, -150.f), fmaxf(s.y, -150.f));
+      const float2 e = make_float2(ex2_approx(s.x), ex2_approx(s.y));
       const int k = (j >> 1) & 1;
-      S2[k] = add2(S2[k], e);
-      A2[k] = fma2(pack2(a, b), e, A2[k]);
+      S2[k] = __fadd2_rn(S2[k], e);
+      A2[k] = __ffma2_rn(s, e, A2[k]);
     }
   }
-  float a, b;
-  unpack2(add2(S2[0], S2[1]), a, b);
-  S = a + b;
-  unpack2(add2(A2[0], A2[1]), a, b);
-  A = a + b;
+  S = (S2[0].x + S2[1].x) + (S2[0].y + S2[1].y);
+  A = (A2[0].x + A2[1].x) + (A2[0].y + A2[1].y);
 }
 
 // One warp per piece. What it costs per bf16 element is about six instructions beside the exponential, whose unit
@@ -274,86 +242,82 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const 
   constexpr int PE = kScorePiece / Ty::ES;      // elements per piece
   constexpr int CE = PE / kScoreChunks;         // elements per chunk
   const int lane = threadIdx.x & 31;
-  const int64_t total = p.B * p.np;
   cudaTriggerProgrammaticLaunchCompletion();   // the finish may be set up while the last pieces run
-  for (int64_t id = (int64_t)blockIdx.x * kScoreWarps + (threadIdx.x >> 5); id < total;
-       id += (int64_t)gridDim.x * kScoreWarps) {
-    const int64_t row = total <= 0xFFFFFFFFLL ? (int64_t)((uint32_t)id / (uint32_t)p.np) : id / p.np;
-    const int64_t e0 = (id - row * p.np) * PE;
-    const int32_t t = p.token[row];
-    if (t == VSAMP_TOKEN_IGNORE) continue;
-    const unsigned char* xr = p.x + row * p.ld * Ty::ES;
-    uint32_t w[kScoreChunks][4];
-    if (p.vec && e0 + PE <= p.V) {
+  const uint32_t id = blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
+  const uint32_t row = p.np > 1 ? __umulhi(id, p.np_mul) >> p.np_shift : id;
+  if (row >= (uint32_t)p.B) return;
+  const int32_t e0 = (int32_t)(id - row * (uint32_t)p.np) * PE;
+  const int32_t t = p.token[row];
+  if (t == VSAMP_TOKEN_IGNORE) return;
+  const int32_t V = (int32_t)p.V;
+  const unsigned char* xr = p.x + (int64_t)row * p.ld * Ty::ES;
+  uint32_t w[kScoreChunks][4];
+  if (p.vec && PE <= V - e0) {
 #pragma unroll
-      for (int i = 0; i < kScoreChunks; ++i) {
-        const uint4 v = ldg_stream(xr + e0 * Ty::ES + i * 512 + lane * 16);
-        w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kScoreChunks; ++i) score_load<T>(xr, e0 + i * CE + lane * Ty::VE, p.V, p.vec, w[i]);
+    for (int i = 0; i < kScoreChunks; ++i) {
+      const uint4 v = ldg_stream(xr + (int64_t)e0 * Ty::ES + i * 512 + lane * 16);
+      w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
     }
-    const float temp = p.temperature ? p.temperature[row] : 1.f;
-    const float c = kLog2e / (temp > 0.f ? temp : 1.f);
-    const bool known = t >= 0 && t < p.V;
-    const float xt = known ? Ty::load(xr, t) : INFINITY;
-
-    // maximum of the lane's vectors, of the chunks and of the piece
-    float m = -INFINITY;
-    if (ALT) {
-      float mine = 0.f;    // lane i < 8: maximum of chunk i
+  } else {
 #pragma unroll
-      for (int i = 0; i < kScoreChunks; ++i) {
-        const float cm = warp_max_nan(
-            max_of_word<T>(max_word<T>(max_word<T>(w[i][0], w[i][1]), max_word<T>(w[i][2], w[i][3]))));
-        if (lane == i) mine = cm;
-        m = max_nan(m, cm);
-      }
-      if (lane < kScoreChunks) p.chunk_max[id * kScoreChunks + lane] = mine;
-    } else {
-      uint32_t a = max_word<T>(w[0][0], w[0][1]), b = max_word<T>(w[0][2], w[0][3]);
-#pragma unroll
-      for (int i = 1; i < kScoreChunks; ++i) {
-        a = max_word<T>(a, max_word<T>(w[i][0], w[i][1]));
-        b = max_word<T>(b, max_word<T>(w[i][2], w[i][3]));
-      }
-      m = warp_max_nan(max_of_word<T>(max_word<T>(a, b)));
-    }
-
-    // tokens before the given one: ties count in the pieces before its own, up to its place in its own
-    uint32_t before = 0;
-    if (known && m >= xt) {   // a piece below the given token has none (false for NaN too)
-      if (t >= e0 + PE) {
-        before = count_larger<T>(w, xt, true);
-      } else if (t < e0) {
-        before = count_larger<T>(w, xt, false);
-      } else {
-        const int at = (int)(t - e0);
-#pragma unroll
-        for (int i = 0; i < kScoreChunks; ++i)
-#pragma unroll
-          for (int j = 0; j < Ty::VE; ++j) {
-            const float x = Ty::at(w[i], j);
-            before += x > xt || (x == xt && i * CE + lane * Ty::VE + j < at) ? 1u : 0u;
-          }
-      }
-    }
-    before = warp_sum_u32(before);
-
-    float S = 0.f, A = 0.f;
-    if (m > -INFINITY && m < INFINITY) {   // false for NaN too
-      // A masked token must add 0 to both sums, and e^s s is NaN at s = -inf: elements are raised to a value so far
-      // below the maximum that its exponential, at 2^-150 or less, is flushed to 0. For bf16 two elements at once, unless
-      // the temperature is so large that no finite bf16 is that low.
-      const float lowest = m - 150.f / c;
-      if (sizeof(T) == 2 && lowest > -3.3e38f) score_sums<T, true>(w, m, c, lowest, S, A);
-      else score_sums<T, false>(w, m, c, lowest, S, A);
-    }
-    S = warp_sum_f(S);
-    A = warp_sum_f(A);
-    if (lane == 0) p.rec[id] = make_float4(m, S, A, __uint_as_float(before));
+    for (int i = 0; i < kScoreChunks; ++i) score_load<T>(xr, (int64_t)e0 + i * CE + lane * Ty::VE, p.V, p.vec, w[i]);
   }
+  const float temp = p.temperature ? p.temperature[row] : 1.f;
+  const float T1 = temp > 0.f ? temp : 1.f, c = p.temperature ? kLog2e / T1 : kLog2e;
+  const bool known = t >= 0 && t < V;
+  const float xt = known ? Ty::load(xr, t) : INFINITY;
+
+  // maximum of the lane's vectors, of the chunks and of the piece
+  float m = -INFINITY;
+  if (ALT) {
+    float mine = 0.f;    // lane i < 8: maximum of chunk i
+#pragma unroll
+    for (int i = 0; i < kScoreChunks; ++i) {
+      const float cm = warp_max_nan(
+          max_of_word<T>(max_word<T>(max_word<T>(w[i][0], w[i][1]), max_word<T>(w[i][2], w[i][3]))));
+      if (lane == i) mine = cm;
+      m = max_nan(m, cm);
+    }
+    if (lane < kScoreChunks) p.chunk_max[(int64_t)id * kScoreChunks + lane] = mine;
+  } else {
+    uint32_t a = max_word<T>(w[0][0], w[0][1]), b = max_word<T>(w[0][2], w[0][3]);
+#pragma unroll
+    for (int i = 1; i < kScoreChunks; ++i) {
+      a = max_word<T>(a, max_word<T>(w[i][0], w[i][1]));
+      b = max_word<T>(b, max_word<T>(w[i][2], w[i][3]));
+    }
+    m = warp_max_nan(max_of_word<T>(max_word<T>(a, b)));
+  }
+
+  // tokens before the given one: ties count in the pieces before its own, up to its place in its own
+  uint32_t before = 0;
+  if (known && m >= xt) {   // a piece below the given token has none (false for NaN too)
+    if (t - e0 >= PE) {
+      before = count_larger<T>(w, xt, true);
+    } else if (t < e0) {
+      before = count_larger<T>(w, xt, false);
+    } else {
+      const int at = t - e0;
+#pragma unroll
+      for (int i = 0; i < kScoreChunks; ++i)
+#pragma unroll
+        for (int j = 0; j < Ty::VE; ++j) {
+          const float x = Ty::at(w[i], j);
+          before += x > xt || (x == xt && i * CE + lane * Ty::VE + j < at) ? 1u : 0u;
+        }
+    }
+  }
+  before = warp_sum_u32(before);
+
+  float S = 0.f, A = 0.f;
+  if (m > -INFINITY && m < INFINITY) {   // false for NaN too
+    const float lowest = fmaf(-104.f, T1, m);   // 104 log2(e) > 150
+    if (lowest > -3.3e38f) score_sums<T, true>(w, m, c, lowest, S, A);
+    else score_sums<T, false>(w, m, c, lowest, S, A);
+  }
+  S = warp_sum_f(S);
+  A = warp_sum_f(A);
+  if (lane == 0) p.rec[id] = make_float4(m, S, A, __uint_as_float(before));
 }
 
 struct ScoreRow {
@@ -373,13 +337,13 @@ __device__ __forceinline__ ScoreRow score_fold(const ScoreParams& p, int64_t row
   r.invT = 1.f / (temp > 0.f ? temp : 1.f);
   const float c = kLog2e / (temp > 0.f ? temp : 1.f);
   float m = -INFINITY;
-  for (int64_t i = lane; i < p.np; i += 32) m = max_nan(m, rec[i].x);
+  for (int i = lane; i < p.np; i += 32) m = max_nan(m, rec[i].x);
   m = warp_max_nan(m);
   float S = 0.f, A = 0.f;
   uint32_t before = 0;
   const bool finite = m > -INFINITY && m < INFINITY;
   if (finite) {
-    for (int64_t i = lane; i < p.np; i += 32) {
+    for (int i = lane; i < p.np; i += 32) {
       const float4 q = rec[i];
       before += __float_as_uint(q.w);
       if (q.x > -INFINITY) {
@@ -526,7 +490,7 @@ __global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(c
     if (skip) {
       if (tid == 0) score_write<T>(p, row, t, ScoreRow{});
     } else {
-      const int64_t nch = p.np * kScoreChunks;
+      const int64_t nch = (int64_t)p.np * kScoreChunks;
       const float* cm = p.chunk_max + row * nch;
       const unsigned char* xr = p.x + row * p.ld * Ty::ES;
       auto each_chunk = [&](auto f) {
@@ -664,21 +628,19 @@ struct GradRow {
 template <typename T>
 __device__ __forceinline__ void grad_vector(const GradRow& r, uint32_t (&w)[4]) {
   using Ty = ScoreType<T>;
-  const uint64_t m2 = pack2(-r.m, -r.m), c2 = pack2(r.c, r.c), k02 = pack2(r.k0, r.k0), k12 = pack2(r.k1, r.k1);
+  const float2 m2 = make_float2(-r.m, -r.m), c2 = make_float2(r.c, r.c);
+  const float2 k02 = make_float2(r.k0, r.k0), k12 = make_float2(r.k1, r.k1);
   uint32_t out[4];
 #pragma unroll
   for (int j = 0; j < Ty::VE; j += 2) {
-    float a, b;
-    unpack2(mul2(add2(pack2(Ty::at(w, j), Ty::at(w, j + 1)), m2), c2), a, b);
-    a = fmaxf(a, -150.f);
-    b = fmaxf(b, -150.f);
-    const uint64_t d = mul2(pack2(ex2_approx(a), ex2_approx(b)), fma2(k12, pack2(a, b), k02));
-    unpack2(d, a, b);
+    float2 s = __fmul2_rn(__fadd2_rn(make_float2(Ty::at(w, j), Ty::at(w, j + 1)), m2), c2);
+    s = make_float2(fmaxf(s.x, -150.f), fmaxf(s.y, -150.f));
+    const float2 d = __fmul2_rn(make_float2(ex2_approx(s.x), ex2_approx(s.y)), __ffma2_rn(k12, s, k02));
     if constexpr (Ty::ES == 4) {
-      out[j] = __float_as_uint(a);
-      out[j + 1] = __float_as_uint(b);
+      out[j] = __float_as_uint(d.x);
+      out[j + 1] = __float_as_uint(d.y);
     } else {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+      const __nv_bfloat162 v = __floats2bfloat162_rn(d.x, d.y);
       memcpy(&out[j / 2], &v, 4);
     }
   }
