@@ -25,6 +25,7 @@ constexpr int kScorePiece = 4096;      // bytes of a row per warp
 constexpr int kScoreChunks = 8;        // 512-byte chunks per piece: one 16-byte vector per lane each
 constexpr int kScoreWarps = 8;
 constexpr int kScoreFinishThreads = 256;
+constexpr int kKeep = 4;               // chunk maxima that a thread of the finish keeps in registers
 constexpr int kScoreChunkList = 2 * VSAMP_SCORE_ALT_MAX + 64;   // chunks read again per row
 constexpr int kScoreList = 512;        // alternatives' candidates kept on chip; more of them take the radix path
 
@@ -327,65 +328,83 @@ struct ScoreRow {
   float invT;
 };
 
-// A warp folds the piece records of a row (every lane returns the same values).
-template <typename T>
-__device__ __forceinline__ ScoreRow score_fold(const ScoreParams& p, int64_t row, int32_t t) {
-  const int lane = threadIdx.x & 31;
-  const float4* rec = p.rec + row * p.np;
-  const float temp = p.temperature ? p.temperature[row] : 1.f;
-  ScoreRow r;
-  r.invT = 1.f / (temp > 0.f ? temp : 1.f);
-  const float c = kLog2e / (temp > 0.f ? temp : 1.f);
-  float m = -INFINITY;
-  for (int i = lane; i < p.np; i += 32) m = max_nan(m, rec[i].x);
-  m = warp_max_nan(m);
-  float S = 0.f, A = 0.f;
-  uint32_t before = 0;
-  const bool finite = m > -INFINITY && m < INFINITY;
-  if (finite) {
-    for (int i = lane; i < p.np; i += 32) {
-      const float4 q = rec[i];
-      before += __float_as_uint(q.w);
-      if (q.x > -INFINITY) {
-        const float d = fmaxf((q.x - m) * c, -150.f);
-        const float f = ex2_approx(d);
-        S = fmaf(f, q.y, S);
-        A = fmaf(f, fmaf(d, q.y, q.z), A);
-      }
+// A warp folds the piece records of a row (every lane returns the same values). The first kFoldKeep records per lane are
+// read at once and kept; `load` may run before the row's token is known.
+constexpr int kFoldKeep = 4;
+struct ScoreFold {
+  float4 rec[kFoldKeep];
+  __device__ __forceinline__ void load(const ScoreParams& p, int64_t row) {
+    const float4* r = p.rec + row * p.np;
+#pragma unroll
+    for (int i = 0; i < kFoldKeep; ++i) {
+      const int k = i * 32 + (int)(threadIdx.x & 31);
+      rec[i] = k < p.np ? r[k] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
     }
   }
-  S = warp_sum_f(S);
-  A = warp_sum_f(A);
-  r.before = warp_sum_u32(before);
-  r.m = m;
-  // S >= 1: log1p keeps the digits of a sum close to 1
-  r.logsum = log1pf(S - 1.f);
-  r.entropy = fmaxf(r.logsum - 0.69314718056f * (A / S), 0.f);
-  r.status = VSAMP_OK;
-  if (!finite) r.status = VSAMP_ERR_NONFINITE;
-  else if (isnan(temp) || isinf(temp) || t < 0 || (int64_t)t >= p.V) r.status = VSAMP_ERR_INVALID_ARG;
-  return r;
+  template <typename F>
+  __device__ __forceinline__ void each(const ScoreParams& p, int64_t row, F f) const {
+#pragma unroll
+    for (int i = 0; i < kFoldKeep; ++i) f(rec[i]);
+    for (int k = kFoldKeep * 32 + (int)(threadIdx.x & 31); k < p.np; k += 32) f(p.rec[row * p.np + k]);
+  }
+  __device__ __forceinline__ ScoreRow row(const ScoreParams& p, int64_t at, int32_t t) const {
+    const float temp = p.temperature ? p.temperature[at] : 1.f;
+    ScoreRow r;
+    const float T1 = temp > 0.f ? temp : 1.f, c = p.temperature ? kLog2e / T1 : kLog2e;   // as for the pieces
+    r.invT = 1.f / T1;
+    float m = -INFINITY;
+    each(p, at, [&](float4 q) { m = max_nan(m, q.x); });
+    m = warp_max_nan(m);
+    float S = 0.f, A = 0.f;
+    uint32_t before = 0;
+    const bool finite = m > -INFINITY && m < INFINITY;
+    if (finite) {
+      each(p, at, [&](float4 q) {
+        before += __float_as_uint(q.w);
+        if (q.x > -INFINITY) {
+          const float d = fmaxf((q.x - m) * c, -150.f);
+          const float f = ex2_approx(d);
+          S = fmaf(f, q.y, S);
+          A = fmaf(f, fmaf(d, q.y, q.z), A);
+        }
+      });
+    }
+    S = warp_sum_f(S);
+    A = warp_sum_f(A);
+    r.before = warp_sum_u32(before);
+    r.m = m;
+    // S >= 1: log1p keeps the digits of a sum close to 1
+    r.logsum = log1pf(S - 1.f);
+    r.entropy = fmaxf(r.logsum - 0.69314718056f * (A / S), 0.f);
+    r.status = VSAMP_OK;
+    if (!finite) r.status = VSAMP_ERR_NONFINITE;
+    else if (isnan(temp) || isinf(temp) || t < 0 || (int64_t)t >= p.V) r.status = VSAMP_ERR_INVALID_ARG;
+    return r;
+  }
+};
+
+// The given token's logit, NaN if it is none.
+template <typename T>
+__device__ __forceinline__ float score_logit(const ScoreParams& p, int64_t row, int32_t t) {
+  return t >= 0 && (int64_t)t < p.V ? ScoreType<T>::load(p.x + row * p.ld * ScoreType<T>::ES, t) : __int_as_float(0x7FC00000);
 }
 
-template <typename T>
-__device__ __forceinline__ void score_write(const ScoreParams& p, int64_t row, int32_t t, const ScoreRow& r) {
-  const float qnan = __int_as_float(0x7FC00000);
+__device__ __forceinline__ void score_write(const ScoreParams& p, int64_t row, int32_t t, float xt, const ScoreRow& r) {
   const bool skip = t == VSAMP_TOKEN_IGNORE;
-  const bool ok = r.status == VSAMP_OK;
-  const float none = skip ? 0.f : qnan;
+  const bool ok = r.status == VSAMP_OK && !skip;
+  const float none = skip ? 0.f : __int_as_float(0x7FC00000);
   if (p.logprob) {
     float lp = none;
-    if (ok && !skip) {
-      const float xt = ScoreType<T>::load(p.x + row * p.ld * ScoreType<T>::ES, t);
+    if (ok) {
       const float temp = p.temperature ? p.temperature[row] : 1.f;
       lp = fminf((xt - r.m) / (temp > 0.f ? temp : 1.f) - r.logsum, 0.f);
     }
     p.logprob[row] = lp;
   }
-  if (p.entropy) p.entropy[row] = ok && !skip ? r.entropy : none;
-  if (p.rank) p.rank[row] = ok && !skip ? (int32_t)r.before : -1;
-  if (p.row_max) p.row_max[row] = ok && !skip ? r.m : none;
-  if (p.row_logsum) p.row_logsum[row] = ok && !skip ? r.logsum : none;
+  if (p.entropy) p.entropy[row] = ok ? r.entropy : none;
+  if (p.rank) p.rank[row] = ok ? (int32_t)r.before : -1;
+  if (p.row_max) p.row_max[row] = ok ? r.m : none;
+  if (p.row_logsum) p.row_logsum[row] = ok ? r.logsum : none;
   if (p.row_status) p.row_status[row] = r.status;
 }
 
@@ -394,10 +413,13 @@ template <typename T>
 __global__ void __launch_bounds__(128) score_finish_kernel(const ScoreParams p) {
   cudaGridDependencySynchronize();   // every piece record is written
   for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); row < p.B; row += (int64_t)gridDim.x * 4) {
+    ScoreFold fold;
+    fold.load(p, row);
     const int32_t t = p.token[row];
+    const float xt = score_logit<T>(p, row, t);
     ScoreRow r{};
-    if (t != VSAMP_TOKEN_IGNORE) r = score_fold<T>(p, row, t);
-    if ((threadIdx.x & 31) == 0) score_write<T>(p, row, t, r);
+    if (t != VSAMP_TOKEN_IGNORE) r = fold.row(p, row, t);
+    if ((threadIdx.x & 31) == 0) score_write(p, row, t, xt, r);
   }
 }
 
@@ -482,23 +504,32 @@ __global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(c
   const int groups = NT / gs;
   cudaGridDependencySynchronize();   // every piece record is written
   for (int64_t row = blockIdx.x; row < p.B; row += gridDim.x) {
+    // what the row needs first is read at once: the first chunk maxima of every thread, the last warp's records
+    const int64_t nch = (int64_t)p.np * kScoreChunks;
+    const float* cm = p.chunk_max + row * nch;
+    float kept[kKeep];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) kept[i] = i * NT + tid < nch ? cm[i * NT + tid] : -INFINITY;
+    ScoreFold fold;
+    if (warp == NW - 1) fold.load(p, row);
     const int32_t t = p.token[row];
     const bool skip = t == VSAMP_TOKEN_IGNORE;
     int32_t* oi = p.alt_idx + row * p.N;
     float* ol = p.alt_lp + row * p.N;
     uint32_t found = 0;
     if (skip) {
-      if (tid == 0) score_write<T>(p, row, t, ScoreRow{});
+      if (tid == 0) score_write(p, row, t, 0.f, ScoreRow{});
     } else {
-      const int64_t nch = (int64_t)p.np * kScoreChunks;
-      const float* cm = p.chunk_max + row * nch;
       const unsigned char* xr = p.x + row * p.ld * Ty::ES;
       auto each_chunk = [&](auto f) {
-#pragma unroll 4
-        for (int64_t i = tid; i < nch; i += NT) {
-          const uint32_t k = key_f32_bits(__float_as_uint(cm[i]));
+        auto one = [&](float x, int64_t i) {
+          const uint32_t k = key_f32_bits(__float_as_uint(x));
           if (k > kNone) f(((uint64_t)k << 32) | (uint32_t)~(uint32_t)i);
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) one(kept[i], i * NT + tid);
+#pragma unroll 4
+        for (int64_t i = kKeep * NT + tid; i < nch; i += NT) one(cm[i], i);
       };
       uint64_t mine = 0;
       each_chunk([&](uint64_t k) { mine = k > mine ? k : mine; });
@@ -513,9 +544,10 @@ __global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(c
       }
       __syncthreads();
       if (warp == NW - 1) {
-        const ScoreRow r = score_fold<T>(p, row, t);
+        const float xt = score_logit<T>(p, row, t);
+        const ScoreRow r = fold.row(p, row, t);
         if (lane == 0) {
-          score_write<T>(p, row, t, r);
+          score_write(p, row, t, xt, r);
           shared_row = r;
         }
       }
@@ -550,17 +582,17 @@ __global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(c
         const uint32_t nc = n_chunks;
         const uint32_t lowest = max((uint32_t)(cut >> 32), kNone + 1);
         auto each_token = [&](auto f) {
-          for (uint32_t i = warp; i < nc; i += 2 * NW) {   // two chunks in flight
-            uint32_t w[2][4];
-            int64_t e[2];
+          for (uint32_t i = warp; i < nc; i += 4 * NW) {   // four chunks in flight
+            uint32_t w[4][4];
+            int64_t e[4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < 4; ++u) {
               const uint32_t at = i + u * NW;
               e[u] = at < nc ? (int64_t)chunks[at] * CE + lane * Ty::VE : p.V;
               score_load<T>(xr, e[u], p.V, p.vec, w[u]);
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
               for (int j = 0; j < Ty::VE; ++j) {
                 const uint32_t k = key_f32_bits(__float_as_uint(Ty::at(w[u], j)));
