@@ -599,60 +599,78 @@ def _elsewhere(t: torch.Tensor, stream):
     """The context a call on tensor t and `stream` has to run in, or None when the current device and stream are it.
 
     Everything a call allocates or converts then belongs to the stream its kernels run on."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
+    if stream is None and index == torch.cuda.current_device():
+        return None
     dev = t.device
-    if dev.type != "cuda":
-        raise ValueError("tensors must be on a CUDA device")
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+    if stream is None:
+        return torch.cuda.device(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
 
 
-def _current(dev) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+def _current(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _token_ids(v, B: int, dev):
+def _at(t, dtype, index: int, n: int, name: str):
+    """The address of a contiguous tensor of at least n elements of dtype on the device, None for None. The small calls
+    of a decode step are bound by their argument checks, so the usual case is one line."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} needs at least {n} elements")
+
+
+def _token_ids(v, n: int, dev):
     """Token ids as a contiguous int32 device tensor; wider ids outside its range stay outside every vocabulary."""
     if isinstance(v, torch.Tensor):
-        if v.dtype == torch.int32 and v.device == dev and v.is_contiguous():
-            return v
-        if v.is_floating_point():
+        if v.dtype is torch.int32:
+            return v if v.device == dev and v.is_contiguous() else v.to(device=dev).contiguous()
+        if v.is_floating_point() or v.is_complex():
             raise TypeError(f"token must hold whole numbers, got {v.dtype}")
-        if v.dtype == torch.int64:
+        if v.dtype is torch.int64:
             v = v.clamp(-(1 << 31), (1 << 31) - 1)
         return v.to(device=dev, dtype=torch.int32).contiguous()
-    return torch.full((B,), int(v), dtype=torch.int32, device=dev)
+    return torch.full((n,), int(v), dtype=torch.int32, device=dev)
 
 
-def _row_values(v, B: int, dev, name):
-    """A per-row fp32 parameter: None, a scalar (broadcast) or a [B] tensor."""
-    if v is None or (isinstance(v, torch.Tensor) and v.dtype == torch.float32 and v.device == dev and v.is_contiguous()):
+def _row_values(v, n: int, dev, name):
+    """A per-row fp32 parameter: None, a scalar (broadcast) or a [n] tensor."""
+    if v is None or (isinstance(v, torch.Tensor) and v.dtype is torch.float32 and v.is_contiguous() and v.device == dev):
         return v
-    return _param(v, B, torch.float32, dev, name)
+    return _param(v, n, torch.float32, dev, name)
 
 
-def _matrix(t: torch.Tensor, name: str, dev, rows=None, cols=None):
-    """Checks a row-major matrix (rows may be padded); returns its row stride in elements."""
-    if t.dim() != 2 or t.device != dev or t.stride(1) != 1 and t.shape[1] > 1:
-        raise ValueError(f"{name} must be a 2-D tensor on {dev} with contiguous rows")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _matrix(t: torch.Tensor, name: str, index: int, rows=None, cols=None):
+    """Checks a row-major matrix (rows may be padded); returns its rows, columns and row stride in elements."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.get_device() != index or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be a 2-D tensor on cuda:{index} with contiguous rows")
+    if (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(shape)}")
+    return shape[0], shape[1], stride[0] if shape[0] > 1 else max(stride[0], shape[1])
 
 
-def _logits_matrix(x: torch.Tensor, V):
-    B, V, ld = _rows(x, V)
-    if not 0 < V <= x.shape[1]:
-        raise ValueError(f"V = {V} is outside the rows of {x.shape[1]} logits")
-    return B, V, ld
-
-
-def _f32_out(t, n: int, dev):
-    return torch.empty(n, dtype=torch.float32, device=dev) if t is None else t
+def _logits_matrix(x: torch.Tensor, V, index: int):
+    B, cols, ld = _matrix(x, "logits", index)
+    if V is None:
+        return B, cols, ld
+    if not 0 < V <= cols:
+        raise ValueError(f"V = {V} is outside the rows of {cols} logits")
+    return B, int(V), ld
 
 
 def vsamp_score_tokens(logits, token, temperature=None, n_alt=0, V=None, logprob=None, entropy=None, rank=None,
@@ -667,35 +685,36 @@ def vsamp_score_tokens(logits, token, temperature=None, n_alt=0, V=None, logprob
         with where:
             return vsamp_score_tokens(logits, token, temperature, n_alt, V, logprob, entropy, rank, alt_idx, alt_lp,
                                       row_max, row_logsum, row_status, workspace)
-    B, V, ld = _logits_matrix(logits, V)
-    dev, dt, n_alt = logits.device, _dtype_code(logits), int(n_alt)
+    dev, at = logits.device, logits.get_device()
+    B, V, ld = _logits_matrix(logits, V, at)
+    dt, n_alt = _dtype_code(logits), int(n_alt)
     if not 0 <= n_alt <= VSAMP_SCORE_ALT_MAX:
         raise ValueError(f"n_alt must be in [0, {VSAMP_SCORE_ALT_MAX}]")
+    f32, i32, u8, empty = torch.float32, torch.int32, torch.uint8, torch.empty
     token = _token_ids(token, B, dev)
     temperature = _row_values(temperature, B, dev, "temperature")
-    logprob, entropy = _f32_out(logprob, B, dev), _f32_out(entropy, B, dev)
-    row_max, row_logsum = _f32_out(row_max, B, dev), _f32_out(row_logsum, B, dev)
-    rank = torch.empty(B, dtype=torch.int32, device=dev) if rank is None else rank
-    row_status = torch.empty(B, dtype=torch.int32, device=dev) if row_status is None else row_status
+    logprob = empty(B, dtype=f32, device=dev) if logprob is None else logprob
+    entropy = empty(B, dtype=f32, device=dev) if entropy is None else entropy
+    row_max = empty(B, dtype=f32, device=dev) if row_max is None else row_max
+    row_logsum = empty(B, dtype=f32, device=dev) if row_logsum is None else row_logsum
+    rank = empty(B, dtype=i32, device=dev) if rank is None else rank
+    row_status = empty(B, dtype=i32, device=dev) if row_status is None else row_status
     if n_alt:
-        alt_idx = torch.empty((B, n_alt), dtype=torch.int32, device=dev) if alt_idx is None else alt_idx
-        alt_lp = torch.empty((B, n_alt), dtype=torch.float32, device=dev) if alt_lp is None else alt_lp
+        alt_idx = empty((B, n_alt), dtype=i32, device=dev) if alt_idx is None else alt_idx
+        alt_lp = empty((B, n_alt), dtype=f32, device=dev) if alt_lp is None else alt_lp
     else:
         alt_idx = alt_lp = None
     lib = load()
     if workspace is None:
-        need = lib.vsamp_score_workspace_size(dt, B, V, n_alt)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    f32, i32 = torch.float32, torch.int32
+        workspace = empty(lib.vsamp_score_workspace_size(dt, B, V, n_alt), dtype=u8, device=dev)
     st = lib.vsamp_score_tokens(
-        logits.data_ptr(), dt, B, V, ld, _ptr(temperature, f32, dev, B, "temperature"),
-        _ptr(token, i32, dev, B, "token"), n_alt, _ptr(logprob, f32, dev, B, "logprob"),
-        _ptr(entropy, f32, dev, B, "entropy"), _ptr(rank, i32, dev, B, "rank"),
-        _ptr(alt_idx, i32, dev, B * n_alt, "alt_idx"), _ptr(alt_lp, f32, dev, B * n_alt, "alt_lp"),
-        _ptr(row_max, f32, dev, B, "row_max"), _ptr(row_logsum, f32, dev, B, "row_logsum"),
-        _ptr(row_status, i32, dev, B, "row_status"), _ptr(workspace, torch.uint8, dev, 0, "workspace"),
-        workspace.numel(), _current(dev))
-    _check(st, "vsamp_score_tokens")
+        logits.data_ptr(), dt, B, V, ld, _at(temperature, f32, at, B, "temperature"), _at(token, i32, at, B, "token"),
+        n_alt, _at(logprob, f32, at, B, "logprob"), _at(entropy, f32, at, B, "entropy"), _at(rank, i32, at, B, "rank"),
+        _at(alt_idx, i32, at, B * n_alt, "alt_idx"), _at(alt_lp, f32, at, B * n_alt, "alt_lp"),
+        _at(row_max, f32, at, B, "row_max"), _at(row_logsum, f32, at, B, "row_logsum"),
+        _at(row_status, i32, at, B, "row_status"), _at(workspace, u8, at, 0, "workspace"), workspace.numel(), _current(at))
+    if st:
+        _check(st, "vsamp_score_tokens")
     return logprob, entropy, rank, alt_idx, alt_lp, row_max, row_logsum, row_status
 
 
@@ -709,25 +728,26 @@ def vsamp_score_tokens_backward(logits, token, dlogprob, row_max, row_logsum, en
         with where:
             return vsamp_score_tokens_backward(logits, token, dlogprob, row_max, row_logsum, entropy, dentropy,
                                                temperature, V, dlogits, row_status)
-    B, V, ld = _logits_matrix(logits, V)
-    dev = logits.device
+    dev, at = logits.device, logits.get_device()
+    B, V, ld = _logits_matrix(logits, V, at)
+    f32, i32 = torch.float32, torch.int32
     token = _token_ids(token, B, dev)
     temperature = _row_values(temperature, B, dev, "temperature")
     dlogprob, dentropy = _row_values(dlogprob, B, dev, "dlogprob"), _row_values(dentropy, B, dev, "dentropy")
     if dlogits is None:
         dlogits = torch.empty((B, V), dtype=logits.dtype, device=dev)
-    elif dlogits.dtype != logits.dtype or dlogits.dim() != 2 or dlogits.shape[1] < V:
+    _, cols, ldd = _matrix(dlogits, "dlogits", at, B)
+    if dlogits.dtype is not logits.dtype or cols < V:
         raise ValueError(f"dlogits must be [{B}, >= {V}] of {logits.dtype}")
-    ldd = _matrix(dlogits, "dlogits", dev, B)
-    row_status = torch.empty(B, dtype=torch.int32, device=dev) if row_status is None else row_status
-    f32, i32 = torch.float32, torch.int32
+    row_status = torch.empty(B, dtype=i32, device=dev) if row_status is None else row_status
     st = load().vsamp_score_tokens_backward(
-        logits.data_ptr(), _dtype_code(logits), B, V, ld, _ptr(temperature, f32, dev, B, "temperature"),
-        _ptr(token, i32, dev, B, "token"), _ptr(dlogprob, f32, dev, B, "dlogprob"),
-        _ptr(dentropy, f32, dev, B, "dentropy"), _ptr(row_max, f32, dev, B, "row_max"),
-        _ptr(row_logsum, f32, dev, B, "row_logsum"), _ptr(entropy, f32, dev, B, "entropy"), dlogits.data_ptr(), ldd,
-        _ptr(row_status, i32, dev, B, "row_status"), _current(dev))
-    _check(st, "vsamp_score_tokens_backward")
+        logits.data_ptr(), _dtype_code(logits), B, V, ld, _at(temperature, f32, at, B, "temperature"),
+        _at(token, i32, at, B, "token"), _at(dlogprob, f32, at, B, "dlogprob"), _at(dentropy, f32, at, B, "dentropy"),
+        _at(row_max, f32, at, B, "row_max"), _at(row_logsum, f32, at, B, "row_logsum"),
+        _at(entropy, f32, at, B, "entropy"), dlogits.data_ptr(), ldd, _at(row_status, i32, at, B, "row_status"),
+        _current(at))
+    if st:
+        _check(st, "vsamp_score_tokens_backward")
     return dlogits, row_status
 
 
@@ -748,7 +768,7 @@ def vsamp_head_pack(codes, scales, zeros=None, group=64, stream=None) -> HeadWei
     if where is not None:
         with where:
             return vsamp_head_pack(codes, scales, zeros, group)
-    dev, group = codes.device, int(group)
+    dev, at, group = codes.device, codes.get_device(), int(group)
     if codes.dim() != 2 or codes.dtype != torch.uint8:
         raise ValueError("codes must be a 2-D uint8 tensor [V, D / 2]")
     V, D = int(codes.shape[0]), 2 * int(codes.shape[1])
@@ -758,13 +778,11 @@ def vsamp_head_pack(codes, scales, zeros=None, group=64, stream=None) -> HeadWei
         if t is not None and tuple(t.shape) != (V, D // group):
             raise ValueError(f"{name} must be [{V}, {D // group}], got {tuple(t.shape)}")
     lib = load()
-    dt = _dtype_code(scales)
+    dt, n = _dtype_code(scales), V * D // group
     need = lib.vsamp_head_packed_size(dt, zeros is not None, V, D, group)
     data = torch.empty(need, dtype=torch.uint8, device=dev)
-    st = lib.vsamp_head_pack(_ptr(codes, torch.uint8, dev, V * D // 2, "codes"),
-                             _ptr(scales, None, dev, V * D // group, "scales"), dt,
-                             _ptr(zeros, torch.uint8, dev, V * D // group, "zeros"), V, D, group, data.data_ptr(), need,
-                             _current(dev))
+    st = lib.vsamp_head_pack(_at(codes, torch.uint8, at, V * D // 2, "codes"), _at(scales, scales.dtype, at, n, "scales"),
+                             dt, _at(zeros, torch.uint8, at, n, "zeros"), V, D, group, data.data_ptr(), need, _current(at))
     _check(st, "vsamp_head_pack")
     return HeadWeights(data, V, D, group, dt, zeros is not None)
 
@@ -776,19 +794,17 @@ def vsamp_head_logits(hidden, head: HeadWeights, out=None, out_dtype=torch.float
     if where is not None:
         with where:
             return vsamp_head_logits(hidden, head, out, out_dtype)
-    dev = hidden.device
-    ldh = _matrix(hidden, "hidden", dev, None, head.D)
-    M = hidden.shape[0]
+    at, V, D = hidden.get_device(), head.V, head.D
+    M, _, ldh = _matrix(hidden, "hidden", at, None, D)
     if out is None:
-        out = torch.empty((M, head.V), dtype=out_dtype, device=dev)
-    ld = _matrix(out, "out", dev, M, head.V)
+        out = torch.empty((M, V), dtype=out_dtype, device=hidden.device)
+    ld = _matrix(out, "out", at, M, V)[2]
     data = head.data
-    if data.device != dev:
-        raise ValueError(f"head weights are on {data.device}, hidden states on {dev}")
-    st = load().vsamp_head_logits(hidden.data_ptr(), _dtype_code(hidden), M, ldh, data.data_ptr(), data.numel(),
-                                  head.scale_dt, head.has_zeros, head.V, head.D, head.group, out.data_ptr(),
-                                  _dtype_code(out), ld, _current(dev))
-    _check(st, "vsamp_head_logits")
+    st = load().vsamp_head_logits(hidden.data_ptr(), _dtype_code(hidden), M, ldh, _at(data, torch.uint8, at, 0, "head"),
+                                  data.numel(), head.scale_dt, head.has_zeros, V, D, head.group, out.data_ptr(),
+                                  _dtype_code(out), ld, _current(at))
+    if st:
+        _check(st, "vsamp_head_logits")
     return out
 
 
@@ -799,19 +815,19 @@ def vsamp_embed(token, table, scale=1.0, out=None, out_dtype=None, row_status=No
     if where is not None:
         with where:
             return vsamp_embed(token, table, scale, out, out_dtype, row_status)
-    dev = table.device
-    ldt = _matrix(table, "table", dev)
-    V, D = table.shape
+    dev, at = table.device, table.get_device()
+    V, D, ldt = _matrix(table, "table", at)
     N = token.numel() if isinstance(token, torch.Tensor) else 1
     token = _token_ids(token, N, dev)
     if out is None:
         out = torch.empty((N, D), dtype=out_dtype or table.dtype, device=dev)
-    ldo = _matrix(out, "out", dev, N, D)
+    ldo = _matrix(out, "out", at, N, D)[2]
     row_status = torch.empty(N, dtype=torch.int32, device=dev) if row_status is None else row_status
-    st = load().vsamp_embed(_ptr(token, torch.int32, dev, N, "token"), N, table.data_ptr(), _dtype_code(table), V, D, ldt,
-                            float(scale), out.data_ptr(), _dtype_code(out), ldo,
-                            _ptr(row_status, torch.int32, dev, N, "row_status"), _current(dev))
-    _check(st, "vsamp_embed")
+    st = load().vsamp_embed(_at(token, torch.int32, at, N, "token"), N, table.data_ptr(), _dtype_code(table), V, D, ldt,
+                            scale, out.data_ptr(), _dtype_code(out), ldo,
+                            _at(row_status, torch.int32, at, N, "row_status"), _current(at))
+    if st:
+        _check(st, "vsamp_embed")
     return out, row_status
 
 
@@ -824,20 +840,20 @@ def vsamp_embed_backward(token, dout, V, scale=1.0, dtable=None, dtype=None, acc
     if where is not None:
         with where:
             return vsamp_embed_backward(token, dout, V, scale, dtable, dtype, accumulate, workspace)
-    dev, V = dout.device, int(V)
-    ldd = _matrix(dout, "dout", dev)
-    N, D = dout.shape
+    dev, at, V = dout.device, dout.get_device(), int(V)
+    N, D, ldd = _matrix(dout, "dout", at)
     token = _token_ids(token, N, dev)
     if dtable is None:
         if accumulate:
             raise ValueError("accumulate needs the table gradient to add to")
         dtable = torch.empty((V, D), dtype=dtype or dout.dtype, device=dev)
-    ldt = _matrix(dtable, "dtable", dev, V, D)
+    ldt = _matrix(dtable, "dtable", at, V, D)[2]
     lib = load()
     if workspace is None:
         workspace = torch.empty(lib.vsamp_embed_workspace_size(N, D), dtype=torch.uint8, device=dev)
-    st = lib.vsamp_embed_backward(_ptr(token, torch.int32, dev, N, "token"), N, dout.data_ptr(), _dtype_code(dout), D,
-                                  ldd, float(scale), V, dtable.data_ptr(), _dtype_code(dtable), ldt, int(accumulate),
-                                  _ptr(workspace, torch.uint8, dev, 0, "workspace"), workspace.numel(), _current(dev))
-    _check(st, "vsamp_embed_backward")
+    st = lib.vsamp_embed_backward(_at(token, torch.int32, at, N, "token"), N, dout.data_ptr(), _dtype_code(dout), D, ldd,
+                                  scale, V, dtable.data_ptr(), _dtype_code(dtable), ldt, accumulate,
+                                  _at(workspace, torch.uint8, at, 0, "workspace"), workspace.numel(), _current(at))
+    if st:
+        _check(st, "vsamp_embed_backward")
     return dtable
