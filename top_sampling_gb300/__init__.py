@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional
 
 import torch
@@ -634,6 +635,23 @@ def _at(t, dtype, index: int, n: int, name: str):
     raise ValueError(f"{name} needs at least {n} elements")
 
 
+_LOCAL = threading.local()
+_SCRATCH_KEPT = 4 << 20   # bytes of the largest workspace that is kept
+
+
+def _scratch(nbytes: int, dev, index: int, stream: int) -> torch.Tensor:
+    """A call's workspace. Small ones are kept per host thread, device and stream, because allocating one costs a decode
+    step's call a third of its host time; nothing is kept in them. A stream's calls never overlap, but those of two
+    threads may interleave on one stream. A call that is captured into a graph gets its own, from the graph's memory."""
+    if nbytes > _SCRATCH_KEPT or torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    kept = _LOCAL.__dict__
+    ws = kept.get((index, stream))
+    if ws is None or ws.numel() < nbytes:
+        ws = kept[(index, stream)] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return ws
+
+
 def _token_ids(v, n: int, dev):
     """Token ids as a contiguous int32 device tensor; wider ids outside its range stay outside every vocabulary."""
     if isinstance(v, torch.Tensor):
@@ -704,15 +722,15 @@ def vsamp_score_tokens(logits, token, temperature=None, n_alt=0, V=None, logprob
         alt_lp = empty((B, n_alt), dtype=f32, device=dev) if alt_lp is None else alt_lp
     else:
         alt_idx = alt_lp = None
-    lib = load()
+    lib, on = load(), _current(at)
     if workspace is None:
-        workspace = empty(lib.vsamp_score_workspace_size(dt, B, V, n_alt), dtype=u8, device=dev)
+        workspace = _scratch(lib.vsamp_score_workspace_size(dt, B, V, n_alt), dev, at, on)
     st = lib.vsamp_score_tokens(
         logits.data_ptr(), dt, B, V, ld, _at(temperature, f32, at, B, "temperature"), _at(token, i32, at, B, "token"),
         n_alt, _at(logprob, f32, at, B, "logprob"), _at(entropy, f32, at, B, "entropy"), _at(rank, i32, at, B, "rank"),
         _at(alt_idx, i32, at, B * n_alt, "alt_idx"), _at(alt_lp, f32, at, B * n_alt, "alt_lp"),
         _at(row_max, f32, at, B, "row_max"), _at(row_logsum, f32, at, B, "row_logsum"),
-        _at(row_status, i32, at, B, "row_status"), _at(workspace, u8, at, 0, "workspace"), workspace.numel(), _current(at))
+        _at(row_status, i32, at, B, "row_status"), _at(workspace, u8, at, 0, "workspace"), workspace.numel(), on)
     if st:
         _check(st, "vsamp_score_tokens")
     return logprob, entropy, rank, alt_idx, alt_lp, row_max, row_logsum, row_status
@@ -848,12 +866,12 @@ def vsamp_embed_backward(token, dout, V, scale=1.0, dtable=None, dtype=None, acc
             raise ValueError("accumulate needs the table gradient to add to")
         dtable = torch.empty((V, D), dtype=dtype or dout.dtype, device=dev)
     ldt = _matrix(dtable, "dtable", at, V, D)[2]
-    lib = load()
+    lib, on = load(), _current(at)
     if workspace is None:
-        workspace = torch.empty(lib.vsamp_embed_workspace_size(N, D), dtype=torch.uint8, device=dev)
+        workspace = _scratch(lib.vsamp_embed_workspace_size(N, D), dev, at, on)
     st = lib.vsamp_embed_backward(_at(token, torch.int32, at, N, "token"), N, dout.data_ptr(), _dtype_code(dout), D, ldd,
                                   scale, V, dtable.data_ptr(), _dtype_code(dtable), ldt, accumulate,
-                                  _at(workspace, torch.uint8, at, 0, "workspace"), workspace.numel(), _current(at))
+                                  _at(workspace, torch.uint8, at, 0, "workspace"), workspace.numel(), on)
     if st:
         _check(st, "vsamp_embed_backward")
     return dtable
