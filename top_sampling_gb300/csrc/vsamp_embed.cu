@@ -63,13 +63,13 @@ static ZeroParams zero_params(const EmbedGradParams& p) {
 template <typename TI, typename TO, int VE>
 static vsamp_status launch_embed_sums(const EmbedGradParams& p, int last, const DeviceInfo& d, cudaStream_t s) {
   const int64_t spans = ceil_div(ceil_div(p.D, VE), kEmbedThreads);
-  const vsamp_status st = launch_1d(embed_sum_kernel<TI, TO, VE>, grid_of(p.sums * spans), kEmbedThreads, 0, s, false, p,
+  const vsamp_status st = launch_1d(embed_sum_kernel<TI, TO, VE>, grid_of(p.sums * spans), kEmbedThreads, 0, s, true, p,
                                     last, (int)spans);
   if (st != VSAMP_OK) return st;
   const int64_t jspans = ceil_div(p.D, kJoinSpan);
   const int64_t most = p.sums * jspans, resident = (int64_t)d.sm_count * 8;   // the list's length is not known here
   const int vec = VE > 1;   // rows of the table begin on a boundary of four elements
-  return launch_1d(embed_join_kernel<TO>, grid_of(most < resident ? most : resident), kEmbedThreads, 0, s, false, p,
+  return launch_1d(embed_join_kernel<TO>, grid_of(most < resident ? most : resident), kEmbedThreads, 0, s, true, p,
                    last, (int)jspans, vec);
 }
 
@@ -80,7 +80,7 @@ static vsamp_status launch_embed_few(const EmbedGradParams& p, cudaStream_t s) {
 }
 
 template <typename TI, typename TO>
-static vsamp_status launch_embed_grad(const EmbedGradParams& p, const DeviceInfo& d, int dev, cudaStream_t s) {
+static vsamp_status launch_embed_grad(EmbedGradParams p, const DeviceInfo& d, int dev, cudaStream_t s) {
   constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
   const bool vec = p.D % VE == 0 && rows_aligned(p.dout, p.ldd, sizeof(TI), VE) &&
                    rows_aligned(p.dtable, p.ldt, sizeof(TO), VE);
@@ -107,11 +107,11 @@ static vsamp_status launch_embed_grad(const EmbedGradParams& p, const DeviceInfo
       }
       if (dev < 64) raised[dev].store(true, std::memory_order_release);
     }
-    // one CTA fits an SM beside the sort's shared memory: one zeroing CTA on each of the others
     const int64_t zero_ctas = ceil_div(zero_warps, kSortOneThreads / 32);
-    const int64_t most = d.sm_count - 1;
+    const int64_t most = 2 * (int64_t)d.sm_count - 1;   // two CTAs fit an SM
+    const int passes = (int)ceil_div(token_bits, 9), digit_bits = (int)ceil_div(token_bits, passes);
     st = launch_1d(embed_sort_one_kernel, grid_of(1 + (zero_ctas < most ? zero_ctas : most)), kSortOneThreads,
-                   (size_t)smem, s, false, p, z, pos_bits, (int)ceil_div(token_bits, kSortBits));
+                   (size_t)smem, s, false, p, z, pos_bits, digit_bits, passes);
     if (st != VSAMP_OK) return st;
   } else {
     if (z.nrows > 0) {

@@ -275,17 +275,21 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_zero_kernel(const ZeroPar
 
 // One CTA sorts up to kSortOne positions on chip, the others write zeros (no z: z.nrows = 0 and a grid of one CTA).
 // A key is token << pos_bits | position: 32 bits hold both, the marker token V included. Least significant digit
-// first, stable: a warp takes consecutive keys 32 at a time, equal digits keep their order.
+// first, stable: a warp takes consecutive keys 32 at a time, equal digits keep their order. A thread's keys and their
+// places among equal digits of its warp stay in registers between the count and the move, so one buffer is enough.
 constexpr int kSortOne = 16384;
 constexpr int kSortOneThreads = 1024;
+constexpr int kSortOnePer = kSortOne / kSortOneThreads;
+constexpr int kSortOneBins = 512;   // digits of up to nine bits: two passes for vocabularies of up to 2^18
 struct SortOneSmem {
-  uint32_t key[2][kSortOne];
-  uint16_t count[kSortOneThreads / 32][kSortBins];
-  uint32_t wsum[kSortBins / 32];
+  uint32_t key[kSortOne];
+  uint16_t count[kSortOneThreads / 32][kSortOneBins];
+  uint32_t wsum[kSortOneBins / 32];
 };
 
 __global__ void __launch_bounds__(kSortOneThreads) embed_sort_one_kernel(const EmbedGradParams p, const ZeroParams z,
-                                                                         int pos_bits, int passes) {
+                                                                         int pos_bits, int digit_bits, int passes) {
+  cudaTriggerProgrammaticLaunchCompletion();   // the sums may be set up meanwhile
   if (blockIdx.x > 0) {
     zero_ranges(z, (int64_t)(blockIdx.x - 1) * (kSortOneThreads / 32) + (threadIdx.x >> 5),
                 (int64_t)(gridDim.x - 1) * (kSortOneThreads / 32));
@@ -297,69 +301,75 @@ __global__ void __launch_bounds__(kSortOneThreads) embed_sort_one_kernel(const E
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int n = (int)p.N, per = (n + NW * 32 - 1) / (NW * 32);   // 32-key steps per warp
   if (t == 0) *p.n_runs = 0;
-  for (int i = t; i < n; i += kSortOneThreads) {
-    const int32_t tok = p.token[i];
-    const uint32_t v = tok >= 0 && (int64_t)tok < p.V ? (uint32_t)tok : (uint32_t)p.V;
-    S.key[0][i] = v << pos_bits | (uint32_t)i;
+#pragma unroll
+  for (int j = 0; j < kSortOnePer; ++j) {   // all loads in flight
+    const int i = j * kSortOneThreads + t;
+    if (i < n) {
+      const int32_t tok = p.token[i];
+      const uint32_t v = tok >= 0 && (int64_t)tok < p.V ? (uint32_t)tok : (uint32_t)p.V;
+      S.key[i] = v << pos_bits | (uint32_t)i;
+    }
   }
+  const int w0 = warp * per * 32 + lane;
+  const uint32_t digit_mask = (1u << digit_bits) - 1u;
   for (int pass = 0; pass < passes; ++pass) {
-    const uint32_t* from = S.key[pass & 1];
-    uint32_t* to = S.key[(pass + 1) & 1];
-    const int shift = pos_bits + pass * kSortBits;
-    for (int i = t; i < NW * kSortBins; i += kSortOneThreads) (&S.count[0][0])[i] = 0;
+    const int shift = pos_bits + pass * digit_bits;
+    for (int i = t; i < NW * kSortOneBins; i += kSortOneThreads) (&S.count[0][0])[i] = 0;
     __syncthreads();
-    const int w0 = warp * per * 32;
-    for (int j = 0; j < per; ++j) {
-      const int i = w0 + j * 32 + lane;
-      const uint32_t d = i < n ? (from[i] >> shift) & (kSortBins - 1) : kSortBins;
-      const uint32_t same = __match_any_sync(kFullMask, d);
-      if (i < n && (same & ((1u << lane) - 1u)) == 0) S.count[warp][d] += (uint16_t)__popc(same);
-      __syncwarp();
+    uint32_t key[kSortOnePer], same[kSortOnePer];
+#pragma unroll
+    for (int j = 0; j < kSortOnePer; ++j) {
+      if (j < per) {
+        const int i = w0 + j * 32;
+        key[j] = i < n ? S.key[i] : 0u;
+        same[j] = __match_any_sync(kFullMask, i < n ? (key[j] >> shift) & digit_mask : kSortOneBins);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kSortOnePer; ++j) {
+      if (j < per) {
+        const bool in = w0 + j * 32 < n;
+        const uint32_t d = (key[j] >> shift) & digit_mask;
+        const uint32_t had = in ? S.count[warp][d] : 0u, before = __popc(same[j] & ((1u << lane) - 1u));
+        __syncwarp();
+        if (in && before == 0) S.count[warp][d] = (uint16_t)(had + __popc(same[j]));
+        __syncwarp();
+        same[j] = had + before;   // the key's place among its warp's keys of the digit
+      }
     }
     __syncthreads();
-    uint32_t all = 0;
-    if (t < kSortBins) {   // this digit's keys, and where they begin
-      for (int w = 0; w < NW; ++w) {
-        const uint32_t c = S.count[w][t];
-        S.count[w][t] = (uint16_t)all;
-        all += c;
-      }
-      uint32_t incl = all;
+    uint32_t all = 0, incl = 0;
+    if (t < kSortOneBins) {   // this digit's keys
+#pragma unroll 8
+      for (int w = 0; w < NW; ++w) all += S.count[w][t];
+      incl = all;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t v = __shfl_up_sync(kFullMask, incl, o);
         if (lane >= o) incl += v;
       }
       if (lane == 31) S.wsum[warp] = incl;
-      all = incl - all;
     }
     __syncthreads();
-    if (t < kSortBins) {
-      for (int w = 0; w < warp; ++w) all += S.wsum[w];
-      for (int w = 0; w < NW; ++w) S.count[w][t] = (uint16_t)(S.count[w][t] + all);
-    }
-    __syncthreads();
-    for (int j = 0; j < per; ++j) {
-      const int i = w0 + j * 32 + lane;
-      const uint32_t key = i < n ? from[i] : 0u;
-      const uint32_t d = i < n ? (key >> shift) & (kSortBins - 1) : kSortBins;
-      const uint32_t same = __match_any_sync(kFullMask, d);
-      const uint32_t before = __popc(same & ((1u << lane) - 1u));
-      uint32_t at = 0;
-      if (i < n) at = S.count[warp][d] + before;
-      __syncwarp();
-      if (i < n) {
-        to[at] = key;
-        if (before == 0) S.count[warp][d] += (uint16_t)__popc(same);
+    if (t < kSortOneBins) {   // where every warp's keys of the digit begin
+      uint32_t run = incl - all;
+      for (int w = 0; w < warp; ++w) run += S.wsum[w];
+#pragma unroll 8
+      for (int w = 0; w < NW; ++w) {
+        const uint32_t c = S.count[w][t];
+        S.count[w][t] = (uint16_t)run;
+        run += c;
       }
-      __syncwarp();
     }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kSortOnePer; ++j)
+      if (j < per && w0 + j * 32 < n) S.key[S.count[warp][(key[j] >> shift) & digit_mask] + same[j]] = key[j];
     __syncthreads();
   }
-  const uint32_t* from = S.key[passes & 1];
   for (int i = t; i < n; i += kSortOneThreads) {
-    const uint32_t v = from[i] >> pos_bits;
-    p.keys[0][i] = make_uint2(v < (uint32_t)p.V ? v : kNoToken, from[i] & ((1u << pos_bits) - 1u));
+    const uint32_t v = S.key[i] >> pos_bits;
+    p.keys[0][i] = make_uint2(v < (uint32_t)p.V ? v : kNoToken, S.key[i] & ((1u << pos_bits) - 1u));
   }
 }
 
@@ -449,6 +459,8 @@ constexpr int kSumBatch = 8;
 template <typename TI, typename TO, int VE>
 __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(const EmbedGradParams p, int last, int spans) {
   const uint2* keys = p.keys[last];
+  cudaGridDependencySynchronize();             // the sorted keys, and the zeros that these sums replace
+  cudaTriggerProgrammaticLaunchCompletion();   // the join may be set up meanwhile
   for (int64_t id = blockIdx.x; id < p.sums * spans; id += gridDim.x) {
     const int64_t tile = spans == 1 ? id : id / spans;
     const int64_t span = id - tile * spans, c = (span * kEmbedThreads + threadIdx.x) * VE;
@@ -515,10 +527,13 @@ __device__ __forceinline__ int64_t run_tiles(const uint2* keys, int64_t tile, in
 }
 
 // Runs over several tiles, from the list that the sums left: a CTA per run and kJoinSpan columns, four per thread, adds
-// the run's parts in tile order, eight in flight.
+// the run's parts in tile order, kJoinBatch in flight.
+constexpr int kJoinBatch = 16;
+
 template <typename TO>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGradParams p, int last, int spans, int vec) {
   const uint2* keys = p.keys[last];
+  cudaGridDependencySynchronize();   // the tiles' parts and the list
   const int64_t total = (int64_t)*p.n_runs * spans;
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
     const int64_t run = id / spans, tile = p.runs[run];
@@ -529,14 +544,21 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGr
     // parts are padded to ldp, a multiple of 8, columns; slot 1 of the first tile, slot 0 of the others
     auto at = [&](int64_t k, int slot) { return *reinterpret_cast<const float4*>(p.part + (k * 2 + slot) * p.ldp + c); };
     float4 sum = at(tile, 1);
-#pragma unroll 8
-    for (int64_t k = tile + 1; k <= end; ++k) {
-      const float4 v = at(k, 0);
+    auto add = [&](const float4& v) {
       sum.x += v.x;
       sum.y += v.y;
       sum.z += v.z;
       sum.w += v.w;
+    };
+    int64_t k = tile + 1;
+    for (; k + kJoinBatch <= end + 1; k += kJoinBatch) {
+      float4 v[kJoinBatch];
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) v[i] = at(k + i, 0);
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) add(v[i]);
     }
+    for (; k <= end; ++k) add(at(k, 0));
     float all[4] = {sum.x, sum.y, sum.z, sum.w};
     if (vec) {
       put_row<TO, 4>(p, tok, c, all);
