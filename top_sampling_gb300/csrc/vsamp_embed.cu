@@ -20,7 +20,7 @@ static int bits_of(int64_t n) {   // values 0 .. n fit
   return bits;
 }
 
-// Elements that a thread takes at once: 16 bytes of the wider type when every row begins on that boundary.
+// Whether every row begins on the boundary of a vector of ve elements.
 static bool rows_aligned(const void* p, int64_t ld, int es, int ve) {
   return (reinterpret_cast<uintptr_t>(p) % (unsigned)(ve * es)) == 0 && ld % ve == 0;
 }
@@ -35,11 +35,10 @@ static vsamp_status launch_embed_ve(const EmbedParams& p, cudaStream_t s) {
 }
 
 template <typename TI, typename TO>
-static vsamp_status launch_embed(const EmbedParams& p, cudaStream_t s) {
-  constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
-  if (p.D % VE == 0 && rows_aligned(p.table, p.ldt, sizeof(TI), VE) && rows_aligned(p.out, p.ldo, sizeof(TO), VE))
-    return launch_embed_ve<TI, TO, VE>(p, s);
-  return launch_embed_ve<TI, TO, 1>(p, s);
+static vsamp_status launch_embed(EmbedParams p, cudaStream_t s) {
+  constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;   // 16 bytes of the wider type
+  p.aligned = rows_aligned(p.table, p.ldt, sizeof(TI), VE) && rows_aligned(p.out, p.ldo, sizeof(TO), VE);
+  return launch_embed_ve<TI, TO, VE>(p, s);
 }
 
 template <typename TO>
@@ -68,9 +67,8 @@ static vsamp_status launch_embed_sums(const EmbedGradParams& p, int last, const 
   if (st != VSAMP_OK) return st;
   const int64_t jspans = ceil_div(p.D, kJoinSpan);
   const int64_t most = p.sums * jspans, resident = (int64_t)d.sm_count * 8;   // the list's length is not known here
-  const int vec = VE > 1;   // rows of the table begin on a boundary of four elements
   return launch_1d(embed_join_kernel<TO>, grid_of(most < resident ? most : resident), kEmbedThreads, 0, s, true, p,
-                   last, (int)jspans, vec);
+                   last, (int)jspans);
 }
 
 template <typename TI, typename TO, int VE>
@@ -82,8 +80,7 @@ static vsamp_status launch_embed_few(const EmbedGradParams& p, cudaStream_t s) {
 template <typename TI, typename TO>
 static vsamp_status launch_embed_grad(EmbedGradParams p, const DeviceInfo& d, int dev, cudaStream_t s) {
   constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
-  const bool vec = p.D % VE == 0 && rows_aligned(p.dout, p.ldd, sizeof(TI), VE) &&
-                   rows_aligned(p.dtable, p.ldt, sizeof(TO), VE);
+  p.aligned = rows_aligned(p.dout, p.ldd, sizeof(TI), VE) && rows_aligned(p.dtable, p.ldt, sizeof(TO), VE);
   vsamp_status st = VSAMP_OK;
   ZeroParams z{};
   if (!p.accumulate) z = zero_params<TO>(p);
@@ -93,7 +90,7 @@ static vsamp_status launch_embed_grad(EmbedGradParams p, const DeviceInfo& d, in
       st = launch_1d(embed_zero_kernel, grid_of(ceil_div(zero_warps, kEmbedThreads / 32)), kEmbedThreads, 0, s, false, z);
       if (st != VSAMP_OK) return st;
     }
-    return vec ? launch_embed_few<TI, TO, VE>(p, s) : launch_embed_few<TI, TO, 1>(p, s);
+    return launch_embed_few<TI, TO, VE>(p, s);
   }
   int last = 0;
   const int pos_bits = bits_of(p.N - 1), token_bits = bits_of(p.V);
@@ -128,7 +125,7 @@ static vsamp_status launch_embed_grad(EmbedGradParams p, const DeviceInfo& d, in
     }
     last = (passes - 1) & 1;
   }
-  return vec ? launch_embed_sums<TI, TO, VE>(p, last, d, s) : launch_embed_sums<TI, TO, 1>(p, last, d, s);
+  return launch_embed_sums<TI, TO, VE>(p, last, d, s);
 }
 
 struct EmbedPlan {

@@ -14,6 +14,7 @@
 
 #include "vsamp.h"
 #include "vsamp_device.cuh"
+#include "vsamp_vec.cuh"
 
 namespace vsamp {
 
@@ -35,6 +36,7 @@ struct EmbedParams {
   unsigned char* out;
   int64_t ldo;
   int32_t* row_status;
+  int aligned;             // every row of the table and of the output begins on a vector's boundary
 };
 
 struct EmbedGradParams {
@@ -46,6 +48,7 @@ struct EmbedGradParams {
   unsigned char* dtable;
   int64_t ldt;
   int accumulate;
+  int aligned;             // every row of dout and of the table begins on a vector's boundary
   uint2* keys[2];          // {token or kNoToken, position}
   uint32_t* hist;          // [tiles, bins]
   float* part;             // [2 * sum tiles, ldp] partial sums of the first and last run of a tile
@@ -56,58 +59,7 @@ struct EmbedGradParams {
   int64_t sums;            // sum tiles
 };
 
-template <typename T>
-__device__ __forceinline__ float elem_load(const unsigned char* p, int64_t i) {
-  if constexpr (sizeof(T) == 4) return reinterpret_cast<const float*>(p)[i];
-  else return __uint_as_float((uint32_t) reinterpret_cast<const unsigned short*>(p)[i] << 16);
-}
-template <typename T>
-__device__ __forceinline__ void elem_store(unsigned char* p, int64_t i, float f) {
-  if constexpr (sizeof(T) == 4) reinterpret_cast<float*>(p)[i] = f;
-  else reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(f);
-}
-
 constexpr int kEmbedThreads = 256;
-
-// VE neighbouring elements as fp32 (VE = 1, or 16 bytes of the wider type involved)
-template <typename T, int VE>
-struct ElemVec {
-  uint32_t w[sizeof(T) * VE >= 4 ? sizeof(T) * VE / 4 : 1];
-  __device__ __forceinline__ void load(const unsigned char* p, int64_t i) {
-    if constexpr (VE == 1) {
-      w[0] = __float_as_uint(elem_load<T>(p, i));
-    } else if constexpr (sizeof(T) * VE == 16) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p + i * (int64_t)sizeof(T));
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(p + i * (int64_t)sizeof(T));
-      w[0] = v.x; w[1] = v.y;
-    }
-  }
-  __device__ __forceinline__ float at(int j) const {
-    if constexpr (VE == 1 || sizeof(T) == 4) return __uint_as_float(w[j]);
-    else return __uint_as_float((j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
-  }
-};
-template <typename T, int VE>
-__device__ __forceinline__ void elem_store_vec(unsigned char* p, int64_t i, const float (&f)[VE]) {
-  if constexpr (VE == 1) {
-    elem_store<T>(p, i, f[0]);
-  } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int j = 0; j < VE; j += 4)
-      *reinterpret_cast<float4*>(p + (i + j) * 4) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
-  } else {
-    uint32_t w[VE / 2];
-#pragma unroll
-    for (int j = 0; j < VE / 2; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-      memcpy(&w[j], &b, 4);
-    }
-    if constexpr (VE == 8) *reinterpret_cast<uint4*>(p + i * 2) = make_uint4(w[0], w[1], w[2], w[3]);
-    else *reinterpret_cast<uint2*>(p + i * 2) = make_uint2(w[0], w[1]);
-  }
-}
 
 // tx threads of a CTA along a row (a power of two), kEmbedThreads / tx rows per CTA, U vectors per thread and row so
 // that their loads are in flight together.
@@ -132,15 +84,20 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams 
     const float fill = skip ? 0.f : __int_as_float(0x7FC00000);
     ElemVec<TI, VE> v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (ok && c0 + u * tx * VE < p.D) v[u].load(src, c0 + u * tx * VE);
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + u * tx * VE;
+      if (ok && c < p.D) v[u].load_row(src + c * (int64_t)sizeof(TI), p.D - c, p.aligned, 0u);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (c0 + u * tx * VE < p.D) {
+      const int64_t c = c0 + u * tx * VE;
+      if (c < p.D) {
         float f[VE];
 #pragma unroll
         for (int j = 0; j < VE; ++j) f[j] = ok ? v[u].at(j) * p.scale : fill;
-        elem_store_vec<TO, VE>(dst, c0 + u * tx * VE, f);
+        ElemVec<TO, VE> o;
+        o.set(f);
+        o.store_row(dst + c * (int64_t)sizeof(TO), p.D - c, p.aligned);
       }
     }
   }
@@ -373,6 +330,12 @@ __global__ void __launch_bounds__(kSortOneThreads) embed_sort_one_kernel(const E
   }
 }
 
+// Columns [c, c + VE) of a position's row of dout (0 beyond D).
+template <typename TI, int VE>
+__device__ __forceinline__ void load_dout(const EmbedGradParams& p, int64_t position, int64_t c, ElemVec<TI, VE>& v) {
+  v.load_row(p.dout + (position * p.ldd + c) * (int64_t)sizeof(TI), p.D - c, p.aligned, 0u);
+}
+
 // Adds `n` rows of dout in order; row i is at position pos(i). Eight rows are in flight at a time.
 template <typename TI, int VE, typename F>
 __device__ __forceinline__ void add_rows(const EmbedGradParams& p, int64_t c, int n, F pos, float (&sum)[VE]) {
@@ -380,7 +343,7 @@ __device__ __forceinline__ void add_rows(const EmbedGradParams& p, int64_t c, in
   for (; i + 8 <= n; i += 8) {
     ElemVec<TI, VE> v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j].load(p.dout, (int64_t)pos(i + j) * p.ldd + c);
+    for (int j = 0; j < 8; ++j) load_dout(p, pos(i + j), c, v[j]);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -388,7 +351,7 @@ __device__ __forceinline__ void add_rows(const EmbedGradParams& p, int64_t c, in
   }
   for (; i < n; ++i) {
     ElemVec<TI, VE> v;
-    v.load(p.dout, (int64_t)pos(i) * p.ldd + c);
+    load_dout(p, pos(i), c, v);
 #pragma unroll
     for (int e = 0; e < VE; ++e) sum[e] += v.at(e);
   }
@@ -397,16 +360,17 @@ __device__ __forceinline__ void add_rows(const EmbedGradParams& p, int64_t c, in
 // One row's span of the table: scale * sum, added or written, one rounding.
 template <typename TO, int VE>
 __device__ __forceinline__ void put_row(const EmbedGradParams& p, uint32_t tok, int64_t c, float (&sum)[VE]) {
-  const int64_t at = (int64_t)tok * p.ldt + c;
+  unsigned char* at = p.dtable + ((int64_t)tok * p.ldt + c) * (int64_t)sizeof(TO);
 #pragma unroll
   for (int e = 0; e < VE; ++e) sum[e] *= p.scale;
+  ElemVec<TO, VE> v;
   if (p.accumulate) {
-    ElemVec<TO, VE> old;
-    old.load(p.dtable, at);
+    v.load_row(at, p.D - c, p.aligned, 0u);
 #pragma unroll
-    for (int e = 0; e < VE; ++e) sum[e] += old.at(e);
+    for (int e = 0; e < VE; ++e) sum[e] += v.at(e);
   }
-  elem_store_vec<TO, VE>(p.dtable, at, sum);
+  v.set(sum);
+  v.store_row(at, p.D - c, p.aligned);
 }
 
 // Few positions (N <= kEmbedFew): a CTA per position and span of columns, no workspace.
@@ -483,7 +447,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(const Embed
       for (int i = 0; i < kSumBatch; ++i) key[i] = b + i < i1 ? keys[b + i] : make_uint2(kNoToken, 0);
 #pragma unroll
       for (int i = 0; i < kSumBatch; ++i)
-        if (key[i].x != kNoToken) v[i].load(p.dout, (int64_t)key[i].y * p.ldd + c);
+        if (key[i].x != kNoToken) load_dout(p, key[i].y, c, v[i]);
       const uint32_t after_batch = b + kSumBatch < i1 ? keys[b + kSumBatch].x : next;
 #pragma unroll
       for (int i = 0; i < kSumBatch; ++i) {
@@ -497,7 +461,10 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(const Embed
               put_row<TO, VE>(p, key[i].x, c, sum);
             } else {
               // slot 0: the tile's first run, slot 1: its last (a run that fills the tile from before has slot 0)
-              elem_store_vec<float, VE>(reinterpret_cast<unsigned char*>(p.part), (tile * 2 + (from_before ? 0 : 1)) * p.ldp + c, sum);
+              // (the parts' rows are padded to whole vectors)
+              ElemVec<float, VE> part;
+              part.set(sum);
+              part.store(reinterpret_cast<unsigned char*>(p.part + (tile * 2 + (from_before ? 0 : 1)) * p.ldp + c), true);
             }
 #pragma unroll
             for (int e = 0; e < VE; ++e) sum[e] = 0.f;
@@ -531,7 +498,7 @@ __device__ __forceinline__ int64_t run_tiles(const uint2* keys, int64_t tile, in
 constexpr int kJoinBatch = 16;
 
 template <typename TO>
-__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGradParams p, int last, int spans, int vec) {
+__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGradParams p, int last, int spans) {
   const uint2* keys = p.keys[last];
   cudaGridDependencySynchronize();   // the tiles' parts and the list
   const int64_t total = (int64_t)*p.n_runs * spans;
@@ -560,15 +527,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGr
     }
     for (; k <= end; ++k) add(at(k, 0));
     float all[4] = {sum.x, sum.y, sum.z, sum.w};
-    if (vec) {
-      put_row<TO, 4>(p, tok, c, all);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float one[1] = {all[e]};
-        if (c + e < p.D) put_row<TO, 1>(p, tok, c + e, one);
-      }
-    }
+    put_row<TO, 4>(p, tok, c, all);
   }
 }
 

@@ -18,6 +18,7 @@
 
 #include "vsamp.h"
 #include "vsamp_device.cuh"
+#include "vsamp_vec.cuh"
 
 namespace vsamp {
 
@@ -130,17 +131,12 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
 template <typename T>
 __device__ __forceinline__ void score_load(const unsigned char* xr, int64_t e, int64_t V, int vec, uint32_t (&w)[4]) {
   using Ty = ScoreType<T>;
-  if (vec && e + Ty::VE <= V) {
-    const uint4 v = ldg_stream(xr + e * Ty::ES);
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    return;
-  }
+  ElemVec<T, Ty::VE> v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = Ty::kMasked;
-  if (e >= V) return;
+  for (int i = 0; i < 4; ++i) v.w[i] = Ty::kMasked;
+  if (e < V) v.load_row(xr + e * Ty::ES, V - e, vec, Ty::kMasked & (Ty::ES == 4 ? 0xFFFFFFFFu : 0xFFFFu));
 #pragma unroll
-  for (int j = 0; j < Ty::VE; ++j)
-    if (e + j < V) Ty::put(w, j, Ty::load(xr, e + j));
+  for (int i = 0; i < 4; ++i) w[i] = v.w[i];
 }
 
 // Maximum of two registers of a vector's type; NaN if either holds one.
@@ -680,9 +676,9 @@ __device__ __forceinline__ void grad_vector(const GradRow& r, uint32_t (&w)[4]) 
   for (int j = 0; j < 4; ++j) w[j] = out[j];
 }
 
-// One CTA per row and span of kGradThreads * kGradVecs vectors. Vectors begin at the row's first 16-byte boundary when
-// the logits' and the gradient's rows have the same one; the elements before and after the whole vectors belong to
-// the row's first CTA. Otherwise the span is taken element by element. Streaming loads and stores: nothing is reused.
+// One CTA per row and span of kGradThreads * kGradVecs vectors. Vectors begin at the first 16-byte boundary of the
+// gradient's row, whatever the logits' row's; the elements before and after the whole vectors belong to the row's first
+// CTA. Streaming loads and stores: nothing is reused.
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGradParams p) {
   using Ty = ScoreType<T>;
@@ -697,17 +693,28 @@ __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGra
     const bool skip = t == VSAMP_TOKEN_IGNORE;
     const int xa = (int)((16 - (reinterpret_cast<uintptr_t>(xr) & 15)) & 15) / Ty::ES;
     const int da = (int)((16 - (reinterpret_cast<uintptr_t>(dr) & 15)) & 15) / Ty::ES;
-    const bool vec = xa == da;
-    const int64_t head = xa < p.V ? xa : p.V, nv = (p.V - head) / VE;
+    const bool same = xa == da;   // the logits' row has the same boundary
+    const int64_t head = da < p.V ? da : p.V, nv = (p.V - head) / VE;
     const int64_t v0 = span * SPAN + threadIdx.x;
     uint32_t w[kGradVecs][4];
-    if (vec && !skip) {
+    if (!skip && same) {
 #pragma unroll
       for (int i = 0; i < kGradVecs; ++i) {
         const int64_t v = v0 + i * kGradThreads;
         if (v < nv) {
           const uint4 q = ldg_stream(xr + (head + v * VE) * Ty::ES);
           w[i][0] = q.x; w[i][1] = q.y; w[i][2] = q.z; w[i][3] = q.w;
+        }
+      }
+    } else if (!skip) {
+#pragma unroll
+      for (int i = 0; i < kGradVecs; ++i) {
+        const int64_t v = v0 + i * kGradThreads;
+        if (v < nv) {
+          ElemVec<T, VE> q;
+          q.load(xr + (head + v * VE) * Ty::ES, false);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[i][k] = q.w[k];
         }
       }
     }
@@ -733,12 +740,6 @@ __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGra
       if (ok) d = r.at(Ty::load(xr, v)) + (v == t ? g * invT : 0.f);
       Ty::store(dr, v, d);
     };
-    if (!vec) {
-      const int64_t e1 = (span + 1) * SPAN * VE < p.V ? (span + 1) * SPAN * VE : p.V;
-#pragma unroll 4
-      for (int64_t e = span * SPAN * VE + threadIdx.x; e < e1; e += kGradThreads) one(e);
-      continue;
-    }
     const int64_t tv = ok ? (t - head) / VE : -1;   // the vector that holds the given token
 #pragma unroll
     for (int i = 0; i < kGradVecs; ++i) {
