@@ -110,6 +110,20 @@ def test_special_hidden_values(ts, dev):
         assert (y[3] == 2.0 ** -121).all() and (y[4] == 2.0 ** 119).all() and (y[5] == -float("inf")).all()
 
 
+def test_largest_fp32_values(ts, dev):
+    """Finite values that would round to an infinite bf16 stay finite."""
+    V, D, group = 16, 32, 32
+    codes = torch.full((V, D // 2), 0x99, dtype=torch.uint8, device=dev)      # weights 1 * scale
+    scales = torch.full((V, 1), 2.0 ** -10, device=dev)
+    head = ts.vsamp_head_pack(codes, scales, group=group)
+    h = torch.zeros((2, D), device=dev)
+    h[0, 4] = torch.finfo(torch.float32).max
+    h[1, 9] = -torch.finfo(torch.float32).max
+    y = tu.f64(ts.vsamp_head_logits(h, head))
+    want, size = tu.head(tu.f64(h), codes.cpu().numpy(), tu.f64(scales), None, group)
+    assert np.all(np.abs(y - want) <= tu.head_tol(size, group, 1, 3) + tu.U * np.abs(want))
+
+
 def test_other_stream_and_graph(ts, dev):
     V, D, group = 5000, 512, 64
     w = _weights(V, D, group, torch.bfloat16, True, dev, 9)

@@ -62,8 +62,9 @@ static ZeroParams zero_params(const EmbedGradParams& p) {
 template <typename TI, typename TO, int VE>
 static vsamp_status launch_embed_sums(const EmbedGradParams& p, int last, const DeviceInfo& d, cudaStream_t s) {
   const int64_t spans = ceil_div(ceil_div(p.D, VE), kEmbedThreads);
-  const vsamp_status st = launch_1d(embed_sum_kernel<TI, TO, VE>, grid_of(p.sums * spans), kEmbedThreads, 0, s, true, p,
-                                    last, (int)spans);
+  const vsamp_status st = launch_1d(p.aligned && p.D % VE == 0 ? embed_sum_kernel<TI, TO, VE, true>
+                                                               : embed_sum_kernel<TI, TO, VE, false>,
+                                    grid_of(p.sums * spans), kEmbedThreads, 0, s, true, p, last, (int)spans);
   if (st != VSAMP_OK) return st;
   const int64_t jspans = ceil_div(p.D, kJoinSpan);
   const int64_t most = p.sums * jspans, resident = (int64_t)d.sm_count * 8;   // the list's length is not known here

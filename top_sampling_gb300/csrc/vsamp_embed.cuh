@@ -330,10 +330,13 @@ __global__ void __launch_bounds__(kSortOneThreads) embed_sort_one_kernel(const E
   }
 }
 
-// Columns [c, c + VE) of a position's row of dout (0 beyond D).
+// Columns [c, c + VE) of a position's row of dout (0 beyond D). whole: every row is aligned whole vectors.
 template <typename TI, int VE>
-__device__ __forceinline__ void load_dout(const EmbedGradParams& p, int64_t position, int64_t c, ElemVec<TI, VE>& v) {
-  v.load_row(p.dout + (position * p.ldd + c) * (int64_t)sizeof(TI), p.D - c, p.aligned, 0u);
+__device__ __forceinline__ void load_dout(const EmbedGradParams& p, bool whole, bool aligned, int64_t position, int64_t c,
+                                          ElemVec<TI, VE>& v) {
+  const unsigned char* at = p.dout + (position * p.ldd + c) * (int64_t)sizeof(TI);
+  if (whole) v.load(at, true);
+  else v.load_row(at, p.D - c, aligned, 0u);
 }
 
 // Adds `n` rows of dout in order; row i is at position pos(i). Eight rows are in flight at a time.
@@ -343,7 +346,7 @@ __device__ __forceinline__ void add_rows(const EmbedGradParams& p, int64_t c, in
   for (; i + 8 <= n; i += 8) {
     ElemVec<TI, VE> v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) load_dout(p, pos(i + j), c, v[j]);
+    for (int j = 0; j < 8; ++j) load_dout(p, false, p.aligned, pos(i + j), c, v[j]);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -351,7 +354,7 @@ __device__ __forceinline__ void add_rows(const EmbedGradParams& p, int64_t c, in
   }
   for (; i < n; ++i) {
     ElemVec<TI, VE> v;
-    load_dout(p, pos(i), c, v);
+    load_dout(p, false, p.aligned, pos(i), c, v);
 #pragma unroll
     for (int e = 0; e < VE; ++e) sum[e] += v.at(e);
   }
@@ -359,18 +362,21 @@ __device__ __forceinline__ void add_rows(const EmbedGradParams& p, int64_t c, in
 
 // One row's span of the table: scale * sum, added or written, one rounding.
 template <typename TO, int VE>
-__device__ __forceinline__ void put_row(const EmbedGradParams& p, uint32_t tok, int64_t c, float (&sum)[VE]) {
+__device__ __forceinline__ void put_row(const EmbedGradParams& p, bool whole, uint32_t tok, int64_t c,
+                                        float (&sum)[VE]) {
   unsigned char* at = p.dtable + ((int64_t)tok * p.ldt + c) * (int64_t)sizeof(TO);
 #pragma unroll
   for (int e = 0; e < VE; ++e) sum[e] *= p.scale;
   ElemVec<TO, VE> v;
   if (p.accumulate) {
-    v.load_row(at, p.D - c, p.aligned, 0u);
+    if (whole) v.load(at, true);
+    else v.load_row(at, p.D - c, p.aligned, 0u);
 #pragma unroll
     for (int e = 0; e < VE; ++e) sum[e] += v.at(e);
   }
   v.set(sum);
-  v.store_row(at, p.D - c, p.aligned);
+  if (whole) v.store(at, true);
+  else v.store_row(at, p.D - c, p.aligned);
 }
 
 // Few positions (N <= kEmbedFew): a CTA per position and span of columns, no workspace.
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const EmbedGra
 #pragma unroll
   for (int e = 0; e < VE; ++e) sum[e] = 0.f;
   add_rows<TI, VE>(p, c, n, [&](int i) { return (int)list[i]; }, sum);
-  put_row<TO, VE>(p, (uint32_t)tok, c, sum);
+  put_row<TO, VE>(p, false, (uint32_t)tok, c, sum);
 }
 
 // Sums of one tile of kEmbedTile sorted positions: a CTA per tile and span of columns. A tile is read in two halves:
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const EmbedGra
 // took twice the time).
 constexpr int kSumBatch = 8;
 
-template <typename TI, typename TO, int VE>
+template <typename TI, typename TO, int VE, bool WHOLE>
 __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(const EmbedGradParams p, int last, int spans) {
   const uint2* keys = p.keys[last];
   cudaGridDependencySynchronize();             // the sorted keys, and the zeros that these sums replace
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(const Embed
       for (int i = 0; i < kSumBatch; ++i) key[i] = b + i < i1 ? keys[b + i] : make_uint2(kNoToken, 0);
 #pragma unroll
       for (int i = 0; i < kSumBatch; ++i)
-        if (key[i].x != kNoToken) load_dout(p, key[i].y, c, v[i]);
+        if (key[i].x != kNoToken) load_dout(p, WHOLE, p.aligned, key[i].y, c, v[i]);
       const uint32_t after_batch = b + kSumBatch < i1 ? keys[b + kSumBatch].x : next;
 #pragma unroll
       for (int i = 0; i < kSumBatch; ++i) {
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(const Embed
           const uint32_t after = end ? next : i + 1 < kSumBatch ? key[i + 1 < kSumBatch ? i + 1 : 0].x : after_batch;
           if (after != key[i].x || end) {
             if (!from_before && after != key[i].x) {
-              put_row<TO, VE>(p, key[i].x, c, sum);
+              put_row<TO, VE>(p, WHOLE, key[i].x, c, sum);
             } else {
               // slot 0: the tile's first run, slot 1: its last (a run that fills the tile from before has slot 0)
               // (the parts' rows are padded to whole vectors)
@@ -527,7 +533,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGr
     }
     for (; k <= end; ++k) add(at(k, 0));
     float all[4] = {sum.x, sum.y, sum.z, sum.w};
-    put_row<TO, 4>(p, tok, c, all);
+    put_row<TO, 4>(p, false, tok, c, all);
   }
 }
 

@@ -148,12 +148,12 @@ __device__ __forceinline__ void head_stage(const HeadParams& p, uint4* sh, int u
         uint32_t w[8];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const __nv_bfloat16 v = __float2bfloat16_rn(x[e]);
-          const uint32_t bits = (uint32_t)__bfloat16_as_ushort(v);
+          uint32_t bits = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x[e]));
+          // a finite value beyond the largest bf16 begins with that; an infinity has no remainder (inf - inf is NaN)
+          if ((bits & 0x7FFFu) == 0x7F80u && !isinf(x[e])) bits -= 1;
           if (e & 1) w[e / 2] |= bits << 16;
           else w[e / 2] = bits;
-          // an infinity has no remainder (inf - inf would turn it into NaN)
-          x[e] = isinf(__bfloat162float(v)) ? 0.f : x[e] - __bfloat162float(v);
+          x[e] = isinf(x[e]) ? 0.f : x[e] - __uint_as_float(bits << 16);
         }
         to[0] = make_uint4(w[0], w[4], w[1], w[5]);
         to[1] = make_uint4(w[2], w[6], w[3], w[7]);
