@@ -101,18 +101,10 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
   return r;
 }
 
-// (a0, a1) += s * (b0, b1), two fused multiply-adds in one instruction
-__device__ __forceinline__ void fma_pair(float& a0, float& a1, float s, float b0, float b1) {
-  asm("{\n\t.reg .b64 a, b, s;\n\t"
-      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
-      "fma.rn.f32x2 a, s, b, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b0), "f"(b1), "f"(s));
-}
-
 // Stages the hidden states of units [u0, u1) as the instruction's second operand, NT column tiles of 8. In step k, lane
-// l needs column 8 n + l/4 at inner positions 2 (l%4) + {0, 1} and + 8; they are stored as [step][8 NT columns][l%4], two
-// registers each, so a column's 16 positions of a step are 32 contiguous bytes and the reads have constant offsets. A
+// l needs column 8 n + l/4 at inner positions 2 (l%4) + {0, 1} and + 8; they are stored as [two
+// steps][8 NT columns][l%4], four registers each (the two of both steps), so a lane reads two steps at once and the
+// reads have constant offsets. A
 // bf16 row is a column; an fp32 row is three (x = hi + mid + lo, each the bf16 nearest to what is left: 24 bits in
 // all), in column tiles of their own, so that one lane holds the sums of all three. Positions beyond D are 0; columns
 // without a row are not written (their part of the product is not used).
@@ -124,7 +116,7 @@ __device__ __forceinline__ void head_stage(const HeadParams& p, uint4* sh, int u
     const int r = i / steps, ks = i - r * steps;
     const int64_t k = (int64_t)u0 * kHeadUnit + ks * 16;
     const bool whole = p.vec && k + 16 <= p.s.D;
-    uint4* to = sh + (ks * (8 * NT) + r) * 2;
+    uint2* to = reinterpret_cast<uint2*>(sh + ((ks >> 1) * (8 * NT) + r) * 4) + (ks & 1);
     if (p.terms == 1) {
       const unsigned short* h = reinterpret_cast<const unsigned short*>(p.hidden) + (p.m0 + r) * p.ldh + k;
       uint32_t w[8];   // pairs of neighbouring positions
@@ -137,8 +129,8 @@ __device__ __forceinline__ void head_stage(const HeadParams& p, uint4* sh, int u
         for (int e = 0; e < 8; ++e)
           w[e] = (k + 2 * e < p.s.D ? h[2 * e] : 0u) | (uint32_t)(k + 2 * e + 1 < p.s.D ? h[2 * e + 1] : 0u) << 16;
       }
-      to[0] = make_uint4(w[0], w[4], w[1], w[5]);
-      to[1] = make_uint4(w[2], w[6], w[3], w[7]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) to[2 * j] = make_uint2(w[j], w[j + 4]);
     } else {
       const float* h = reinterpret_cast<const float*>(p.hidden) + (p.m0 + r) * p.ldh + k;
       float x[16];
@@ -155,9 +147,9 @@ __device__ __forceinline__ void head_stage(const HeadParams& p, uint4* sh, int u
           else w[e / 2] = bits;
           x[e] = isinf(x[e]) ? 0.f : x[e] - __uint_as_float(bits << 16);
         }
-        to[0] = make_uint4(w[0], w[4], w[1], w[5]);
-        to[1] = make_uint4(w[2], w[6], w[3], w[7]);
-        to += p.term_tiles * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[2 * j] = make_uint2(w[j], w[j + 4]);
+        to += p.term_tiles * 64;
       }
     }
   }
@@ -255,13 +247,11 @@ __global__ void __launch_bounds__(MAXW * 32, 1) head_kernel(const HeadParams p) 
 
   for (int64_t first = first0; first < nt; first += stride) {
     const int64_t tile = first + mine;
-    float acc[RT][NT][4];
+    float2 acc[RT][NT][2];   // rows l/4 and l/4 + 8, two columns each
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t][n][j] = 0.f;
+      for (int n = 0; n < NT; ++n) acc[t][n][0] = acc[t][n][1] = make_float2(0.f, 0.f);
     for (int c0 = 0; c0 < p.units; c0 += p.chunk) {
       if (p.chunk < p.units || first == first0) {
         __syncthreads();   // the last chunk has been read
@@ -273,11 +263,11 @@ __global__ void __launch_bounds__(MAXW * 32, 1) head_kernel(const HeadParams p) 
         copy_async_wait<PF - 1>();
         __syncwarp();
         const uint32_t rec = ring + (turn++ & (PF - 1)) * slot_bytes;
-        const uint2* su = reinterpret_cast<const uint2*>(head_smem) + (u - c0) * (kHeadUnitSteps * 32 * NT) + lane;
+        const uint4* su = reinterpret_cast<const uint4*>(head_smem) + (u - c0) * (kHeadUnitSteps / 2 * 32 * NT) + lane;
         // a group of 128 fills a record, smaller ones may leave the last record with fewer blocks and groups
         const int blocks = NG == 1 ? 2 : min(nb - 2 * u, 2), groups = min(ng - u * NG, NG);
         float part[RT][NT][4];
-        uint4 q4[RT];
+        uint4 q4[RT], h4[NT];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           if (NG == 1 || g < groups) {
@@ -306,9 +296,13 @@ __global__ void __launch_bounds__(MAXW * 32, 1) head_kernel(const HeadParams p) 
 #pragma unroll
             for (int i = 0; i < GS; ++i) {
               const int k = g * GS + i;
+              if (k % 2 == 0) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) h4[n] = su[(k / 2 * NT + n) * 32];
+              }
               uint2 h[NT];
 #pragma unroll
-              for (int n = 0; n < NT; ++n) h[n] = su[(k * NT + n) * 32];
+              for (int n = 0; n < NT; ++n) h[n] = k % 2 == 0 ? make_uint2(h4[n].x, h4[n].y) : make_uint2(h4[n].z, h4[n].w);
 #pragma unroll
               for (int t = 0; t < RT; ++t) {
                 if (k % 4 == 0) q4[t] = reinterpret_cast<const uint4*>(head_smem + rec + t * record)[(k / 4) * 32 + lane];
@@ -330,8 +324,8 @@ __global__ void __launch_bounds__(MAXW * 32, 1) head_kernel(const HeadParams p) 
             for (int t = 0; t < RT; ++t)
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                fma_pair(acc[t][n][0], acc[t][n][1], slo[t], part[t][n][0], part[t][n][1]);
-                fma_pair(acc[t][n][2], acc[t][n][3], shi[t], part[t][n][2], part[t][n][3]);
+                acc[t][n][0] = __ffma2_rn(make_float2(slo[t], slo[t]), make_float2(part[t][n][0], part[t][n][1]), acc[t][n][0]);
+                acc[t][n][1] = __ffma2_rn(make_float2(shi[t], shi[t]), make_float2(part[t][n][2], part[t][n][3]), acc[t][n][1]);
               }
           }
         }
@@ -341,15 +335,15 @@ __global__ void __launch_bounds__(MAXW * 32, 1) head_kernel(const HeadParams p) 
     }
     if (p.split > 1) {
       // the parts are added in order by the first warp of the set
-      float* red = reinterpret_cast<float*>(head_smem + p.red_off);
-      constexpr int W = RT * NT * 4;
+      float2* red = reinterpret_cast<float2*>(head_smem + p.red_off);
+      constexpr int W = RT * NT * 2;
       if (part_of > 0) {
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) red[(warp * W + (t * NT + n) * 4 + j) * 32 + lane] = acc[t][n][j];
+            for (int j = 0; j < 2; ++j) red[(warp * W + (t * NT + n) * 2 + j) * 32 + lane] = acc[t][n][j];
       }
       __syncthreads();
       if (part_of == 0) {
@@ -359,7 +353,8 @@ __global__ void __launch_bounds__(MAXW * 32, 1) head_kernel(const HeadParams p) 
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) acc[t][n][j] += red[((warp + o) * W + (t * NT + n) * 4 + j) * 32 + lane];
+              for (int j = 0; j < 2; ++j)
+                acc[t][n][j] = __fadd2_rn(acc[t][n][j], red[((warp + o) * W + (t * NT + n) * 2 + j) * 32 + lane]);
       }
       __syncthreads();
       if (part_of > 0) continue;
@@ -374,10 +369,11 @@ __global__ void __launch_bounds__(MAXW * 32, 1) head_kernel(const HeadParams p) 
           for (int j = 0; j < 4; ++j) {
             const int64_t v = (tile + t) * 16 + (lane >> 2) + (j >> 1) * 8;
             const int r = n * 8 + 2 * (lane & 3) + (j & 1);
-            float y = acc[t][n][j];
+            auto sum = [&](int i) { return (j & 1) ? acc[t][i][j >> 1].y : acc[t][i][j >> 1].x; };
+            float y = sum(n);
             if (NT % 3 == 0 && p.terms == 3) {   // smallest terms first
               constexpr int TT = NT / 3;
-              if (n < TT) y += acc[t][(n + TT) % NT][j] + acc[t][(n + 2 * TT) % NT][j];
+              if (n < TT) y += sum((n + TT) % NT) + sum((n + 2 * TT) % NT);
             }
             if (r < rows && v < s.V) {
               const int64_t at = (p.m0 + r) * p.ld + v;
