@@ -105,6 +105,13 @@ __device__ __forceinline__ bool mbar_wait_bounded(void* bar, uint32_t parity, lo
   }
 }
 
+// First statement of a kernel whose launch may overlap the stream's previous one (launch_1d in vsamp_grid.h): waits until
+// that kernel has finished and its writes are visible, then lets the next such launch be set up.
+__device__ __forceinline__ void begin_overlapped() {
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+}
+
 // Cluster-wide barrier of all threads that publishes this thread's earlier shared-memory writes to the
 // peers (a release restricted to shared memory, so stores to global memory still in flight are not
 // waited for) and acquires theirs. It also synchronises the threads of this CTA.

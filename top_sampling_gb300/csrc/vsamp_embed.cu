@@ -31,7 +31,7 @@ static vsamp_status launch_embed_ve(const EmbedParams& p, cudaStream_t s) {
   int tx = 1;   // threads along a row
   while (tx < kEmbedThreads && tx * kEmbedUnroll < nv) tx *= 2;
   const int64_t spans = ceil_div(nv, (int64_t)tx * kEmbedUnroll), rows = ceil_div(p.N, kEmbedThreads / tx);
-  return launch_1d(embed_kernel<TI, TO, VE>, grid_of(rows * spans), kEmbedThreads, 0, s, false, p, tx, (int)spans);
+  return launch_1d(embed_kernel<TI, TO, VE>, grid_of(rows * spans), kEmbedThreads, 0, s, p, tx, (int)spans);
 }
 
 template <typename TI, typename TO>
@@ -64,18 +64,18 @@ static vsamp_status launch_embed_sums(const EmbedGradParams& p, int last, const 
   const int64_t spans = ceil_div(ceil_div(p.D, VE), kEmbedThreads);
   const vsamp_status st = launch_1d(p.aligned && p.D % VE == 0 ? embed_sum_kernel<TI, TO, VE, true>
                                                                : embed_sum_kernel<TI, TO, VE, false>,
-                                    grid_of(p.sums * spans), kEmbedThreads, 0, s, true, p, last, (int)spans);
+                                    grid_of(p.sums * spans), kEmbedThreads, 0, s, p, last, (int)spans);
   if (st != VSAMP_OK) return st;
   const int64_t jspans = ceil_div(p.D, kJoinSpan);
   const int64_t most = p.sums * jspans, resident = (int64_t)d.sm_count * 8;   // the list's length is not known here
-  return launch_1d(embed_join_kernel<TO>, grid_of(most < resident ? most : resident), kEmbedThreads, 0, s, true, p,
+  return launch_1d(embed_join_kernel<TO>, grid_of(most < resident ? most : resident), kEmbedThreads, 0, s, p,
                    last, (int)jspans);
 }
 
 template <typename TI, typename TO, int VE>
 static vsamp_status launch_embed_few(const EmbedGradParams& p, cudaStream_t s) {
   const int64_t spans = ceil_div(ceil_div(p.D, VE), kEmbedThreads);
-  return launch_1d(embed_few_kernel<TI, TO, VE>, grid_of(p.N * spans), kEmbedThreads, 0, s, false, p, (int)spans);
+  return launch_1d(embed_few_kernel<TI, TO, VE>, grid_of(p.N * spans), kEmbedThreads, 0, s, p, (int)spans);
 }
 
 template <typename TI, typename TO>
@@ -88,7 +88,7 @@ static vsamp_status launch_embed_grad(EmbedGradParams p, const DeviceInfo& d, in
   const int64_t zero_warps = z.nrows < (int64_t)d.sm_count * 64 ? z.nrows : (int64_t)d.sm_count * 64;
   if (p.N <= kEmbedFew) {
     if (z.nrows > 0) {
-      st = launch_1d(embed_zero_kernel, grid_of(ceil_div(zero_warps, kEmbedThreads / 32)), kEmbedThreads, 0, s, false, z);
+      st = launch_1d(embed_zero_kernel, grid_of(ceil_div(zero_warps, kEmbedThreads / 32)), kEmbedThreads, 0, s, z);
       if (st != VSAMP_OK) return st;
     }
     return launch_embed_few<TI, TO, VE>(p, s);
@@ -109,19 +109,19 @@ static vsamp_status launch_embed_grad(EmbedGradParams p, const DeviceInfo& d, in
     const int64_t most = 2 * (int64_t)d.sm_count - 1;   // two CTAs fit an SM
     const int passes = (int)ceil_div(token_bits, 9), digit_bits = (int)ceil_div(token_bits, passes);
     st = launch_1d(embed_sort_one_kernel, grid_of(1 + (zero_ctas < most ? zero_ctas : most)), kSortOneThreads,
-                   (size_t)smem, s, false, p, z, pos_bits, digit_bits, passes);
+                   (size_t)smem, s, p, z, pos_bits, digit_bits, passes);
     if (st != VSAMP_OK) return st;
   } else {
     if (z.nrows > 0) {
-      st = launch_1d(embed_zero_kernel, grid_of(ceil_div(zero_warps, kEmbedThreads / 32)), kEmbedThreads, 0, s, false, z);
+      st = launch_1d(embed_zero_kernel, grid_of(ceil_div(zero_warps, kEmbedThreads / 32)), kEmbedThreads, 0, s, z);
       if (st != VSAMP_OK) return st;
     }
     // the marker's low bits are larger than any token's: V itself fits token_bits
     const int passes = (int)ceil_div(token_bits, kSortBits);
     for (int k = 0; k < passes; ++k) {
-      st = launch_1d(embed_hist_kernel, grid_of(p.tiles), kSortThreads, 0, s, false, p, k);
+      st = launch_1d(embed_hist_kernel, grid_of(p.tiles), kSortThreads, 0, s, p, k);
       if (st != VSAMP_OK) return st;
-      st = launch_1d(embed_scatter_kernel, grid_of(p.tiles), kSortThreads, 0, s, false, p, k);
+      st = launch_1d(embed_scatter_kernel, grid_of(p.tiles), kSortThreads, 0, s, p, k);
       if (st != VSAMP_OK) return st;
     }
     last = (passes - 1) & 1;

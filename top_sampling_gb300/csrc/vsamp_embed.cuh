@@ -68,6 +68,7 @@ constexpr int kEmbedUnroll = 4;
 template <typename TI, typename TO, int VE>
 __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams p, int tx, int spans) {
   constexpr int U = kEmbedUnroll;
+  begin_overlapped();
   const int col = threadIdx.x & (tx - 1), per = kEmbedThreads / tx;
   const int64_t total = (p.N + per - 1) / per * spans;
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
@@ -114,6 +115,7 @@ __device__ __forceinline__ uint2 embed_key(const EmbedGradParams& p, int pass, i
 
 __global__ void __launch_bounds__(kSortThreads) embed_hist_kernel(const EmbedGradParams p, int pass) {
   __shared__ uint32_t hist[kSortBins];
+  begin_overlapped();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.n_runs = 0;
   for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
     for (int i = threadIdx.x; i < kSortBins; i += kSortThreads) hist[i] = 0;
@@ -136,6 +138,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const Embed
   __shared__ uint32_t count[NW][kSortBins];   // keys of each digit in every warp's part of the tile
   __shared__ uint32_t wsum[kSortBins / 32];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  begin_overlapped();
   for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
     uint32_t all = 0, earlier = 0;
     if (t < kSortBins) {
@@ -227,6 +230,7 @@ __device__ __forceinline__ void zero_ranges(const ZeroParams& z, int64_t warp, i
 }
 
 __global__ void __launch_bounds__(kEmbedThreads) embed_zero_kernel(const ZeroParams z) {
+  begin_overlapped();
   zero_ranges(z, (int64_t)blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5), (int64_t)gridDim.x * (kEmbedThreads / 32));
 }
 
@@ -246,7 +250,7 @@ struct SortOneSmem {
 
 __global__ void __launch_bounds__(kSortOneThreads) embed_sort_one_kernel(const EmbedGradParams p, const ZeroParams z,
                                                                          int pos_bits, int digit_bits, int passes) {
-  cudaTriggerProgrammaticLaunchCompletion();   // the sums may be set up meanwhile
+  begin_overlapped();
   if (blockIdx.x > 0) {
     zero_ranges(z, (int64_t)(blockIdx.x - 1) * (kSortOneThreads / 32) + (threadIdx.x >> 5),
                 (int64_t)(gridDim.x - 1) * (kSortOneThreads / 32));
@@ -387,6 +391,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const EmbedGra
   __shared__ uint32_t bits[kEmbedFew / 32];
   __shared__ uint16_t list[kEmbedFew];
   __shared__ int count;
+  begin_overlapped();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n0 = (int)(blockIdx.x / spans), N = (int)p.N;
   const int32_t tok = p.token[n0];
@@ -429,8 +434,7 @@ constexpr int kSumBatch = 8;
 template <typename TI, typename TO, int VE, bool WHOLE>
 __global__ void __launch_bounds__(kEmbedThreads, 3) embed_sum_kernel(const EmbedGradParams p, int last, int spans) {
   const uint2* keys = p.keys[last];
-  cudaGridDependencySynchronize();             // the sorted keys, and the zeros that these sums replace
-  cudaTriggerProgrammaticLaunchCompletion();   // the join may be set up meanwhile
+  begin_overlapped();
   for (int64_t id = blockIdx.x; id < p.sums * spans; id += gridDim.x) {
     const int64_t tile = spans == 1 ? id : id / spans;
     const int64_t span = id - tile * spans, c = (span * kEmbedThreads + threadIdx.x) * VE;
@@ -506,7 +510,7 @@ constexpr int kJoinBatch = 16;
 template <typename TO>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(const EmbedGradParams p, int last, int spans) {
   const uint2* keys = p.keys[last];
-  cudaGridDependencySynchronize();   // the tiles' parts and the list
+  begin_overlapped();
   const int64_t total = (int64_t)*p.n_runs * spans;
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
     const int64_t run = id / spans, tile = p.runs[run];

@@ -11,11 +11,11 @@ namespace vsamp {
 // CTAs of a launch over n blocks of work; the kernels stride over what is beyond it.
 inline unsigned grid_of(int64_t n) { return (unsigned)(n < 0x3FFFFFFFLL ? n : 0x3FFFFFFFLL); }
 
-// `overlap`: the launch may begin while the stream's previous kernel drains (the kernel itself waits for that
-// kernel's writes with cudaGridDependencySynchronize before it touches memory).
+// A launch that may be set up while the stream's previous kernel drains; the kernel begins with begin_overlapped(), which
+// waits for that kernel's writes before any memory is touched. Back-to-back calls save about a microsecond each.
 template <typename... KArgs, typename... Args>
 vsamp_status launch_1d(void (*kern)(KArgs...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
-                       bool overlap, Args... args) {
+                       Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
@@ -25,7 +25,7 @@ vsamp_status launch_1d(void (*kern)(KArgs...), unsigned grid, unsigned threads, 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = overlap ? 1 : 0;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
     cudaGetLastError();
     return VSAMP_ERR_CUDA;

@@ -6,6 +6,7 @@ namespace vsamp {
 
 // One thread per 32-bit word of codes, then per scale and zero point.
 __global__ void __launch_bounds__(256) head_pack_kernel(const HeadPackParams p) {
+  begin_overlapped();
   const HeadShape s = p.s;
   const int64_t nb = s.blocks(), ng = s.groups(), per_unit = kHeadUnit / s.group;
   const int64_t words = s.tiles() * nb * 128, scales = s.tiles() * ng * 16;
@@ -98,7 +99,7 @@ vsamp_status vsamp_head_pack(const uint8_t* codes, const void* scales, vsamp_dty
   p.zeros = zeros;
   p.packed = static_cast<unsigned char*>(packed);
   return launch_1d(head_pack_kernel, grid_of((s.tiles() * s.blocks() * 128 + 1023) / 1024), 256, 0,
-                   static_cast<cudaStream_t>(stream), false, p);
+                   static_cast<cudaStream_t>(stream), p);
 }
 
 vsamp_status vsamp_head_logits(const void* hidden, vsamp_dtype dt, int64_t M, int64_t ldh, const void* packed,

@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(MAXW * 32, 1) head_kernel(const HeadParams p) 
   constexpr int GS = GROUP / 16;          // steps per group
   constexpr int NG = kHeadUnit / GROUP;   // groups per unit
   extern __shared__ __align__(128) unsigned char head_smem[];
+  begin_overlapped();
   const HeadShape s = p.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int GB = 16 * (SB + (ZEROS ? 1 : 0));         // bytes of a group's scales and zero points

@@ -47,7 +47,7 @@ static vsamp_status launch_head_cfg(HeadParams p, const DeviceInfo& d, int dev, 
     if (dev < 64) raised[dev].store(true, std::memory_order_release);
   }
   const int64_t ctas = (sets * p.split + warps - 1) / warps;
-  return launch_1d(kern, grid_of(ctas < sms ? ctas : sms), (unsigned)warps * 32, (size_t)smem, stream, false, p);
+  return launch_1d(kern, grid_of(ctas < sms ? ctas : sms), (unsigned)warps * 32, (size_t)smem, stream, p);
 }
 
 template <int NT, int RT, int GROUP, int PF, int MAXW>

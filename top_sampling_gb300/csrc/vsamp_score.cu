@@ -14,17 +14,17 @@ static vsamp_status launch_score(const ScoreParams& p, cudaStream_t s) {
   const unsigned grid = grid_of((p.B * p.np + kScoreWarps - 1) / kScoreWarps);
   const vsamp_status st =
       launch_1d(p.N > 0 ? score_piece_kernel<T, true> : score_piece_kernel<T, false>, grid, kScoreWarps * 32, 0, s,
-                false, p);
+                p);
   if (st != VSAMP_OK) return st;
-  if (p.N > 0) return launch_1d(score_finish_alt_kernel<T>, grid_of(p.B), kScoreFinishThreads, 0, s, true, p);
-  return launch_1d(score_finish_kernel<T>, grid_of((p.B + 3) / 4), 128, 0, s, true, p);
+  if (p.N > 0) return launch_1d(score_finish_alt_kernel<T>, grid_of(p.B), kScoreFinishThreads, 0, s, p);
+  return launch_1d(score_finish_kernel<T>, grid_of((p.B + 3) / 4), 128, 0, s, p);
 }
 
 template <typename T>
 static vsamp_status launch_score_grad(ScoreGradParams p, cudaStream_t s) {
   constexpr int64_t SPAN = (int64_t)kGradThreads * kGradVecs * ScoreType<T>::VE;
   p.spans = (p.V + SPAN - 1) / SPAN;   // covers the whole vectors wherever they begin
-  return launch_1d(score_grad_kernel<T>, grid_of(p.B * p.spans), kGradThreads, 0, s, false, p);
+  return launch_1d(score_grad_kernel<T>, grid_of(p.B * p.spans), kGradThreads, 0, s, p);
 }
 
 static vsamp_status score_check(const void* logits, vsamp_dtype dt, int64_t B, int64_t V, int64_t ld) {

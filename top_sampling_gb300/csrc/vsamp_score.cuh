@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const 
   constexpr int PE = kScorePiece / Ty::ES;      // elements per piece
   constexpr int CE = PE / kScoreChunks;         // elements per chunk
   const int lane = threadIdx.x & 31;
-  cudaTriggerProgrammaticLaunchCompletion();   // the finish may be set up while the last pieces run
+  begin_overlapped();
   const uint32_t id = blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
   const uint32_t row = p.np > 1 ? __umulhi(id, p.np_mul) >> p.np_shift : id;
   if (row >= (uint32_t)p.B) return;
@@ -407,7 +407,7 @@ __device__ __forceinline__ void score_write(const ScoreParams& p, int64_t row, i
 // No alternatives: one warp per row.
 template <typename T>
 __global__ void __launch_bounds__(128) score_finish_kernel(const ScoreParams p) {
-  cudaGridDependencySynchronize();   // every piece record is written
+  begin_overlapped();
   for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); row < p.B; row += (int64_t)gridDim.x * 4) {
     ScoreFold fold;
     fold.load(p, row);
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(c
   // threads per group: a few groups for every alternative
   const int gs = p.N <= NT / 16 ? 8 : p.N <= NT / 8 ? 4 : p.N <= NT / 4 ? 2 : 1;
   const int groups = NT / gs;
-  cudaGridDependencySynchronize();   // every piece record is written
+  begin_overlapped();
   for (int64_t row = blockIdx.x; row < p.B; row += gridDim.x) {
     // what the row needs first is read at once: the first chunk maxima of every thread, the last warp's records
     const int64_t nch = (int64_t)p.np * kScoreChunks;
@@ -684,6 +684,7 @@ __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGra
   using Ty = ScoreType<T>;
   constexpr int VE = Ty::VE;
   constexpr int64_t SPAN = (int64_t)kGradThreads * kGradVecs;   // vectors
+  begin_overlapped();
   const int64_t total = p.B * p.spans;
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
     const int64_t row = id / p.spans, span = id - row * p.spans;
