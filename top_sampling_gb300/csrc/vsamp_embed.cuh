@@ -61,8 +61,8 @@ struct EmbedGradParams {
 
 constexpr int kEmbedThreads = 256;
 
-// tx threads of a CTA along a row (a power of two), kEmbedThreads / tx rows per CTA, U vectors per thread and row so
-// that their loads are in flight together.
+// tx threads of a CTA along a row (a power of two), kEmbedThreads / tx rows per CTA, kEmbedUnroll vectors per thread and
+// row so that their loads are in flight together (two: 43 us, four: 35 us for 16384 x 4096 bf16, 82% of the copy rate).
 constexpr int kEmbedUnroll = 4;
 
 template <typename TI, typename TO, int VE>
@@ -238,6 +238,8 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_zero_kernel(const ZeroPar
 // A key is token << pos_bits | position: 32 bits hold both, the marker token V included. Least significant digit
 // first, stable: a warp takes consecutive keys 32 at a time, equal digits keep their order. A thread's keys and their
 // places among equal digits of its warp stay in registers between the count and the move, so one buffer is enough.
+// 16384 positions take about 30 us in one CTA, bound by the warp matches; beside the zeros of a large table (1.2 GB, 186
+// us) they cost nothing.
 constexpr int kSortOne = 16384;
 constexpr int kSortOneThreads = 1024;
 constexpr int kSortOnePer = kSortOne / kSortOneThreads;
@@ -383,7 +385,9 @@ __device__ __forceinline__ void put_row(const EmbedGradParams& p, bool whole, ui
   else v.store_row(at, p.D - c, p.aligned);
 }
 
-// Few positions (N <= kEmbedFew): a CTA per position and span of columns, no workspace.
+// Few positions (N <= kEmbedFew): a CTA per position and span of columns, no workspace. Every CTA compares its token
+// with all of them (4 KB at most, from L2), which is cheaper than a sort's launches: 509 positions of 1001 fp32 columns
+// take 7 us against 29 with the sort. Beyond about a thousand the comparisons and the longest run's chain grow.
 constexpr int kEmbedFew = 1024;
 
 template <typename TI, typename TO, int VE>
@@ -428,7 +432,8 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_few_kernel(const EmbedGra
 
 // Sums of one tile of kEmbedTile sorted positions: a CTA per tile and span of columns. A tile is read in two halves:
 // eight rows in flight per thread and three CTAs per SM (all sixteen at once held 174 registers, one CTA per SM, and
-// took twice the time).
+// took twice the time). 16384 x 4096 bf16: 35 us for 190 MB read and written. Writing part of the zeros from this launch
+// instead, beside the sums, was slower at every split (264 us and more for the whole gradient against 235).
 constexpr int kSumBatch = 8;
 
 template <typename TI, typename TO, int VE, bool WHOLE>
@@ -503,7 +508,8 @@ __device__ __forceinline__ int64_t run_tiles(const uint2* keys, int64_t tile, in
   return lo - tile;
 }
 
-// Runs over several tiles, from the list that the sums left: a CTA per run and kJoinSpan columns, four per thread, adds
+// Runs over several tiles, from the list that the sums left (a fixed grid: the list's length is only known on the device):
+// a CTA per run and kJoinSpan columns, four per thread, adds
 // the run's parts in tile order, kJoinBatch in flight.
 constexpr int kJoinBatch = 16;
 

@@ -5,9 +5,15 @@
 // the tens: a few rows of hidden states against the whole vocabulary. So the kernel is a stream over the weights
 // that feeds the warp-level matrix instruction straight from registers: q - z is at most 15 in magnitude, exact in
 // bf16, products with bf16 hidden states are exact, sums are fp32, and the group's scale multiplies the fp32 sum of
-// its group. (Weights widened through shared or tensor memory for tcgen05 would cost four times their bytes of
-// on-chip traffic for a product that has at most 64 columns.) fp32 hidden states are split into three bf16 terms,
-// multiplied one after the other.
+// its group. fp32 hidden states are split into three bf16 terms, each a column of its own.
+//
+// What bounds it. M = 1: the bytes (151936 x 4096, groups of 128: 54.9 us, 88% of the copy rate). From about eight rows
+// on the issue slots: widening costs 11 instructions per eight weights and lane, a product of eight columns about four
+// slots and eight cycles of its unit (measured alone: 8.1 cycles; beside 12 independent multiply-adds 16.4), so 24 rows
+// take 70 us where the bytes take 37 (151936 x 2560, groups of 32).
+// Tried instead for many rows: tcgen05 with the scale folded into the weights as two exact bf16 terms in tensor memory,
+// so that one accumulator runs over all groups. 24 rows took 117 us (one block of 64 in flight per 128 rows), 64 rows
+// of 50000 x 4096 107 us against 127, and the long accumulation cost digits (3.5e-6 of the result against 1.6e-7).
 //
 // Packed layout. Vocabulary rows in tiles of 16, the inner dimension in units of 128 (two blocks of 64): the record of
 // a tile and unit is contiguous, so a warp streams its tile's records in order. A record holds, for each of its one
@@ -102,12 +108,11 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
 }
 
 // Stages the hidden states of units [u0, u1) as the instruction's second operand, NT column tiles of 8. In step k, lane
-// l needs column 8 n + l/4 at inner positions 2 (l%4) + {0, 1} and + 8; they are stored as [two
-// steps][8 NT columns][l%4], four registers each (the two of both steps), so a lane reads two steps at once and the
-// reads have constant offsets. A
-// bf16 row is a column; an fp32 row is three (x = hi + mid + lo, each the bf16 nearest to what is left: 24 bits in
-// all), in column tiles of their own, so that one lane holds the sums of all three. Positions beyond D are 0; columns
-// without a row are not written (their part of the product is not used).
+// l needs column 8 n + l/4 at inner positions 2 (l%4) + {0, 1} and + 8; they are stored as
+// [two steps][8 NT columns][l%4], four registers each (the two of both steps), so a lane reads two steps at once and the
+// reads have constant offsets. A bf16 row is a column; an fp32 row is three (x = hi + mid + lo, each the bf16 nearest to
+// what is left: 24 bits in all), in column tiles of their own, so that one lane holds the sums of all three. Positions
+// beyond D are 0; columns without a row are not written (their part of the product is not used).
 template <int NT>
 __device__ __forceinline__ void head_stage(const HeadParams& p, uint4* sh, int u0, int u1) {
   const int rows = p.rows, steps = (u1 - u0) * kHeadUnitSteps, n = steps * rows;
@@ -166,9 +171,10 @@ __device__ __forceinline__ void copy_async_wait() {
 }
 
 // RT tiles of 16 vocabulary rows per warp, NT tiles of 8 columns (hidden rows, or their terms), groups of GROUP, scales
-// of SB bytes. Every warp streams the records of its row tiles
-// through a ring of PF slots in shared memory (PF records of each tile in flight, no registers held by loads), across
-// the ends of tiles. p.split warps of a CTA share a set of row tiles, each with a contiguous part of its units.
+// of SB bytes. Every warp streams the records of its row tiles through a ring of PF slots in shared memory (PF records of
+// each tile in flight, no registers held by loads: with the records in registers the loop spilled), across the ends of
+// tiles. Several row tiles per warp share the reads of the staged states and hide each other's latency. p.split warps
+// of a CTA share a set of row tiles, each with a contiguous part of its units.
 template <int NT, int RT, int GROUP, int SB, bool ZEROS, int PF, int MAXW>
 __global__ void __launch_bounds__(MAXW * 32, 1) head_kernel(const HeadParams p) {
   static_assert((PF & (PF - 1)) == 0, "slots are taken in turn by masking");
