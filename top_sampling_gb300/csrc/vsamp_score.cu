@@ -1,5 +1,6 @@
 // vsamp_score_tokens and vsamp_score_tokens_backward: argument checks and launches.
 #include "vsamp_grid.h"
+#include "vsamp_host.h"
 #include "vsamp_score.cuh"
 
 namespace vsamp {
@@ -10,7 +11,15 @@ static int64_t score_pieces(vsamp_dtype dt, int64_t V) {
 }
 
 template <typename T>
-static vsamp_status launch_score(const ScoreParams& p, cudaStream_t s) {
+static vsamp_status launch_score(const ScoreParams& p, const DeviceInfo& d, cudaStream_t s) {
+  // One launch where a cluster's warps take a piece each and the pieces fill the device once at most: it saves a launch
+  // (64 rows of 32000 fp32 with 20 alternatives: 7.4 against 8.2 us, and less host time); beyond, the finish of a row
+  // holds up its cluster's place (256 rows: 15.9 against 12.4 us; 256 of 151936 bf16, two pieces a warp: 30 against 26).
+  if (p.np <= 8 * kScoreWarps && p.B * p.np <= 16 * (int64_t)d.sm_count) {
+    const int C = (p.np + kScoreWarps - 1) / kScoreWarps;
+    return launch_clusters(p.N > 0 ? score_row_kernel<T, true> : score_row_kernel<T, false>, (unsigned)(p.B * C),
+                           (unsigned)C, kScoreWarps * 32, (size_t)p.np * (p.N > 0 ? 48 : 16), s, p);
+  }
   const unsigned grid = grid_of((p.B * p.np + kScoreWarps - 1) / kScoreWarps);
   const vsamp_status st =
       launch_1d(p.N > 0 ? score_piece_kernel<T, true> : score_piece_kernel<T, false>, grid, kScoreWarps * 32, 0, s,
@@ -91,7 +100,15 @@ vsamp_status vsamp_score_tokens(const void* logits, vsamp_dtype dt, int64_t B, i
   p.row_logsum = row_logsum;
   p.row_status = row_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return dt == VSAMP_F32 ? launch_score<float>(p, s) : launch_score<__nv_bfloat16>(p, s);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return VSAMP_ERR_CUDA;
+  }
+  DeviceInfo d;
+  st = device_info(dev, d);
+  if (st != VSAMP_OK) return st;
+  return dt == VSAMP_F32 ? launch_score<float>(p, d, s) : launch_score<__nv_bfloat16>(p, d, s);
 }
 
 vsamp_status vsamp_score_tokens_backward(const void* logits, vsamp_dtype dt, int64_t B, int64_t V, int64_t ld,

@@ -231,24 +231,15 @@ __device__ __forceinline__ void score_sums(const uint32_t (&w)[kScoreChunks][4],
   A = (A2[0].x + A2[1].x) + (A2[0].y + A2[1].y);
 }
 
-// One warp per piece, the piece in registers: 32 warps per SM hold 128 KB of loads in flight. About six instructions per
-// bf16 element beside the exponential. 2048 x 151936 bf16, a quarter of the rows ignored: 80.6 us with the finish, 87%
-// of the copy rate; small batches are bound by the two launches and their first loads (256 rows: 25 us with 20
-// alternatives where the bytes take 12; 4 rows of 32000: 7.4 us). A persistent form that copies the next piece to shared
-// memory meanwhile ran 15% more instructions and was slower (108 against 91 us at the time).
+// One warp, one piece of a row: its record, and the maxima of its chunks. The piece is held in registers.
 template <typename T, bool ALT>
-__global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const ScoreParams p) {
+__device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, int piece, int32_t t, float4* rec,
+                                            float* chunk_max) {
   using Ty = ScoreType<T>;
   constexpr int PE = kScorePiece / Ty::ES;      // elements per piece
   constexpr int CE = PE / kScoreChunks;         // elements per chunk
   const int lane = threadIdx.x & 31;
-  begin_overlapped();
-  const uint32_t id = blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
-  const uint32_t row = p.np > 1 ? __umulhi(id, p.np_mul) >> p.np_shift : id;
-  if (row >= (uint32_t)p.B) return;
-  const int32_t e0 = (int32_t)(id - row * (uint32_t)p.np) * PE;
-  const int32_t t = p.token[row];
-  if (t == VSAMP_TOKEN_IGNORE) return;
+  const int32_t e0 = piece * PE;
   const int32_t V = (int32_t)p.V;
   const unsigned char* xr = p.x + (int64_t)row * p.ld * Ty::ES;
   uint32_t w[kScoreChunks][4];
@@ -278,7 +269,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const 
       if (lane == i) mine = cm;
       m = max_nan(m, cm);
     }
-    if (lane < kScoreChunks) p.chunk_max[(int64_t)id * kScoreChunks + lane] = mine;
+    if (lane < kScoreChunks) chunk_max[lane] = mine;
   } else {
     uint32_t a = max_word<T>(w[0][0], w[0][1]), b = max_word<T>(w[0][2], w[0][3]);
 #pragma unroll
@@ -317,7 +308,24 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const 
   }
   S = warp_sum_f(S);
   A = warp_sum_f(A);
-  if (lane == 0) p.rec[id] = make_float4(m, S, A, __uint_as_float(before));
+  if (lane == 0) *rec = make_float4(m, S, A, __uint_as_float(before));
+}
+
+// One warp per piece, the piece in registers: 32 warps per SM hold 128 KB of loads in flight. About six instructions per
+// bf16 element beside the exponential. 2048 x 151936 bf16, a quarter of the rows ignored: 80.6 us with the finish, 87%
+// of the copy rate; small batches are bound by the two launches and their first loads (256 rows: 25 us with 20
+// alternatives where the bytes take 12; 4 rows of 32000: 7.4 us). A persistent form that copies the next piece to shared
+// memory meanwhile ran 15% more instructions and was slower (108 against 91 us at the time).
+template <typename T, bool ALT>
+__global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const ScoreParams p) {
+  begin_overlapped();
+  const uint32_t id = blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
+  const uint32_t row = p.np > 1 ? __umulhi(id, p.np_mul) >> p.np_shift : id;
+  if (row >= (uint32_t)p.B) return;
+  const int32_t t = p.token[row];
+  if (t == VSAMP_TOKEN_IGNORE) return;
+  score_piece<T, ALT>(p, row, (int)(id - row * (uint32_t)p.np), t, p.rec + id,
+                      ALT ? p.chunk_max + (int64_t)id * kScoreChunks : nullptr);
 }
 
 struct ScoreRow {
@@ -331,9 +339,11 @@ struct ScoreRow {
 // read at once and kept; `load` may run before the row's token is known.
 constexpr int kFoldKeep = 4;
 struct ScoreFold {
+  const float4* all;
   float4 rec[kFoldKeep];
-  __device__ __forceinline__ void load(const ScoreParams& p, int64_t row) {
-    const float4* r = p.rec + row * p.np;
+  // the row's records, in global or shared memory
+  __device__ __forceinline__ void load(const ScoreParams& p, const float4* r) {
+    all = r;
 #pragma unroll
     for (int i = 0; i < kFoldKeep; ++i) {
       const int k = i * 32 + (int)(threadIdx.x & 31);
@@ -341,10 +351,10 @@ struct ScoreFold {
     }
   }
   template <typename F>
-  __device__ __forceinline__ void each(const ScoreParams& p, int64_t row, F f) const {
+  __device__ __forceinline__ void each(const ScoreParams& p, F f) const {
 #pragma unroll
     for (int i = 0; i < kFoldKeep; ++i) f(rec[i]);
-    for (int k = kFoldKeep * 32 + (int)(threadIdx.x & 31); k < p.np; k += 32) f(p.rec[row * p.np + k]);
+    for (int k = kFoldKeep * 32 + (int)(threadIdx.x & 31); k < p.np; k += 32) f(all[k]);
   }
   __device__ __forceinline__ ScoreRow row(const ScoreParams& p, int64_t at, int32_t t) const {
     const float temp = p.temperature ? p.temperature[at] : 1.f;
@@ -352,13 +362,13 @@ struct ScoreFold {
     const float T1 = temp > 0.f ? temp : 1.f, c = p.temperature ? kLog2e / T1 : kLog2e;   // as for the pieces
     r.invT = 1.f / T1;
     float m = -INFINITY;
-    each(p, at, [&](float4 q) { m = max_nan(m, q.x); });
+    each(p, [&](float4 q) { m = max_nan(m, q.x); });
     m = warp_max_nan(m);
     float S = 0.f, A = 0.f;
     uint32_t before = 0;
     const bool finite = m > -INFINITY && m < INFINITY;
     if (finite) {
-      each(p, at, [&](float4 q) {
+      each(p, [&](float4 q) {
         before += __float_as_uint(q.w);
         if (q.x > -INFINITY) {
           const float d = fmaxf((q.x - m) * c, -150.f);
@@ -413,7 +423,7 @@ __global__ void __launch_bounds__(128) score_finish_kernel(const ScoreParams p) 
   begin_overlapped();
   for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5); row < p.B; row += (int64_t)gridDim.x * 4) {
     ScoreFold fold;
-    fold.load(p, row);
+    fold.load(p, p.rec + row * p.np);
     const int32_t t = p.token[row];
     const float xt = score_logit<T>(p, row, t);
     ScoreRow r{};
@@ -479,163 +489,231 @@ __device__ uint64_t score_radix_select(F for_each, uint32_t want, uint32_t* hist
 //      chunks reach, so every alternative does;
 //   2. the chunks at or above the bound are listed (their number is close to N; an arrangement that lists many more
 //      is cut to the N that the lemma above needs by a radix search);
-//   3. the tokens of the listed chunks at or above the bound are listed, again close to N of them (more than the list
-//      holds: the last alternative is found by radix search), and each one's place is the number of larger ones.
+//   3. the tokens of the listed chunks at or above the bound are listed, again close to N of them (if they are more than
+//      the list holds, above a bound from every thread's largest token, and failing that by a radix search for the last
+//      alternative), and each one's place is the number of larger ones.
 // Keys are (value, index) pairs in the order's sense, all different. Bound by latency: a chain of about eight dependent
 // steps, 5 to 6 us beside the pieces' kernel, whatever N (20 alternatives of 256 rows: 25.5 us against 20.3 without).
+struct ScoreAltSmem {
+  __align__(16) uint64_t list[kScoreList];
+  __align__(16) uint64_t best[kScoreFinishThreads];
+  uint32_t hist[256];
+  uint32_t bc[3];
+  int32_t chunks[kScoreChunkList];
+  uint32_t n_chunks, n_list;
+  uint64_t bound;
+  ScoreRow row;
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(const ScoreParams p) {
+__device__ __forceinline__ void score_finish_alt(const ScoreParams& p, int64_t row, int32_t t, const float4* rec,
+                                                 const float* cm, ScoreAltSmem& sm) {
   using Ty = ScoreType<T>;
   constexpr int CE = kScorePiece / Ty::ES / kScoreChunks;
   constexpr int NT = kScoreFinishThreads, NW = NT / 32;
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t bc[3];
-  __shared__ __align__(16) uint64_t list[kScoreList];
-  __shared__ __align__(16) uint64_t best[NT];
-  __shared__ int32_t chunks[kScoreChunkList];
-  __shared__ uint32_t n_chunks, n_list;
-  __shared__ uint64_t bound;
-  __shared__ ScoreRow shared_row;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float qnan = __int_as_float(0x7FC00000);
   constexpr uint32_t kNone = 0x007FFFFFu;   // key of -inf
-  // threads per group: a few groups for every alternative
-  const int gs = p.N <= NT / 16 ? 8 : p.N <= NT / 8 ? 4 : p.N <= NT / 4 ? 2 : 1;
-  const int groups = NT / gs;
-  begin_overlapped();
-  for (int64_t row = blockIdx.x; row < p.B; row += gridDim.x) {
-    // what the row needs first is read at once: the first chunk maxima of every thread, the last warp's records
-    const int64_t nch = (int64_t)p.np * kScoreChunks;
-    const float* cm = p.chunk_max + row * nch;
-    float kept[kKeep];
+  // threads per group: as many as leave three groups with chunks for every alternative, eight at most
+  const int holders = p.np * kScoreChunks < NT ? p.np * kScoreChunks : NT;
+  const int gs = holders >= 24 * p.N ? 8 : holders >= 12 * p.N ? 4 : holders >= 6 * p.N ? 2 : 1;
+  const int groups = (holders + gs - 1) / gs;
+  // what the row needs first is read at once: the first chunk maxima of every thread, the last warp's records
+  const int64_t nch = (int64_t)p.np * kScoreChunks;
+  float kept[kKeep];
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i) kept[i] = i * NT + tid < nch ? cm[i * NT + tid] : -INFINITY;
-    ScoreFold fold;
-    if (warp == NW - 1) fold.load(p, row);
-    const int32_t t = p.token[row];
-    const bool skip = t == VSAMP_TOKEN_IGNORE;
-    int32_t* oi = p.alt_idx + row * p.N;
-    float* ol = p.alt_lp + row * p.N;
-    uint32_t found = 0;
-    if (skip) {
-      if (tid == 0) score_write(p, row, t, 0.f, ScoreRow{});
-    } else {
-      const unsigned char* xr = p.x + row * p.ld * Ty::ES;
-      auto each_chunk = [&](auto f) {
-        auto one = [&](float x, int64_t i) {
-          const uint32_t k = key_f32_bits(__float_as_uint(x));
-          if (k > kNone) f(((uint64_t)k << 32) | (uint32_t)~(uint32_t)i);
-        };
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i) one(kept[i], i * NT + tid);
-#pragma unroll 4
-        for (int64_t i = kKeep * NT + tid; i < nch; i += NT) one(cm[i], i);
+  for (int i = 0; i < kKeep; ++i) kept[i] = i * NT + tid < nch ? cm[i * NT + tid] : -INFINITY;
+  ScoreFold fold;
+  if (warp == NW - 1) fold.load(p, rec);
+  const bool skip = t == VSAMP_TOKEN_IGNORE;
+  int32_t* oi = p.alt_idx + row * p.N;
+  float* ol = p.alt_lp + row * p.N;
+  uint32_t found = 0;
+  if (skip) {
+    if (tid == 0) score_write(p, row, t, 0.f, ScoreRow{});
+  } else {
+    const unsigned char* xr = p.x + row * p.ld * Ty::ES;
+    auto each_chunk = [&](auto f) {
+      auto one = [&](float x, int64_t i) {
+        const uint32_t k = key_f32_bits(__float_as_uint(x));
+        if (k > kNone) f(((uint64_t)k << 32) | (uint32_t)~(uint32_t)i);
       };
-      uint64_t mine = 0;
-      each_chunk([&](uint64_t k) { mine = k > mine ? k : mine; });
-      for (int o = 1; o < gs; o <<= 1) {
-        const uint64_t v = __shfl_xor_sync(kFullMask, mine, o);
-        mine = v > mine ? v : mine;
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) one(kept[i], i * NT + tid);
+#pragma unroll 4
+      for (int64_t i = kKeep * NT + tid; i < nch; i += NT) one(cm[i], i);
+    };
+    uint64_t mine = 0;
+    each_chunk([&](uint64_t k) { mine = k > mine ? k : mine; });
+    for (int o = 1; o < gs; o <<= 1) {
+      const uint64_t v = __shfl_xor_sync(kFullMask, mine, o);
+      mine = v > mine ? v : mine;
+    }
+    if (tid % gs == 0) sm.best[tid / gs] = mine;
+    if (tid == 0) {
+      sm.n_chunks = sm.n_list = 0;
+      sm.bound = 0;
+    }
+    __syncthreads();
+    if (warp == NW - 1) {
+      const float xt = score_logit<T>(p, row, t);
+      const ScoreRow r = fold.row(p, row, t);
+      if (lane == 0) {
+        score_write(p, row, t, xt, r);
+        sm.row = r;
       }
-      if (tid % gs == 0) best[tid / gs] = mine;
-      if (tid == 0) {
-        n_chunks = n_list = 0;
-        bound = 0;
-      }
-      __syncthreads();
-      if (warp == NW - 1) {
-        const float xt = score_logit<T>(p, row, t);
-        const ScoreRow r = fold.row(p, row, t);
-        if (lane == 0) {
-          score_write(p, row, t, xt, r);
-          shared_row = r;
-        }
-      }
-      for (int g = tid; g < groups; g += NT - 32) {   // the first warps: the fold is the last one's
-        if (warp == NW - 1) break;
-        const uint64_t k = best[g];
-        int larger = 0;
+    }
+    for (int g = tid; g < groups; g += NT - 32) {   // the first warps: the fold is the last one's
+      if (warp == NW - 1) break;
+      const uint64_t k = sm.best[g];
+      int larger = 0;
 #pragma unroll 8
-        for (int i = 0; i < groups; ++i) larger += best[i] > k ? 1 : 0;
-        if (larger == p.N - 1 && k > 0) bound = k;     // one group, if that many groups have a token
-      }
-      __syncthreads();
-      uint64_t cut = bound;
-      const ScoreRow r = shared_row;
-      if (r.status == VSAMP_OK) {
-        auto list_chunks = [&]() {
-          each_chunk([&](uint64_t k) {
-            if (k >= cut) {
-              const uint32_t at = atomicAdd(&n_chunks, 1u);
-              if (at < kScoreChunkList) chunks[at] = (int32_t)~(uint32_t)k;
-            }
-          });
-          __syncthreads();
-        };
-        list_chunks();
-        if (n_chunks > 2 * (uint32_t)p.N + 64) {   // far more than N: at least N of them, so the search finds its N-th
-          cut = score_radix_select(each_chunk, (uint32_t)p.N, hist, bc);
-          if (tid == 0) n_chunks = 0;
-          __syncthreads();
-          list_chunks();
-        }
-        const uint32_t nc = n_chunks;
-        const uint32_t lowest = max((uint32_t)(cut >> 32), kNone + 1);
-        auto each_token = [&](auto f) {
-          for (uint32_t i = warp; i < nc; i += 4 * NW) {   // four chunks in flight
-            uint32_t w[4][4];
-            int64_t e[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint32_t at = i + u * NW;
-              e[u] = at < nc ? (int64_t)chunks[at] * CE + lane * Ty::VE : p.V;
-              score_load<T>(xr, e[u], p.V, p.vec, w[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-              for (int j = 0; j < Ty::VE; ++j) {
-                const uint32_t k = key_f32_bits(__float_as_uint(Ty::at(w[u], j)));
-                if (k >= lowest) f(((uint64_t)k << 32) | (uint32_t)~(uint32_t)(e[u] + j));
-              }
+      for (int i = 0; i < groups; ++i) larger += sm.best[i] > k ? 1 : 0;
+      if (larger == p.N - 1 && k > 0) sm.bound = k;     // one group, if that many groups have a token
+    }
+    __syncthreads();
+    uint64_t cut = sm.bound;
+    const ScoreRow r = sm.row;
+    if (r.status == VSAMP_OK) {
+      auto list_chunks = [&]() {
+        each_chunk([&](uint64_t k) {
+          if (k >= cut) {
+            const uint32_t at = atomicAdd(&sm.n_chunks, 1u);
+            if (at < kScoreChunkList) sm.chunks[at] = (int32_t)~(uint32_t)k;
           }
-        };
-        each_token([&](uint64_t k) {
-          const uint32_t at = atomicAdd(&n_list, 1u);
-          if (at < kScoreList) list[at] = k;
         });
         __syncthreads();
-        uint32_t n = n_list;
-        if (n > kScoreList) {
-          // more candidates than the list holds: find the last alternative by radix search, list the N exactly
-          const uint64_t last = score_radix_select(each_token, (uint32_t)p.N, hist, bc);
-          if (tid == 0) n_list = 0;
-          __syncthreads();
-          each_token([&](uint64_t k) {
-            if (k >= last) list[atomicAdd(&n_list, 1u)] = k;
-          });
-          __syncthreads();
-          n = n_list;
-        }
-        found = n < (uint32_t)p.N ? n : (uint32_t)p.N;
-        for (uint32_t i = tid; i < n; i += NT) {
-          const uint64_t k = list[i];
-          uint32_t place = 0;
-#pragma unroll 4
-          for (uint32_t j = 0; j < n; ++j) place += list[j] > k ? 1u : 0u;
-          if (place < (uint32_t)p.N) {
-            oi[place] = (int32_t)~(uint32_t)k;
-            const float s = (value_of_key32((uint32_t)(k >> 32)) - r.m) * r.invT;
-            ol[place] = fminf(s - r.logsum, 0.f);
+      };
+      list_chunks();
+      if (sm.n_chunks > 2 * (uint32_t)p.N + 64) {   // far more than N: at least N of them, so the search finds its N-th
+        cut = score_radix_select(each_chunk, (uint32_t)p.N, sm.hist, sm.bc);
+        if (tid == 0) sm.n_chunks = 0;
+        __syncthreads();
+        list_chunks();
+      }
+      const uint32_t nc = sm.n_chunks;
+      const uint32_t lowest = max((uint32_t)(cut >> 32), kNone + 1);
+      auto each_token = [&](auto f) {
+        for (uint32_t i = warp; i < nc; i += 4 * NW) {   // four sm.chunks in flight
+          uint32_t w[4][4];
+          int64_t e[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t at = i + u * NW;
+            e[u] = at < nc ? (int64_t)sm.chunks[at] * CE + lane * Ty::VE : p.V;
+            score_load<T>(xr, e[u], p.V, p.vec, w[u]);
           }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int j = 0; j < Ty::VE; ++j) {
+              const uint32_t k = key_f32_bits(__float_as_uint(Ty::at(w[u], j)));
+              if (k >= lowest) f(((uint64_t)k << 32) | (uint32_t)~(uint32_t)(e[u] + j));
+            }
+        }
+      };
+      each_token([&](uint64_t k) {
+        const uint32_t at = atomicAdd(&sm.n_list, 1u);
+        if (at < kScoreList) sm.list[at] = k;
+      });
+      __syncthreads();
+      uint32_t n = sm.n_list;
+      if (n > kScoreList) {
+        // too many (a row of few chunks, or of many equal tokens): a bound from every thread's largest token
+        uint64_t top = 0;
+        each_token([&](uint64_t k) { top = k > top ? k : top; });
+        sm.best[tid] = top;
+        if (tid == 0) {
+          sm.bound = 0;
+          sm.n_list = 0;
+        }
+        __syncthreads();
+        int larger = 0;
+#pragma unroll 8
+        for (int i = 0; i < NT; ++i) larger += sm.best[i] > top ? 1 : 0;
+        if (larger == p.N - 1 && top > 0) sm.bound = top;
+        __syncthreads();
+        const uint64_t above = sm.bound;
+        each_token([&](uint64_t k) {
+          if (k >= above) {
+            const uint32_t at = atomicAdd(&sm.n_list, 1u);
+            if (at < kScoreList) sm.list[at] = k;
+          }
+        });
+        __syncthreads();
+        n = sm.n_list;
+      }
+      if (n > kScoreList) {
+        // still more: find the last alternative by radix search, list the N exactly
+        const uint64_t last = score_radix_select(each_token, (uint32_t)p.N, sm.hist, sm.bc);
+        if (tid == 0) sm.n_list = 0;
+        __syncthreads();
+        each_token([&](uint64_t k) {
+          if (k >= last) sm.list[atomicAdd(&sm.n_list, 1u)] = k;
+        });
+        __syncthreads();
+        n = sm.n_list;
+      }
+      found = n < (uint32_t)p.N ? n : (uint32_t)p.N;
+      for (uint32_t i = tid; i < n; i += NT) {
+        const uint64_t k = sm.list[i];
+        uint32_t place = 0;
+#pragma unroll 4
+        for (uint32_t j = 0; j < n; ++j) place += sm.list[j] > k ? 1u : 0u;
+        if (place < (uint32_t)p.N) {
+          oi[place] = (int32_t)~(uint32_t)k;
+          const float s = (value_of_key32((uint32_t)(k >> 32)) - r.m) * r.invT;
+          ol[place] = fminf(s - r.logsum, 0.f);
         }
       }
     }
-    for (uint32_t j = found + tid; j < (uint32_t)p.N; j += NT) {
-      oi[j] = -1;
-      ol[j] = qnan;
-    }
+  }
+  for (uint32_t j = found + tid; j < (uint32_t)p.N; j += NT) {
+    oi[j] = -1;
+    ol[j] = qnan;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(const ScoreParams p) {
+  __shared__ ScoreAltSmem sm;
+  begin_overlapped();
+  for (int64_t row = blockIdx.x; row < p.B; row += gridDim.x) {
+    score_finish_alt<T>(p, row, p.token[row], p.rec + row * p.np, p.chunk_max + row * p.np * kScoreChunks, sm);
     __syncthreads();   // the next row reuses the shared arrays
+  }
+}
+
+// Both steps in one launch: a cluster of CTAs takes a row, its warps write the records of their pieces into the first
+// CTA's shared memory, and that CTA finishes the row while other rows' clusters run their pieces.
+template <typename T, bool ALT>
+__global__ void __launch_bounds__(kScoreWarps * 32, 4) score_row_kernel(const ScoreParams p) {
+  static_assert(kScoreWarps * 32 == kScoreFinishThreads, "the first CTA's threads finish the row");
+  extern __shared__ __align__(16) unsigned char score_smem[];   // first CTA: [np] records, [np, 8] chunk maxima
+  __shared__ ScoreAltSmem sm;
+  begin_overlapped();
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank(), row = blockIdx.x / C;
+  float4* rec = reinterpret_cast<float4*>(score_smem);
+  float* cm = reinterpret_cast<float*>(rec + p.np);
+  const int32_t t = p.token[row];
+  if (t != VSAMP_TOKEN_IGNORE) {
+    float4* rec0 = cluster.map_shared_rank(rec, 0);
+    float* cm0 = cluster.map_shared_rank(cm, 0);
+    for (int piece = rank * kScoreWarps + (threadIdx.x >> 5); piece < p.np; piece += C * kScoreWarps)
+      score_piece<T, ALT>(p, row, piece, t, rec0 + piece, cm0 + piece * kScoreChunks);
+  }
+  cluster.sync();   // every record is in the first CTA
+  if (rank != 0) return;
+  if (ALT) {
+    score_finish_alt<T>(p, row, t, rec, cm, sm);
+  } else if (threadIdx.x < 32) {
+    ScoreFold fold;
+    fold.load(p, rec);
+    const float xt = score_logit<T>(p, row, t);
+    ScoreRow r{};
+    if (t != VSAMP_TOKEN_IGNORE) r = fold.row(p, row, t);
+    if (threadIdx.x == 0) score_write(p, row, t, xt, r);
   }
 }
 
