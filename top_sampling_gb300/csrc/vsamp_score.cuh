@@ -231,6 +231,30 @@ __device__ __forceinline__ void score_sums(const uint32_t (&w)[kScoreChunks][4],
   A = (A2[0].x + A2[1].x) + (A2[0].y + A2[1].y);
 }
 
+// A piece that begins s bytes (4 WS + 2 odd) past a 16-byte boundary, from the aligned vectors around it: w holds the
+// lane's vector of every chunk, `extra` the vector after the piece (lane 0). A lane's elements begin in its own vector and
+// end in the next lane's, lane 31's in the next chunk's first.
+template <int WS>
+__device__ __forceinline__ void realign_piece(uint32_t (&w)[kScoreChunks][4], const uint4& extra, uint32_t odd) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t last[4] = {extra.x, extra.y, extra.z, extra.w};
+#pragma unroll
+  for (int i = 0; i < kScoreChunks; ++i) {
+    uint32_t c[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      c[k] = w[i][k];
+      c[4 + k] = 0;
+      if (k <= WS) {
+        const uint32_t after = i + 1 < kScoreChunks ? w[i + 1 < kScoreChunks ? i + 1 : 0][k] : last[k];
+        c[4 + k] = __shfl_sync(kFullMask, lane == 0 ? after : w[i][k], (lane + 1) & 31);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[i][k] = __funnelshift_r(c[k + WS], c[k + WS + 1 < 8 ? k + WS + 1 : 7], odd * 8);
+  }
+}
+
 // One warp, one piece of a row: its record, and the maxima of its chunks. The piece is held in registers.
 template <typename T, bool ALT>
 __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, int piece, int32_t t, float4* rec,
@@ -243,11 +267,23 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
   const int32_t V = (int32_t)p.V;
   const unsigned char* xr = p.x + (int64_t)row * p.ld * Ty::ES;
   uint32_t w[kScoreChunks][4];
-  if (p.vec && PE <= V - e0) {
+  if (PE <= V - e0) {
+    const unsigned char* at = xr + (int64_t)e0 * Ty::ES;
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 15);   // the same for the whole row
+    at += lane * 16 - (int)off;
 #pragma unroll
     for (int i = 0; i < kScoreChunks; ++i) {
-      const uint4 v = ldg_stream(xr + (int64_t)e0 * Ty::ES + i * 512 + lane * 16);
+      const uint4 v = ldg_stream(at + i * 512);
       w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+    }
+    if (off) {
+      // the vectors before the first and after the last element hold elements of the piece, too
+      uint4 extra = make_uint4(0, 0, 0, 0);
+      if (lane == 0) extra = ldg_stream(at + kScorePiece);
+      if (off < 4) realign_piece<0>(w, extra, off & 2);
+      else if (off < 8) realign_piece<1>(w, extra, off & 2);
+      else if (off < 12) realign_piece<2>(w, extra, off & 2);
+      else realign_piece<3>(w, extra, off & 2);
     }
   } else {
 #pragma unroll
@@ -288,14 +324,17 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
     } else if (t < e0) {
       before = count_larger<T>(w, xt, false);
     } else {
+      // the larger ones, and the equal ones of the vectors before its own; in its own vector one by one
       const int at = t - e0;
+      before = count_larger<T>(w, xt, false);
 #pragma unroll
-      for (int i = 0; i < kScoreChunks; ++i)
+      for (int i = 0; i < kScoreChunks; ++i) {
+        const int first = i * CE + lane * Ty::VE;
+        if (first < at) {
 #pragma unroll
-        for (int j = 0; j < Ty::VE; ++j) {
-          const float x = Ty::at(w[i], j);
-          before += x > xt || (x == xt && i * CE + lane * Ty::VE + j < at) ? 1u : 0u;
+          for (int j = 0; j < Ty::VE; ++j) before += Ty::at(w[i], j) == xt && first + j < at ? 1u : 0u;
         }
+      }
     }
   }
   before = warp_sum_u32(before);
@@ -612,12 +651,19 @@ __device__ __forceinline__ void score_finish_alt(const ScoreParams& p, int64_t r
             }
         }
       };
-      each_token([&](uint64_t k) {
-        const uint32_t at = atomicAdd(&sm.n_list, 1u);
-        if (at < kScoreList) sm.list[at] = k;
-      });
-      __syncthreads();
-      uint32_t n = sm.n_list;
+      // (once the list has run over, the rest is not counted: that many atomics on one word would take microseconds)
+      auto to_list = [&](uint64_t k) {
+        if (*reinterpret_cast<volatile uint32_t*>(&sm.n_list) <= kScoreList) {
+          const uint32_t at = atomicAdd(&sm.n_list, 1u);
+          if (at < kScoreList) sm.list[at] = k;
+        }
+      };
+      uint32_t n = kScoreList + 1;
+      if (cut != 0 || nc * CE <= kScoreList) {   // without a bound every token passes
+        each_token(to_list);
+        __syncthreads();
+        n = sm.n_list;
+      }
       if (n > kScoreList) {
         // too many (a row of few chunks, or of many equal tokens): a bound from every thread's largest token
         uint64_t top = 0;
@@ -635,10 +681,7 @@ __device__ __forceinline__ void score_finish_alt(const ScoreParams& p, int64_t r
         __syncthreads();
         const uint64_t above = sm.bound;
         each_token([&](uint64_t k) {
-          if (k >= above) {
-            const uint32_t at = atomicAdd(&sm.n_list, 1u);
-            if (at < kScoreList) sm.list[at] = k;
-          }
+          if (k >= above) to_list(k);
         });
         __syncthreads();
         n = sm.n_list;
