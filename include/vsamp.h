@@ -352,7 +352,7 @@ vsamp_status vsamp_shard_merge(const vsamp_piece_rec* recs, const vsamp_shard_wi
  *   workspace  vsamp_score_workspace_size bytes, 16-byte aligned; needs no initialisation, not shared by calls
  *              that may overlap.
  * Every row is read once, in pieces of 4 KB that depend on V alone: the results of a row do not depend on B, the
- * stride or the launch. Two launches on `stream`. */
+ * stride or the launch. One launch on `stream` for small batches, two for others. */
 #define VSAMP_SCORE_ALT_MAX 128
 size_t vsamp_score_workspace_size(vsamp_dtype dt, int64_t B, int64_t V, int32_t N);
 vsamp_status vsamp_score_tokens(const void* logits, vsamp_dtype dt, int64_t B, int64_t V, int64_t ld,

@@ -137,6 +137,37 @@ def test_alternatives_of_adverse_rows(ts, dev, dtype):
         _check(ts, _rows(a, dtype, dev), token, None, n)
 
 
+@pytest.mark.parametrize("n", [20, 128])
+def test_alternatives_of_long_adverse_rows(ts, dev, n):
+    """A million tokens whose chunks (of 128 fp32 tokens, dealt to 256 threads in turn) defeat the bound: tokens in fewer
+    threads' chunks than there are alternatives; large tokens in the chunks of fewer groups of threads."""
+    rng = np.random.default_rng(n)
+    V = 1 << 20
+    thread = (np.arange(V) // 128) % 256
+    a = rng.normal(0.0, 1.0, size=(2, V)).astype(np.float32)
+    a[0, thread >= 100] = -np.inf
+    a[1, thread < 8 * 19] += 100.0
+    live = int(np.flatnonzero(a[0] > -np.inf)[12345])
+    _check(ts, _rows(a, torch.float32, dev), [live, 7], None, n)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_one_launch_and_two_agree(ts, dev, dtype):
+    """A large batch takes two launches, each of its rows alone one: the same bits."""
+    rng = np.random.default_rng(12)
+    B, V = 700, 10007
+    a = rng.normal(0.0, 3.0, size=(B, V)).astype(np.float32)
+    x = _rows(a, dtype, dev)
+    tok = torch.from_numpy(rng.integers(0, V, size=B).astype(np.int32)).to(dev)
+    T = torch.from_numpy(rng.uniform(0.5, 2.0, size=B).astype(np.float32)).to(dev)
+    for n in (0, 20):
+        all_rows = ts.vsamp_score_tokens(x, tok, temperature=T, n_alt=n)
+        for r in (0, 1, 333, B - 1):
+            one = ts.vsamp_score_tokens(x[r:r + 1], tok[r:r + 1], temperature=T[r:r + 1], n_alt=n)
+            for p, q in zip(all_rows, one):
+                assert (p is None and q is None) or torch.equal(p[r:r + 1], q)
+
+
 def test_large_vocabulary(ts, dev):
     g = torch.Generator(device=dev).manual_seed(5)
     x = (torch.randn((3, 151936), generator=g, device=dev) * 2.5).to(torch.bfloat16)

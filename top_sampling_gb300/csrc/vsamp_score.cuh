@@ -233,7 +233,8 @@ __device__ __forceinline__ void score_sums(const uint32_t (&w)[kScoreChunks][4],
 
 // A piece that begins s bytes (4 WS + 2 odd) past a 16-byte boundary, from the aligned vectors around it: w holds the
 // lane's vector of every chunk, `extra` the vector after the piece (lane 0). A lane's elements begin in its own vector and
-// end in the next lane's, lane 31's in the next chunk's first.
+// end in the next lane's, lane 31's in the next chunk's first. (2048 x 151935 bf16: 109 us, aligned rows 98; by 32-bit
+// words 180.)
 template <int WS>
 __device__ __forceinline__ void realign_piece(uint32_t (&w)[kScoreChunks][4], const uint4& extra, uint32_t odd) {
   const int lane = threadIdx.x & 31;
@@ -351,9 +352,9 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
 }
 
 // One warp per piece, the piece in registers: 32 warps per SM hold 128 KB of loads in flight. About six instructions per
-// bf16 element beside the exponential. 2048 x 151936 bf16, a quarter of the rows ignored: 80.6 us with the finish, 87%
-// of the copy rate; small batches are bound by the two launches and their first loads (256 rows: 25 us with 20
-// alternatives where the bytes take 12; 4 rows of 32000: 7.4 us). A persistent form that copies the next piece to shared
+// bf16 element beside the exponential. 2048 x 151936 bf16, a quarter of the rows ignored: 78 us with the finish, 90% of
+// the copy rate; small batches are bound by the two launches and their first loads (256 rows: 24.5 us with 20
+// alternatives where the bytes take 12). A persistent form that copies the next piece to shared
 // memory meanwhile ran 15% more instructions and was slower (108 against 91 us at the time).
 template <typename T, bool ALT>
 __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const ScoreParams p) {
@@ -532,7 +533,7 @@ __device__ uint64_t score_radix_select(F for_each, uint32_t want, uint32_t* hist
 //      the list holds, above a bound from every thread's largest token, and failing that by a radix search for the last
 //      alternative), and each one's place is the number of larger ones.
 // Keys are (value, index) pairs in the order's sense, all different. Bound by latency: a chain of about eight dependent
-// steps, 5 to 6 us beside the pieces' kernel, whatever N (20 alternatives of 256 rows: 25.5 us against 20.3 without).
+// steps, about 5 us beside the pieces' kernel, whatever N (20 alternatives of 256 rows: 24.5 us against 19 without).
 struct ScoreAltSmem {
   __align__(16) uint64_t list[kScoreList];
   __align__(16) uint64_t best[kScoreFinishThreads];
@@ -728,7 +729,8 @@ __global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(c
 }
 
 // Both steps in one launch: a cluster of CTAs takes a row, its warps write the records of their pieces into the first
-// CTA's shared memory, and that CTA finishes the row while other rows' clusters run their pieces.
+// CTA's shared memory, and that CTA finishes the row. For small batches (see the launch): 4 x 32000 fp32 with five
+// alternatives 6.2 us, bound by the chain of dependent steps.
 template <typename T, bool ALT>
 __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_row_kernel(const ScoreParams p) {
   static_assert(kScoreWarps * 32 == kScoreFinishThreads, "the first CTA's threads finish the row");
