@@ -85,6 +85,7 @@ def test_embed_refusals(lib):
     for change in (dict(t=None), dict(w=None), dict(y=None), dict(N=0), dict(V=0), dict(D=0), dict(ldt=7), dict(ldo=7),
                    dict(dt=4), dict(odt=4), dict(w=ODD), dict(y=ODD)):
         assert _call(lib.vsamp_embed, good, **change) == BAD, change
+    assert _call(lib.vsamp_embed, good, D=1 << 30, ldt=1 << 30, ldo=1 << 30) == UNSUPPORTED
     assert lib.vsamp_embed_workspace_size(0, 8) == 0 and lib.vsamp_embed_workspace_size(8, 0) == 0
     need = lib.vsamp_embed_workspace_size(100, 8)
     good = dict(t=P, N=100, g=P, dt=F32, D=8, ldd=8, scale=1.0, V=10, d=P, odt=F32, ldt=8, acc=0, ws=P, n=need, s=None)

@@ -31,7 +31,8 @@ static vsamp_status launch_embed_ve(const EmbedParams& p, cudaStream_t s) {
   int tx = 1;   // threads along a row
   while (tx < kEmbedThreads && tx * kEmbedUnroll < nv) tx *= 2;
   const int64_t spans = ceil_div(nv, (int64_t)tx * kEmbedUnroll), rows = ceil_div(p.N, kEmbedThreads / tx);
-  return launch_1d(embed_kernel<TI, TO, VE>, grid_of(rows * spans), kEmbedThreads, 0, s, p, tx, (int)spans);
+  return launch_1d(p.aligned && p.D % VE == 0 ? embed_kernel<TI, TO, VE, true> : embed_kernel<TI, TO, VE, false>,
+                   grid_of(rows * spans), kEmbedThreads, 0, s, p, tx, (int)spans);
 }
 
 template <typename TI, typename TO>
@@ -159,7 +160,7 @@ vsamp_status vsamp_embed(const int32_t* token, int64_t N, const void* table, vsa
   if (!token || !table || !out || !type_ok(dt) || !type_ok(out_dt)) return VSAMP_ERR_INVALID_ARG;
   if (N <= 0 || V <= 0 || D <= 0 || ldt < D || ldo < D) return VSAMP_ERR_INVALID_ARG;
   if (!elem_aligned(table, dt) || !elem_aligned(out, out_dt)) return VSAMP_ERR_INVALID_ARG;
-  if (V > 0x7FFFFFF0LL || N > 0x7FFFFFFFLL || D > 0x7FFFFFFFLL) return VSAMP_ERR_UNSUPPORTED;
+  if (V > 0x7FFFFFF0LL || N > 0x7FFFFFFFLL || D > 0x3FFFFFFFLL) return VSAMP_ERR_UNSUPPORTED;
   EmbedParams p{};
   p.token = token;
   p.N = N;
@@ -179,7 +180,7 @@ vsamp_status vsamp_embed(const int32_t* token, int64_t N, const void* table, vsa
 }
 
 size_t vsamp_embed_workspace_size(int64_t N, int64_t D) {
-  if (N <= 0 || D <= 0 || N > 0x7FFFFFFFLL || D > 0x7FFFFFFFLL) return 0;
+  if (N <= 0 || D <= 0 || N > 0x7FFFFFFFLL || D > 0x3FFFFFFFLL) return 0;
   return embed_plan(N, D).total;
 }
 
@@ -190,7 +191,7 @@ vsamp_status vsamp_embed_backward(const int32_t* token, int64_t N, const void* d
   if (!token || !dout || !dtable || !type_ok(dt) || !type_ok(table_dt)) return VSAMP_ERR_INVALID_ARG;
   if (N <= 0 || V <= 0 || D <= 0 || ldt < D || ldd < D) return VSAMP_ERR_INVALID_ARG;
   if (!elem_aligned(dout, dt) || !elem_aligned(dtable, table_dt)) return VSAMP_ERR_INVALID_ARG;
-  if (V > 0x7FFFFFF0LL || N > 0x7FFFFFFFLL || D > 0x7FFFFFFFLL) return VSAMP_ERR_UNSUPPORTED;
+  if (V > 0x7FFFFFF0LL || N > 0x7FFFFFFFLL || D > 0x3FFFFFFFLL) return VSAMP_ERR_UNSUPPORTED;
   const EmbedPlan e = embed_plan(N, D);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0 || workspace_bytes < e.total)
     return VSAMP_ERR_INVALID_ARG;
