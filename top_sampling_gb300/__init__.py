@@ -603,7 +603,7 @@ def _elsewhere(t: torch.Tensor, stream):
     index = t.get_device()
     if index < 0:
         raise ValueError(f"tensors must be on a CUDA device, got {t.device}")
-    if stream is None and index == torch.cuda.current_device():
+    if stream is None and index == torch._C._cuda_getDevice():
         return None
     dev = t.device
     if stream is None:
@@ -656,7 +656,7 @@ def _token_ids(v, n: int, dev):
     """Token ids as a contiguous int32 device tensor; wider ids outside its range stay outside every vocabulary."""
     if isinstance(v, torch.Tensor):
         if v.dtype is torch.int32:
-            return v if v.device == dev and v.is_contiguous() else v.to(device=dev).contiguous()
+            return v if v.is_contiguous() and v.device == dev else v.to(device=dev).contiguous()
         if v.is_floating_point() or v.is_complex():
             raise TypeError(f"token must hold whole numbers, got {v.dtype}")
         if v.dtype is torch.int64:
@@ -674,12 +674,15 @@ def _row_values(v, n: int, dev, name):
 
 def _matrix(t: torch.Tensor, name: str, index: int, rows=None, cols=None):
     """Checks a row-major matrix (rows may be padded); returns its rows, columns and row stride in elements."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or t.get_device() != index or (stride[1] != 1 and shape[1] > 1):
+    try:
+        (r, c), (s0, s1) = t.shape, t.stride()
+    except ValueError:
+        r = None
+    if r is None or t.get_device() != index or (s1 != 1 and c > 1):
         raise ValueError(f"{name} must be a 2-D tensor on cuda:{index} with contiguous rows")
-    if (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(shape)}")
-    return shape[0], shape[1], stride[0] if shape[0] > 1 else max(stride[0], shape[1])
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got [{r}, {c}]")
+    return r, c, s0 if r > 1 or s0 > c else c
 
 
 def _logits_matrix(x: torch.Tensor, V, index: int):
