@@ -26,20 +26,21 @@ static bool rows_aligned(const void* p, int64_t ld, int es, int ve) {
 }
 
 template <typename TI, typename TO, int VE>
-static vsamp_status launch_embed_ve(const EmbedParams& p, cudaStream_t s) {
+static vsamp_status launch_embed_ve(const EmbedParams& p, bool whole, cudaStream_t s) {
   const int64_t nv = ceil_div(p.D, VE);
   int tx = 1;   // threads along a row
   while (tx < kEmbedThreads && tx * kEmbedUnroll < nv) tx *= 2;
   const int64_t spans = ceil_div(nv, (int64_t)tx * kEmbedUnroll), rows = ceil_div(p.N, kEmbedThreads / tx);
-  return launch_1d(p.aligned && p.D % VE == 0 ? embed_kernel<TI, TO, VE, true> : embed_kernel<TI, TO, VE, false>,
+  return launch_1d(whole ? embed_kernel<TI, TO, VE, true> : embed_kernel<TI, TO, VE, false>,
                    grid_of(rows * spans), kEmbedThreads, 0, s, p, tx, (int)spans);
 }
 
 template <typename TI, typename TO>
-static vsamp_status launch_embed(EmbedParams p, cudaStream_t s) {
+static vsamp_status launch_embed(const EmbedParams& p, cudaStream_t s) {
   constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;   // 16 bytes of the wider type
-  p.aligned = rows_aligned(p.table, p.ldt, sizeof(TI), VE) && rows_aligned(p.out, p.ldo, sizeof(TO), VE);
-  return launch_embed_ve<TI, TO, VE>(p, s);
+  const bool whole = p.D % VE == 0 && rows_aligned(p.table, p.ldt, sizeof(TI), VE) &&
+                     rows_aligned(p.out, p.ldo, sizeof(TO), VE);
+  return launch_embed_ve<TI, TO, VE>(p, whole, s);
 }
 
 template <typename TO>

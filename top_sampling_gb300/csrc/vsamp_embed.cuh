@@ -36,8 +36,6 @@ struct EmbedParams {
   unsigned char* out;
   int64_t ldo;
   int32_t* row_status;
-  int aligned;             // every row of the table and of the output begins on a vector's boundary
-                           // (WHOLE: and has whole vectors)
 };
 
 struct EmbedGradParams {
@@ -62,6 +60,7 @@ struct EmbedGradParams {
 
 constexpr int kEmbedThreads = 256;
 
+// WHOLE: every row of the table and of the output is whole aligned vectors.
 // tx threads of a CTA along a row (a power of two), kEmbedThreads / tx rows per CTA, kEmbedUnroll vectors per thread and
 // row so that their loads are in flight together (two took a sixth longer; 16384 x 4096 bf16: 32 us, 90% of the copy rate).
 constexpr int kEmbedUnroll = 4;
@@ -81,32 +80,50 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams 
     const bool skip = t == VSAMP_TOKEN_IGNORE;
     const bool ok = t >= 0 && (int64_t)t < p.V;
     if (p.row_status && c0 == 0) p.row_status[n] = ok || skip ? VSAMP_OK : VSAMP_ERR_INVALID_ARG;
-    const unsigned char* src = p.table + ((ok ? (int64_t)t * p.ldt : 0) + c0) * (int64_t)sizeof(TI);
-    unsigned char* dst = p.out + (n * p.ldo + c0) * (int64_t)sizeof(TO);
+    const unsigned char* src = p.table + (ok ? (int64_t)t * p.ldt : 0) * (int64_t)sizeof(TI);
+    unsigned char* dst = p.out + n * p.ldo * (int64_t)sizeof(TO);
+    // vectors begin at the output row's first boundary of a vector; the elements before it go one by one
+    constexpr int OB = VE * (int)sizeof(TO), IB = VE * (int)sizeof(TI);
+    const int head = WHOLE ? 0 : (int)((OB - (reinterpret_cast<uintptr_t>(dst) & (OB - 1))) & (OB - 1)) / (int)sizeof(TO);
+    const int first = head + c0;
+    src += (int64_t)first * (int)sizeof(TI);
+    dst += (int64_t)first * (int)sizeof(TO);
+    const bool aligned = WHOLE || (reinterpret_cast<uintptr_t>(src) & (IB - 1)) == 0;
     ElemVec<TI, VE> v[U];
     if (ok) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = u * tx * VE;
-        if (c0 + c < D) {
+        if (first + c < D) {
           if (WHOLE) v[u].load(src + c * (int)sizeof(TI), true);
-          else v[u].load_row(src + c * (int)sizeof(TI), D - c0 - c, p.aligned, 0u);
+          else v[u].load_row(src + c * (int)sizeof(TI), D - first - c, aligned, 0u);
         }
       }
     }
     const float fill = skip ? 0.f : __int_as_float(0x7FC00000);
+    auto put = [&](const ElemVec<TI, VE>& x, ElemVec<TO, VE>& o) {
+      float f[VE];
+#pragma unroll
+      for (int j = 0; j < VE; ++j) f[j] = ok ? x.at(j) * p.scale : fill;
+      o.set(f);
+    };
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c = u * tx * VE;
-      if (c0 + c < D) {
-        float f[VE];
-#pragma unroll
-        for (int j = 0; j < VE; ++j) f[j] = ok ? v[u].at(j) * p.scale : fill;
+      if (first + c < D) {
         ElemVec<TO, VE> o;
-        o.set(f);
+        put(v[u], o);
         if (WHOLE) o.store(dst + c * (int)sizeof(TO), true);
-        else o.store_row(dst + c * (int)sizeof(TO), D - c0 - c, p.aligned);
+        else o.store_row(dst + c * (int)sizeof(TO), D - first - c, true);
       }
+    }
+    if (!WHOLE && c0 == 0 && head > 0) {
+      const int left = head < D ? head : D;
+      ElemVec<TI, VE> x;
+      ElemVec<TO, VE> o;
+      if (ok) x.load_some(src - (int64_t)head * (int)sizeof(TI), left, 0u);
+      put(x, o);
+      o.store_some(dst - (int64_t)head * (int)sizeof(TO), left);
     }
   }
 }
