@@ -85,6 +85,37 @@ def test_random_rows(ts, dev, dtype, V, n, pad):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [0, 20])
+def test_extreme_temperatures(ts, dev, dtype, n):
+    rng = np.random.default_rng(21)
+    temps = [1e-3, 1e-7, 1e-9, 1e-12, 1e-20, 1e-30, 1e4, 1e20, 3e38]
+    a = rng.normal(0.0, 2.5, size=(len(temps), 5001)).astype(np.float32)
+    a[:, ::3] = -np.inf
+    a[2, 1] = a[2, 4000] = 30.0                        # two equal maxima: each takes half
+    token = [int(np.argmax(a[r])) if r % 2 else 1 for r in range(len(temps))]
+    x = _rows(a, dtype, dev)
+    _check(ts, x, token, temps, n)
+    # quotients by a temperature below 1e-38 overflow: the maximum keeps the log-probability 0
+    top = [int(np.argmax(tu.f64(x)[r])) for r in range(len(temps))]
+    out = ts.vsamp_score_tokens(x, torch.tensor(top, device=dev), temperature=1e-40, n_alt=1)
+    assert (out[7] == 0).all() and (out[4][:, 0] == out[0]).all()
+    for r in range(len(temps)):
+        ties = int((tu.f64(x)[r] == tu.f64(x)[r].max()).sum())
+        assert abs(float(out[0][r]) + np.log(ties)) <= tu.LOGSUM_TOL
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_smallest_temperature_at_a_maximum_of_zero(ts, dev, dtype):
+    # m - 104 T is a value of its own below m = 0 at every T: masked tokens must still add nothing
+    a = np.full((1, 5001), -np.inf, np.float32)
+    a[0, 7], a[0, 9] = 0.0, -1.0
+    for t in (1e-40, 3e-39, 1e-38, 1e-30):
+        out = ts.vsamp_score_tokens(_rows(a, dtype, dev), torch.tensor([7], device=dev), temperature=t, n_alt=2)
+        assert float(out[0][0]) == 0.0 and int(out[7][0]) == 0
+        assert out[3][0].tolist() == [7, 9]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n", [0, 20, 128])
 def test_masked_tokens(ts, dev, dtype, n):
     rng = np.random.default_rng(n + 1)

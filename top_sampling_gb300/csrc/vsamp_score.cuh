@@ -103,6 +103,10 @@ struct ScoreType<__nv_bfloat16> {
   }
 };
 
+// log2(e) / T and 1 / T, finite for every T > 0 (below about 1e-38 the quotients overflow, and 0 * inf is NaN)
+__device__ __forceinline__ float score_rate(float T) { return fminf(kLog2e / T, 3.4e38f); }
+__device__ __forceinline__ float score_inverse(float T) { return fminf(1.f / T, 3.4e38f); }
+
 // max that returns NaN when either operand is NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -200,7 +204,8 @@ __device__ __forceinline__ uint32_t count_larger(const uint32_t (&w)[kScoreChunk
 
 // A lane's sums of 2^s2 and s2 2^s2, s2 = (x - m) c, over its vectors. A masked token must add 0 to both, and s2 2^s2
 // is NaN at s2 = -inf: elements are raised to `lowest`, whose exponential is flushed to 0 (2^-150), two bf16 at once
-// (RAISE), or, at a temperature so large that no finite value is that low, the products are.
+// (RAISE), or, at a temperature so large that no finite value is that low, or so small that no value lies between, the
+// products are.
 // (One fused multiply-add x c - m c instead of the difference and the product is 8% fewer instructions, but then the
 // maximum's own exponential is not exactly 1, and a row with one likely token loses the digits of its log-probability.)
 template <typename T, bool RAISE>
@@ -291,7 +296,7 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
     for (int i = 0; i < kScoreChunks; ++i) score_load<T>(xr, (int64_t)e0 + i * CE + lane * Ty::VE, p.V, p.vec, w[i]);
   }
   const float temp = p.temperature ? p.temperature[row] : 1.f;
-  const float T1 = temp > 0.f ? temp : 1.f, c = p.temperature ? kLog2e / T1 : kLog2e;
+  const float T1 = temp > 0.f ? temp : 1.f, c = p.temperature ? score_rate(T1) : kLog2e;
   const bool known = t >= 0 && t < V;
   const float xt = known ? Ty::load(xr, t) : INFINITY;
 
@@ -342,8 +347,10 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
 
   float S = 0.f, A = 0.f;
   if (m > -INFINITY && m < INFINITY) {   // false for NaN too
-    const float lowest = fmaf(-104.f, T1, m);   // 104 log2(e) > 150
-    if (lowest > -3.3e38f) score_sums<T, true>(w, m, c, lowest, S, A);
+    // 104 log2(e) > 150; below m, too: at a temperature far below the maximum's last place it is m itself. A rate held
+    // at the largest float (score_rate) no longer brings it to 2^-150.
+    const float lowest = fmaf(-104.f, T1, m);
+    if (lowest < m && lowest > -3.3e38f && c < 3.4e38f) score_sums<T, true>(w, m, c, lowest, S, A);
     else score_sums<T, false>(w, m, c, lowest, S, A);
   }
   S = warp_sum_f(S);
@@ -399,8 +406,8 @@ struct ScoreFold {
   __device__ __forceinline__ ScoreRow row(const ScoreParams& p, int64_t at, int32_t t) const {
     const float temp = p.temperature ? p.temperature[at] : 1.f;
     ScoreRow r;
-    const float T1 = temp > 0.f ? temp : 1.f, c = p.temperature ? kLog2e / T1 : kLog2e;   // as for the pieces
-    r.invT = 1.f / T1;
+    const float T1 = temp > 0.f ? temp : 1.f, c = p.temperature ? score_rate(T1) : kLog2e;   // as for the pieces
+    r.invT = score_inverse(T1);
     float m = -INFINITY;
     each(p, [&](float4 q) { m = max_nan(m, q.x); });
     m = warp_max_nan(m);
@@ -852,13 +859,13 @@ __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGra
     const float H = p.dentropy ? p.entropy[row] : 0.f;
     const bool args = t >= 0 && (int64_t)t < p.V && !isnan(temp) && !isinf(temp);
     const bool ok = args && isfinite(m) && isfinite(ls) && isfinite(H);
-    const float T1 = temp > 0.f ? temp : 1.f, invT = 1.f / T1;
+    const float T1 = temp > 0.f ? temp : 1.f, invT = score_inverse(T1);
     const float scale = -expf(-ls) * invT;
     const float g = !skip && p.dlogprob ? p.dlogprob[row] : 0.f;
     const float h = !skip && p.dentropy ? p.dentropy[row] : 0.f;
     GradRow r;
     r.m = m;
-    r.c = kLog2e / T1;
+    r.c = score_rate(T1);
     r.k0 = (g + h * (H - ls)) * scale;
     r.k1 = h * 0.69314718056f * scale;
     const float fill = skip ? 0.f : __int_as_float(0x7FC00000);
