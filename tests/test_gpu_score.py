@@ -183,6 +183,23 @@ def test_alternatives_of_long_adverse_rows(ts, dev, n):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,V", [(3, 5000), (1500, 5000), (40, 40000)])
+def test_more_candidates_than_the_list_holds_on_every_call(ts, dev, dtype, B, V):
+    """Every token of every row ties, so each row's listing runs over and is begun anew, in the form of one launch and in
+    that of two: the first tokens on every one of many calls, whatever the warps' timing."""
+    x = torch.full((B, V), 1.5, dtype=dtype, device=dev)
+    x[1::3, ::2] = -3.0                                # half of the tokens tie: the odd ones
+    tok = torch.full((B,), V - 1, dtype=torch.int32, device=dev)
+    for n in (1, 20, 128):
+        want = torch.arange(n, dtype=torch.int32, device=dev).repeat(B, 1)
+        want[1::3] = want[1::3] * 2 + 1
+        outs = [ts.vsamp_score_tokens(x, tok, n_alt=n) for _ in range(20)]
+        for out in outs:
+            assert torch.equal(out[3], want) and not out[7].any()
+            assert all(torch.equal(p, q) for p, q in zip(out, outs[0]))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_one_launch_and_two_agree(ts, dev, dtype):
     """A large batch takes two launches, each of its rows alone one: the same bits."""
     rng = np.random.default_rng(12)

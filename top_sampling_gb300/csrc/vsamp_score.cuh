@@ -674,6 +674,7 @@ __device__ __forceinline__ void score_finish_alt(const ScoreParams& p, int64_t r
       }
       if (n > kScoreList) {
         // too many (a row of few chunks, or of many equal tokens): a bound from every thread's largest token
+        __syncthreads();   // every thread has read the count that is set back below, so all of them are here
         uint64_t top = 0;
         each_token([&](uint64_t k) { top = k > top ? k : top; });
         sm.best[tid] = top;
