@@ -200,6 +200,25 @@ def test_more_candidates_than_the_list_holds_on_every_call(ts, dev, dtype, B, V)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,V", [(2, 60), (16, 32000), (40, 60000)])
+def test_short_clusters_on_every_call(ts, dev, dtype, B, V):
+    """The form of one launch, whose CTAs write their pieces' records into the first CTA of their cluster: pieces of a few
+    elements (a record is ready at once), several CTAs per row, ignored rows between, one call right behind another."""
+    g = torch.Generator(device=dev).manual_seed(B)
+    x = torch.randn((B, V), generator=g, device=dev).to(dtype)
+    tok = torch.randint(0, V, (B,), generator=g, device=dev, dtype=torch.int32)
+    tok[1::5] = tu.IGNORE
+    first = ts.vsamp_score_tokens(x, tok, n_alt=20)
+    outs = [ts.vsamp_score_tokens(x, tok, n_alt=20) for _ in range(50)]
+    reps = 5000 // (B * ((V + 2047) // 2048)) + 1                                 # more pieces than one launch takes
+    wide = ts.vsamp_score_tokens(x.repeat(reps, 1), tok.repeat(reps), n_alt=20)
+    for out in outs:
+        for p, q, w in zip(out, first, wide):
+            assert torch.equal(p.view(torch.int32), q.view(torch.int32))
+            assert torch.equal(p.view(torch.int32), w[:B].contiguous().view(torch.int32))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_one_launch_and_two_agree(ts, dev, dtype):
     """A large batch takes two launches, each of its rows alone one: the same bits."""
     rng = np.random.default_rng(12)

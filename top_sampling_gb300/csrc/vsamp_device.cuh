@@ -121,6 +121,14 @@ __device__ __forceinline__ void cluster_barrier_shared() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// The two halves of a barrier that shows every CTA of the cluster to have begun: a CTA's shared memory may be written by
+// its peers only after that. Each thread calls both once, before any other cluster barrier; what stands between them
+// overlaps the wait.
+__device__ __forceinline__ void cluster_begun_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_begun_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // ------------------------------------------------------------------------------------------------
 // Distributed shared memory: a CTA's shared address mapped into the address window of CTA `rank` of
 // the cluster, stores and an acquire-release atomic add there.

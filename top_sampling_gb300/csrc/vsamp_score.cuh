@@ -744,12 +744,14 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_row_kernel(const Sc
   static_assert(kScoreWarps * 32 == kScoreFinishThreads, "the first CTA's threads finish the row");
   extern __shared__ __align__(16) unsigned char score_smem[];   // first CTA: [np] records, [np, 8] chunk maxima
   __shared__ ScoreAltSmem sm;
+  cluster_begun_arrive();
   begin_overlapped();
   cg::cluster_group cluster = cg::this_cluster();
   const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank(), row = blockIdx.x / C;
   float4* rec = reinterpret_cast<float4*>(score_smem);
   float* cm = reinterpret_cast<float*>(rec + p.np);
   const int32_t t = p.token[row];
+  cluster_begun_wait();   // the first CTA's shared memory may be written
   if (t != VSAMP_TOKEN_IGNORE) {
     float4* rec0 = cluster.map_shared_rank(rec, 0);
     float* cm0 = cluster.map_shared_rank(cm, 0);
