@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(NW * 32, (NW >= 8 ? 3 : 6)) stats_kernel(const
   const int p0 = crank * ppc;
   const int p1 = min(np, p0 + ppc);
   cg::cluster_group cluster = cg::this_cluster();
+  cluster_begun_arrive();
   uint4* heads = cluster.map_shared_rank(&S.gather[0], 0);   // CTA 0's record heads (generic address)
   if (t < NW * NB) mbar_init(&S.bar[t / NB][t % NB], 1);
   fence_mbar_init();
@@ -107,6 +108,8 @@ __global__ void __launch_bounds__(NW * 32, (NW >= 8 ? 3 : 6)) stats_kernel(const
   const float Teff = temp0 > 0.f ? temp0 : 1.f;   // T <= 0 (greedy) reads as T = 1
   const float invT = 1.f / Teff;
   const float c1 = kLog2e * invT;
+
+  cluster_begun_wait();   // CTA 0's shared memory may be written
 
   // ---- every warp streams its pieces ----
   for (int i = 0; i < nw; ++i) {
