@@ -45,3 +45,17 @@ def test_statistics_of_short_rows(ts, dev, monkeypatch, dtype, piece, tail):
     monkeypatch.setenv("VSAMP_STATS_C", "8")
     for out in [both() for _ in range(CALLS)]:
         assert all(torch.equal(p, q) for p, q in zip(out, alone))
+
+
+@pytest.mark.parametrize("dtype,piece", [(torch.float32, 1024), (torch.bfloat16, 2048)])
+def test_streaming_sampler_of_short_rows(ts, dev, monkeypatch, dtype, piece):
+    """Records and draw codes of short rows, against the sampler that keeps them in a workspace."""
+    B, V = 300, 7 * piece + 3
+    x = torch.randn((B, V), device=dev).to(dtype)
+    seed = torch.arange(B, device=dev)
+    kw = dict(temperature=0.9, top_k=50, seed=seed, step=3, want_stats=True)
+    want = _bits(ts.vsamp_sample_ws(x, **kw))
+    monkeypatch.setenv("VSAMP_SAMPLE_STREAM", "1")
+    monkeypatch.setenv("VSAMP_SSTREAM_C", "8")
+    for out in [_bits(ts.vsamp_sample(x, **kw)) for _ in range(CALLS)]:
+        assert all(torch.equal(p, q) for p, q in zip(out, want))

@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) sample_stream_kernel(const 
   const int p0 = crank * ppc;
   const int p1 = min(np, p0 + ppc);
   cg::cluster_group cluster = cg::this_cluster();
+  cluster_begun_arrive();
   Smem* s0 = cluster.map_shared_rank(&S, 0);   // CTA 0's shared memory (generic address)
   PieceRec* recs0 = &s0->recs[0];
   uint32_t* codes0 = &s0->fin.codes[0];
@@ -81,6 +82,8 @@ __global__ void __launch_bounds__(kStreamThreads, 3) sample_stream_kernel(const 
     st_hi = (uint32_t)(stp >> 32);
     if (p.row_id) rid = p.row_id[row];
   }
+
+  cluster_begun_wait();   // CTA 0's shared memory may be written
 
   // ---- every warp streams its pieces: the record and the codes into CTA 0 ----
   for (int i = 0; i < nw; ++i) {
