@@ -29,12 +29,13 @@ struct ElemVec {
 #pragma unroll
       for (int i = 0; i < W; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
     } else {
-      // the words that hold the elements: the halves before the first and after the last one are dropped
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(p - 2);
-      uint32_t a = q[0];
+      // the whole words between the first and the last element, and these two alone: nothing but the elements is read
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p + 2);
+      uint32_t a = (uint32_t)h[0] << 16;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const uint32_t b = q[i + 1];
+        const uint32_t b = i + 1 < W ? q[i] : (uint32_t)h[VE - 1];
         w[i] = __funnelshift_r(a, b, 16);
         a = b;
       }
