@@ -351,6 +351,8 @@ vsamp_status vsamp_shard_merge(const vsamp_piece_rec* recs, const vsamp_shard_wi
  *   (VSAMP_ERR_NONFINITE); another token outside [0, V), a NaN or infinite temperature (VSAMP_ERR_INVALID_ARG).
  *   workspace  vsamp_score_workspace_size bytes, 16-byte aligned; needs no initialisation, not shared by calls
  *              that may overlap.
+ * Nothing before the first row's first logit or behind the last row's last one is read; what lies between two rows
+ *   (ld > V) may be read and has no effect.
  * Every row is read once, in pieces of 4 KB that depend on V alone: the results of a row do not depend on B, the
  * stride or the launch. One launch on `stream` for small batches, two for others. */
 #define VSAMP_SCORE_ALT_MAX 128

@@ -183,6 +183,20 @@ def test_alternatives_of_long_adverse_rows(ts, dev, n):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("extra", [0, 1, 5])
+def test_whole_pieces_at_the_ends_of_unaligned_logits(ts, dev, dtype, extra):
+    """The first and the last piece of the logits are whole and begin on any boundary; what stands around them is NaN."""
+    V = 2 * 4096 // dtype.itemsize + extra
+    rng = np.random.default_rng(extra)
+    a = rng.normal(0.0, 2.5, size=(3, V)).astype(np.float32)
+    for off in range(1, 16 // dtype.itemsize):
+        flat = torch.full((off + a.size + 16,), float("nan"), dtype=dtype, device=dev)
+        x = flat[off:off + a.size].view(3, V)
+        x.copy_(torch.from_numpy(a))
+        _check(ts, x, [0, V - 1, V - 1], [1.0, 0.7, 1.3], 20)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("B,V", [(3, 5000), (1500, 5000), (40, 40000)])
 def test_more_candidates_than_the_list_holds_on_every_call(ts, dev, dtype, B, V):
     """Every token of every row ties, so each row's listing runs over and is begun anew, in the form of one launch and in

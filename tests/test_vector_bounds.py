@@ -46,8 +46,20 @@ static int check() {
   return 0;
 }
 
+// every address and length around a buffer of 100 bytes at an odd place, against the vectors one by one
+static int check_inside() {
+  const uintptr_t begin = 1000 + 6, end = begin + 100;
+  for (uintptr_t at = begin; at < end; at += 2)
+    for (uintptr_t n = 2; at + n <= end; n += 2) {
+      bool in = true;
+      for (uintptr_t v = at / 16; v <= (at + n - 1) / 16; ++v) in = in && v * 16 >= begin && v * 16 + 16 <= end;
+      if (vsamp::vectors_inside(at, n, begin, end) != in) return printf("%d bytes at %d\n", (int)n, (int)at), 1;
+    }
+  return 0;
+}
+
 int main() {
-  return check<float, 4>() || check<__nv_bfloat16, 4>() || check<__nv_bfloat16, 8>();
+  return check_inside() || check<float, 4>() || check<__nv_bfloat16, 4>() || check<__nv_bfloat16, 8>();
 }
 """
 

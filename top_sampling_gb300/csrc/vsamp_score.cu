@@ -89,6 +89,14 @@ vsamp_status vsamp_score_tokens(const void* logits, vsamp_dtype dt, int64_t B, i
   while ((1LL << l) < np) ++l;
   p.np_mul = (uint32_t)(((1ULL << (31 + l)) + (uint64_t)np - 1) / (uint64_t)np);
   p.np_shift = l - 1;
+  // the aligned vectors around the first or the last whole piece may reach out of the logits: these take loads of elements
+  const uintptr_t x0 = reinterpret_cast<uintptr_t>(logits), xl = x0 + (uintptr_t)((B - 1) * ld * es);
+  const uintptr_t x1 = xl + (uintptr_t)(V * es);
+  const int64_t whole = V * es / kScorePiece;
+  p.inner0 = vectors_inside(x0, kScorePiece, x0, x1) ? 0u : 1u;
+  p.inner1 = (uint32_t)(B * np);
+  if (whole > 0 && !vectors_inside(xl + (uintptr_t)((whole - 1) * kScorePiece), kScorePiece, x0, x1))
+    p.inner1 = (uint32_t)((B - 1) * np + whole - 1);
   p.rec = static_cast<float4*>(workspace);
   p.chunk_max = N > 0 ? reinterpret_cast<float*>(p.rec + B * np) : nullptr;
   p.logprob = logprob;

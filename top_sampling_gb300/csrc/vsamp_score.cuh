@@ -40,6 +40,7 @@ struct ScoreParams {
   int np;                // pieces per row; B * np < 2^31
   uint32_t np_mul;       // id / np = umulhi(id, np_mul) >> np_shift for np > 1
   int np_shift;
+  uint32_t inner0, inner1;   // whole pieces in [inner0, inner1) are read by aligned vectors (all but one at the very ends)
   float4* rec;           // [B, np] {m_p, S_p, A_p, tokens before the given one}
   float* chunk_max;      // [B, np, 8] (N > 0)
   float* logprob;
@@ -261,10 +262,11 @@ __device__ __forceinline__ void realign_piece(uint32_t (&w)[kScoreChunks][4], co
   }
 }
 
-// One warp, one piece of a row: its record, and the maxima of its chunks. The piece is held in registers.
+// One warp, one piece of a row (the id-th of all): its record, and the maxima of its chunks. The piece is held in
+// registers.
 template <typename T, bool ALT>
-__device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, int piece, int32_t t, float4* rec,
-                                            float* chunk_max) {
+__device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, int piece, uint32_t id, int32_t t,
+                                            float4* rec, float* chunk_max) {
   using Ty = ScoreType<T>;
   constexpr int PE = kScorePiece / Ty::ES;      // elements per piece
   constexpr int CE = PE / kScoreChunks;         // elements per chunk
@@ -273,7 +275,7 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
   const int32_t V = (int32_t)p.V;
   const unsigned char* xr = p.x + (int64_t)row * p.ld * Ty::ES;
   uint32_t w[kScoreChunks][4];
-  if (PE <= V - e0) {
+  if (PE <= V - e0 && id >= p.inner0 && id < p.inner1) {
     const unsigned char* at = xr + (int64_t)e0 * Ty::ES;
     const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(at) & 15);   // the same for the whole row
     at += lane * 16 - (int)off;
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_piece_kernel(const 
   if (row >= (uint32_t)p.B) return;
   const int32_t t = p.token[row];
   if (t == VSAMP_TOKEN_IGNORE) return;
-  score_piece<T, ALT>(p, row, (int)(id - row * (uint32_t)p.np), t, p.rec + id,
+  score_piece<T, ALT>(p, row, (int)(id - row * (uint32_t)p.np), id, t, p.rec + id,
                       ALT ? p.chunk_max + (int64_t)id * kScoreChunks : nullptr);
 }
 
@@ -756,7 +758,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_row_kernel(const Sc
     float4* rec0 = cluster.map_shared_rank(rec, 0);
     float* cm0 = cluster.map_shared_rank(cm, 0);
     for (int piece = rank * kScoreWarps + (threadIdx.x >> 5); piece < p.np; piece += C * kScoreWarps)
-      score_piece<T, ALT>(p, row, piece, t, rec0 + piece, cm0 + piece * kScoreChunks);
+      score_piece<T, ALT>(p, row, piece, row * (uint32_t)p.np + piece, t, rec0 + piece, cm0 + piece * kScoreChunks);
   }
   cluster.sync();   // every record is in the first CTA
   if (rank != 0) return;

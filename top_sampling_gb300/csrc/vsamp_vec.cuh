@@ -10,6 +10,11 @@
 
 namespace vsamp {
 
+// Whether the whole aligned 16-byte vectors that hold the `bytes` bytes at `at` lie in [begin, end).
+inline bool vectors_inside(uintptr_t at, uintptr_t bytes, uintptr_t begin, uintptr_t end) {
+  return at - (at & 15) >= begin && at + bytes + ((0 - (at + bytes)) & 15) <= end;
+}
+
 template <typename T, int VE>
 struct ElemVec {
   static constexpr int ES = (int)sizeof(T), W = VE * ES / 4;   // 32-bit words
