@@ -369,7 +369,7 @@ vsamp_status vsamp_score_tokens(const void* logits, vsamp_dtype dt, int64_t B, i
  *   row_max, row_logsum, entropy  as vsamp_score_tokens wrote them for the same logits, tokens and temperature.
  *   dlogits   [B, ldd] of the logits' type, rounded once; it may be the logits' own buffer with the same stride
  *             (the logits are then replaced).
- * Masked tokens have p = 0. An ignored row's gradient is 0. A row that vsamp_score_tokens refused gets NaN and its
+ * Masked tokens have p = 0, and so have tokens with exp(s_v) below 2^-126. An ignored row's gradient is 0. A row that vsamp_score_tokens refused gets NaN and its
  * status. One launch on `stream`. */
 vsamp_status vsamp_score_tokens_backward(const void* logits, vsamp_dtype dt, int64_t B, int64_t V, int64_t ld,
                                          const float* temperature, const int32_t* token, const float* dlogprob,

@@ -1,0 +1,56 @@
+"""Token scores and their gradient where the formulas leave fp32's range on the way: smallest and largest temperatures,
+differences of logits beyond the largest fp32 value, largest incoming gradients."""
+import numpy as np
+import pytest
+
+import tables_util as tu
+from test_gpu_score import DTYPES, _rows, dev, ts  # noqa: F401
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def _gradient(ts, x, token, temps, g, h):
+    """The gradient against the formula's. Where its bound reaches past the type's largest value an infinity is as good."""
+    d = x.device
+    tok, T = torch.tensor(token, dtype=torch.int32, device=d), torch.tensor(temps, dtype=torch.float32, device=d)
+    gt, ht = torch.tensor(g, dtype=torch.float32, device=d), torch.tensor(h, dtype=torch.float32, device=d)
+    f = ts.vsamp_score_tokens(x, tok, temperature=T)
+    out, st = ts.vsamp_score_tokens_backward(x, tok, gt, f[5], f[6], entropy=f[1], dentropy=ht, temperature=T)
+    assert not st.any() and not torch.isnan(out).any()
+    got, xs = tu.f64(out), tu.f64(x)
+    largest = torch.finfo(x.dtype).max
+    for r in range(len(token)):
+        want, size = tu.grad_row(xs[r], token[r], float(np.float32(temps[r])), float(np.float32(g[r])),
+                                 float(np.float32(h[r])))
+        tol = tu.GRAD_REL * size + tu.HALF[x.dtype] * np.abs(want) + 1e-37
+        near, beyond = np.abs(want) + tol <= largest, np.abs(want) - tol > largest
+        assert np.all(np.abs(got[r] - want)[near] <= tol[near]), (r, temps[r])
+        assert np.all(got[r][beyond] == np.inf * np.sign(want[beyond])), (r, temps[r])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradient_at_extreme_temperatures(ts, dev, dtype):
+    temps = [1e-20, 1e-30, 1e-36, 3e-37, 1e-38, 1e-40, 1e-44, 1e30, 3e37, 3e38]
+    rng = np.random.default_rng(5)
+    a = rng.normal(0.0, 2.5, size=(len(temps), 3001)).astype(np.float32)
+    a[:, ::3] = -np.inf
+    a[::2, 1] = a[::2, 2000] = 30.0                            # two equal maxima: each takes half
+    token = [int(np.argmax(a[r])) if r % 3 else 4 for r in range(len(temps))]
+    x = _rows(a, dtype, dev)
+    for g, h in ((1e-3, 1e-2), (1.0, -0.5), (40.0, 3.0)):
+        _gradient(ts, x, token, temps, [g] * len(temps), [h] * len(temps))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_masked_tokens_have_no_gradient_whatever_comes_in(ts, dev, dtype):
+    rng = np.random.default_rng(6)
+    a = rng.normal(0.0, 2.5, size=(4, 3001)).astype(np.float32)
+    a[:, ::3] = -np.inf
+    x = _rows(a, dtype, dev)
+    tok = torch.tensor([1, 4, 2000, 7], dtype=torch.int32, device=dev)
+    f = ts.vsamp_score_tokens(x, tok)
+    for g, h in ((3e38, 0.0), (0.0, 2e36), (-1e38, 1e36)):
+        d, st = ts.vsamp_score_tokens_backward(x, tok, torch.full((4,), g, device=dev), f[5], f[6], entropy=f[1],
+                                               dentropy=torch.full((4,), h, device=dev))
+        assert not st.any() and not torch.isnan(d).any() and not d[:, ::3].any()

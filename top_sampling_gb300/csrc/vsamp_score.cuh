@@ -784,11 +784,18 @@ constexpr int kGradVecs = 4;   // 16-byte vectors per thread
 
 // One row's constants. With q = 2^s2, s2 = (x - m) log2(e) / T, the gradient off the given token is
 //   -p (g + h (log p + H)) / T = q (k0 + k1 s2)
+// Where k0 + k1 s2 could pass fp32's range (smallest temperatures, largest g and h) the constants are held without 1 / T,
+// which comes last, in two factors: a token without probability then has the gradient 0, not 0 * inf.
 struct GradRow {
   float m, c, k0, k1;
-  __device__ __forceinline__ float at(float x) const {
+  float inv, scale;   // 1 / T = inv * scale
+  bool plain;         // k0 and k1 hold 1 / T
+  // the gradient of a token; own is g for the given one, 0 for the others
+  __device__ __forceinline__ float at(float x, float own) const {
     const float s = fmaxf((x - m) * c, -150.f);   // a masked token: 2^-150 is 0 in the flushed exponential
-    return ex2_approx(s) * fmaf(k1, s, k0);
+    const float q = ex2_approx(s);
+    if (plain) return q * fmaf(k1, s, k0) + own * inv;
+    return ((q > 0.f ? fmaf(q * s, k1, q * k0) : 0.f) + own) * inv * scale;
   }
 };
 
@@ -864,24 +871,31 @@ __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGra
     const float H = p.dentropy ? p.entropy[row] : 0.f;
     const bool args = t >= 0 && (int64_t)t < p.V && !isnan(temp) && !isinf(temp);
     const bool ok = args && isfinite(m) && isfinite(ls) && isfinite(H);
-    const float T1 = temp > 0.f ? temp : 1.f, invT = score_inverse(T1);
-    const float scale = -expf(-ls) * invT;
+    const float T1 = temp > 0.f ? temp : 1.f;
     const float g = !skip && p.dlogprob ? p.dlogprob[row] : 0.f;
     const float h = !skip && p.dentropy ? p.dentropy[row] : 0.f;
     GradRow r;
     r.m = m;
     r.c = score_rate(T1);
-    r.k0 = (g + h * (H - ls)) * scale;
-    r.k1 = h * 0.69314718056f * scale;
+    r.scale = T1 < 1e-37f ? 0x1p60f : 1.f;
+    r.inv = 1.f / (T1 * r.scale);
+    const float e = -expf(-ls);
+    r.k0 = (g + h * (H - ls)) * (e * r.inv);
+    r.k1 = h * 0.69314718056f * (e * r.inv);
+    r.plain = r.scale == 1.f && !(fmaf(fabsf(r.k1), 150.f, fabsf(r.k0)) > 3.4e38f);
+    if (!r.plain) {
+      r.k0 = (g + h * (H - ls)) * e;
+      r.k1 = h * 0.69314718056f * e;
+    }
     const float fill = skip ? 0.f : __int_as_float(0x7FC00000);
     if (p.row_status && span == 0 && threadIdx.x == 0)
       p.row_status[row] = skip || ok ? VSAMP_OK : args ? VSAMP_ERR_NONFINITE : VSAMP_ERR_INVALID_ARG;
     auto one = [&](int64_t v) {
       float d = fill;
-      if (ok) d = r.at(Ty::load(xr, v)) + (v == t ? g * invT : 0.f);
+      if (ok) d = r.at(Ty::load(xr, v), v == t ? g : 0.f);
       Ty::store(dr, v, d);
     };
-    const int64_t tv = ok ? (t - head) / VE : -1;   // the vector that holds the given token
+    const int64_t tv = ok && t >= head ? (t - head) / VE : -1;   // the vector that holds the given token
 #pragma unroll
     for (int i = 0; i < kGradVecs; ++i) {
       const int64_t v = v0 + i * kGradThreads;
@@ -889,13 +903,13 @@ __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGra
         if (!ok) {
           const uint32_t b = skip ? 0u : Ty::ES == 4 ? 0x7FC00000u : 0x7FC07FC0u;
           w[i][0] = w[i][1] = w[i][2] = w[i][3] = b;
-        } else if (v != tv || t < head) {
+        } else if (r.plain && v != tv) {
           grad_vector<T>(r, w[i]);
         } else {
           const int at = (int)(t - head - v * VE);
           float f[VE];
 #pragma unroll
-          for (int j = 0; j < VE; ++j) f[j] = r.at(Ty::at(w[i], j)) + (j == at ? g * invT : 0.f);
+          for (int j = 0; j < VE; ++j) f[j] = r.at(Ty::at(w[i], j), j == at ? g : 0.f);
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
             if constexpr (Ty::ES == 4) w[i][j] = __float_as_uint(f[j]);
