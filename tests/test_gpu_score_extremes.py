@@ -54,3 +54,17 @@ def test_masked_tokens_have_no_gradient_whatever_comes_in(ts, dev, dtype):
         d, st = ts.vsamp_score_tokens_backward(x, tok, torch.full((4,), g, device=dev), f[5], f[6], entropy=f[1],
                                                dentropy=torch.full((4,), h, device=dev))
         assert not st.any() and not torch.isnan(d).any() and not d[:, ::3].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", [5001, 40001])
+def test_alternatives_and_given_tokens_have_the_same_scores(ts, dev, dtype, V):
+    """The log-probability of a token is one value, whether it is given or among the alternatives."""
+    B, n = 64, 20
+    g = torch.Generator(device=dev).manual_seed(V)
+    x = (torch.randn((B, V), generator=g, device=dev) * 2.5).to(dtype)
+    T = torch.rand(B, generator=g, device=dev) * 2 + 0.2
+    out = ts.vsamp_score_tokens(x, 0, temperature=T, n_alt=n)
+    for j in (0, 1, 7, n - 1):
+        one = ts.vsamp_score_tokens(x, out[3][:, j].contiguous(), temperature=T)
+        assert torch.equal(one[0], out[4][:, j]) and (one[2] == j).all()

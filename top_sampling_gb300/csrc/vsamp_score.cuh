@@ -104,9 +104,8 @@ struct ScoreType<__nv_bfloat16> {
   }
 };
 
-// log2(e) / T and 1 / T, finite for every T > 0 (below about 1e-38 the quotients overflow, and 0 * inf is NaN)
+// log2(e) / T, finite for every T > 0 (below about 1e-38 the quotient overflows, and 0 * inf is NaN)
 __device__ __forceinline__ float score_rate(float T) { return fminf(kLog2e / T, 3.4e38f); }
-__device__ __forceinline__ float score_inverse(float T) { return fminf(1.f / T, 3.4e38f); }
 
 // max that returns NaN when either operand is NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -381,7 +380,9 @@ struct ScoreRow {
   int status;
   float m, logsum, entropy;
   uint32_t before;
-  float invT;
+  float T;
+  // the log-probability of a token from its logit: the same for the given token and for an alternative
+  __device__ __forceinline__ float logprob(float x) const { return fminf((x - m) / T - logsum, 0.f); }
 };
 
 // A warp folds the piece records of a row (every lane returns the same values). The first kFoldKeep records per lane are
@@ -409,7 +410,7 @@ struct ScoreFold {
     const float temp = p.temperature ? p.temperature[at] : 1.f;
     ScoreRow r;
     const float T1 = temp > 0.f ? temp : 1.f, c = p.temperature ? score_rate(T1) : kLog2e;   // as for the pieces
-    r.invT = score_inverse(T1);
+    r.T = T1;
     float m = -INFINITY;
     each(p, [&](float4 q) { m = max_nan(m, q.x); });
     m = warp_max_nan(m);
@@ -451,14 +452,7 @@ __device__ __forceinline__ void score_write(const ScoreParams& p, int64_t row, i
   const bool skip = t == VSAMP_TOKEN_IGNORE;
   const bool ok = r.status == VSAMP_OK && !skip;
   const float none = skip ? 0.f : __int_as_float(0x7FC00000);
-  if (p.logprob) {
-    float lp = none;
-    if (ok) {
-      const float temp = p.temperature ? p.temperature[row] : 1.f;
-      lp = fminf((xt - r.m) / (temp > 0.f ? temp : 1.f) - r.logsum, 0.f);
-    }
-    p.logprob[row] = lp;
-  }
+  if (p.logprob) p.logprob[row] = ok ? r.logprob(xt) : none;
   if (p.entropy) p.entropy[row] = ok ? r.entropy : none;
   if (p.rank) p.rank[row] = ok ? (int32_t)r.before : -1;
   if (p.row_max) p.row_max[row] = ok ? r.m : none;
@@ -716,8 +710,7 @@ __device__ __forceinline__ void score_finish_alt(const ScoreParams& p, int64_t r
         for (uint32_t j = 0; j < n; ++j) place += sm.list[j] > k ? 1u : 0u;
         if (place < (uint32_t)p.N) {
           oi[place] = (int32_t)~(uint32_t)k;
-          const float s = (value_of_key32((uint32_t)(k >> 32)) - r.m) * r.invT;
-          ol[place] = fminf(s - r.logsum, 0.f);
+          ol[place] = r.logprob(value_of_key32((uint32_t)(k >> 32)));
         }
       }
     }
