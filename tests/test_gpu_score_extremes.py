@@ -4,14 +4,15 @@ import numpy as np
 import pytest
 
 import tables_util as tu
-from test_gpu_score import DTYPES, _rows, dev, ts  # noqa: F401
+from test_gpu_score import DTYPES, _check, _rows, dev, ts  # noqa: F401
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 
 def _gradient(ts, x, token, temps, g, h):
-    """The gradient against the formula's. Where its bound reaches past the type's largest value an infinity is as good."""
+    """The gradient against the formula's. Where its bound reaches past the type's largest value an infinity is as good;
+    a token whose exponential is below 2^-126 (allowing for its rounding) may count as one without probability."""
     d = x.device
     tok, T = torch.tensor(token, dtype=torch.int32, device=d), torch.tensor(temps, dtype=torch.float32, device=d)
     gt, ht = torch.tensor(g, dtype=torch.float32, device=d), torch.tensor(h, dtype=torch.float32, device=d)
@@ -23,7 +24,10 @@ def _gradient(ts, x, token, temps, g, h):
     for r in range(len(token)):
         want, size = tu.grad_row(xs[r], token[r], float(np.float32(temps[r])), float(np.float32(g[r])),
                                  float(np.float32(h[r])))
-        tol = tu.GRAD_REL * size + tu.HALF[x.dtype] * np.abs(want) + 1e-37
+        t = float(np.float32(temps[r]))
+        small = np.exp((xs[r] - xs[r].max()) / t) < 2.0 ** -125
+        small[token[r]] = False
+        tol = np.where(small, size, tu.GRAD_REL * size) + tu.HALF[x.dtype] * np.abs(want) + 1e-37
         near, beyond = np.abs(want) + tol <= largest, np.abs(want) - tol > largest
         assert np.all(np.abs(got[r] - want)[near] <= tol[near]), (r, temps[r])
         assert np.all(got[r][beyond] == np.inf * np.sign(want[beyond])), (r, temps[r])
@@ -68,3 +72,38 @@ def test_alternatives_and_given_tokens_have_the_same_scores(ts, dev, dtype, V):
     for j in (0, 1, 7, n - 1):
         one = ts.vsamp_score_tokens(x, out[3][:, j].contiguous(), temperature=T)
         assert torch.equal(one[0], out[4][:, j]) and (one[2] == j).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [0, 20])
+def test_differences_beyond_the_largest_value(ts, dev, monkeypatch, dtype, n):
+    """Finite logits whose difference is not, at temperatures that bring it back; at T = 1 a log-probability beyond the
+    largest value is an infinity."""
+    def score_row(*args):
+        status, lp, *rest = exact(*args)
+        return (status, -np.inf if lp < -torch.finfo(torch.float32).max else lp, *rest)
+
+    exact = tu.score_row
+    monkeypatch.setattr(tu, "score_row", score_row)
+    temps = [2e36, 1e37, 1e38, 3e38, 1.0, 4e36]
+    rng = np.random.default_rng(9)
+    a = rng.uniform(-3e38, 3e38, size=(len(temps), 5001)).astype(np.float32)
+    a[:, ::3] = -np.inf
+    a[5] = -1.1e38                                             # far below two equal maxima
+    a[5, 10] = a[5, 4000] = 3e38
+    x = _rows(a, dtype, dev)
+    _check(ts, x, [1, 2, 4, 5, 7, 10], temps, n)
+    _check(ts, x, [int(np.nanargmax(tu.f64(x)[r])) for r in range(len(temps))], temps, n)
+    _gradient(ts, x, [1, 2, 4, 5, 7, 10], temps, [1e38] * len(temps), [1e37] * len(temps))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [0, 20])
+def test_smallest_differences_at_smallest_temperatures(ts, dev, dtype, n):
+    temps = [1e-39, 3e-39, 1e-38, 5e-38, 2e-37, 1e-36]
+    rng = np.random.default_rng(10)
+    a = (rng.integers(-60, 0, size=(len(temps), 5001)) * 2.0 ** -128).astype(np.float32)      # subnormal values
+    a[:, ::3] = -np.inf
+    x = _rows(a, dtype, dev)
+    _check(ts, x, [1, 2, 4, 5, 7, 10], temps, n)
+    _gradient(ts, x, [1, 2, 4, 5, 7, 10], temps, [1.0] * len(temps), [0.1] * len(temps))

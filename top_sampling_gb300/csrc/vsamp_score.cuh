@@ -104,8 +104,27 @@ struct ScoreType<__nv_bfloat16> {
   }
 };
 
-// log2(e) / T, finite for every T > 0 (below about 1e-38 the quotient overflows, and 0 * inf is NaN)
-__device__ __forceinline__ float score_rate(float T) { return fminf(kLog2e / T, 3.4e38f); }
+// s_v log2(e) = ((x down - m down) up) c for a temperature T > 0, where no step but the last leaves fp32's range when the
+// result does not. `scale` is 1 for ordinary temperatures; below 1e-37 it is 2^60 and stands in `up` (1 / T would
+// overflow), above 1e36 it is 2^-60 and stands in `down` (x - m could, and 1 / T loses digits).
+struct ScoreRate {
+  float T, c, scale, up, down;
+  static __device__ __forceinline__ float read(const float* temperature, int64_t row) {
+    return temperature && temperature[row] > 0.f ? temperature[row] : 1.f;
+  }
+  static __device__ __forceinline__ bool ordinary(float T) { return T >= 1e-37f && T <= 1e36f; }
+  static __device__ __forceinline__ ScoreRate of(float T) {
+    ScoreRate r;
+    r.T = T;
+    r.scale = ordinary(T) ? 1.f : T < 1.f ? 0x1p60f : 0x1p-60f;
+    r.up = fmaxf(r.scale, 1.f);
+    r.down = fminf(r.scale, 1.f);
+    r.c = kLog2e / (T * r.scale);
+    return r;
+  }
+  __device__ __forceinline__ float exponent(float x, float m) const { return fmaf(x, down, -m * down) * up * c; }
+  __device__ __forceinline__ float s(float x, float m) const { return fmaf(x, down, -m * down) / (T * down); }
+};
 
 // max that returns NaN when either operand is NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -202,17 +221,18 @@ __device__ __forceinline__ uint32_t count_larger(const uint32_t (&w)[kScoreChunk
   }
 }
 
-// A lane's sums of 2^s2 and s2 2^s2, s2 = (x - m) c, over its vectors. A masked token must add 0 to both, and s2 2^s2
-// is NaN at s2 = -inf: elements are raised to `lowest`, whose exponential is flushed to 0 (2^-150), two bf16 at once
-// (RAISE), or, at a temperature so large that no finite value is that low, or so small that no value lies between, the
-// products are.
+// A lane's sums of 2^s2 and s2 2^s2 over its vectors. A masked token must add 0 to both, and s2 2^s2 is NaN at s2 = -inf.
+// RAISE, for ordinary temperatures: s2 = (x - m) c, and elements are raised to `lowest`, whose exponential is flushed to
+// 0 (2^-150), two bf16 at once. Otherwise (a temperature so large that no finite value is that low, or so small that no
+// value lies between, or outside ScoreRate's ordinary ones) the exponents are raised.
 // (One fused multiply-add x c - m c instead of the difference and the product is 8% fewer instructions, but then the
 // maximum's own exponential is not exactly 1, and a row with one likely token loses the digits of its log-probability.)
 template <typename T, bool RAISE>
-__device__ __forceinline__ void score_sums(const uint32_t (&w)[kScoreChunks][4], float m, float c, float lowest, float& S,
-                                           float& A) {
+__device__ __forceinline__ void score_sums(const uint32_t (&w)[kScoreChunks][4], float m, const ScoreRate& r, float lowest,
+                                           float& S, float& A) {
   using Ty = ScoreType<T>;
-  const float2 m2 = make_float2(-m, -m), c2 = make_float2(c, c);
+  const float md = RAISE ? -m : -m * r.down;
+  const float2 m2 = make_float2(md, md), c2 = make_float2(r.c, r.c);
   float2 S2[2] = {{0.f, 0.f}, {0.f, 0.f}}, A2[2] = {{0.f, 0.f}, {0.f, 0.f}};
   uint32_t low = __float_as_uint(lowest);
   if (sizeof(T) == 2) low = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rd(lowest)) * 0x10001u;
@@ -224,8 +244,14 @@ __device__ __forceinline__ void score_sums(const uint32_t (&w)[kScoreChunks][4],
 #pragma unroll
     for (int j = 0; j < Ty::VE; j += 2) {
       const float2 x = make_float2(Ty::at(v, j), Ty::at(v, j + 1));
-      float2 s = __fmul2_rn(__fadd2_rn(x, m2), c2);
-      if (!RAISE) s = make_float2(fmaxf(s.x, -150.f), fmaxf(s.y, -150.f));
+      float2 s;
+      if (RAISE) {
+        s = __fmul2_rn(__fadd2_rn(x, m2), c2);
+      } else {
+        const float2 d = __ffma2_rn(x, make_float2(r.down, r.down), m2);
+        s = __fmul2_rn(__fmul2_rn(d, make_float2(r.up, r.up)), c2);
+        s = make_float2(fmaxf(s.x, -150.f), fmaxf(s.y, -150.f));
+      }
       const float2 e = make_float2(ex2_approx(s.x), ex2_approx(s.y));
       const int k = (j >> 1) & 1;
       S2[k] = __fadd2_rn(S2[k], e);
@@ -296,8 +322,7 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
 #pragma unroll
     for (int i = 0; i < kScoreChunks; ++i) score_load<T>(xr, (int64_t)e0 + i * CE + lane * Ty::VE, p.V, p.vec, w[i]);
   }
-  const float temp = p.temperature ? p.temperature[row] : 1.f;
-  const float T1 = temp > 0.f ? temp : 1.f, c = p.temperature ? score_rate(T1) : kLog2e;
+  const float T1 = ScoreRate::read(p.temperature, row), c = p.temperature ? kLog2e / T1 : kLog2e;
   const bool known = t >= 0 && t < V;
   const float xt = known ? Ty::load(xr, t) : INFINITY;
 
@@ -348,11 +373,12 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
 
   float S = 0.f, A = 0.f;
   if (m > -INFINITY && m < INFINITY) {   // false for NaN too
-    // 104 log2(e) > 150; below m, too: at a temperature far below the maximum's last place it is m itself. A rate held
-    // at the largest float (score_rate) no longer brings it to 2^-150.
+    // 104 log2(e) > 150; below m, too: at a temperature far below the maximum's last place it is m itself
     const float lowest = fmaf(-104.f, T1, m);
-    if (lowest < m && lowest > -3.3e38f && c < 3.4e38f) score_sums<T, true>(w, m, c, lowest, S, A);
-    else score_sums<T, false>(w, m, c, lowest, S, A);
+    if (ScoreRate::ordinary(T1) && lowest < m && lowest > -3.3e38f)
+      score_sums<T, true>(w, m, ScoreRate{T1, c, 1.f, 1.f, 1.f}, lowest, S, A);
+    else
+      score_sums<T, false>(w, m, ScoreRate::of(T1), lowest, S, A);
   }
   S = warp_sum_f(S);
   A = warp_sum_f(A);
@@ -380,9 +406,9 @@ struct ScoreRow {
   int status;
   float m, logsum, entropy;
   uint32_t before;
-  float T;
+  ScoreRate rate;
   // the log-probability of a token from its logit: the same for the given token and for an alternative
-  __device__ __forceinline__ float logprob(float x) const { return fminf((x - m) / T - logsum, 0.f); }
+  __device__ __forceinline__ float logprob(float x) const { return fminf(rate.s(x, m) - logsum, 0.f); }
 };
 
 // A warp folds the piece records of a row (every lane returns the same values). The first kFoldKeep records per lane are
@@ -409,8 +435,7 @@ struct ScoreFold {
   __device__ __forceinline__ ScoreRow row(const ScoreParams& p, int64_t at, int32_t t) const {
     const float temp = p.temperature ? p.temperature[at] : 1.f;
     ScoreRow r;
-    const float T1 = temp > 0.f ? temp : 1.f, c = p.temperature ? score_rate(T1) : kLog2e;   // as for the pieces
-    r.T = T1;
+    r.rate = ScoreRate::of(ScoreRate::read(p.temperature, at));
     float m = -INFINITY;
     each(p, [&](float4 q) { m = max_nan(m, q.x); });
     m = warp_max_nan(m);
@@ -421,7 +446,7 @@ struct ScoreFold {
       each(p, [&](float4 q) {
         before += __float_as_uint(q.w);
         if (q.x > -INFINITY) {
-          const float d = fmaxf((q.x - m) * c, -150.f);
+          const float d = fmaxf(r.rate.exponent(q.x, m), -150.f);
           const float f = ex2_approx(d);
           S = fmaf(f, q.y, S);
           A = fmaf(f, fmaf(d, q.y, q.z), A);
@@ -777,18 +802,23 @@ constexpr int kGradVecs = 4;   // 16-byte vectors per thread
 
 // One row's constants. With q = 2^s2, s2 = (x - m) log2(e) / T, the gradient off the given token is
 //   -p (g + h (log p + H)) / T = q (k0 + k1 s2)
-// Where k0 + k1 s2 could pass fp32's range (smallest temperatures, largest g and h) the constants are held without 1 / T,
-// which comes last, in two factors: a token without probability then has the gradient 0, not 0 * inf.
 struct GradRow {
   float m, c, k0, k1;
-  float inv, scale;   // 1 / T = inv * scale
-  bool plain;         // k0 and k1 hold 1 / T
-  // the gradient of a token; own is g for the given one, 0 for the others
-  __device__ __forceinline__ float at(float x, float own) const {
+  __device__ __forceinline__ float at(float x) const {
     const float s = fmaxf((x - m) * c, -150.f);   // a masked token: 2^-150 is 0 in the flushed exponential
-    const float q = ex2_approx(s);
-    if (plain) return q * fmaf(k1, s, k0) + own * inv;
-    return ((q > 0.f ? fmaf(q * s, k1, q * k0) : 0.f) + own) * inv * scale;
+    return ex2_approx(s) * fmaf(k1, s, k0);
+  }
+};
+
+// The same where k0 + k1 s2 could pass fp32's range (extreme temperatures, largest g and h): the constants are held
+// without 1 / T, which comes last, and a token without probability has the gradient 0, not 0 * inf.
+struct GradRowWide {
+  ScoreRate rate;
+  float m, k0, k1;
+  // own: g for the given token, 0 for the others
+  __device__ __forceinline__ float at(float x, float own) const {
+    const float s = fmaxf(rate.exponent(x, m), -150.f), q = ex2_approx(s);
+    return ((q > 0.f ? fmaf(q * s, k1, q * k0) : 0.f) + own) * (1.f / (rate.T * rate.scale)) * rate.scale;
   }
 };
 
@@ -864,28 +894,28 @@ __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGra
     const float H = p.dentropy ? p.entropy[row] : 0.f;
     const bool args = t >= 0 && (int64_t)t < p.V && !isnan(temp) && !isinf(temp);
     const bool ok = args && isfinite(m) && isfinite(ls) && isfinite(H);
-    const float T1 = temp > 0.f ? temp : 1.f;
+    const float T1 = temp > 0.f ? temp : 1.f, invT = 1.f / T1, e = -expf(-ls);
     const float g = !skip && p.dlogprob ? p.dlogprob[row] : 0.f;
     const float h = !skip && p.dentropy ? p.dentropy[row] : 0.f;
     GradRow r;
     r.m = m;
-    r.c = score_rate(T1);
-    r.scale = T1 < 1e-37f ? 0x1p60f : 1.f;
-    r.inv = 1.f / (T1 * r.scale);
-    const float e = -expf(-ls);
-    r.k0 = (g + h * (H - ls)) * (e * r.inv);
-    r.k1 = h * 0.69314718056f * (e * r.inv);
-    r.plain = r.scale == 1.f && !(fmaf(fabsf(r.k1), 150.f, fabsf(r.k0)) > 3.4e38f);
-    if (!r.plain) {
-      r.k0 = (g + h * (H - ls)) * e;
-      r.k1 = h * 0.69314718056f * e;
-    }
+    r.c = kLog2e / T1;
+    r.k0 = (g + h * (H - ls)) * (e * invT);
+    r.k1 = h * 0.69314718056f * (e * invT);
+    const bool wide = !ScoreRate::ordinary(T1) || fmaf(fabsf(r.k1), 150.f, fabsf(r.k0)) > 3.4e38f;
     const float fill = skip ? 0.f : __int_as_float(0x7FC00000);
     if (p.row_status && span == 0 && threadIdx.x == 0)
       p.row_status[row] = skip || ok ? VSAMP_OK : args ? VSAMP_ERR_NONFINITE : VSAMP_ERR_INVALID_ARG;
+    if (ok && wide) {   // a rare row: element by element
+      const GradRowWide rw{ScoreRate::of(T1), m, (g + h * (H - ls)) * e, h * 0.69314718056f * e};
+      const int64_t first = span == 0 ? 0 : head + span * SPAN * VE, last = head + (span + 1) * SPAN * VE;
+      for (int64_t v = first + threadIdx.x; v < (span + 1 == p.spans || last > p.V ? p.V : last); v += kGradThreads)
+        Ty::store(dr, v, rw.at(Ty::load(xr, v), v == t ? g : 0.f));
+      continue;
+    }
     auto one = [&](int64_t v) {
       float d = fill;
-      if (ok) d = r.at(Ty::load(xr, v), v == t ? g : 0.f);
+      if (ok) d = r.at(Ty::load(xr, v)) + (v == t ? g * invT : 0.f);
       Ty::store(dr, v, d);
     };
     const int64_t tv = ok && t >= head ? (t - head) / VE : -1;   // the vector that holds the given token
@@ -896,13 +926,13 @@ __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGra
         if (!ok) {
           const uint32_t b = skip ? 0u : Ty::ES == 4 ? 0x7FC00000u : 0x7FC07FC0u;
           w[i][0] = w[i][1] = w[i][2] = w[i][3] = b;
-        } else if (r.plain && v != tv) {
+        } else if (v != tv) {
           grad_vector<T>(r, w[i]);
         } else {
           const int at = (int)(t - head - v * VE);
           float f[VE];
 #pragma unroll
-          for (int j = 0; j < VE; ++j) f[j] = r.at(Ty::at(w[i], j), j == at ? g : 0.f);
+          for (int j = 0; j < VE; ++j) f[j] = r.at(Ty::at(w[i], j)) + (j == at ? g * invT : 0.f);
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
             if constexpr (Ty::ES == 4) w[i][j] = __float_as_uint(f[j]);
