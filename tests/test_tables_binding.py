@@ -1,0 +1,29 @@
+"""What the binding of the vocabulary-side operators takes, refuses and keeps."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import top_sampling_gb300 as ts  # noqa: E402
+
+
+def test_rows_of_alternatives():
+    flat = torch.zeros(12)
+    assert ts._alternatives(flat, 3, "alt_lp") is flat
+    assert ts._alternatives(flat.view(4, 3), 3, "alt_lp").shape == (4, 3)
+    for shape in ((3, 4), (2, 6)):
+        with pytest.raises(ValueError):
+            ts._alternatives(flat.view(shape), 3, "alt_lp")
+
+
+@pytest.mark.gpu
+def test_wider_arrays_of_alternatives_are_refused():
+    dev = torch.device("cuda:0")
+    x, tok = torch.randn(3, 100, device=dev), torch.zeros(3, dtype=torch.int32, device=dev)
+    idx, lp = torch.zeros(3, 64, dtype=torch.int32, device=dev), torch.zeros(3, 64, device=dev)
+    with pytest.raises(ValueError):
+        ts.vsamp_score_tokens(x, tok, n_alt=20, alt_idx=idx)
+    with pytest.raises(ValueError):
+        ts.vsamp_score_tokens(x, tok, n_alt=20, alt_lp=lp)
+    # more rows than the batch are fine
+    out = ts.vsamp_score_tokens(x[:2], tok[:2], n_alt=64, alt_idx=idx, alt_lp=lp)
+    assert out[3] is idx and not idx[2].any()

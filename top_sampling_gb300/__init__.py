@@ -694,6 +694,13 @@ def _logits_matrix(x: torch.Tensor, V, index: int):
     return B, int(V), ld
 
 
+def _alternatives(t, n_alt: int, name: str):
+    """A caller's array of alternatives: rows of n_alt, which is how the library fills it."""
+    if t.dim() > 1 and t.shape[-1] != n_alt:
+        raise ValueError(f"{name} must have rows of {n_alt}, got {tuple(t.shape)}")
+    return t
+
+
 def vsamp_score_tokens(logits, token, temperature=None, n_alt=0, V=None, logprob=None, entropy=None, rank=None,
                        alt_idx=None, alt_lp=None, row_max=None, row_logsum=None, row_status=None, workspace=None,
                        stream=None):
@@ -721,8 +728,8 @@ def vsamp_score_tokens(logits, token, temperature=None, n_alt=0, V=None, logprob
     rank = empty(B, dtype=i32, device=dev) if rank is None else rank
     row_status = empty(B, dtype=i32, device=dev) if row_status is None else row_status
     if n_alt:
-        alt_idx = empty((B, n_alt), dtype=i32, device=dev) if alt_idx is None else alt_idx
-        alt_lp = empty((B, n_alt), dtype=f32, device=dev) if alt_lp is None else alt_lp
+        alt_idx = empty((B, n_alt), dtype=i32, device=dev) if alt_idx is None else _alternatives(alt_idx, n_alt, "alt_idx")
+        alt_lp = empty((B, n_alt), dtype=f32, device=dev) if alt_lp is None else _alternatives(alt_lp, n_alt, "alt_lp")
     else:
         alt_idx = alt_lp = None
     lib, on = load(), _current(at)
