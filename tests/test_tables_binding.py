@@ -27,3 +27,16 @@ def test_wider_arrays_of_alternatives_are_refused():
     # more rows than the batch are fine
     out = ts.vsamp_score_tokens(x[:2], tok[:2], n_alt=64, alt_idx=idx, alt_lp=lp)
     assert out[3] is idx and not idx[2].any()
+
+
+def test_token_ids_outside_32_bits_stay_outside_every_vocabulary():
+    cpu = torch.device("cpu")
+    low, high = -(1 << 31), (1 << 31) - 1
+    far = torch.tensor([1 << 40, -(1 << 40), (1 << 32) - 100, 5])
+    assert ts._token_ids(far, 4, cpu).tolist() == [high, low, high, 5]
+    wide = torch.tensor([(1 << 32) - 100, 7], dtype=torch.int64).to(torch.uint32)     # -100 in 32 bits marks ignored tokens
+    assert ts._token_ids(wide, 2, cpu).tolist() == [high, 7]
+    assert ts._token_ids(1 << 40, 2, cpu).tolist() == [high, high]
+    assert ts._token_ids(-(1 << 40), 1, cpu).tolist() == [low]
+    for dt in (torch.int8, torch.int16, torch.uint8, torch.int32):
+        assert ts._token_ids(torch.tensor([3, 100], dtype=dt), 2, cpu).tolist() == [3, 100]

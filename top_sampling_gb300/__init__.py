@@ -659,10 +659,10 @@ def _token_ids(v, n: int, dev):
             return v if v.is_contiguous() and v.device == dev else v.to(device=dev).contiguous()
         if v.is_floating_point() or v.is_complex():
             raise TypeError(f"token must hold whole numbers, got {v.dtype}")
-        if v.dtype is torch.int64:
-            v = v.clamp(-(1 << 31), (1 << 31) - 1)
+        if v.dtype.itemsize > 2:
+            v = v.to(torch.int64).clamp(-(1 << 31), (1 << 31) - 1)
         return v.to(device=dev, dtype=torch.int32).contiguous()
-    return torch.full((n,), int(v), dtype=torch.int32, device=dev)
+    return torch.full((n,), min(max(int(v), -(1 << 31)), (1 << 31) - 1), dtype=torch.int32, device=dev)
 
 
 def _row_values(v, n: int, dev, name):
