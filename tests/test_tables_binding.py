@@ -40,3 +40,18 @@ def test_token_ids_outside_32_bits_stay_outside_every_vocabulary():
     assert ts._token_ids(-(1 << 40), 1, cpu).tolist() == [low]
     for dt in (torch.int8, torch.int16, torch.uint8, torch.int32):
         assert ts._token_ids(torch.tensor([3, 100], dtype=dt), 2, cpu).tolist() == [3, 100]
+
+
+def test_kept_workspaces_are_few(monkeypatch):
+    """A program that goes through many streams does not keep a workspace for each of them."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(ts, "_LOCAL", type(ts._LOCAL)())
+    cpu = torch.device("cpu")
+    first = ts._scratch(100, cpu, 0, 1)
+    assert ts._scratch(60, cpu, 0, 1) is first and ts._scratch(200, cpu, 0, 1).numel() == 200
+    for stream in range(2, 100):
+        mine = ts._scratch(100, cpu, 0, stream)
+        assert ts._scratch(100, cpu, 0, stream) is mine
+    kept = ts._LOCAL.__dict__
+    assert len(kept) <= ts._SCRATCH_STREAMS and (0, 99) in kept
+    assert ts._scratch(ts._SCRATCH_KEPT + 1, cpu, 0, 99).numel() > kept[(0, 99)].numel()

@@ -637,17 +637,21 @@ def _at(t, dtype, index: int, n: int, name: str):
 
 _LOCAL = threading.local()
 _SCRATCH_KEPT = 4 << 20   # bytes of the largest workspace that is kept
+_SCRATCH_STREAMS = 8      # workspaces kept per host thread
 
 
 def _scratch(nbytes: int, dev, index: int, stream: int) -> torch.Tensor:
     """A call's workspace. Small ones are kept per host thread, device and stream, because allocating one costs a decode
-    step's call a third of its host time; nothing is kept in them. A stream's calls never overlap, but those of two
-    threads may interleave on one stream. A call that is captured into a graph gets its own, from the graph's memory."""
+    step's call a third of its host time; nothing is kept in them, and a thread keeps those of its latest streams only. A
+    stream's calls never overlap, but those of two threads may interleave on one stream. A call that is captured into a
+    graph gets its own, from the graph's memory."""
     if nbytes > _SCRATCH_KEPT or torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     kept = _LOCAL.__dict__
     ws = kept.get((index, stream))
     if ws is None or ws.numel() < nbytes:
+        if ws is None and len(kept) >= _SCRATCH_STREAMS:
+            del kept[next(iter(kept))]   # the oldest: its stream's later calls allocate anew
         ws = kept[(index, stream)] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     return ws
 
