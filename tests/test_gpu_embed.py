@@ -152,3 +152,21 @@ def test_other_stream_and_graph(ts, dev):
     ds.copy_(dout)
     graph.replay()
     assert torch.equal(d, ref) and torch.equal(y, table[tok.long()])
+
+
+@pytest.mark.parametrize("V,D", [(300, 40), (20000, 500)])            # a small table, and one of 40 MB
+@pytest.mark.parametrize("N", [255, 256, 257, 1023, 1024, 1025])
+def test_gradient_on_both_sides_of_the_forms_limits(ts, dev, N, V, D):
+    """The forms of few and of many positions, written whole and added, with the workspace that the library asks for."""
+    rng = np.random.default_rng(N)
+    tok = rng.integers(0, V, size=N).astype(np.int32)
+    tok[: N // 4] = 3
+    tok[::9] = tu.IGNORE
+    dout = torch.from_numpy(rng.normal(size=(N, D)).astype(np.float32)).to(dev)
+    lib = ts.load()
+    ws = torch.empty(lib.vsamp_embed_workspace_size(N, D), dtype=torch.uint8, device=dev)
+    for accumulate in (False, True):
+        want, tol = tu.embed_grad(tok.astype(np.int64), tu.f64(dout), V, 2.0, np.ones((V, D)) if accumulate else None)
+        d = ts.vsamp_embed_backward(torch.from_numpy(tok).to(dev), dout, V, scale=2.0, workspace=ws,
+                                    dtable=torch.ones((V, D), device=dev), accumulate=accumulate)
+        assert np.all(np.abs(tu.f64(d) - want) <= tol + tu.U * np.abs(want))

@@ -80,6 +80,18 @@ static vsamp_status launch_embed_few(const EmbedGradParams& p, cudaStream_t s) {
   return launch_1d(embed_few_kernel<TI, TO, VE>, grid_of(p.N * spans), kEmbedThreads, 0, s, p, (int)spans);
 }
 
+// Whether a call takes the form of few positions (embed_few_kernel) instead of the sort. Added to the table it wins as far
+// as it goes (1,024 positions: 1,001 fp32 columns 10.4 against 22.0 us, 8,192 columns 18.6 against 27.5, 64 columns 6.5
+// against 16.8). Written whole it waits for the zeros, which the sort runs beside: it wins up to about 300 positions
+// (256: 15.1 against 17.1 us for a table of 65 MB, 17.1 against 18.7 for 77 MB; 384: 24.0 against 17.2 and 23.7 against
+// 19.2; 1,024: 25.3 against 17.9), and with small tables, whose zeros are short (2 MB, 1,024 positions: 11.5 against 14.9
+// us; 26 MB, 700: 11.7 against 15.9). A table of 1.2 GB takes 192 against 190 us at 256 positions.
+// The tokens are not known here: 1,024 positions of one token, added in one chain, take 84 us against 20.
+constexpr int64_t kFewWhole = 256, kFewSmallTable = 32 << 20;
+static bool takes_few(int64_t N, bool accumulate, int64_t table_bytes) {
+  return N <= (accumulate || table_bytes <= kFewSmallTable ? (int64_t)kEmbedFew : kFewWhole);
+}
+
 template <typename TI, typename TO>
 static vsamp_status launch_embed_grad(EmbedGradParams p, const DeviceInfo& d, int dev, cudaStream_t s) {
   constexpr int VE = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4;
@@ -88,7 +100,7 @@ static vsamp_status launch_embed_grad(EmbedGradParams p, const DeviceInfo& d, in
   ZeroParams z{};
   if (!p.accumulate) z = zero_params<TO>(p);
   const int64_t zero_warps = z.nrows < (int64_t)d.sm_count * 64 ? z.nrows : (int64_t)d.sm_count * 64;
-  if (p.N <= kEmbedFew) {
+  if (takes_few(p.N, p.accumulate, p.V * p.D * (int64_t)sizeof(TO))) {
     if (z.nrows > 0) {
       st = launch_1d(embed_zero_kernel, grid_of(ceil_div(zero_warps, kEmbedThreads / 32)), kEmbedThreads, 0, s, z);
       if (st != VSAMP_OK) return st;
@@ -145,7 +157,7 @@ static EmbedPlan embed_plan(int64_t N, int64_t D) {
   e.hist = up((size_t)e.tiles * kSortBins * 4);
   e.part = up((size_t)e.sums * 2 * (size_t)e.ldp * 4);
   e.runs = up((size_t)e.sums * 4) + 256;
-  e.total = N <= kEmbedFew ? 16 : 2 * e.keys + e.hist + e.part + e.runs;   // few positions need none
+  e.total = 2 * e.keys + e.hist + e.part + e.runs;
   return e;
 }
 
@@ -182,7 +194,7 @@ vsamp_status vsamp_embed(const int32_t* token, int64_t N, const void* table, vsa
 
 size_t vsamp_embed_workspace_size(int64_t N, int64_t D) {
   if (N <= 0 || D <= 0 || N > 0x7FFFFFFFLL || D > 0x3FFFFFFFLL) return 0;
-  return embed_plan(N, D).total;
+  return N <= kFewWhole ? 16 : embed_plan(N, D).total;   // few positions need none
 }
 
 vsamp_status vsamp_embed_backward(const int32_t* token, int64_t N, const void* dout, vsamp_dtype dt, int64_t D,
@@ -194,7 +206,8 @@ vsamp_status vsamp_embed_backward(const int32_t* token, int64_t N, const void* d
   if (!elem_aligned(dout, dt) || !elem_aligned(dtable, table_dt)) return VSAMP_ERR_INVALID_ARG;
   if (V > 0x7FFFFFF0LL || N > 0x7FFFFFFFLL || D > 0x3FFFFFFFLL) return VSAMP_ERR_UNSUPPORTED;
   const EmbedPlan e = embed_plan(N, D);
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0 || workspace_bytes < e.total)
+  const size_t need = takes_few(N, accumulate != 0, V * D * (table_dt == VSAMP_F32 ? 4 : 2)) ? 16 : e.total;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0 || workspace_bytes < need)
     return VSAMP_ERR_INVALID_ARG;
   EmbedGradParams p{};
   p.token = token;
