@@ -369,8 +369,8 @@ vsamp_status vsamp_score_tokens(const void* logits, vsamp_dtype dt, int64_t B, i
  *   row_max, row_logsum, entropy  as vsamp_score_tokens wrote them for the same logits, tokens and temperature.
  *   dlogits   [B, ldd] of the logits' type, rounded once; it may be the logits' own buffer with the same stride
  *             (the logits are then replaced).
- * Masked tokens have p = 0, and so have tokens with exp(s_v) below 2^-126. An ignored row's gradient is 0. A row that vsamp_score_tokens refused gets NaN and its
- * status. One launch on `stream`. */
+ * Masked tokens have p = 0, and so have tokens with exp(s_v) below 2^-126. An ignored row's gradient is 0. A row that
+ * vsamp_score_tokens refused gets NaN and its status. One launch on `stream`. */
 vsamp_status vsamp_score_tokens_backward(const void* logits, vsamp_dtype dt, int64_t B, int64_t V, int64_t ld,
                                          const float* temperature, const int32_t* token, const float* dlogprob,
                                          const float* dentropy, const float* row_max, const float* row_logsum,
@@ -386,7 +386,8 @@ vsamp_status vsamp_score_tokens_backward(const void* logits, vsamp_dtype dt, int
  * vsamp_head_pack lays the weights out once (vsamp_head_packed_size bytes, 16-byte aligned) for any number of
  * vsamp_head_logits calls. hidden is [M, ldh], fp32 or bf16, logits [M, ld], fp32 or bf16 (the sampler's input);
  * scale_dt, has_zeros, V, D and group are those of the pack. Products are exact, sums fp32, one rounding at the end.
- * The weights are read once per 64 hidden rows: the call is meant for the few rows of a decode step. */
+ * The weights are read once per 64 bf16 hidden rows, or per 16 fp32 ones (each of those is three columns of the
+ * product): the call is meant for the few rows of a decode step. */
 size_t vsamp_head_packed_size(vsamp_dtype scale_dt, int32_t has_zeros, int64_t V, int64_t D, int32_t group);
 vsamp_status vsamp_head_pack(const uint8_t* codes, const void* scales, vsamp_dtype scale_dt, const uint8_t* zeros,
                              int64_t V, int64_t D, int32_t group, void* packed, size_t packed_bytes, void* stream);

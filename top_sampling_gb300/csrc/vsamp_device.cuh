@@ -105,8 +105,9 @@ __device__ __forceinline__ bool mbar_wait_bounded(void* bar, uint32_t parity, lo
   }
 }
 
-// First statement of a kernel whose launch may overlap the stream's previous one (launch_1d in vsamp_grid.h): waits until
-// that kernel has finished and its writes are visible, then lets the next such launch be set up.
+// Stands before the first memory access of a kernel whose launch may overlap the stream's previous one (launch_1d in
+// vsamp_grid.h): waits until that kernel has finished and its writes are visible, then lets the next such launch be set
+// up.
 __device__ __forceinline__ void begin_overlapped() {
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();

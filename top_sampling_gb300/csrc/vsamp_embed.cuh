@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_zero_kernel(const ZeroPar
 // first, stable: a warp takes consecutive keys 32 at a time, equal digits keep their order. A thread's keys and their
 // places among equal digits of its warp stay in registers between the count and the move, so one buffer is enough.
 // 16384 positions take about 30 us in one CTA, bound by the warp matches; beside the zeros of a large table (1.2 GB, 186
-// us) they cost nothing.
+// us) they cost nothing. Where the zeros end sooner, or nothing is zeroed, the sort stands alone: 16384 positions take 64
+// us into 32000 x 1024 bf16 (bytes: 15), about what the sort in several launches takes for one position more (63).
 constexpr int kSortOne = 16384;
 constexpr int kSortOneThreads = 1024;
 constexpr int kSortOnePer = kSortOne / kSortOneThreads;

@@ -7,13 +7,19 @@
 // bf16, products with bf16 hidden states are exact, sums are fp32, and the group's scale multiplies the fp32 sum of
 // its group. fp32 hidden states are split into three bf16 terms, each a column of its own.
 //
-// What bounds it. M = 1: the bytes (151936 x 4096, groups of 128: 54.9 us, 88% of the copy rate). From about eight rows
-// on the issue slots: widening costs 11 instructions per eight weights and lane, a product of eight columns about four
-// slots and eight cycles of its unit (measured alone: 8.1 cycles; beside 12 independent multiply-adds 16.4), so 24 rows
-// take 70 us where the bytes take 37 (151936 x 2560, groups of 32).
+// What bounds it. M = 1: the bytes (151936 x 4096, groups of 128: 55 us, 87% of the copy rate). From about eight rows on
+// the issue slots and the matrix unit together: widening costs 11 instructions per eight weights and lane, a product of
+// eight columns about four slots and eight cycles of its unit (measured alone: 8.1 cycles; beside 12 independent
+// multiply-adds 16.4), so 24 rows take 70 us where the bytes take 37 (151936 x 2560, groups of 32). From six column tiles
+// on (33 rows) a warp holds one row tile, so every matrix step reads all staged states from shared memory again for 16
+// vocabulary rows (2 KB at eight tiles, 16 cycles of an SM's shared memory), and long rows are staged in parts on every
+// round: 64 rows of 50000 x 4096 take 127 us where the bytes take 18, with instructions in 31% of the issue slots.
+// The states are three columns each in fp32 and the weights are read once per 16 of them (50000 x 4096: 38 us for one row,
+// 50 for 8, 97 for 9, 119 for 16, 475 for 64; bf16 25, 28, 32, 35, 127).
 // Tried instead for many rows: tcgen05 with the scale folded into the weights as two exact bf16 terms in tensor memory,
 // so that one accumulator runs over all groups. 24 rows took 117 us (one block of 64 in flight per 128 rows), 64 rows
-// of 50000 x 4096 107 us against 127, and the long accumulation cost digits (3.5e-6 of the result against 1.6e-7).
+// of 50000 x 4096 107 us against 127, and the long accumulation cost digits (3.5e-6 of the result against 1.6e-7). Both
+// come from the folding; an accumulator per group, scaled in fp32 as here, was not tried.
 //
 // Packed layout. Vocabulary rows in tiles of 16, the inner dimension in units of 128 (two blocks of 64): the record of
 // a tile and unit is contiguous, so a warp streams its tile's records in order. A record holds, for each of its one

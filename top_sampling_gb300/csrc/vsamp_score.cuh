@@ -386,8 +386,8 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
 }
 
 // One warp per piece, the piece in registers: 32 warps per SM hold 128 KB of loads in flight. About six instructions per
-// bf16 element beside the exponential. 2048 x 151936 bf16, a quarter of the rows ignored: 78 us with the finish, 90% of
-// the copy rate; small batches are bound by the two launches and their first loads (256 rows: 24.5 us with 20
+// bf16 element beside the exponential. 2048 x 151936 bf16, a quarter of the rows ignored: 79 us with the finish, 88% of
+// the copy rate; small batches are bound by the two launches and their first loads (256 rows: 24.0 us with 20
 // alternatives where the bytes take 12). A persistent form that copies the next piece to shared
 // memory meanwhile ran 15% more instructions and was slower (108 against 91 us at the time).
 template <typename T, bool ALT>
@@ -561,7 +561,7 @@ __device__ uint64_t score_radix_select(F for_each, uint32_t want, uint32_t* hist
 //      the list holds, above a bound from every thread's largest token, and failing that by a radix search for the last
 //      alternative), and each one's place is the number of larger ones.
 // Keys are (value, index) pairs in the order's sense, all different. Bound by latency: a chain of about eight dependent
-// steps, about 5 us beside the pieces' kernel, whatever N (20 alternatives of 256 rows: 24.5 us against 19 without).
+// steps, about 5 us beside the pieces' kernel, whatever N (20 alternatives of 256 rows: 24.0 us against 18.3 without).
 struct ScoreAltSmem {
   __align__(16) uint64_t list[kScoreList];
   __align__(16) uint64_t best[kScoreFinishThreads];
@@ -848,7 +848,7 @@ __device__ __forceinline__ void grad_vector(const GradRow& r, uint32_t (&w)[4]) 
 // One CTA per row and span of kGradThreads * kGradVecs vectors. Vectors begin at the first 16-byte boundary of the
 // gradient's row, whatever the logits' row's; the elements before and after the whole vectors belong to the row's first
 // CTA. Streaming loads and stores: nothing is reused. Bound by the bytes: 2048 x 151936 bf16, a quarter of the rows
-// ignored, 166 us, 98% of the copy rate.
+// ignored, 162.5 us, the copy rate.
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads) score_grad_kernel(const ScoreGradParams p) {
   using Ty = ScoreType<T>;
