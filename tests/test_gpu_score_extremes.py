@@ -107,3 +107,36 @@ def test_smallest_differences_at_smallest_temperatures(ts, dev, dtype, n):
     x = _rows(a, dtype, dev)
     _check(ts, x, [1, 2, 4, 5, 7, 10], temps, n)
     _gradient(ts, x, [1, 2, 4, 5, 7, 10], temps, [1.0] * len(temps), [0.1] * len(temps))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V,pad", [(1, 0), (2, 0), (37, 1), (5001, 0), (5001, 3), (40007, 0)])
+def test_one_likely_token_keeps_the_digits_of_the_others(ts, dev, dtype, V, pad):
+    """Rows whose largest token outweighs all others by up to 2^40: log S and the token's log-probability are held to the
+    bound of a sum of the others, relative to it. The exponents that weigh are within 30 of the largest of the others."""
+    rng = np.random.default_rng(V)
+    tops = [3.0, 8.0, 14.0, 20.0, 27.0]
+    a = rng.normal(0.0, 1.0, size=(2 * len(tops), V)).astype(np.float32)
+    a[len(tops):, : V // 2] = -np.inf                              # a row whose other half is masked
+    place = [0, V - 1, V // 2, V - 1 - V // 3, V // 7] * 2
+    for r, (top, at) in enumerate(zip(tops * 2, place)):
+        a[r, at] = top + np.log(V)
+    x = _rows(a, dtype, dev, pad)
+    reps = 5000 // (len(a) * ((V + 1023) // 1024)) + 1             # many rows take two launches
+    xs = tu.f64(x)
+    for temps in (None, [1.0, 0.9, 1.1, 1.0, 0.8] * 2):
+        T = None if temps is None else torch.tensor(temps, device=dev)
+        tok = torch.tensor(place, dtype=torch.int32, device=dev)
+        out = ts.vsamp_score_tokens(x, tok, temperature=T, n_alt=3)
+        many = ts.vsamp_score_tokens(x.repeat(reps, 1), tok.repeat(reps), n_alt=3,
+                                     temperature=None if T is None else T.repeat(reps))
+        for p, q in zip(out, many):
+            assert torch.equal(p.view(torch.int32), q[: len(a)].contiguous().view(torch.int32))
+        for r in range(len(a)):
+            t = 1.0 if temps is None else float(np.float32(temps[r]))
+            s = (xs[r] - xs[r].max()) / t
+            others = np.exp(np.delete(s, place[r])).sum()
+            want = np.log1p(others)
+            scale = (tu.LOGSUM_TOL + 3 * tu.U * (tops[r % len(tops)] + np.log(V)) / t + 4 * tu.U) * others
+            assert abs(float(out[6][r]) - want) <= scale, (r, temps, float(out[6][r]), want)
+            assert abs(float(out[0][r]) + want) <= scale, (r, temps, float(out[0][r]), want)

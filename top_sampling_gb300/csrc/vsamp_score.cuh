@@ -41,7 +41,7 @@ struct ScoreParams {
   uint32_t np_mul;       // id / np = umulhi(id, np_mul) >> np_shift for np > 1
   int np_shift;
   uint32_t inner0, inner1;   // whole pieces in [inner0, inner1) are read by aligned vectors (all but one at the very ends)
-  float4* rec;           // [B, np] {m_p, S_p, A_p, tokens before the given one}
+  float4* rec;           // [B, np] {m_p, S_p, or below 1 for S_p - 1, A_p, tokens before the given one}
   float* chunk_max;      // [B, np, 8] (N > 0)
   float* logprob;
   float* entropy;
@@ -287,6 +287,26 @@ __device__ __forceinline__ void realign_piece(uint32_t (&w)[kScoreChunks][4], co
   }
 }
 
+// The sum of a piece in which one token outweighs all others (S < 2), without that token: beside its 1 the others' digits
+// are lost, and with them those of the row's log S. One lane's sum holds the 1; that lane's 128 bytes are read again, a
+// word per lane. Below 1.
+template <typename T>
+__device__ __forceinline__ float sum_of_others(const unsigned char* xr, int32_t e0, int32_t V, float m, const ScoreRate& r,
+                                               float mine) {
+  using Ty = ScoreType<T>;
+  constexpr int CE = kScorePiece / Ty::ES / kScoreChunks, WE = 4 / Ty::ES;   // elements per chunk, per word
+  const int lane = threadIdx.x & 31;
+  const int holder = (__ffs(__ballot_sync(kFullMask, mine >= 1.f)) - 1) & 31;
+  float S = lane == holder ? 0.f : mine;
+  const int64_t e = (int64_t)e0 + (lane >> 2) * CE + holder * Ty::VE + (lane & 3) * WE;
+#pragma unroll
+  for (int j = 0; j < WE; ++j) {
+    const float x = V - e > j ? Ty::load(xr, e + j) : -INFINITY;
+    S += x == m ? 0.f : ex2_approx(fmaxf(r.exponent(x, m), -150.f));
+  }
+  return fminf(warp_sum_f(S), 0x1.fffffep-1f);
+}
+
 // One warp, one piece of a row (the id-th of all): its record, and the maxima of its chunks. The piece is held in
 // registers.
 template <typename T, bool ALT>
@@ -375,13 +395,15 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
   if (m > -INFINITY && m < INFINITY) {   // false for NaN too
     // 104 log2(e) > 150; below m, too: at a temperature far below the maximum's last place it is m itself
     const float lowest = fmaf(-104.f, T1, m);
-    if (ScoreRate::ordinary(T1) && lowest < m && lowest > -3.3e38f)
-      score_sums<T, true>(w, m, ScoreRate{T1, c, 1.f, 1.f, 1.f}, lowest, S, A);
+    float mine;   // this lane's sum
+    if (__builtin_expect(ScoreRate::ordinary(T1) && lowest < m && lowest > -3.3e38f, 1))
+      score_sums<T, true>(w, m, ScoreRate{T1, c, 1.f, 1.f, 1.f}, lowest, mine, A);
     else
-      score_sums<T, false>(w, m, ScoreRate::of(T1), lowest, S, A);
+      score_sums<T, false>(w, m, ScoreRate::of(T1), lowest, mine, A);
+    S = warp_sum_f(mine);
+    if (__builtin_expect(S < 2.f, 0)) S = sum_of_others<T>(xr, e0, V, m, ScoreRate::of(T1), mine);
+    A = warp_sum_f(A);
   }
-  S = warp_sum_f(S);
-  A = warp_sum_f(A);
   if (lane == 0) *rec = make_float4(m, S, A, __uint_as_float(before));
 }
 
@@ -440,26 +462,29 @@ struct ScoreFold {
     each(p, [&](float4 q) { m = max_nan(m, q.x); });
     m = warp_max_nan(m);
     float S = 0.f, A = 0.f;
-    uint32_t before = 0;
+    uint32_t before = 0, ones = 0;   // pieces of which S holds all but the maximum's own 1
     const bool finite = m > -INFINITY && m < INFINITY;
     if (finite) {
       each(p, [&](float4 q) {
         before += __float_as_uint(q.w);
         if (q.x > -INFINITY) {
           const float d = fmaxf(r.rate.exponent(q.x, m), -150.f);
-          const float f = ex2_approx(d);
-          S = fmaf(f, q.y, S);
-          A = fmaf(f, fmaf(d, q.y, q.z), A);
+          const float f = ex2_approx(d), sum = q.y < 1.f ? q.y + 1.f : q.y;
+          const bool one = q.y < 1.f && q.x == m;
+          ones += one ? 1u : 0u;
+          S = fmaf(f, one ? q.y : sum, S);
+          A = fmaf(f, fmaf(d, sum, q.z), A);
         }
       });
     }
     S = warp_sum_f(S);
     A = warp_sum_f(A);
+    ones = warp_sum_u32(ones);
     r.before = warp_sum_u32(before);
     r.m = m;
-    // S >= 1: log1p keeps the digits of a sum close to 1
-    r.logsum = log1pf(S - 1.f);
-    r.entropy = fmaxf(r.logsum - 0.69314718056f * (A / S), 0.f);
+    // log1p of the sum without one 1, which keeps the digits of the others' where one token outweighs them
+    r.logsum = log1pf(S + ((float)ones - 1.f));
+    r.entropy = fmaxf(r.logsum - 0.69314718056f * (A / (S + (float)ones)), 0.f);
     r.status = VSAMP_OK;
     if (!finite) r.status = VSAMP_ERR_NONFINITE;
     else if (isnan(temp) || isinf(temp) || t < 0 || (int64_t)t >= p.V) r.status = VSAMP_ERR_INVALID_ARG;
