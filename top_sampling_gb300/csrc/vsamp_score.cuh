@@ -9,6 +9,8 @@
 // and S_p, A_p are formed relative to it, so no pass waits for the row maximum and the sums of a row depend on V
 // alone. A second launch folds the pieces of every row:
 //   S = sum 2^((m_p - m) c) S_p,   A = sum 2^((m_p - m) c) (A_p + (m_p - m) c S_p),   c = log2(e) / T.
+// A piece with S_p < 2, in which one token outweighs the others, records S_p - 1 without that token's 1, beside which
+// the others' digits would be lost.
 // -inf marks a masked token (probability 0); NaN and +inf are row errors.
 //
 // Alternatives. A piece also records the maxima of its eight 512-byte chunks. The first N tokens of the order lie in
@@ -408,8 +410,8 @@ __device__ __forceinline__ void score_piece(const ScoreParams& p, uint32_t row, 
 }
 
 // One warp per piece, the piece in registers: 32 warps per SM hold 128 KB of loads in flight. About six instructions per
-// bf16 element beside the exponential. 2048 x 151936 bf16, a quarter of the rows ignored: 79 us with the finish, 88% of
-// the copy rate; small batches are bound by the two launches and their first loads (256 rows: 24.0 us with 20
+// bf16 element beside the exponential. 2048 x 151936 bf16, a quarter of the rows ignored: 79.5 us with the finish, 88% of
+// the copy rate; small batches are bound by the two launches and their first loads (256 rows: 24.6 us with 20
 // alternatives where the bytes take 12). A persistent form that copies the next piece to shared
 // memory meanwhile ran 15% more instructions and was slower (108 against 91 us at the time).
 template <typename T, bool ALT>
@@ -586,7 +588,7 @@ __device__ uint64_t score_radix_select(F for_each, uint32_t want, uint32_t* hist
 //      the list holds, above a bound from every thread's largest token, and failing that by a radix search for the last
 //      alternative), and each one's place is the number of larger ones.
 // Keys are (value, index) pairs in the order's sense, all different. Bound by latency: a chain of about eight dependent
-// steps, about 5 us beside the pieces' kernel, whatever N (20 alternatives of 256 rows: 24.0 us against 18.3 without).
+// steps, about 5 us beside the pieces' kernel, whatever N (20 alternatives of 256 rows: 24.6 us against 18.7 without).
 struct ScoreAltSmem {
   __align__(16) uint64_t list[kScoreList];
   __align__(16) uint64_t best[kScoreFinishThreads];
@@ -783,7 +785,7 @@ __global__ void __launch_bounds__(kScoreFinishThreads) score_finish_alt_kernel(c
 
 // Both steps in one launch: a cluster of CTAs takes a row, its warps write the records of their pieces into the first
 // CTA's shared memory, and that CTA finishes the row. For small batches (see the launch): 4 x 32000 fp32 with five
-// alternatives 6.2 us, bound by the chain of dependent steps.
+// alternatives 6.5 us, bound by the chain of dependent steps.
 template <typename T, bool ALT>
 __global__ void __launch_bounds__(kScoreWarps * 32, 4) score_row_kernel(const ScoreParams p) {
   static_assert(kScoreWarps * 32 == kScoreFinishThreads, "the first CTA's threads finish the row");
