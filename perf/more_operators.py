@@ -195,7 +195,7 @@ def prepare(case, seed):
                     y, sc = _to_blocks(x[p])
                     codes[p] = y.clamp(-TOP, TOP).to(F8).reshape(-1)[:x[p].numel()]
                     scales[b] = sc
-        s["parts"] = parts
+        s["parts"], s["grads"] = parts, [s["grad"][p] for p in parts]
         if own:
             # an optimiser's object: the tensors that it updates, checked once
             import top_sampling_gb300 as ts
@@ -281,7 +281,7 @@ def _adamw_one(s, k):
     case, p = s["case"], s["parts"][k]
     step, n = case["step"], p.stop - p.start
     value = (s["master"] if case["master"] else s["param"])[p].float()
-    g = s["grad"][p].float() * s["grad_scale"]
+    g = s["grads"][k].float() * s["grad_scale"]
     b = s["blocks"][k] if case["bits"] == 8 else None
     if b is None:
         m, v = s["m"][p], s["v"][p]
@@ -328,7 +328,7 @@ def run(state):
             return {k: s[k] for k in ("codes", "scales", "codes_t", "scales_t") if k in s}
         if kind == "product":
             return ts.vsamp_block_matmul(s["A"], s["B"], out=s["out"], accumulate=case["add"])
-        ts.vsamp_adamw(s["state"], [s["grad"][p] for p in s["parts"]], lr=LR, step=case["step"], beta1=BETA1, beta2=BETA2,
+        ts.vsamp_adamw(s["state"], s["grads"], lr=LR, step=case["step"], beta1=BETA1, beta2=BETA2,
                        eps=EPS, weight_decay=DECAY, grad_scale=s["grad_scale"])
         return _adamw_out(s)
     if kind == "quant":
