@@ -416,6 +416,92 @@ vsamp_status vsamp_embed_backward(const int32_t* token, int64_t N, const void* d
                                   int64_t ldt, int32_t accumulate, void* workspace, size_t workspace_bytes,
                                   void* stream);
 
+/* ---------------------------------------------------------------------------------------------------
+ * 8-bit matrices in blocks of 128: quantisation, the product of two of them (logits of many hidden rows, the gradients
+ * of hidden states and weights), and the optimiser step of the tables. Streams, ownership and errors are as above.
+ *
+ * A matrix [rows, cols] is held as e4m3 codes (1 sign, 4 exponent, 3 fraction bits, largest value 448) [rows, ld], ld a
+ * multiple of 16, the first on a 16-byte boundary, and one fp32 scale per block along the columns, the inner dimension
+ * of every product; the last blocks may be short. An element is code * scale.
+ *   VSAMP_BLOCK_ROW   blocks of 1 x 128: scale of row r, columns 128 j .. 128 j + 127 at scales[j * lds + r], lds >= rows
+ *                     a multiple of 4, the first on a 16-byte boundary
+ *   VSAMP_BLOCK_TILE  blocks of 128 x 128: scale of rows 128 i .., columns 128 j .. at scales[i * lds + j],
+ *                     lds >= ceil(cols / 128)
+ * --------------------------------------------------------------------------------------------------- */
+typedef enum vsamp_block_kind {
+  VSAMP_BLOCK_ROW = 0,
+  VSAMP_BLOCK_TILE = 1
+} vsamp_block_kind;
+
+/* Quantises x [R, ldx] (fp32 or bf16, C columns) and, in the same pass, x transposed:
+ *   scale = max(largest magnitude of the block / 448, 2^-126),  code = e4m3(x * (1 / scale)), to nearest even
+ *   codes [R, ldc], scales       of x, blocks along its columns (both NULL: not written)
+ *   codes_t [C, ldt], scales_t   of x^T, blocks along the rows of x (both NULL: not written)
+ * Of VSAMP_BLOCK_TILE the two hold the same codes and scales transposed. A block with NaN or an infinity has the scale
+ * NaN and the codes 0: whatever is computed with it is NaN. What lies behind a row's last code is left as it is.
+ * One launch on `stream`. */
+vsamp_status vsamp_block_quantize(const void* x, vsamp_dtype dt, int64_t R, int64_t C, int64_t ldx,
+                                  vsamp_block_kind kind, uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
+                                  uint8_t* codes_t, int64_t ldt, float* scales_t, int64_t ldst, void* stream);
+
+/* Product of two 8-bit matrices over their columns:
+ *   out[m, n] = sum over blocks j of sa[m, j] * sb[n, j] * sum over k in j of a[m, k] * b[n, k]   (+ out[m, n])
+ *   a [M, lda]   codes and VSAMP_BLOCK_ROW scales (activations, gradients)
+ *   b [N, ldb]   codes and scales of b_kind (weights: VSAMP_BLOCK_TILE; the other operand of a weight gradient: _ROW)
+ *   K            columns of both
+ *   out [M, ldo] fp32 or bf16; accumulate != 0 adds to what it holds
+ * Products are exact, a block's sum and the sum over blocks fp32, one rounding at the end. A NaN scale makes its row's
+ * (or block of columns') results NaN; other results do not depend on it. Sums are formed in an order that depends on
+ * the sizes alone: the same call gives the same result.
+ *   workspace  vsamp_block_matmul_workspace_size bytes (0 for most sizes: NULL is fine), 16-byte aligned; needs no
+ *              initialisation, not shared by calls that may overlap. */
+size_t vsamp_block_matmul_workspace_size(int64_t M, int64_t N, int64_t K);
+vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa, const uint8_t* b,
+                                int64_t ldb, const float* sb, int64_t ldsb, vsamp_block_kind b_kind, int64_t M,
+                                int64_t N, int64_t K, void* out, vsamp_dtype out_dt, int64_t ldo, int32_t accumulate,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* One tensor of an optimiser step (device pointers; no tensor may appear twice in a step). */
+typedef struct vsamp_adamw_tensor {
+  void* param;         /* [n] of param_dt */
+  float* master;       /* [n], or NULL: param itself is updated */
+  const void* grad;    /* [n] of grad_dt */
+  void* m;             /* [n] first moments: fp32, or e4m3 codes */
+  void* v;             /* [n] second moments: fp32, or e4m3 codes of their square roots */
+  float* m_scale;      /* [ceil(n / 128)] with 8-bit states, NULL otherwise */
+  float* v_scale;
+  int64_t n;           /* 0: nothing is done; at most 2^34 */
+  uint32_t index;      /* counter word of the random numbers: another one for every tensor of the model */
+  uint32_t reserved;
+} vsamp_adamw_tensor;
+
+typedef struct vsamp_adamw_rule {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;             /* 1 for the first step */
+  uint64_t seed;            /* key of the random numbers */
+  const float* lr_dev;      /* device scalar that replaces lr, or NULL */
+  const int64_t* step_dev;  /* device scalar that replaces step, or NULL; below 1: the call changes nothing */
+  const float* grad_scale;  /* device scalar that every gradient is multiplied with (clipping, a loss scale), or NULL */
+} vsamp_adamw_rule;
+
+/* The AdamW step of many tensors, with decoupled weight decay, in fp32:
+ *   g = grad * grad_scale, m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr (weight_decay p + (m / (1 - beta1^step)) / (sqrt(v) / sqrt(1 - beta2^step) + eps))
+ * `tensors` and `rule` are HOST pointers, read before the call returns. One launch per 384 tensors.
+ *   param_dt    fp32, or bf16: with a master that one is updated and param gets its rounding; without, param is rounded
+ *               stochastically (16 random bits are added below the kept ones), so that small steps are not lost
+ *   state_bits  32, or 8: e4m3 codes with a scale (largest magnitude / 448, at least 2^-126) per 128 elements from the
+ *               tensor's first, of m and of r = sqrt(v). Values between two codes go to one of them at random, to the
+ *               nearer with more probability, so that moments follow changes below a code's step; r > 0 is never
+ *               rounded to 0. p is computed from the moments before that rounding. A block with NaN or an infinity gets
+ *               the scale NaN.
+ *   Random numbers: word i & 3 of Philox4x32-10 at counter (i >> 2, 0, step mod 2^32, index) with key `seed` for element i:
+ *               its upper 16 bits h for m, its lower ones for r: floor(y / s + (h + 0.5) 2^-16) s for a magnitude y in
+ *               units of the scale, s the distance of e4m3 values at y; for a bf16 parameter the lower 16 bits of the
+ *               word at counter (i >> 2, 2^31, ...). The same call gives the same result. */
+vsamp_status vsamp_adamw(const vsamp_adamw_tensor* tensors, int32_t count, vsamp_dtype param_dt, vsamp_dtype grad_dt,
+                         int32_t state_bits, const vsamp_adamw_rule* rule, void* stream);
+
 /* Static description of a status code. */
 const char* vsamp_status_string(vsamp_status s);
 

@@ -30,6 +30,9 @@ VSAMP_F32 = 0
 VSAMP_BF16 = 1
 VSAMP_TOKEN_IGNORE = -100              # a token that is not scored and gets no gradient
 VSAMP_SCORE_ALT_MAX = 128              # most alternatives of vsamp_score_tokens
+VSAMP_BLOCK_ROW = 0                    # 8-bit blocks of 1 x 128
+VSAMP_BLOCK_TILE = 1                   # 8-bit blocks of 128 x 128
+BLOCK = 128                            # elements of an 8-bit block along the inner dimension
 
 EXPORTED = ("vsamp_softmax_lse", "vsamp_topk_select", "vsamp_topp_minp_mask", "vsamp_sample",
             "vsamp_sample_ws", "vsamp_sample_workspace_size", "vsamp_sample_static", "vsamp_logprob", "vsamp_topn_logprobs", "vsamp_kept_logprob",
@@ -38,6 +41,7 @@ EXPORTED = ("vsamp_softmax_lse", "vsamp_topk_select", "vsamp_topp_minp_mask", "v
             "vsamp_score_workspace_size", "vsamp_score_tokens", "vsamp_score_tokens_backward",
             "vsamp_head_packed_size", "vsamp_head_pack", "vsamp_head_logits",
             "vsamp_embed", "vsamp_embed_workspace_size", "vsamp_embed_backward",
+            "vsamp_block_quantize", "vsamp_block_matmul_workspace_size", "vsamp_block_matmul", "vsamp_adamw",
             "vsamp_status_string",
             "vsamp_device_info", "vsamp_version")
 
@@ -112,8 +116,13 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.vsamp_embed_workspace_size.argtypes = [i64, i64]
     lib.vsamp_embed_workspace_size.restype = sz
     lib.vsamp_embed_backward.argtypes = [vp, i64, vp, st, i64, i64, f32, i64, vp, st, i64, i32, vp, sz, vp]
+    lib.vsamp_block_quantize.argtypes = [vp, st, i64, i64, i64, st, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.vsamp_block_matmul_workspace_size.argtypes = [i64, i64, i64]
+    lib.vsamp_block_matmul_workspace_size.restype = sz
+    lib.vsamp_block_matmul.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, st, i64, i64, i64, vp, st, i64, i32, vp, sz, vp]
+    lib.vsamp_adamw.argtypes = [vp, i32, st, st, i32, vp, vp]
     for f in ("vsamp_score_tokens", "vsamp_score_tokens_backward", "vsamp_head_pack", "vsamp_head_logits",
-              "vsamp_embed", "vsamp_embed_backward"):
+              "vsamp_embed", "vsamp_embed_backward", "vsamp_block_quantize", "vsamp_block_matmul", "vsamp_adamw"):
         getattr(lib, f).restype = st
     lib.vsamp_status_string.argtypes = [st]
     lib.vsamp_status_string.restype = ctypes.c_char_p
@@ -889,3 +898,264 @@ def vsamp_embed_backward(token, dout, V, scale=1.0, dtable=None, dtype=None, acc
     if st:
         _check(st, "vsamp_embed_backward")
     return dtable
+
+
+# ------------------------------------------------------------------------------------------------
+# 8-bit matrices in blocks of 128 and the optimiser step
+# ------------------------------------------------------------------------------------------------
+class BlockTensor:
+    """A matrix [rows, cols] as e4m3 codes and one scale per block: an element is code * scale.
+
+    codes   [rows, cols] float8_e4m3fn or uint8, each row on a 16-byte boundary (a view of rows of whole 16 bytes)
+    scales  fp32: [ceil(cols / 128), rows] for blocks of 1 x 128, each row of it on a 16-byte boundary (a view of rows of
+            whole four scales); [ceil(rows / 128), ceil(cols / 128)] for blocks of 128 x 128 (``tile``)
+    """
+
+    __slots__ = ("codes", "scales", "rows", "cols", "tile", "ld", "lds")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, tile: bool = False):
+        if codes.dtype not in (torch.float8_e4m3fn, torch.uint8) or scales.dtype is not torch.float32:
+            raise TypeError(f"codes must be float8_e4m3fn or uint8 and scales float32, got {codes.dtype} and {scales.dtype}")
+        index = codes.get_device()
+        if index < 0:
+            raise ValueError(f"tensors must be on a CUDA device, got {codes.device}")
+        self.rows, self.cols, ld = _matrix(codes, "codes", index)
+        across, down = -(-self.cols // BLOCK), -(-self.rows // BLOCK)
+        _, _, lds = _matrix(scales, "scales", index, *((down, across) if tile else (across, self.rows)))
+        # the stride of a single row says nothing
+        self.ld = ld if self.rows > 1 else -(-self.cols // 16) * 16
+        self.lds = lds if tile or across > 1 else -(-self.rows // 4) * 4
+        self.codes, self.scales, self.tile = codes, scales, bool(tile)
+        if self.ld % 16 or codes.data_ptr() % 16:
+            raise ValueError("every row of codes must begin on a 16-byte boundary")
+        if not tile and (self.lds % 4 or scales.data_ptr() % 16):
+            raise ValueError("every row of scales must begin on a 16-byte boundary")
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, tile: bool = False, device="cuda") -> "BlockTensor":
+        """An uninitialised one."""
+        codes = torch.empty((rows, -(-cols // 16) * 16), dtype=torch.float8_e4m3fn, device=device)[:, :cols]
+        if tile:
+            scales = torch.empty((-(-rows // BLOCK), -(-cols // BLOCK)), dtype=torch.float32, device=device)
+        else:
+            scales = torch.empty((-(-cols // BLOCK), -(-rows // 4) * 4), dtype=torch.float32, device=device)[:, :rows]
+        return cls(codes, scales, tile)
+
+    def dequantize(self, dtype=torch.float32) -> torch.Tensor:
+        """The values, [rows, cols]."""
+        s = self.scales.repeat_interleave(BLOCK, 0)[:self.rows] if self.tile else self.scales.t()
+        values = self.codes.view(torch.float8_e4m3fn).to(torch.float32) * s.repeat_interleave(BLOCK, 1)[:, :self.cols]
+        return values.to(dtype)
+
+
+def _block_out(out, rows: int, cols: int, tile: bool, index: int, dev, name: str) -> BlockTensor:
+    if out is None:
+        return BlockTensor.empty(rows, cols, tile, dev)
+    if (out.rows, out.cols, out.tile) != (rows, cols, tile) or out.codes.get_device() != index:
+        raise ValueError(f"{name} must be a BlockTensor [{rows}, {cols}] with tile={tile} on cuda:{index}, got "
+                         f"[{out.rows}, {out.cols}] with tile={out.tile} on {out.codes.device}")
+    return out
+
+
+def vsamp_block_quantize(x, tile=False, plain=True, transposed=False, out=None, out_t=None, stream=None):
+    """Quantises x [R, C] (fp32 or bf16) into e4m3 blocks of 1 x 128 along its columns, or of 128 x 128 (``tile``), and
+    its transpose into blocks along the rows of x, both from one read of x. Returns (the matrix, its transpose) as
+    BlockTensors, None for one that is not asked for."""
+    where = _elsewhere(x, stream)
+    if where is not None:
+        with where:
+            return vsamp_block_quantize(x, tile, plain, transposed, out, out_t)
+    dev, at, tile = x.device, x.get_device(), bool(tile)
+    R, C, ldx = _matrix(x, "x", at)
+    if not (plain or transposed):
+        raise ValueError("nothing is asked for: plain or transposed must be true")
+    dt = _dtype_code(x)
+    a = _block_out(out, R, C, tile, at, dev, "out") if plain else None
+    b = _block_out(out_t, C, R, tile, at, dev, "out_t") if transposed else None
+    st = load().vsamp_block_quantize(
+        x.data_ptr(), dt, R, C, ldx, VSAMP_BLOCK_TILE if tile else VSAMP_BLOCK_ROW,
+        *((a.codes.data_ptr(), a.ld, a.scales.data_ptr(), a.lds) if a is not None else (None, 0, None, 0)),
+        *((b.codes.data_ptr(), b.ld, b.scales.data_ptr(), b.lds) if b is not None else (None, 0, None, 0)), _current(at))
+    if st:
+        _check(st, "vsamp_block_quantize")
+    return a, b
+
+
+def vsamp_block_matmul(a: BlockTensor, b: BlockTensor, out=None, out_dtype=torch.bfloat16, accumulate=False,
+                       workspace=None, stream=None):
+    """a [M, K] times b [N, K] transposed: [M, N] in fp32 or bf16. a has blocks of 1 x 128 (activations, gradients), b of
+    128 x 128 (weights) or of 1 x 128. ``out`` (rows may be padded) or a new tensor of out_dtype is returned;
+    accumulate adds to what ``out`` holds."""
+    where = _elsewhere(a.codes, stream)
+    if where is not None:
+        with where:
+            return vsamp_block_matmul(a, b, out, out_dtype, accumulate, workspace)
+    at = a.codes.get_device()
+    M, N, K = a.rows, b.rows, a.cols
+    if b.cols != K or b.codes.get_device() != at:
+        raise ValueError(f"b must be [N, {K}] on cuda:{at}, got [{b.rows}, {b.cols}] on {b.codes.device}")
+    if a.tile:
+        raise ValueError("a must have blocks of 1 x 128")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs the product to add to")
+        out = torch.empty((M, N), dtype=out_dtype, device=a.codes.device)
+    ld = _matrix(out, "out", at, M, N)[2]
+    lib, on = load(), _current(at)
+    need = lib.vsamp_block_matmul_workspace_size(M, N, K)
+    if workspace is None and need:
+        workspace = _scratch(need, a.codes.device, at, on)
+    st = lib.vsamp_block_matmul(
+        a.codes.data_ptr(), a.ld, a.scales.data_ptr(), a.lds, b.codes.data_ptr(), b.ld, b.scales.data_ptr(), b.lds, b.tile,
+        M, N, K, out.data_ptr(), _dtype_code(out), ld, accumulate, _at(workspace, torch.uint8, at, 0, "workspace"),
+        0 if workspace is None else workspace.numel(), on)
+    if st:
+        _check(st, "vsamp_block_matmul")
+    return out
+
+
+class vsamp_adamw_rule(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64), ("seed", ctypes.c_uint64),
+                ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
+
+
+# vsamp_adamw_tensor as 64-bit words: param, master, grad, m, v, m_scale, v_scale, n, index (and 32 bits that are not used)
+_ADAMW_WORDS, _ADAMW_GRAD, _ADAMW_N = 9, 2, 7
+
+
+class AdamWState:
+    """The tensors that an AdamW step updates, checked once: parameters, masters and moments (vsamp_adamw_state)."""
+
+    __slots__ = ("params", "masters", "m", "v", "m_scale", "v_scale", "bits", "device", "index", "sizes", "groups")
+
+
+def _adamw_list(given, n: int, name: str):
+    given = list(given)
+    if len(given) != n:
+        raise ValueError(f"{name} must have {n} entries, got {len(given)}")
+    return given
+
+
+def vsamp_adamw_state(params, bits=32, masters=None, m=None, v=None, m_scale=None, v_scale=None) -> AdamWState:
+    """What vsamp_adamw updates: params, a sequence of contiguous fp32 or bf16 tensors of one device, and their moments
+    with 32 or 8 bits, new ones of zeros unless given (as lists of tensors: fp32; or float8_e4m3fn or uint8 codes of the
+    first moments and of the second ones' square roots, with fp32 scales per 128 elements).
+
+    masters: True for new fp32 copies of the bf16 parameters, a list of given ones (None for fp32 parameters), or None: bf16
+    parameters are then rounded stochastically."""
+    s = AdamWState()
+    s.params = list(params)
+    n = len(s.params)
+    if n == 0 or bits not in (8, 32):
+        raise ValueError(f"parameters and 8 or 32 bits are wanted, got {n} and {bits}")
+    s.bits, s.device, s.index = bits, s.params[0].device, s.params[0].get_device()
+    if s.index < 0:
+        raise ValueError(f"tensors must be on a CUDA device, got {s.device}")
+    for p in s.params:
+        _dtype_code(p)
+        _at(p, p.dtype, s.index, 0, "params")
+    s.sizes = [p.numel() for p in s.params]
+    blocks = [-(-k // BLOCK) for k in s.sizes]
+    if masters is None:
+        s.masters = [None] * n
+    elif masters is True:
+        s.masters = [p.detach().float() if p.dtype is torch.bfloat16 else None for p in s.params]
+    else:
+        s.masters = _adamw_list(masters, n, "masters")
+    for p, w in zip(s.params, s.masters):
+        if w is not None and (p.dtype is torch.float32 or w.numel() != p.numel()):
+            raise ValueError("masters belong to bf16 parameters and have their sizes")
+
+    def moments(given, name):
+        dt = torch.float8_e4m3fn if bits == 8 else torch.float32
+        if given is None:
+            return [torch.zeros(k, dtype=dt, device=s.device) for k in s.sizes]
+        given = _adamw_list(given, n, name)
+        for t, k in zip(given, s.sizes):
+            _at(t, torch.uint8 if bits == 8 and t.dtype is torch.uint8 else dt, s.index, k, name)
+        return given
+
+    def scales(given, name):
+        if bits == 32:
+            if given is not None:
+                raise ValueError(f"{name} belongs to moments of 8 bits")
+            return [None] * n
+        given = [torch.zeros(k, device=s.device) for k in blocks] if given is None else _adamw_list(given, n, name)
+        for t, k in zip(given, blocks):
+            _at(t, torch.float32, s.index, k, name)
+        return given
+
+    s.m, s.v = moments(m, "m"), moments(v, "v")
+    s.m_scale, s.v_scale = scales(m_scale, "m_scale"), scales(v_scale, "v_scale")
+    if (m is None) != (v is None) or (bits == 8 and not (m is None) == (m_scale is None) == (v_scale is None)):
+        raise ValueError("moments are given together, with their scales, or not at all")
+    # every array is written by its own elements' threads alone
+    spans = []
+    state = 1 if bits == 8 else 4
+    for i, k in enumerate(s.sizes):
+        for t, size in ((s.params[i], k * s.params[i].element_size()), (s.masters[i], 4 * k), (s.m[i], state * k),
+                        (s.v[i], state * k), (s.m_scale[i], 4 * blocks[i]), (s.v_scale[i], 4 * blocks[i])):
+            if t is not None and size:
+                spans.append((t.data_ptr(), t.data_ptr() + size))
+    spans.sort()
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError("tensors that a step writes share memory")
+    s.groups = []
+    for dt in (torch.float32, torch.bfloat16):
+        for with_master in (False, True):
+            at = [i for i in range(n) if s.params[i].dtype is dt and (s.masters[i] is not None) == with_master]
+            if at:
+                for i in at:
+                    _at(s.masters[i], torch.float32, s.index, s.sizes[i], "masters")
+                words = [[0 if t is None else t.data_ptr() for t in (s.params[i], s.masters[i], None, s.m[i], s.v[i],
+                                                                     s.m_scale[i], s.v_scale[i])] + [s.sizes[i], i]
+                         for i in at]
+                s.groups.append((_dtype_code(s.params[at[0]]), at, torch.tensor(words, dtype=torch.int64)))
+    return s
+
+
+def _device_scalar(v, dtype, index: int, name: str):
+    """The address of a device scalar, None for a number of the host."""
+    return _at(v, dtype, index, 1, name) if isinstance(v, torch.Tensor) else None
+
+
+def vsamp_adamw(state: AdamWState, grads, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=None,
+                seed=0, stream=None):
+    """One AdamW step of the state's tensors, in place. grads: their gradients in the same order, contiguous, fp32 or bf16,
+    None for a tensor that is left as it is. lr (fp32) and step (int64) are numbers or device tensors of one element, so
+    that a captured step can be replayed; grad_scale is None or an fp32 device tensor of one element. A device step below
+    1 changes nothing. seed keys the random numbers of 8-bit moments and of bf16 parameters without masters."""
+    where = _elsewhere(state.params[0], stream)
+    if where is not None:
+        with where:
+            return vsamp_adamw(state, grads, lr, step, beta1, beta2, eps, weight_decay, grad_scale, seed)
+    at = state.index
+    f32, bf16 = torch.float32, torch.bfloat16
+    grads = _adamw_list(grads, len(state.params), "grads")
+    on_device = [isinstance(t, torch.Tensor) for t in (lr, step)]
+    rule = vsamp_adamw_rule(0.0 if on_device[0] else lr, beta1, beta2, eps, weight_decay, 1 if on_device[1] else step,
+                            int(seed) & ((1 << 64) - 1), _device_scalar(lr, f32, at, "lr"),
+                            _device_scalar(step, torch.int64, at, "step"), _at(grad_scale, f32, at, 1, "grad_scale"))
+    lib, on = load(), _current(at)
+    for dt, members, words in state.groups:
+        found = []
+        for i in members:
+            g = grads[i]
+            if g is None:
+                found.append((0, None))
+                continue
+            if g.numel() != state.sizes[i] or (g.dtype is not f32 and g.dtype is not bf16):
+                raise ValueError(f"gradient {i} must be {state.sizes[i]} elements of float32 or bfloat16, got {g.numel()} of "
+                                 f"{g.dtype}")
+            found.append((_at(g, g.dtype, at, 0, "grads"), g.dtype))
+        kinds = {k for _, k in found} - {None}
+        for kind in kinds:
+            table = words.clone()
+            table[:, _ADAMW_GRAD] = torch.tensor([p for p, _ in found], dtype=torch.int64)
+            if len(kinds) > 1 or any(k is None for _, k in found):
+                table[:, _ADAMW_N] *= torch.tensor([k is kind for _, k in found])
+            st = lib.vsamp_adamw(table.data_ptr(), len(members), dt, VSAMP_F32 if kind is f32 else VSAMP_BF16, state.bits,
+                                 ctypes.byref(rule), on)
+            if st:
+                _check(st, "vsamp_adamw")

@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libvsamp.so")
 
 SOURCES = ["vsamp_api.cu", "vsamp_inst_f32.cu", "vsamp_inst_bf16.cu", "vsamp_sample_f32.cu", "vsamp_sample_bf16.cu", "vsamp_split_f32.cu", "vsamp_split_bf16.cu",
            "vsamp_score.cu", "vsamp_head.cu", "vsamp_head_g32.cu", "vsamp_head_g64.cu", "vsamp_head_g128.cu",
-           "vsamp_embed.cu"]
+           "vsamp_embed.cu", "vsamp_block.cu", "vsamp_adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -647,6 +647,6 @@ vsamp_status vsamp_device_info(int device, vsamp_limits* out) {
   return VSAMP_OK;
 }
 
-int32_t vsamp_version(void) { return (1 << 16) | 1; }
+int32_t vsamp_version(void) { return (1 << 16) | 2; }
 
 }  // extern "C"
