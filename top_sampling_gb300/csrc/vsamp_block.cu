@@ -1,4 +1,6 @@
 // vsamp_block_quantize and vsamp_block_matmul: argument checks and launches.
+#include <atomic>
+
 #include "vsamp_block_matmul.cuh"
 #include "vsamp_block_quant.cuh"
 #include "vsamp_grid.h"
@@ -24,6 +26,73 @@ static vsamp_status launch_quant(const BlockQuantParams& p, cudaStream_t s) {
   if (p.codes && p.codes_t) return launch_1d(block_quant_kernel<T, TILE, true, true>, grid, kQuantThreads, 0, s, p);
   if (p.codes) return launch_1d(block_quant_kernel<T, TILE, true, false>, grid, kQuantThreads, 0, s, p);
   return launch_1d(block_quant_kernel<T, TILE, false, true>, grid, kQuantThreads, 0, s, p);
+}
+
+// cuTensorMapEncodeTiled of the installed driver, or null.
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiled encode_tiled() {
+  static std::atomic<void*> found{nullptr};
+  void* fn = found.load(std::memory_order_acquire);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+        how != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    found.store(fn, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiled>(fn);
+}
+
+// A map of a code matrix for copies of box_rows rows of one block.
+static bool codes_map(CUtensorMap& map, const uint8_t* codes, int64_t ld, int64_t rows, int64_t cols, int box_rows) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  const cuuint64_t size[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)ld};
+  const cuuint32_t box[2] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), size, stride, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int64_t kMmSms = 152;   // the division of the inner dimension goes by sizes alone
+
+// Parts of the inner dimension. A CTA's time goes by the blocks that it walks over and about six blocks' worth for each
+// tile's start and end; parts are written and read again. The fewest blocks of the longest CTA win.
+static int mm_parts(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((M + kMmRows - 1) / kMmRows) * ((N + kMmCols - 1) / kMmCols), blocks = ceil_blocks(K);
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= 64 && (s == 1 || blocks / s >= 4); ++s) {
+    double t = (double)((tiles * s + kMmSms - 1) / kMmSms) * ((double)((blocks + s - 1) / s) + 6);
+    if (s > 1) t += 8 + (double)M * N * s * 8 / 1.5e6;
+    if (s == 1 || t < least * 0.95) {
+      best = s;
+      least = t;
+    }
+  }
+  return best;
+}
+
+template <typename TO, bool TILE>
+static vsamp_status launch_matmul(const BlockMatmulParams& p, const CUtensorMap& a, const CUtensorMap& b,
+                                  const DeviceInfo& d, int dev, cudaStream_t s) {
+  auto kern = block_matmul_kernel<TO, TILE>;
+  static std::atomic<bool> raised[64];
+  if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return VSAMP_ERR_CUDA;
+    }
+    if (dev < 64) raised[dev].store(true, std::memory_order_release);
+  }
+  const vsamp_status st = launch_1d(kern, grid_of(p.items < d.sm_count ? p.items : d.sm_count), kMmThreads, kMmSmem, s, p, a, b);
+  if (st != VSAMP_OK || p.parts == 1) return st;
+  const int64_t ctas = (p.M * (p.ldp / 4) + 255) / 256, most = (int64_t)d.sm_count * 8;
+  return launch_1d(block_matmul_join_kernel<TO>, grid_of(ctas < most ? ctas : most), 256, 0, s, p);
 }
 
 }  // namespace vsamp
@@ -64,10 +133,9 @@ vsamp_status vsamp_block_quantize(const void* x, vsamp_dtype dt, int64_t R, int6
 }
 
 size_t vsamp_block_matmul_workspace_size(int64_t M, int64_t N, int64_t K) {
-  (void)M;
-  (void)N;
-  (void)K;
-  return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || M > 0x7FFFFF00LL || N > 0x7FFFFF00LL || K > 0x7FFFFF00LL) return 0;
+  const int parts = mm_parts(M, N, K);
+  return parts > 1 ? (size_t)parts * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4 : 0;
 }
 
 vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa, const uint8_t* b,
@@ -78,31 +146,48 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   if (M <= 0 || N <= 0 || K <= 0 || ldo < N || !at_multiple(out, out_dt == VSAMP_F32 ? 4 : 2)) return VSAMP_ERR_INVALID_ARG;
   if (!matrix_ok(a, lda, sa, ldsa, VSAMP_BLOCK_ROW, M, K) || !matrix_ok(b, ldb, sb, ldsb, b_kind, N, K))
     return VSAMP_ERR_INVALID_ARG;
+  if (M > 0x7FFFFF00LL || N > 0x7FFFFF00LL || K > 0x7FFFFF00LL) return VSAMP_ERR_UNSUPPORTED;
   const size_t need = vsamp_block_matmul_workspace_size(M, N, K);
   if (need && (!workspace || !at_multiple(workspace, 16) || workspace_bytes < need)) return VSAMP_ERR_INVALID_ARG;
-  if (M > 0x7FFFFF00LL || N > 0x7FFFFF00LL || K > 0x7FFFFF00LL) return VSAMP_ERR_UNSUPPORTED;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return VSAMP_ERR_CUDA;
+  }
+  DeviceInfo d;
+  const vsamp_status st = device_info(dev, d);
+  if (st != VSAMP_OK) return st;
+  if (d.optin < kMmSmem) return VSAMP_ERR_UNSUPPORTED;
   BlockMatmulParams p{};
-  p.a = a;
-  p.b = b;
   p.sa = sa;
   p.sb = sb;
-  p.lda = lda;
   p.ldsa = ldsa;
-  p.ldb = ldb;
   p.ldsb = ldsb;
   p.M = M;
   p.N = N;
-  p.K = K;
   p.ldo = ldo;
   p.out = static_cast<unsigned char*>(out);
+  p.blocks = (int)ceil_blocks(K);
+  p.row_tiles = (int)((M + kMmRows - 1) / kMmRows);
+  p.parts = mm_parts(M, N, K);
+  p.items = (int64_t)p.row_tiles * ((N + kMmCols - 1) / kMmCols) * p.parts;
+  p.part = static_cast<float*>(workspace);
+  p.ldp = (N + 3) / 4 * 4;
+  p.a_rows = (int)(M < kMmRows ? M : kMmRows);
   p.accumulate = accumulate != 0;
+  const int es = out_dt == VSAMP_F32 ? 4 : 2;
+  p.vec = at_multiple(out, 16) && ldo * es % 16 == 0;
+  const long long wc = env_ll("VSAMP_WAIT_CYCLES", 0);
+  p.wait_cycles = wc > 0 ? wc : 4000000000LL;   // ~2 s at the maximum SM clock
+  p.drop_loads = env_int("VSAMP_TEST_DROP_LOADS", 0) != 0 ? 1 : 0;
+  CUtensorMap a_map, b_map;
+  if (!codes_map(a_map, a, lda, M, K, p.a_rows) || !codes_map(b_map, b, ldb, N, K, kMmCols)) return VSAMP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = grid_of(((M + 63) / 64) * ((N + 63) / 64));
+  const bool tile = b_kind == VSAMP_BLOCK_TILE;
   if (out_dt == VSAMP_F32)
-    return launch_1d(b_kind == VSAMP_BLOCK_TILE ? block_matmul_kernel<float, true> : block_matmul_kernel<float, false>, grid,
-                     256, 0, s, p);
-  return launch_1d(b_kind == VSAMP_BLOCK_TILE ? block_matmul_kernel<__nv_bfloat16, true>
-                                              : block_matmul_kernel<__nv_bfloat16, false>, grid, 256, 0, s, p);
+    return tile ? launch_matmul<float, true>(p, a_map, b_map, d, dev, s) : launch_matmul<float, false>(p, a_map, b_map, d, dev, s);
+  return tile ? launch_matmul<__nv_bfloat16, true>(p, a_map, b_map, d, dev, s)
+              : launch_matmul<__nv_bfloat16, false>(p, a_map, b_map, d, dev, s);
 }
 
 }  // extern "C"
