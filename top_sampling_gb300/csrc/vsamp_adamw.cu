@@ -11,7 +11,7 @@ static bool at_multiple(const void* p, unsigned bytes) { return (reinterpret_cas
 
 template <typename TP, typename TG>
 static vsamp_status launch_adamw(const AdamParams& p, bool master, bool bits8, const DeviceInfo& d, cudaStream_t s) {
-  const int64_t most = (int64_t)d.sm_count * 8;
+  const int64_t most = (int64_t)d.sm_count * kAdamPerSm;
   const unsigned grid = (unsigned)(p.chunks < most ? p.chunks : most);
   if constexpr (sizeof(TP) == 2) {
     if (master)
@@ -79,8 +79,10 @@ extern "C" vsamp_status vsamp_adamw(const vsamp_adamw_tensor* tensors, int32_t c
     p.c2 = (float)(1.0 / std::sqrt(-std::expm1((double)r.step * std::log(r.beta2))));
   }
   p.step = (uint32_t)r.step;
-  p.k0 = (uint32_t)r.seed;
-  p.k1 = (uint32_t)(r.seed >> 32);
+  for (uint32_t k = 0; k < 10; ++k) {
+    p.k0[k] = (uint32_t)r.seed + k * 0x9E3779B9u;
+    p.k1[k] = (uint32_t)(r.seed >> 32) + k * 0xBB67AE85u;
+  }
   p.lr_dev = r.lr_dev;
   p.step_dev = r.step_dev;
   p.grad_scale = r.grad_scale;

@@ -14,6 +14,7 @@
 namespace vsamp {
 
 constexpr int kAdamThreads = 256;
+constexpr int kAdamPerSm = 3;        // CTAs per SM
 constexpr int kAdamTensors = 384;    // of 80 bytes: 30,720 of a launch's 32,764 parameter bytes
 constexpr int kAdamChunk = 32;       // blocks of 128 elements that a CTA takes at a time
 
@@ -37,76 +38,222 @@ struct AdamParams {
   uint32_t count, chunks;
   float lr, b1, b2, one_b1, one_b2, eps, wd;
   float ln_b1, ln_b2, c1, c2;      // logarithms of the betas; 1 / (1 - b1^t), 1 / sqrt(1 - b2^t) of the host's step
-  uint32_t step, k0, k1;
+  uint32_t step, k0[10], k1[10];   // Philox round keys
   const float* lr_dev;
   const int64_t* step_dev;
   const float* grad_scale;
 };
 static_assert(sizeof(AdamTensor) == 80 && sizeof(AdamParams) <= 32764, "kernel parameters");
 
+// Philox4x32-10 with the round keys in the kernel's parameters: operands of the exclusive ors, no registers.
+__device__ __forceinline__ uint4 adam_words(const AdamParams& p, uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3) {
+  uint4 c = make_uint4(c0, c1, c2, c3);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    unsigned long long p0, p1;
+    asm("mul.wide.u32 %0, %1, %2;" : "=l"(p0) : "r"(c.x), "r"(0xD2511F53u));
+    asm("mul.wide.u32 %0, %1, %2;" : "=l"(p1) : "r"(c.z), "r"(0xCD9E8D57u));
+    c = make_uint4((uint32_t)(p1 >> 32) ^ c.y ^ p.k0[r], (uint32_t)p1, (uint32_t)(p0 >> 32) ^ c.w ^ p.k1[r], (uint32_t)p0);
+  }
+  return c;
+}
+
 // A magnitude in units of the scale to one of the two e4m3 values next to it, up with the probability of its place
-// between them: h is 16 random bits. Below 2^-6 the values are 2^-9 apart, above it 2^-3 of the power of two below.
-__device__ __forceinline__ float e4m3_stochastic(float y, uint32_t h) {
-  const int e = max((int)(__float_as_uint(y) >> 23) - 127, -6) - 3;
-  const float up = __uint_as_float((uint32_t)(127 - e) << 23), down = __uint_as_float((uint32_t)(127 + e) << 23);
-  return fminf(floorf(fmaf(y, up, ((float)h + 0.5f) * 0x1p-16f)) * down, kE4m3Max);
+// between them: u is 16 random bits, times 16, and 8. e4m3 keeps three fraction bits, so 20 bits of an fp32 magnitude are
+// dropped: the random bits are added below the kept ones and carry into them. Below 2^-6 the values are 2^-9 apart: those
+// of [2^-6, 2^-5), minus 2^-6.
+__device__ __forceinline__ float e4m3_stochastic(float y, uint32_t u) {
+  const float base = y < 0x1p-6f ? 0x1p-6f : 0.0f;
+  const float q = __uint_as_float((__float_as_uint(y + base) + u) & 0xFFF00000u) - base;
+  return fminf(q, kE4m3Max);
 }
 
-__device__ __forceinline__ float e4m3_to_float(uint32_t code) {
+// Two e4m3 codes (the lower 16 bits) as fp32.
+__device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
   uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(code & 0xFFu));
-  return __half2float(__ushort_as_half((unsigned short)(r & 0xFFFFu)));
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(codes));
+  __half2 h;
+  memcpy(&h, &r, 4);
+  return __half22float2(h);
 }
 
-template <typename T>
+// A root, a quotient and a reciprocal of about one unit's error each: their errors are far below what the step, lr times
+// the quotient, has of the parameter.
+__device__ __forceinline__ float sqrt_near(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_near(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The scale of a block of moments; inv is what they are multiplied with, 0 for a block that is not finite.
+__device__ __forceinline__ float moment_scale(uint32_t amax_bits, float& inv) {
+  const float s = fmaxf(__uint_as_float(amax_bits) * (1.0f / kE4m3Max), 0x1p-126f);
+  const bool bad = amax_bits >= kInfBits;
+  inv = bad ? 0.0f : rcp_near(s);
+  return bad ? __uint_as_float(0x7FC00000u) : s;
+}
+
+template <typename T, bool FULL>
 __device__ __forceinline__ void adam_load(const unsigned char* base, int64_t i, int left, bool aligned, float (&f)[4]) {
   ElemVec<T, 4> e;
   const unsigned char* p = base + i * (int64_t)sizeof(T);
-  if (left >= 4) e.load(p, aligned);
-  else e.load_some(p, left, 0u);
+  if (FULL) e.load(p, true);
+  else e.load_row(p, left, aligned, 0u);
 #pragma unroll
   for (int j = 0; j < 4; ++j) f[j] = e.at(j);
 }
-template <typename T>
+template <typename T, bool FULL>
 __device__ __forceinline__ void adam_store(unsigned char* base, int64_t i, int left, bool aligned, const float (&f)[4]) {
   ElemVec<T, 4> e;
   e.set(f);
   unsigned char* p = base + i * (int64_t)sizeof(T);
-  if (left >= 4) e.store(p, aligned);
-  else e.store_some(p, left);
+  if (FULL) e.store(p, true);
+  else e.store_row(p, left, aligned);
 }
+template <bool FULL>
 __device__ __forceinline__ uint32_t codes_load(const unsigned char* base, int64_t i, int left, bool aligned) {
-  if (left >= 4 && aligned) return *reinterpret_cast<const uint32_t*>(base + i);
+  if (FULL || (left >= 4 && aligned)) return *reinterpret_cast<const uint32_t*>(base + i);
   uint32_t w = 0u;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (j < left) w |= (uint32_t)base[i + j] << (8 * j);
   return w;
 }
+template <bool FULL>
 __device__ __forceinline__ void codes_store(unsigned char* base, int64_t i, int left, bool aligned, uint32_t w) {
-  if (left >= 4 && aligned) *reinterpret_cast<uint32_t*>(base + i) = w;
+  if (FULL || (left >= 4 && aligned)) *reinterpret_cast<uint32_t*>(base + i) = w;
   else
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (j < left) base[i + j] = (unsigned char)(w >> (8 * j));
 }
 
-template <typename TP, typename TG, bool MASTER, bool BITS8>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamParams p) {
-  begin_overlapped();
+struct AdamNow {   // the step's numbers, whether they came from the host or the device
+  float gs, lr, c1, c2;
+  uint32_t step;
+};
+
+// Blocks b, b + kAdamThreads / 32, ... (U of them) of a tensor by one warp: all loads first. FULL: whole blocks on aligned
+// addresses.
+template <typename TP, typename TG, bool MASTER, bool BITS8, int U, bool FULL>
+__device__ __forceinline__ void adam_blocks(const AdamParams& p, const AdamTensor& t, const AdamNow& now, int64_t b0, int lane) {
   constexpr bool kDrawParam = sizeof(TP) == 2 && !MASTER;   // a bf16 parameter without master is rounded at random
+  const bool aligned = t.aligned != 0;
+  float value[U][4], g[U][4], m[U][4], v[U][4], ms[U], vs[U];
+  uint32_t mw[U], vw[U];
+  int left[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t b = b0 + u * (kAdamThreads / 32), i = b * kBlock + lane * 4;
+    left[u] = FULL ? 4 : (int)(t.n - i < 4 ? (t.n - i > 0 ? t.n - i : 0) : 4);
+    if (MASTER) adam_load<float, FULL>(reinterpret_cast<const unsigned char*>(t.master), i, left[u], aligned, value[u]);
+    else adam_load<TP, FULL>(t.param, i, left[u], aligned, value[u]);
+    adam_load<TG, FULL>(t.grad, i, left[u], aligned, g[u]);
+    if (BITS8) {
+      mw[u] = codes_load<FULL>(t.m, i, left[u], aligned);
+      vw[u] = codes_load<FULL>(t.v, i, left[u], aligned);
+      ms[u] = t.m_scale[b];
+      vs[u] = t.v_scale[b];
+    } else {
+      adam_load<float, FULL>(t.m, i, left[u], aligned, m[u]);
+      adam_load<float, FULL>(t.v, i, left[u], aligned, v[u]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t b = b0 + u * (kAdamThreads / 32), i = b * kBlock + lane * 4;
+    if (BITS8) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const float2 a = e4m3_values(mw[u] >> (8 * j)), r = e4m3_values(vw[u] >> (8 * j));
+        m[u][j] = a.x * ms[u];
+        m[u][j + 1] = a.y * ms[u];
+        v[u][j] = r.x * vs[u];
+        v[u][j + 1] = r.y * vs[u];
+        v[u][j] *= v[u][j];
+        v[u][j + 1] *= v[u][j + 1];
+      }
+    }
+    float root[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float gj = g[u][j] * now.gs;
+      m[u][j] = fmaf(p.b1, m[u][j], p.one_b1 * gj);
+      v[u][j] = fmaf(p.b2, v[u][j], p.one_b2 * gj * gj);
+      root[j] = sqrt_near(v[u][j]);
+      const float change = __fdividef(m[u][j] * now.c1, fmaf(root[j], now.c2, p.eps));
+      value[u][j] = fmaf(-now.lr, fmaf(p.wd, value[u][j], change), value[u][j]);
+    }
+    if (MASTER) adam_store<float, FULL>(reinterpret_cast<unsigned char*>(t.master), i, left[u], aligned, value[u]);
+    if (kDrawParam) {
+      const uint4 w = adam_words(p, (uint32_t)(i >> 2), 0x80000000u, now.step, t.index);
+      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((__float_as_uint(value[u][j]) & kInfBits) != kInfBits)
+          value[u][j] = __uint_as_float((__float_as_uint(value[u][j]) + (h[j] & 0xFFFFu)) & 0xFFFF0000u);
+    }
+    adam_store<TP, FULL>(t.param, i, left[u], aligned, value[u]);
+    if (BITS8) {
+      uint32_t ma = 0u, va = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (FULL || j < left[u]) {
+          ma = max(ma, __float_as_uint(m[u][j]) & 0x7FFFFFFFu);
+          va = max(va, __float_as_uint(root[j]) & 0x7FFFFFFFu);
+        }
+      ma = warp_max_u32(ma);
+      va = warp_max_u32(va);
+      float mi, vi;
+      const float m_new = moment_scale(ma, mi), v_new = moment_scale(va, vi);
+      const uint4 w = adam_words(p, (uint32_t)(i >> 2), 0u, now.step, t.index);
+      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+      float y[4], r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[j] = copysignf(e4m3_stochastic(fabsf(m[u][j]) * mi, ((h[j] >> 12) & 0xFFFF0u) | 8u), m[u][j]);
+        r[j] = e4m3_stochastic(root[j] * vi, ((h[j] << 4) & 0xFFFF0u) | 8u);
+        if (root[j] > 0.0f) r[j] = fmaxf(r[j], 0x1p-9f);
+      }
+      uint32_t mc = e4m3_quad(y[0], y[1], y[2], y[3]), vc = e4m3_quad(r[0], r[1], r[2], r[3]);
+      if (ma >= kInfBits) mc = 0u;
+      if (va >= kInfBits) vc = 0u;
+      codes_store<FULL>(t.m, i, left[u], aligned, mc);
+      codes_store<FULL>(t.v, i, left[u], aligned, vc);
+      if (lane == 0) {
+        t.m_scale[b] = m_new;
+        t.v_scale[b] = v_new;
+      }
+    } else {
+      adam_store<float, FULL>(t.m, i, left[u], aligned, m[u]);
+      adam_store<float, FULL>(t.v, i, left[u], aligned, v[u]);
+    }
+  }
+}
+
+template <typename TP, typename TG, bool MASTER, bool BITS8>
+__global__ void __launch_bounds__(kAdamThreads, kAdamPerSm) adamw_kernel(const __grid_constant__ AdamParams p) {
+  begin_overlapped();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float gs = p.grad_scale ? *p.grad_scale : 1.0f;
-  const float lr = p.lr_dev ? *p.lr_dev : p.lr;
-  float c1 = p.c1, c2 = p.c2;
-  uint32_t step = p.step;
+  AdamNow now;
+  now.gs = p.grad_scale ? *p.grad_scale : 1.0f;
+  now.lr = p.lr_dev ? *p.lr_dev : p.lr;
+  now.c1 = p.c1;
+  now.c2 = p.c2;
+  now.step = p.step;
   if (p.step_dev) {
     const int64_t t = *p.step_dev;
     if (t < 1) return;
-    step = (uint32_t)t;
-    c1 = 1.0f / -expm1f((float)t * p.ln_b1);
-    c2 = rsqrtf(-expm1f((float)t * p.ln_b2));
+    now.step = (uint32_t)t;
+    now.c1 = 1.0f / -expm1f((float)t * p.ln_b1);
+    now.c2 = rsqrtf(-expm1f((float)t * p.ln_b2));
   }
+  constexpr int W = kAdamThreads / 32;
   for (uint32_t chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
     uint32_t lo = 0, hi = p.count;   // the last tensor whose first chunk is not behind this one
     while (hi - lo > 1) {
@@ -117,81 +264,11 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
     const AdamTensor& t = p.t[lo];
     const int64_t blocks = (t.n + kBlock - 1) / kBlock, begin = (int64_t)(chunk - t.first_chunk) * kAdamChunk;
     const int64_t end = begin + kAdamChunk < blocks ? begin + kAdamChunk : blocks;
-    const bool aligned = t.aligned != 0;
-    for (int64_t b = begin + warp; b < end; b += kAdamThreads / 32) {
-      const int64_t i = b * kBlock + lane * 4;
-      const int left = (int)(t.n - i < 4 ? (t.n - i > 0 ? t.n - i : 0) : 4);
-      float value[4], g[4], m[4], v[4], root[4];
-      if (MASTER) adam_load<float>(reinterpret_cast<const unsigned char*>(t.master), i, left, aligned, value);
-      else adam_load<TP>(t.param, i, left, aligned, value);
-      adam_load<TG>(t.grad, i, left, aligned, g);
-      if (BITS8) {
-        const uint32_t mw = codes_load(t.m, i, left, aligned), vw = codes_load(t.v, i, left, aligned);
-        const float ms = t.m_scale[b], vs = t.v_scale[b];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          m[j] = e4m3_to_float(mw >> (8 * j)) * ms;
-          v[j] = e4m3_to_float(vw >> (8 * j)) * vs;
-          v[j] *= v[j];
-        }
-      } else {
-        adam_load<float>(t.m, i, left, aligned, m);
-        adam_load<float>(t.v, i, left, aligned, v);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        g[j] *= gs;
-        m[j] = fmaf(p.b1, m[j], p.one_b1 * g[j]);
-        v[j] = fmaf(p.b2, v[j], p.one_b2 * g[j] * g[j]);
-        root[j] = sqrtf(v[j]);
-        const float change = m[j] * c1 / fmaf(root[j], c2, p.eps);
-        value[j] = fmaf(-lr, fmaf(p.wd, value[j], change), value[j]);
-      }
-      if (MASTER) adam_store<float>(reinterpret_cast<unsigned char*>(t.master), i, left, aligned, value);
-      if (kDrawParam) {
-        const uint4 w = philox4x32_10(make_uint4((uint32_t)(i >> 2), 0x80000000u, step, t.index), {p.k0, p.k1});
-        const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if ((__float_as_uint(value[j]) & kInfBits) != kInfBits)
-            value[j] = __uint_as_float((__float_as_uint(value[j]) + (h[j] & 0xFFFFu)) & 0xFFFF0000u);
-      }
-      adam_store<TP>(t.param, i, left, aligned, value);
-      if (BITS8) {
-        uint32_t ma = 0u, va = 0u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < left) {
-            ma = max(ma, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-            va = max(va, __float_as_uint(root[j]) & 0x7FFFFFFFu);
-          }
-        ma = warp_max_u32(ma);
-        va = warp_max_u32(va);
-        float mi, vi;
-        const float ms = block_scale(ma, mi), vs = block_scale(va, vi);
-        const uint4 w = philox4x32_10(make_uint4((uint32_t)(i >> 2), 0u, step, t.index), {p.k0, p.k1});
-        const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-        float y[4], r[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[j] = copysignf(e4m3_stochastic(fabsf(m[j]) * mi, h[j] >> 16), m[j]);
-          r[j] = e4m3_stochastic(root[j] * vi, h[j] & 0xFFFFu);
-          if (root[j] > 0.0f) r[j] = fmaxf(r[j], 0x1p-9f);
-        }
-        uint32_t mw = e4m3_quad(y[0], y[1], y[2], y[3]), vw = e4m3_quad(r[0], r[1], r[2], r[3]);
-        if (ma >= kInfBits) mw = 0u;
-        if (va >= kInfBits) vw = 0u;
-        codes_store(t.m, i, left, aligned, mw);
-        codes_store(t.v, i, left, aligned, vw);
-        if (lane == 0) {
-          t.m_scale[b] = ms;
-          t.v_scale[b] = vs;
-        }
-      } else {
-        adam_store<float>(t.m, i, left, aligned, m);
-        adam_store<float>(t.v, i, left, aligned, v);
-      }
-    }
+    const int64_t whole = t.aligned ? (end < t.n / kBlock ? end : t.n / kBlock) : begin;   // up to here in whole vectors
+    int64_t b = begin + warp;
+    for (; b + W < whole; b += 2 * W) adam_blocks<TP, TG, MASTER, BITS8, 2, true>(p, t, now, b, lane);
+    for (; b < whole; b += W) adam_blocks<TP, TG, MASTER, BITS8, 1, true>(p, t, now, b, lane);
+    for (; b < end; b += W) adam_blocks<TP, TG, MASTER, BITS8, 1, false>(p, t, now, b, lane);
   }
 }
 

@@ -51,27 +51,153 @@ __device__ __forceinline__ uint32_t e4m3_quad(float a, float b, float c, float d
   return e4m3_pair(a, b) | (e4m3_pair(c, d) << 16);
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if one of them is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// A thread's 8 x 8 elements as they were read, and their largest magnitudes per row and per column as fp32 values.
 template <typename T>
-struct QuantRow {   // eight elements of a row
-  static constexpr int VE = sizeof(T) == 4 ? 4 : 8, N = 8 / VE;
-  static __device__ __forceinline__ void load(const unsigned char* p, int left, bool aligned, float (&v)[8]) {
+struct QuantTile;
+
+template <>
+struct QuantTile<float> {
+  float v[8][8];
+  __device__ __forceinline__ void load_row(int i, const unsigned char* p, int left, bool aligned) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      ElemVec<T, VE> e;
-      const int n = left - k * VE;
-      if (n >= VE) e.load(p + k * VE * sizeof(T), aligned);
-      else e.load_some(p + k * VE * sizeof(T), n, 0u);
+    for (int k = 0; k < 2; ++k) {
+      ElemVec<float, 4> e;
+      e.load_row(p + k * 16, left - k * 4, aligned, 0u);
 #pragma unroll
-      for (int j = 0; j < VE; ++j) v[k * VE + j] = e.at(j);
+      for (int j = 0; j < 4; ++j) v[i][k * 4 + j] = e.at(j);
     }
+  }
+  __device__ __forceinline__ void clear_row(int i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+  }
+  __device__ __forceinline__ float at(int i, int j) const { return v[i][j]; }
+  __device__ __forceinline__ void forget() {}
+  // the largest of every row over the 16 lanes of this thread's rows; the lane's own row (lane & 7) is returned
+  __device__ __forceinline__ float row_max(int lane) const {
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m[i] = fabsf(v[i][0]);
+#pragma unroll
+      for (int j = 1; j < 8; ++j) m[i] = max_nan(m[i], fabsf(v[i][j]));
+    }
+    // halves of the rows are exchanged for halves of the lanes: 8 + 4 + ... values per step instead of 8 each time
+#pragma unroll
+    for (int o = 4; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < o) {
+          const bool up = (lane & o) != 0;
+          const float mine = up ? m[i + o] : m[i], other = up ? m[i] : m[i + o];
+          m[i] = max_nan(mine, __shfl_xor_sync(kFullMask, other, o));
+        }
+    return max_nan(m[0], __shfl_xor_sync(kFullMask, m[0], 8));
+  }
+  // the largest of every column over this warp's rows, to the warp's 128 words of shared memory
+  __device__ __forceinline__ void column_max(int lane, float* to) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float m = fabsf(v[0][j]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(v[i][j]));
+      m = max_nan(m, __shfl_xor_sync(kFullMask, m, 16));
+      if (lane < 16) to[(lane & 15) * 8 + j] = m;
+    }
+  }
+  __device__ __forceinline__ float all_max() const {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[i][j]));
+    return m;
+  }
+};
+
+template <>
+struct QuantTile<__nv_bfloat16> {   // pairs stay packed: half the registers, two maxima per instruction
+  uint32_t v[8][4];
+  __device__ __forceinline__ void load_row(int i, const unsigned char* p, int left, bool aligned) {
+    ElemVec<__nv_bfloat16, 8> e;
+    e.load_row(p, left, aligned, 0u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[i][j] = e.w[j];
+  }
+  __device__ __forceinline__ void clear_row(int i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[i][j] = 0u;
+  }
+  __device__ __forceinline__ float at(int i, int j) const {
+    return __uint_as_float(j & 1 ? v[i][j >> 1] & 0xFFFF0000u : v[i][j >> 1] << 16);
+  }
+  // Between the two outputs: the fp32 values of the first are not kept in registers for the second.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+r"(v[i][j]));
+  }
+  __device__ __forceinline__ uint32_t mag(int i, int j) const { return v[i][j] & 0x7FFF7FFFu; }
+  __device__ __forceinline__ float row_max(int lane) const {
+    uint32_t m[4];   // rows i and i + 4 in one word
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = max_nan_bf16x2(max_nan_bf16x2(mag(i, 0), mag(i, 1)), max_nan_bf16x2(mag(i, 2), mag(i, 3)));
+      const uint32_t b = max_nan_bf16x2(max_nan_bf16x2(mag(i + 4, 0), mag(i + 4, 1)), max_nan_bf16x2(mag(i + 4, 2), mag(i + 4, 3)));
+      m[i] = max_nan_bf16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    }
+#pragma unroll
+    for (int o = 2; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < o) {
+          const bool up = (lane & o) != 0;
+          const uint32_t mine = up ? m[i + o] : m[i], other = up ? m[i] : m[i + o];
+          m[i] = max_nan_bf16x2(mine, __shfl_xor_sync(kFullMask, other, o));
+        }
+    uint32_t r = max_nan_bf16x2(m[0], __shfl_xor_sync(kFullMask, m[0], 4));
+    r = max_nan_bf16x2(r, __shfl_xor_sync(kFullMask, r, 8));
+    return __uint_as_float(lane & 4 ? r & 0xFFFF0000u : r << 16);
+  }
+  __device__ __forceinline__ void column_max(int lane, float* to) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t m = mag(0, j);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = max_nan_bf16x2(m, mag(i, j));
+      m = max_nan_bf16x2(m, __shfl_xor_sync(kFullMask, m, 16));
+      if (lane < 16)
+        *reinterpret_cast<float2*>(to + (lane & 15) * 8 + 2 * j) =
+            make_float2(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    }
+  }
+  __device__ __forceinline__ float all_max() const {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = max_nan_bf16x2(m, mag(i, j));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
   }
 };
 
 template <typename T, bool TILE, bool PLAIN, bool TURNED>
-__global__ void __launch_bounds__(kQuantThreads) block_quant_kernel(const BlockQuantParams p) {
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 4 ? 2 : PLAIN && TURNED ? 3 : 4) block_quant_kernel(const BlockQuantParams p) {
   begin_overlapped();
   __shared__ __align__(16) unsigned char turned[TURNED ? kBlock * kBlock : 16];
-  __shared__ uint32_t maxima[8][kBlock];
+  __shared__ __align__(16) float maxima[8][kBlock];
   __shared__ __align__(16) float inverse[kBlock];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = (lane & 15) * 8, r0 = warp * 16 + (lane >> 4) * 8;   // this thread's 8 x 8 elements
@@ -79,37 +205,22 @@ __global__ void __launch_bounds__(kQuantThreads) block_quant_kernel(const BlockQ
     const int64_t rt = tile / p.col_tiles, ct = tile - rt * p.col_tiles;
     const int64_t row = rt * kBlock + r0, col = ct * kBlock + c0;
     const int left = (int)(p.C - col < 8 ? p.C - col : 8);
-    float v[8][8];
+    const int rows = (int)(p.R - row < 8 ? p.R - row : 8);
+    QuantTile<T> x;
+    const unsigned char* from = p.x + (row * p.ldx + col) * (int64_t)sizeof(T);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (row + i < p.R && left > 0)
-        QuantRow<T>::load(p.x + ((row + i) * p.ldx + col) * (int64_t)sizeof(T), left, p.aligned != 0, v[i]);
-      else
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+      if (i < rows && left > 0) x.load_row(i, from + i * p.ldx * (int64_t)sizeof(T), left, p.aligned != 0);
+      else x.clear_row(i);
     }
-    uint32_t rmax[8], cmax[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) rmax[i] = cmax[i] = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __float_as_uint(v[i][j]) & 0x7FFFFFFFu;
-        rmax[i] = max(rmax[i], b);
-        cmax[j] = max(cmax[j], b);
-      }
     float tile_inv = 0.0f;
     bool tile_bad = false;
     if (TILE) {
-      uint32_t m = 0u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, rmax[i]);
-      m = warp_max_u32(m);
-      if (lane == 0) maxima[warp][0] = m;
+      uint32_t m = warp_max_u32(__float_as_uint(x.all_max()));
+      if (lane == 0) maxima[warp][0] = __uint_as_float(m);
       __syncthreads();
 #pragma unroll
-      for (int w = 0; w < 8; ++w) m = max(m, maxima[w][0]);
+      for (int w = 0; w < 8; ++w) m = max(m, __float_as_uint(maxima[w][0]));
       const float s = block_scale(m, tile_inv);
       tile_bad = m >= kInfBits;
       if (threadIdx.x == 0) {
@@ -118,45 +229,42 @@ __global__ void __launch_bounds__(kQuantThreads) block_quant_kernel(const BlockQ
       }
     }
     if (PLAIN) {
+      float own_inv = tile_inv;   // of the row lane & 7; below 0 for one that is not finite
+      if (!TILE) {
+        const uint32_t m = __float_as_uint(x.row_max(lane));
+        const float s = block_scale(m, own_inv);
+        if (m >= kInfBits) own_inv = -1.0f;
+        const int64_t r = row + (lane & 7);
+        if ((lane & 8) == 0 && r < p.R) p.scales[ct * p.lds + r] = s;
+      }
+      unsigned char* to = p.codes + row * p.ldc + col;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float inv = tile_inv;
-        bool bad = tile_bad;
-        if (!TILE) {
-          uint32_t m = rmax[i];
-#pragma unroll
-          for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, o));
-          const float s = block_scale(m, inv);
-          bad = m >= kInfBits;
-          if ((lane & 15) == i && row + i < p.R) p.scales[ct * p.lds + row + i] = s;
-        }
-        if (row + i < p.R && left > 0) {
-          uint2 w;
-          w.x = e4m3_quad(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-          w.y = e4m3_quad(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
-          if (bad) w.x = w.y = 0u;
-          unsigned char* to = p.codes + (row + i) * p.ldc + col;
+        const float inv = TILE ? tile_inv : __shfl_sync(kFullMask, own_inv, (lane & 16) + i);
+        uint2 w;
+        w.x = e4m3_quad(x.at(i, 0) * inv, x.at(i, 1) * inv, x.at(i, 2) * inv, x.at(i, 3) * inv);
+        w.y = e4m3_quad(x.at(i, 4) * inv, x.at(i, 5) * inv, x.at(i, 6) * inv, x.at(i, 7) * inv);
+        if (TILE ? tile_bad : inv < 0.0f) w.x = w.y = 0u;
+        if (i < rows && left > 0) {
           if (left == 8) *reinterpret_cast<uint2*>(to) = w;
           else
             for (int j = 0; j < left; ++j) to[j] = (unsigned char)((j < 4 ? w.x : w.y) >> ((j & 3) * 8));
         }
+        to += p.ldc;
       }
     }
     if (TURNED) {
+      x.forget();
       if (!TILE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t m = max(cmax[j], __shfl_xor_sync(kFullMask, cmax[j], 16));
-          if (lane < 16) maxima[warp][c0 + j] = m;
-        }
+        x.column_max(lane, maxima[warp]);
         __syncthreads();
         if (threadIdx.x < kBlock) {
-          uint32_t m = 0u;
+          float m = maxima[0][threadIdx.x];
 #pragma unroll
-          for (int w = 0; w < 8; ++w) m = max(m, maxima[w][threadIdx.x]);
+          for (int w = 1; w < 8; ++w) m = max_nan(m, maxima[w][threadIdx.x]);
           float inv;
-          const float s = block_scale(m, inv);
-          inverse[threadIdx.x] = m >= kInfBits ? -1.0f : inv;   // -1 marks a block that is not finite
+          const float s = block_scale(__float_as_uint(m), inv);
+          inverse[threadIdx.x] = __float_as_uint(m) >= kInfBits ? -1.0f : inv;
           const int64_t c = ct * kBlock + threadIdx.x;
           if (c < p.C) p.scales_t[rt * p.ldst + c] = s;
         }
@@ -166,8 +274,8 @@ __global__ void __launch_bounds__(kQuantThreads) block_quant_kernel(const BlockQ
       for (int j = 0; j < 8; ++j) {
         const float inv = TILE ? tile_inv : inverse[c0 + j];
         uint2 w;
-        w.x = e4m3_quad(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv);
-        w.y = e4m3_quad(v[4][j] * inv, v[5][j] * inv, v[6][j] * inv, v[7][j] * inv);
+        w.x = e4m3_quad(x.at(0, j) * inv, x.at(1, j) * inv, x.at(2, j) * inv, x.at(3, j) * inv);
+        w.y = e4m3_quad(x.at(4, j) * inv, x.at(5, j) * inv, x.at(6, j) * inv, x.at(7, j) * inv);
         if (TILE ? tile_bad : inv < 0.0f) w.x = w.y = 0u;
         // 16-byte pieces of a row of 128 are permuted by the column's upper bits: two-way conflicts instead of sixteen
         const int c = c0 + j, piece = (r0 >> 4) ^ ((c >> 3) & 7);
