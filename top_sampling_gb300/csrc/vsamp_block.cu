@@ -58,7 +58,36 @@ static bool codes_map(CUtensorMap& map, const uint8_t* codes, int64_t ld, int64_
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A map of the scales of 1 x 128 blocks, [blocks, rows], for copies of box_rows rows' scales of one block.
+static bool scales_map(CUtensorMap& map, const float* scales, int64_t ld, int64_t rows, int64_t cols, int box_rows) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  const cuuint64_t size[2] = {(cuuint64_t)rows, (cuuint64_t)ceil_blocks(cols)}, stride[1] = {(cuuint64_t)ld * 4};
+  const cuuint32_t box[2] = {(cuuint32_t)box_rows, 1}, step[2] = {1, 1};
+  return encode(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(scales), size, stride, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A map of [parts, rows, cols] results for boxes of 32 rows of 128 bytes.
+static bool results_map(CUtensorMap& map, void* out, bool f32, int64_t ld, int64_t rows, int64_t cols, int parts) {
+  const EncodeTiled encode = encode_tiled();
+  if (!encode) return false;
+  const cuuint64_t es = f32 ? 4 : 2;
+  const cuuint64_t size[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+  const cuuint64_t stride[2] = {(cuuint64_t)ld * es, (cuuint64_t)(rows * ld) * es};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / es), 32, 1}, step[3] = {1, 1, 1};
+  return encode(&map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, size, stride, box,
+                step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int64_t kMmSms = 152;   // the division of the inner dimension goes by sizes alone
+
+// Whether the numbers of rows, columns, blocks and tiles keep within the kernel's 32-bit arithmetic.
+static bool mm_fits(int64_t M, int64_t N, int64_t K) {
+  return M <= 0x7FFFFE00LL && N <= 0x7FFFFE00LL && K <= 0x7FFFFE00LL && (double)M * N < 3e13;
+}
 
 // Parts of the inner dimension. A CTA's time goes by the blocks that it walks over and about six blocks' worth for each
 // tile's start and end; parts are written and read again. The fewest blocks of the longest CTA win.
@@ -77,9 +106,13 @@ static int mm_parts(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
+struct MatmulMaps {
+  CUtensorMap a, b, o, sa, sb;
+};
+
 template <typename TO, bool TILE>
-static vsamp_status launch_matmul(const BlockMatmulParams& p, const CUtensorMap& a, const CUtensorMap& b,
-                                  const DeviceInfo& d, int dev, cudaStream_t s) {
+static vsamp_status launch_matmul(const BlockMatmulParams& p, const MatmulMaps& m, const DeviceInfo& d, int dev,
+                                  cudaStream_t s) {
   auto kern = block_matmul_kernel<TO, TILE>;
   static std::atomic<bool> raised[64];
   if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
@@ -89,9 +122,10 @@ static vsamp_status launch_matmul(const BlockMatmulParams& p, const CUtensorMap&
     }
     if (dev < 64) raised[dev].store(true, std::memory_order_release);
   }
-  const vsamp_status st = launch_1d(kern, grid_of(p.items < d.sm_count ? p.items : d.sm_count), kMmThreads, kMmSmem, s, p, a, b);
+  const vsamp_status st = launch_1d(kern, grid_of(p.items < d.sm_count ? p.items : d.sm_count), kMmThreads, kMmSmem, s, p,
+                                    m.a, m.b, m.o, m.sa, m.sb);
   if (st != VSAMP_OK || p.parts == 1) return st;
-  const int64_t ctas = (p.M * (p.ldp / 4) + 255) / 256, most = (int64_t)d.sm_count * 8;
+  const int64_t ctas = ((int64_t)p.M * (p.ldp / 4) + 255) / 256, most = (int64_t)d.sm_count * 8;
   return launch_1d(block_matmul_join_kernel<TO>, grid_of(ctas < most ? ctas : most), 256, 0, s, p);
 }
 
@@ -133,7 +167,7 @@ vsamp_status vsamp_block_quantize(const void* x, vsamp_dtype dt, int64_t R, int6
 }
 
 size_t vsamp_block_matmul_workspace_size(int64_t M, int64_t N, int64_t K) {
-  if (M <= 0 || N <= 0 || K <= 0 || M > 0x7FFFFF00LL || N > 0x7FFFFF00LL || K > 0x7FFFFF00LL) return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || !mm_fits(M, N, K)) return 0;
   const int parts = mm_parts(M, N, K);
   return parts > 1 ? (size_t)parts * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4 : 0;
 }
@@ -146,7 +180,7 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   if (M <= 0 || N <= 0 || K <= 0 || ldo < N || !at_multiple(out, out_dt == VSAMP_F32 ? 4 : 2)) return VSAMP_ERR_INVALID_ARG;
   if (!matrix_ok(a, lda, sa, ldsa, VSAMP_BLOCK_ROW, M, K) || !matrix_ok(b, ldb, sb, ldsb, b_kind, N, K))
     return VSAMP_ERR_INVALID_ARG;
-  if (M > 0x7FFFFF00LL || N > 0x7FFFFF00LL || K > 0x7FFFFF00LL) return VSAMP_ERR_UNSUPPORTED;
+  if (!mm_fits(M, N, K)) return VSAMP_ERR_UNSUPPORTED;
   const size_t need = vsamp_block_matmul_workspace_size(M, N, K);
   if (need && (!workspace || !at_multiple(workspace, 16) || workspace_bytes < need)) return VSAMP_ERR_INVALID_ARG;
   int dev = 0;
@@ -159,35 +193,37 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   if (st != VSAMP_OK) return st;
   if (d.optin < kMmSmem) return VSAMP_ERR_UNSUPPORTED;
   BlockMatmulParams p{};
-  p.sa = sa;
   p.sb = sb;
-  p.ldsa = ldsa;
   p.ldsb = ldsb;
-  p.M = M;
-  p.N = N;
+  p.M = (int)M;
+  p.N = (int)N;
   p.ldo = ldo;
   p.out = static_cast<unsigned char*>(out);
   p.blocks = (int)ceil_blocks(K);
   p.row_tiles = (int)((M + kMmRows - 1) / kMmRows);
   p.parts = mm_parts(M, N, K);
-  p.items = (int64_t)p.row_tiles * ((N + kMmCols - 1) / kMmCols) * p.parts;
+  p.items = (int)(p.row_tiles * ((N + kMmCols - 1) / kMmCols) * p.parts);
   p.part = static_cast<float*>(workspace);
   p.ldp = (N + 3) / 4 * 4;
   p.a_rows = (int)(M < kMmRows ? M : kMmRows);
   p.accumulate = accumulate != 0;
   const int es = out_dt == VSAMP_F32 ? 4 : 2;
-  p.vec = at_multiple(out, 16) && ldo * es % 16 == 0;
+  // bf16 sums are added and rounded once, by the warps themselves; a stride of a tensor map has 40 bits
+  p.boxes = at_multiple(out, 16) && ldo * es % 16 == 0 && !(p.accumulate && es == 2) && (double)M * ldo * es < 1e12;
   const long long wc = env_ll("VSAMP_WAIT_CYCLES", 0);
   p.wait_cycles = wc > 0 ? wc : 4000000000LL;   // ~2 s at the maximum SM clock
   p.drop_loads = env_int("VSAMP_TEST_DROP_LOADS", 0) != 0 ? 1 : 0;
-  CUtensorMap a_map, b_map;
-  if (!codes_map(a_map, a, lda, M, K, p.a_rows) || !codes_map(b_map, b, ldb, N, K, kMmCols)) return VSAMP_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool tile = b_kind == VSAMP_BLOCK_TILE;
-  if (out_dt == VSAMP_F32)
-    return tile ? launch_matmul<float, true>(p, a_map, b_map, d, dev, s) : launch_matmul<float, false>(p, a_map, b_map, d, dev, s);
-  return tile ? launch_matmul<__nv_bfloat16, true>(p, a_map, b_map, d, dev, s)
-              : launch_matmul<__nv_bfloat16, false>(p, a_map, b_map, d, dev, s);
+  MatmulMaps m{};
+  if (!codes_map(m.a, a, lda, M, K, p.a_rows) || !codes_map(m.b, b, ldb, N, K, kMmCols) ||
+      !scales_map(m.sa, sa, ldsa, M, K, kMmRows) || (!tile && !scales_map(m.sb, sb, ldsb, N, K, kMmCols)))
+    return VSAMP_ERR_CUDA;
+  if (p.parts > 1 ? !results_map(m.o, p.part, true, p.ldp, M, N, p.parts)
+                  : p.boxes && !results_map(m.o, out, es == 4, ldo, M, N, 1))
+    return VSAMP_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (out_dt == VSAMP_F32) return tile ? launch_matmul<float, true>(p, m, d, dev, s) : launch_matmul<float, false>(p, m, d, dev, s);
+  return tile ? launch_matmul<__nv_bfloat16, true>(p, m, d, dev, s) : launch_matmul<__nv_bfloat16, false>(p, m, d, dev, s);
 }
 
 }  // extern "C"

@@ -4,9 +4,9 @@
 //
 // One CTA per SM walks over tiles of 128 x 256 results. A warp copies blocks of both operands into a ring in shared memory
 // (tensor copies with the 128-byte swizzle the tensor cores read), another issues four products of 32 inner elements per
-// block into one of two accumulators in tensor memory, and eight warps take each finished block out of tensor memory and
+// block into one of two accumulators in tensor memory, and sixteen warps take each finished block out of tensor memory and
 // add it, scaled, to fp32 sums in registers: the sum of a block's 128 products is the only one that the tensor core
-// forms. A row of a is a lane, so its scale is one register; a 128 x 128 block's scale of b is the same for a warp's 128
+// forms. A row of a is a lane, so its scale is one register; a 128 x 128 block's scale of b is the same for a warp's 64
 // columns, and with one scale per row of b the column scales are read from shared memory as broadcasts.
 //
 // Every wait is bounded. A CTA one of whose waits gave up lets its copies and products end, frees its tensor memory and
@@ -18,135 +18,155 @@
 
 namespace vsamp {
 
-constexpr int kMmRows = 128, kMmCols = 256, kMmStages = 4;
-constexpr int kMmThreads = 320;                     // eight warps of sums, the copying warp, the issuing warp
+constexpr int kMmRows = 128, kMmCols = 256, kMmStages = 3;
+constexpr int kMmWarps = 16;                        // warps of sums: 32 rows x 64 columns each
+constexpr int kMmThreads = kMmWarps * 32 + 128;     // and a warpgroup with the copying and the issuing warp
+constexpr int kMmSumRegs = 112, kMmOtherRegs = 32;  // registers per thread: 512 x 112 + 128 x 32 of the launch's 640 x 96
 constexpr int kMmABytes = kMmRows * kBlock, kMmBBytes = kMmCols * kBlock, kMmStageBytes = kMmABytes + kMmBBytes;
 constexpr int kMmColumns = 512;                     // of tensor memory: two accumulators
-constexpr int kMmOutOff = kMmStages * kMmStageBytes;            // 2 KB per warp to turn results into rows
-constexpr int kMmScaleOff = kMmOutOff + 8 * 2048;               // two sets of 128 column scales per warp
-constexpr int kMmBarOff = kMmScaleOff + 8 * 2 * 128 * 4;
-constexpr int kMmSmem = kMmBarOff + 128 + 1024;                 // and what aligns the ring to 1024 bytes
+constexpr int kMmOutOff = kMmStages * kMmStageBytes;            // per warp 32 rows of 128 bytes of results
+// A block's scales, 128 of rows and 256 of columns, have a ring of their own: they are read after the block's products are
+// done, when its stage may be written again. Block n is copied once the products of block n - kMmStages are done, whose
+// accumulator had held block n - kMmStages - 2: every warp has read that one's scales, so six sets would do.
+constexpr int kMmScaleSets = 8, kMmScaleBytes = (kMmRows + kMmCols) * 4;
+constexpr int kMmScaleOff = kMmOutOff + kMmWarps * 4096;
+constexpr int kMmBarOff = kMmScaleOff + kMmScaleSets * kMmScaleBytes;
+constexpr int kMmSmem = kMmBarOff + 256 + 1024;                 // and what aligns the ring to 1024 bytes
 
 struct BlockMatmulParams {
-  const float* sa;
-  const float* sb;
-  int64_t ldsa, ldsb;
-  int64_t M, N, ldo;
-  int64_t items;             // tiles times parts of the inner dimension
+  const float* sb;           // of 128 x 128 blocks: the others come by their tensor map
+  int64_t ldsb, ldo;
+  int M, N;
+  int items;                 // tiles times parts of the inner dimension
   unsigned char* out;
   float* part;               // [parts, M, ldp] sums of a part each, when there are several
   int64_t ldp;
   int row_tiles, blocks, parts;
   int a_rows;                // rows of a per copy
-  int accumulate, vec;       // vec: rows of the output begin on 16-byte boundaries
+  int accumulate;
+  int boxes;                 // results leave as boxes of the output's tensor map: its rows begin on 16-byte boundaries
   int drop_loads;            // test: copies are expected and never made
   long long wait_cycles;
 };
 
 struct MmItem {
-  int64_t m0, n0;
-  int j0, j1;
+  int m0, n0, j0, j1;
 };
-__device__ __forceinline__ MmItem mm_item(const BlockMatmulParams& p, int64_t item) {
-  const int64_t tile = item / p.parts;
-  const int part = (int)(item - tile * p.parts);
-  const int64_t nt = tile / p.row_tiles;
+__device__ __forceinline__ MmItem mm_item(const BlockMatmulParams& p, int item) {
+  const int tile = item / p.parts, part = item - tile * p.parts, nt = tile / p.row_tiles;
   MmItem w;
   w.m0 = (tile - nt * p.row_tiles) * kMmRows;
   w.n0 = nt * kMmCols;
-  w.j0 = (int)((int64_t)p.blocks * part / p.parts);
-  w.j1 = (int)((int64_t)p.blocks * (part + 1) / p.parts);
+  w.j0 = p.blocks * part / p.parts;
+  w.j1 = p.blocks * (part + 1) / p.parts;
   return w;
 }
 
-// 32 rows of a warp's results, 128 columns from n0 on, to rows of T: written, or added to what is there in fp32.
-template <typename T, bool ADD>
-__device__ __forceinline__ void mm_store(const float2 (&acc)[64], unsigned char* turn, T* out, int64_t ldo, int64_t m0,
-                                         int64_t M, int64_t n0, int64_t N, int lane, bool vec) {
-  constexpr bool F32 = sizeof(T) == 4 || ADD;   // what is turned: fp32, or what is written
-  constexpr int W = F32 ? 4 : 8;                // elements of 16 bytes
-  constexpr int C = 4 * W;                      // columns per turn: 64 bytes of a row
+// A row's 128 bytes of results, 32 fp32 or 64 bf16 columns, to the lane's row of the warp's box. Its 16-byte pieces are
+// permuted by the row (the 128-byte swizzle): no bank conflicts on either side.
+template <typename T>
+__device__ __forceinline__ void mm_box_row(const float2 (&acc)[32], int c, unsigned char* box, int lane) {
 #pragma unroll
-  for (int c = 0; c < 128 / C; ++c) {
-    if (n0 + c * C >= N) break;
-    // 16-byte pieces of a row are permuted by the row, so that neither side meets bank conflicts
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < 8; ++q) {
+    uint4 w;
+    if constexpr (sizeof(T) == 4) {
+      const float2 a = acc[c * 16 + q * 2], b = acc[c * 16 + q * 2 + 1];
+      w = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    } else {
       uint32_t u[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if constexpr (F32) {
-          const float2 a = acc[c * 8 + q * 2 + i / 2];
-          u[i] = __float_as_uint(i & 1 ? a.y : a.x);
-        } else {
-          const __nv_bfloat162 h = __float22bfloat162_rn(acc[c * 16 + q * 4 + i]);
-          memcpy(&u[i], &h, 4);
-        }
+        const __nv_bfloat162 h = __float22bfloat162_rn(acc[q * 4 + i]);
+        memcpy(&u[i], &h, 4);
       }
-      *reinterpret_cast<uint4*>(turn + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+      w = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    __syncwarp();
+    *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
+  }
+}
+
+// A warp's 32 rows x 64 columns to boxes of the map; the copies run on while the warp goes on.
+template <typename T>
+__device__ __forceinline__ void mm_store_boxes(const float2 (&acc)[32], unsigned char* box, const CUtensorMap* map, int m0,
+                                               int n0, int N, int part, int lane, bool add) {
+  constexpr int C = 128 / sizeof(T);   // columns of a box
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2), q = lane & 3;
-      const uint4 w = *reinterpret_cast<const uint4*>(turn + r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
-      const int64_t m = m0 + r, n = n0 + c * C + q * W;
-      if (m < M && n < N) {
-        unsigned char* to = reinterpret_cast<unsigned char*>(out + m * ldo + n);
-        const int left = (int)(N - n < W ? N - n : W);
-        if constexpr (ADD) {
-          ElemVec<T, 4> e;
-          e.load_row(to, left, vec, 0u);
-          const float f[4] = {e.at(0) + __uint_as_float(w.x), e.at(1) + __uint_as_float(w.y), e.at(2) + __uint_as_float(w.z),
-                              e.at(3) + __uint_as_float(w.w)};
-          e.set(f);
-          e.store_row(to, left, vec);
+  for (int c = 0; c < 64 / C; ++c) {
+    if (n0 + c * C >= N) break;
+    if (lane == 0) bulk_read_done();   // of the box's last use
+    __syncwarp();
+    mm_box_row<T>(acc, c, box, lane);
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) tma_store_3d(map, n0 + c * C, m0, part, smem_addr(box), add);
+  }
+}
+
+// The same to rows at any address: a lane per column, fp32 in the box.
+template <typename T>
+__device__ __forceinline__ void mm_store_rows(const float2 (&acc)[32], unsigned char* box, T* out, int64_t ldo, int m0, int M,
+                                              int n0, int N, int lane, bool add) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int n = n0 + c * 32 + lane;
+    if (n0 + c * 32 >= N) break;
+    __syncwarp();
+    mm_box_row<float>(acc, c, box, lane);
+    __syncwarp();
+    if (n < N) {
+      const int rows = M - m0 < 32 ? M - m0 : 32;
+      T* to = out + m0 * ldo + n;
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r, to += ldo) {
+        const float v = *reinterpret_cast<const float*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+        if constexpr (sizeof(T) == 4) {
+          // one addition per element and call: the same result every time
+          if (add) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(to), "f"(v) : "memory");
+          else *to = v;
         } else {
-          ElemVec<T, W> e;
-          e.w[0] = w.x;
-          e.w[1] = w.y;
-          e.w[2] = w.z;
-          e.w[3] = w.w;
-          e.store_row(to, left, vec);
+          *to = (T)(add ? v + (float)*to : v);
         }
       }
     }
-    __syncwarp();
   }
 }
 
 template <typename TO, bool TILE>
 __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const BlockMatmulParams p,
                                                                      const __grid_constant__ CUtensorMap a_map,
-                                                                     const __grid_constant__ CUtensorMap b_map) {
+                                                                     const __grid_constant__ CUtensorMap b_map,
+                                                                     const __grid_constant__ CUtensorMap o_map,
+                                                                     const __grid_constant__ CUtensorMap sa_map,
+                                                                     const __grid_constant__ CUtensorMap sb_map) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u);
   const uint32_t ring = smem_addr(smem);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kMmBarOff);   // a stage's copies have landed
-  uint64_t* empty = full + kMmStages;                               // a stage's products are done
-  uint64_t* done = empty + kMmStages;                               // an accumulator holds a block
-  uint64_t* taken = done + 2;                                       // an accumulator has been read
+  uint64_t* done = full + kMmStages;                                // a stage's products are done: an accumulator holds them
+  uint64_t* taken = done + kMmStages;                               // an accumulator has been read
   uint64_t* drain = taken + 2;
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* scaled = drain + 1;                                     // a set of scales has landed
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(scaled + kMmScaleSets);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMmStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
       mbar_init(&done[i], 1);
-      mbar_init(&taken[i], 8);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&taken[i], kMmWarps);
+    for (int i = 0; i < kMmScaleSets; ++i) mbar_init(&scaled[i], 1);
     mbar_init(drain, 1);
     *dead = 0;
     fence_mbar_init();
   }
-  if (warp == 9) tmem_alloc(smem_addr(tmem_at), kMmColumns);
-  if (threadIdx.x == 256) {
+  if (warp == kMmWarps + 1) tmem_alloc(smem_addr(tmem_at), kMmColumns);
+  if (threadIdx.x == kMmWarps * 32) {
     tma_prefetch_map(&a_map);
     tma_prefetch_map(&b_map);
+    tma_prefetch_map(&sa_map);
+    if (!TILE) tma_prefetch_map(&sb_map);
+    if (p.boxes) tma_prefetch_map(&o_map);
   }
   tcgen05_fence_before();
   __syncthreads();
@@ -156,34 +176,41 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
   uint32_t n = 0;   // blocks so far, of every warp by itself
   bool alive = true;
 
-  if (warp == 8) {
-    if (lane == 0) {
+  if (warp >= kMmWarps) {
+    fewer_registers<kMmOtherRegs>();
+    uint32_t s = 0, turn = 0;   // stage of block n, and the parity of its phase
+    if (warp == kMmWarps && lane == 0) {
       const uint32_t bytes = (uint32_t)(p.a_rows * kBlock + kMmBBytes);
-      for (int64_t item = blockIdx.x; alive && item < p.items; item += gridDim.x) {
+      for (int item = blockIdx.x; alive && item < p.items; item += gridDim.x) {
         const MmItem w = mm_item(p, item);
         for (int j = w.j0; j < w.j1; ++j, ++n) {
-          const uint32_t s = n % kMmStages, turn = n / kMmStages;
-          if (!wait_alive(&empty[s], (turn & 1) ^ 1, dead, p.wait_cycles)) {
+          if (!wait_alive(&done[s], turn ^ 1, dead, p.wait_cycles)) {
             alive = false;
             break;
           }
+          const uint32_t set = n % kMmScaleSets, to = ring + kMmScaleOff + set * kMmScaleBytes;
           mbar_arrive_expect_tx(&full[s], bytes);
+          mbar_arrive_expect_tx(&scaled[set], TILE ? kMmRows * 4 : kMmScaleBytes);
           if (!p.drop_loads) {
-            tma_load_2d(ring + s * kMmStageBytes, &a_map, j * kBlock, (int32_t)w.m0, smem_addr(&full[s]));
-            tma_load_2d(ring + s * kMmStageBytes + kMmABytes, &b_map, j * kBlock, (int32_t)w.n0, smem_addr(&full[s]));
+            tma_load_2d(to, &sa_map, w.m0, j, smem_addr(&scaled[set]));
+            if (!TILE) tma_load_2d(to + kMmRows * 4, &sb_map, w.n0, j, smem_addr(&scaled[set]));
+            tma_load_2d(ring + s * kMmStageBytes, &a_map, j * kBlock, w.m0, smem_addr(&full[s]));
+            tma_load_2d(ring + s * kMmStageBytes + kMmABytes, &b_map, j * kBlock, w.n0, smem_addr(&full[s]));
+          }
+          if (++s == kMmStages) {
+            s = 0;
+            turn ^= 1;
           }
         }
       }
-    }
-  } else if (warp == 9) {
-    if (lane == 0) {
+    } else if (warp == kMmWarps + 1 && lane == 0) {
       constexpr uint32_t idesc = umma_e4m3(kMmRows, kMmCols);
-      for (int64_t item = blockIdx.x; alive && item < p.items; item += gridDim.x) {
+      for (int item = blockIdx.x; alive && item < p.items; item += gridDim.x) {
         const MmItem w = mm_item(p, item);
         for (int j = w.j0; j < w.j1; ++j, ++n) {
-          const uint32_t s = n % kMmStages, b = n & 1;
+          const uint32_t b = n & 1;
           if (!wait_alive(&taken[b], ((n >> 1) & 1) ^ 1, dead, p.wait_cycles) ||
-              !wait_alive(&full[s], (n / kMmStages) & 1, dead, p.wait_cycles)) {
+              !wait_alive(&full[s], turn, dead, p.wait_cycles)) {
             alive = false;
             break;
           }
@@ -191,117 +218,118 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
           const uint64_t da = umma_operand(ring + s * kMmStageBytes), db = umma_operand(ring + s * kMmStageBytes + kMmABytes);
 #pragma unroll
           for (int k = 0; k < kBlock / 32; ++k) umma_f8(tmem + b * kMmCols, da + 2 * k, db + 2 * k, idesc, k > 0);
-          umma_commit(smem_addr(&empty[s]));
-          umma_commit(smem_addr(&done[b]));
+          umma_commit(smem_addr(&done[s]));
+          if (++s == kMmStages) {
+            s = 0;
+            turn ^= 1;
+          }
         }
       }
     }
   } else {
-    const int half = warp >> 2;                        // columns 128 half .. of the tile
+    more_registers<kMmSumRegs>();
+    const int quarter = warp >> 2;                     // columns 64 quarter .. of the tile
     const uint32_t lanes = (uint32_t)(warp & 3) * 32;  // of tensor memory: rows of the tile
-    unsigned char* turn = smem + kMmOutOff + warp * 2048;
-    float* cols = reinterpret_cast<float*>(smem + kMmScaleOff) + warp * 256;
-    const uint32_t from = tmem + (lanes << 16) + half * 128;
-    for (int64_t item = blockIdx.x; item < p.items; item += gridDim.x) {
+    unsigned char* box = smem + kMmOutOff + warp * 4096;
+    float* cols = reinterpret_cast<float*>(smem + kMmScaleOff) + warp * 128;
+    const uint32_t from = tmem + (lanes << 16) + quarter * 64;
+    uint32_t s = 0, turn = 0;
+    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
       const MmItem w = mm_item(p, item);
-      const int64_t row0 = w.m0 + lanes, col0 = w.n0 + half * 128;
+      const int row0 = w.m0 + (int)lanes, col0 = w.n0 + quarter * 64;
       const bool active = row0 < p.M && col0 < p.N;    // otherwise the warp has no results here
-      float2 acc[64];
+      float2 acc[32];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      const float* sa = p.sa + row0 + lane;
-      const bool row = row0 + lane < p.M;
-      // scales are fetched two blocks ahead
-      auto row_scale = [&](int j) { return row && j < w.j1 ? sa[j * p.ldsa] : 0.0f; };
-      auto col_scale = [&](int j) -> float4 {
-        float4 c = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (!active || j >= w.j1) return c;
-        if (TILE) {
-          c.x = p.sb[col0 / kBlock * p.ldsb + j];
-        } else {
-          const int64_t at = col0 + lane * 4;
-          const float* q = p.sb + j * p.ldsb + at;
-          if (at + 4 <= p.N) c = *reinterpret_cast<const float4*>(q);
-          else {
-            if (at < p.N) c.x = q[0];
-            if (at + 1 < p.N) c.y = q[1];
-            if (at + 2 < p.N) c.z = q[2];
-          }
-        }
-        return c;
-      };
-      float r0 = row_scale(w.j0), r1 = row_scale(w.j0 + 1);
-      float4 c0 = col_scale(w.j0), c1 = col_scale(w.j0 + 1);
+      for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
+      // A row's scale is the lane's. The scale of 128 x 128 blocks is one for the warp: a lane holds that of every 32nd
+      // block, fetched 32 blocks ahead; the columns' scales are read from shared memory.
+      const float* sb = p.sb + (TILE ? col0 / kBlock * p.ldsb : 0);
+      auto tile_scales = [&](int j) { return TILE && active && j + lane < w.j1 ? sb[j + lane] : 0.0f; };
+      float now = tile_scales(w.j0), next = tile_scales(w.j0 + 32);
       for (int j = w.j0; alive && j < w.j1; ++j, ++n) {
-        const uint32_t b = n & 1;
-        const float rs = r0;
-        const float4 cs = c0;
-        r0 = r1;
-        c0 = c1;
-        r1 = row_scale(j + 2);
-        c1 = col_scale(j + 2);
-        if (!TILE) *reinterpret_cast<float4*>(cols + b * 128 + lane * 4) = cs;
-        const bool ok = wait_alive(&done[b], (n >> 1) & 1, dead, p.wait_cycles);
-        alive = __all_sync(kFullMask, ok);   // also orders the column scales within the warp
+        const uint32_t b = n & 1, set = n % kMmScaleSets;
+        const float* scales = reinterpret_cast<const float*>(smem + kMmScaleOff + set * kMmScaleBytes);
+        const float* cb = scales + kMmRows + quarter * 64;
+        bool ok = wait_alive(&scaled[set], (n / kMmScaleSets) & 1, dead, p.wait_cycles);
+        float rs = ok ? scales[lanes + lane] : 0.0f;
+        if (TILE) {
+          const int k = (j - w.j0) & 31;
+          if (k == 0 && j > w.j0) {
+            now = next;
+            next = tile_scales(j + 32);
+          }
+          rs *= __shfl_sync(kFullMask, now, k);
+        }
+        ok = ok && wait_alive(&done[s], turn, dead, p.wait_cycles);
+        if (++s == kMmStages) {
+          s = 0;
+          turn ^= 1;
+        }
+        alive = __all_sync(kFullMask, ok);
         if (!alive) break;
         tcgen05_fence_after();
+        const float2 s2 = make_float2(rs, rs);
         if (active) {
-          const float2 s = TILE ? make_float2(rs * cs.x, rs * cs.x) : make_float2(rs, rs);
-          const float* cb = cols + b * 128;
-          float t[2][16];
-          tmem_load16(from + b * kMmCols, t[0]);
-          tmem_wait(t[0]);
+          float t[32];
+          tmem_load32(from + b * kMmCols, t);
+          tmem_wait(t);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (c < 7) tmem_load16(from + b * kMmCols + (c + 1) * 16, t[(c + 1) & 1]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 v = make_float2(t[c & 1][2 * i], t[c & 1][2 * i + 1]);
-              if (TILE) {
-                acc[c * 8 + i] = __ffma2_rn(v, s, acc[c * 8 + i]);
-              } else {
-                const float2 q = *reinterpret_cast<const float2*>(cb + c * 16 + 2 * i);
-                acc[c * 8 + i] = __ffma2_rn(__fmul2_rn(v, s), q, acc[c * 8 + i]);
-              }
-            }
-            if (c < 7) tmem_wait(t[(c + 1) & 1]);
+          for (int i = 0; i < 16; ++i) {
+            const float2 v = make_float2(t[2 * i], t[2 * i + 1]);
+            acc[i] = TILE ? __ffma2_rn(v, s2, acc[i])
+                          : __ffma2_rn(__fmul2_rn(v, s2), *reinterpret_cast<const float2*>(cb + 2 * i), acc[i]);
           }
+          tmem_load32(from + b * kMmCols + 32, t);
+          tmem_wait(t);
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&taken[b]));
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 v = make_float2(t[2 * i], t[2 * i + 1]);
+            acc[16 + i] = TILE ? __ffma2_rn(v, s2, acc[16 + i])
+                               : __ffma2_rn(__fmul2_rn(v, s2), *reinterpret_cast<const float2*>(cb + 32 + 2 * i), acc[16 + i]);
+          }
+        } else if (lane == 0) {
+          mbar_arrive(smem_addr(&taken[b]));
         }
-        tcgen05_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&taken[b]));
       }
       if (!alive) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
+        for (int i = 0; i < 32; ++i) acc[i] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
       }
       if (active) {
+        const int part = item % p.parts;
+        const bool add = p.accumulate != 0;
         if (p.parts > 1) {
-          float* to = p.part + (item % p.parts) * p.M * p.ldp;
-          mm_store<float, false>(acc, turn, to, p.ldp, row0, p.M, col0, p.N, lane, true);
-        } else if (p.accumulate) {
-          mm_store<TO, true>(acc, turn, reinterpret_cast<TO*>(p.out), p.ldo, row0, p.M, col0, p.N, lane, p.vec != 0);
+          mm_store_boxes<float>(acc, box, &o_map, row0, col0, p.N, part, lane, false);
+        } else if (p.boxes) {
+          mm_store_boxes<TO>(acc, box, &o_map, row0, col0, p.N, 0, lane, add);
         } else {
-          mm_store<TO, false>(acc, turn, reinterpret_cast<TO*>(p.out), p.ldo, row0, p.M, col0, p.N, lane, p.vec != 0);
+          mm_store_rows<TO>(acc, box, reinterpret_cast<TO*>(p.out), p.ldo, row0, p.M, col0, p.N, lane, add);
         }
       }
     }
+    if (lane == 0) bulk_done();
   }
   __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
   if (*dead) {
     // copies and products under way end before shared and tensor memory are given up
-    if (threadIdx.x == 256 && !p.drop_loads)
+    if (threadIdx.x == kMmWarps * 32 && !p.drop_loads)
       for (uint32_t k = n < kMmStages ? 0 : n - kMmStages; k < n; ++k)
         (void)mbar_wait_bounded(&full[k % kMmStages], (k / kMmStages) & 1, 4000000000LL);
-    if (threadIdx.x == 288) {
+    if (threadIdx.x == kMmWarps * 32 && !p.drop_loads)
+      for (uint32_t k = n < kMmScaleSets ? 0 : n - kMmScaleSets; k < n; ++k)
+        (void)mbar_wait_bounded(&scaled[k % kMmScaleSets], (k / kMmScaleSets) & 1, 4000000000LL);
+    if (threadIdx.x == kMmWarps * 32 + 32) {
       umma_commit(smem_addr(drain));
       (void)mbar_wait_bounded(drain, 0, 4000000000LL);
     }
     __syncthreads();
   }
-  if (warp == 9) {
+  if (warp == kMmWarps + 1) {
     __syncwarp();
     tcgen05_fence_after();
     tmem_free(tmem, kMmColumns);
@@ -312,13 +340,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
 template <typename TO>
 __global__ void __launch_bounds__(256) block_matmul_join_kernel(const BlockMatmulParams p) {
   begin_overlapped();
-  const int64_t quads = p.ldp / 4, total = p.M * quads;
+  const int64_t quads = p.ldp / 4, total = (int64_t)p.M * quads;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / quads, n = (i - m * quads) * 4;
     const float* q = p.part + m * p.ldp + n;
     float4 s = *reinterpret_cast<const float4*>(q);
     for (int k = 1; k < p.parts; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(q + k * p.M * p.ldp);
+      const float4 v = *reinterpret_cast<const float4*>(q + k * (int64_t)p.M * p.ldp);
       s.x += v.x;
       s.y += v.y;
       s.z += v.z;
