@@ -89,14 +89,18 @@ static bool mm_fits(int64_t M, int64_t N, int64_t K) {
   return M <= 0x7FFFFE00LL && N <= 0x7FFFFE00LL && K <= 0x7FFFFE00LL && (double)M * N < 3e13;
 }
 
+// Whether pairs of CTAs take tiles of 256 rows.
+static bool mm_pair(int64_t M) { return M > kMmRows; }
+
 // Parts of the inner dimension. A CTA's time goes by the blocks that it walks over and about six blocks' worth for each
 // tile's start and end; parts are written and read again. The fewest blocks of the longest CTA win.
 static int mm_parts(int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = ((M + kMmRows - 1) / kMmRows) * ((N + kMmCols - 1) / kMmCols), blocks = ceil_blocks(K);
+  const int64_t g = mm_pair(M) ? 2 : 1, rows = kMmRows * g;
+  const int64_t tiles = ((M + rows - 1) / rows) * ((N + kMmCols - 1) / kMmCols), blocks = ceil_blocks(K), at_once = kMmSms / g;
   int best = 1;
   double least = 0;
   for (int s = 1; s <= 64 && (s == 1 || blocks / s >= 4); ++s) {
-    double t = (double)((tiles * s + kMmSms - 1) / kMmSms) * ((double)((blocks + s - 1) / s) + 6);
+    double t = (double)((tiles * s + at_once - 1) / at_once) * ((double)((blocks + s - 1) / s) + 6);
     if (s > 1) t += 8 + (double)M * N * s * 8 / 1.5e6;
     if (s == 1 || t < least * 0.95) {
       best = s;
@@ -110,20 +114,29 @@ struct MatmulMaps {
   CUtensorMap a, b, o, sa, sb;
 };
 
-template <typename TO, bool TILE>
-static vsamp_status launch_matmul(const BlockMatmulParams& p, const MatmulMaps& m, const DeviceInfo& d, int dev,
-                                  cudaStream_t s) {
-  auto kern = block_matmul_kernel<TO, TILE>;
+template <typename TO, bool TILE, int G>
+static vsamp_status launch_matmul_g(const BlockMatmulParams& p, const MatmulMaps& m, const DeviceInfo& d, int dev,
+                                    cudaStream_t s) {
+  auto kern = block_matmul_kernel<TO, TILE, G>;
+  constexpr int smem = MmShape<G>::Smem;
   static std::atomic<bool> raised[64];
   if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmem) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
       cudaGetLastError();
       return VSAMP_ERR_CUDA;
     }
     if (dev < 64) raised[dev].store(true, std::memory_order_release);
   }
-  const vsamp_status st = launch_1d(kern, grid_of(p.items < d.sm_count ? p.items : d.sm_count), kMmThreads, kMmSmem, s, p,
-                                    m.a, m.b, m.o, m.sa, m.sb);
+  const int64_t most = d.sm_count / G;
+  const unsigned grid = (unsigned)(p.items < most ? p.items : most) * G;
+  if (G == 1) return launch_1d(kern, grid, kMmThreads, smem, s, p, m.a, m.b, m.o, m.sa, m.sb);
+  return launch_clusters(kern, grid, G, kMmThreads, smem, s, p, m.a, m.b, m.o, m.sa, m.sb);
+}
+
+template <typename TO, bool TILE>
+static vsamp_status launch_matmul(const BlockMatmulParams& p, const MatmulMaps& m, bool pair, const DeviceInfo& d, int dev,
+                                  cudaStream_t s) {
+  const vsamp_status st = pair ? launch_matmul_g<TO, TILE, 2>(p, m, d, dev, s) : launch_matmul_g<TO, TILE, 1>(p, m, d, dev, s);
   if (st != VSAMP_OK || p.parts == 1) return st;
   const int64_t ctas = ((int64_t)p.M * (p.ldp / 4) + 255) / 256, most = (int64_t)d.sm_count * 8;
   return launch_1d(block_matmul_join_kernel<TO>, grid_of(ctas < most ? ctas : most), 256, 0, s, p);
@@ -191,7 +204,9 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   DeviceInfo d;
   const vsamp_status st = device_info(dev, d);
   if (st != VSAMP_OK) return st;
-  if (d.optin < kMmSmem) return VSAMP_ERR_UNSUPPORTED;
+  if (d.optin < MmShape<1>::Smem || d.optin < MmShape<2>::Smem) return VSAMP_ERR_UNSUPPORTED;
+  const bool pair = mm_pair(M);
+  const int64_t tile_rows = pair ? 2 * kMmRows : kMmRows;
   BlockMatmulParams p{};
   p.sb = sb;
   p.ldsb = ldsb;
@@ -200,7 +215,7 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   p.ldo = ldo;
   p.out = static_cast<unsigned char*>(out);
   p.blocks = (int)ceil_blocks(K);
-  p.row_tiles = (int)((M + kMmRows - 1) / kMmRows);
+  p.row_tiles = (int)((M + tile_rows - 1) / tile_rows);
   p.parts = mm_parts(M, N, K);
   p.items = (int)(p.row_tiles * ((N + kMmCols - 1) / kMmCols) * p.parts);
   p.part = static_cast<float*>(workspace);
@@ -215,15 +230,15 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   p.drop_loads = env_int("VSAMP_TEST_DROP_LOADS", 0) != 0 ? 1 : 0;
   const bool tile = b_kind == VSAMP_BLOCK_TILE;
   MatmulMaps m{};
-  if (!codes_map(m.a, a, lda, M, K, p.a_rows) || !codes_map(m.b, b, ldb, N, K, kMmCols) ||
+  if (!codes_map(m.a, a, lda, M, K, p.a_rows) || !codes_map(m.b, b, ldb, N, K, pair ? kMmCols / 2 : kMmCols) ||
       !scales_map(m.sa, sa, ldsa, M, K, kMmRows) || (!tile && !scales_map(m.sb, sb, ldsb, N, K, kMmCols)))
     return VSAMP_ERR_CUDA;
   if (p.parts > 1 ? !results_map(m.o, p.part, true, p.ldp, M, N, p.parts)
                   : p.boxes && !results_map(m.o, out, es == 4, ldo, M, N, 1))
     return VSAMP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (out_dt == VSAMP_F32) return tile ? launch_matmul<float, true>(p, m, d, dev, s) : launch_matmul<float, false>(p, m, d, dev, s);
-  return tile ? launch_matmul<__nv_bfloat16, true>(p, m, d, dev, s) : launch_matmul<__nv_bfloat16, false>(p, m, d, dev, s);
+  if (out_dt == VSAMP_F32) return tile ? launch_matmul<float, true>(p, m, pair, d, dev, s) : launch_matmul<float, false>(p, m, pair, d, dev, s);
+  return tile ? launch_matmul<__nv_bfloat16, true>(p, m, pair, d, dev, s) : launch_matmul<__nv_bfloat16, false>(p, m, pair, d, dev, s);
 }
 
 }  // extern "C"

@@ -2,12 +2,18 @@
 //
 //   out[m, n] = sum over blocks j of sa[m, j] * sb[n, j] * sum over k in j of a[m, k] * b[n, k]
 //
-// One CTA per SM walks over tiles of 128 x 256 results. A warp copies blocks of both operands into a ring in shared memory
-// (tensor copies with the 128-byte swizzle the tensor cores read), another issues four products of 32 inner elements per
-// block into one of two accumulators in tensor memory, and sixteen warps take each finished block out of tensor memory and
-// add it, scaled, to fp32 sums in registers: the sum of a block's 128 products is the only one that the tensor core
-// forms. A row of a is a lane, so its scale is one register; a 128 x 128 block's scale of b is the same for a warp's 64
-// columns, and with one scale per row of b the column scales are read from shared memory as broadcasts.
+// One CTA per SM walks over tiles of 128 x 256 results, or a pair of CTAs over tiles of 256 x 256. A warp copies blocks of
+// both operands into a ring in shared memory (tensor copies with the 128-byte swizzle the tensor cores read), another issues
+// four products of 32 inner elements per block into one of two accumulators in tensor memory, and sixteen warps take each
+// finished block out of tensor memory and add it, scaled, to fp32 sums in registers: the sum of a block's 128 products is
+// the only one that the tensor core forms. A row of a is a lane, so its scale is one register; a 128 x 128 block's scale of
+// b is the same for a warp's 64 columns, and with one scale per row of b the column scales are read from shared memory as
+// broadcasts.
+//
+// What bounds it with many rows: a CTA alone writes 48 KB per block into shared memory and its tensor core reads them again,
+// 750 cycles at 128 bytes per cycle for products of 512; in a pair each CTA holds half of b, 64 KB both ways. A product
+// waits for its accumulator to have been read, two blocks back: the chain of completion (about 240 cycles), reading and
+// release (190) of both accumulators is what is left.
 //
 // Every wait is bounded. A CTA one of whose waits gave up lets its copies and products end, frees its tensor memory and
 // leaves NaN in the results that it had not finished.
@@ -18,20 +24,26 @@
 
 namespace vsamp {
 
-constexpr int kMmRows = 128, kMmCols = 256, kMmStages = 3;
+constexpr int kMmRows = 128, kMmCols = 256;         // results of a CTA by itself; of a CTA of a pair as many
 constexpr int kMmWarps = 16;                        // warps of sums: 32 rows x 64 columns each
 constexpr int kMmThreads = kMmWarps * 32 + 128;     // and a warpgroup with the copying and the issuing warp
 constexpr int kMmSumRegs = 112, kMmOtherRegs = 32;  // registers per thread: 512 x 112 + 128 x 32 of the launch's 640 x 96
-constexpr int kMmABytes = kMmRows * kBlock, kMmBBytes = kMmCols * kBlock, kMmStageBytes = kMmABytes + kMmBBytes;
 constexpr int kMmColumns = 512;                     // of tensor memory: two accumulators
-constexpr int kMmOutOff = kMmStages * kMmStageBytes;            // per warp 32 rows of 128 bytes of results
 // A block's scales, 128 of rows and 256 of columns, have a ring of their own: they are read after the block's products are
-// done, when its stage may be written again. Block n is copied once the products of block n - kMmStages are done, whose
-// accumulator had held block n - kMmStages - 2: every warp has read that one's scales, so six sets would do.
+// done, when its stage may be written again. Block n is copied once the products of block n - stages are done, whose
+// accumulator had held block n - stages - 2: every warp has read the scales of the block before that one, so eight sets do
+// for up to five stages.
 constexpr int kMmScaleSets = 8, kMmScaleBytes = (kMmRows + kMmCols) * 4;
-constexpr int kMmScaleOff = kMmOutOff + kMmWarps * 4096;
-constexpr int kMmBarOff = kMmScaleOff + kMmScaleSets * kMmScaleBytes;
-constexpr int kMmSmem = kMmBarOff + 256 + 1024;                 // and what aligns the ring to 1024 bytes
+
+template <int G>
+struct MmShape {
+  static constexpr int ABytes = kMmRows * kBlock, BRows = kMmCols / G, BBytes = BRows * kBlock;
+  static constexpr int StageBytes = ABytes + BBytes, Stages = G == 1 ? 3 : 4;
+  static constexpr int OutOff = Stages * StageBytes;            // per warp 32 rows of 128 bytes of results
+  static constexpr int ScaleOff = OutOff + kMmWarps * 4096;
+  static constexpr int BarOff = ScaleOff + kMmScaleSets * kMmScaleBytes;
+  static constexpr int Smem = BarOff + 256 + 1024;              // and what aligns the ring to 1024 bytes
+};
 
 struct BlockMatmulParams {
   const float* sb;           // of 128 x 128 blocks: the others come by their tensor map
@@ -52,10 +64,11 @@ struct BlockMatmulParams {
 struct MmItem {
   int m0, n0, j0, j1;
 };
+template <int G>
 __device__ __forceinline__ MmItem mm_item(const BlockMatmulParams& p, int item) {
   const int tile = item / p.parts, part = item - tile * p.parts, nt = tile / p.row_tiles;
   MmItem w;
-  w.m0 = (tile - nt * p.row_tiles) * kMmRows;
+  w.m0 = (tile - nt * p.row_tiles) * (kMmRows * G);
   w.n0 = nt * kMmCols;
   w.j0 = p.blocks * part / p.parts;
   w.j1 = p.blocks * (part + 1) / p.parts;
@@ -131,36 +144,40 @@ __device__ __forceinline__ void mm_store_rows(const float2 (&acc)[32], unsigned 
   }
 }
 
-template <typename TO, bool TILE>
+template <typename TO, bool TILE, int G>
 __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const BlockMatmulParams p,
                                                                      const __grid_constant__ CUtensorMap a_map,
                                                                      const __grid_constant__ CUtensorMap b_map,
                                                                      const __grid_constant__ CUtensorMap o_map,
                                                                      const __grid_constant__ CUtensorMap sa_map,
                                                                      const __grid_constant__ CUtensorMap sb_map) {
+  using S = MmShape<G>;
+  constexpr bool kPair = G == 2;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u);
   const uint32_t ring = smem_addr(smem);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kMmBarOff);   // a stage's copies have landed
-  uint64_t* done = full + kMmStages;                                // a stage's products are done: an accumulator holds them
-  uint64_t* taken = done + kMmStages;                               // an accumulator has been read
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::BarOff);   // a stage's copies have landed (rank 0's)
+  uint64_t* done = full + S::Stages;                                // a stage's products are done: an accumulator holds them
+  uint64_t* taken = done + S::Stages;                               // an accumulator has been read (rank 0's)
   uint64_t* drain = taken + 2;
   uint64_t* scaled = drain + 1;                                     // a set of scales has landed
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(scaled + kMmScaleSets);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t rank = kPair ? blockIdx.x & 1 : 0;
+  const int first = blockIdx.x / G, stride = gridDim.x / G;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMmStages; ++i) {
+    for (int i = 0; i < S::Stages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&done[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&taken[i], kMmWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&taken[i], kMmWarps * G);
     for (int i = 0; i < kMmScaleSets; ++i) mbar_init(&scaled[i], 1);
     mbar_init(drain, 1);
     *dead = 0;
     fence_mbar_init();
   }
-  if (warp == kMmWarps + 1) tmem_alloc(smem_addr(tmem_at), kMmColumns);
+  if (warp == kMmWarps + 1) tmem_alloc<G>(smem_addr(tmem_at), kMmColumns);
   if (threadIdx.x == kMmWarps * 32) {
     tma_prefetch_map(&a_map);
     tma_prefetch_map(&b_map);
@@ -170,6 +187,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
   }
   tcgen05_fence_before();
   __syncthreads();
+  if (kPair) cluster_barrier_shared();   // the barriers and tensor memory of both CTAs are ready
   tcgen05_fence_after();
   const uint32_t tmem = *tmem_at;
   begin_overlapped();
@@ -180,33 +198,41 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
     fewer_registers<kMmOtherRegs>();
     uint32_t s = 0, turn = 0;   // stage of block n, and the parity of its phase
     if (warp == kMmWarps && lane == 0) {
-      const uint32_t bytes = (uint32_t)(p.a_rows * kBlock + kMmBBytes);
-      for (int item = blockIdx.x; alive && item < p.items; item += gridDim.x) {
-        const MmItem w = mm_item(p, item);
+      const uint32_t bytes = (uint32_t)(p.a_rows * kBlock + S::BBytes) * G;
+      for (int item = first; alive && item < p.items; item += stride) {
+        const MmItem w = mm_item<G>(p, item);
         for (int j = w.j0; j < w.j1; ++j, ++n) {
           if (!wait_alive(&done[s], turn ^ 1, dead, p.wait_cycles)) {
             alive = false;
             break;
           }
-          const uint32_t set = n % kMmScaleSets, to = ring + kMmScaleOff + set * kMmScaleBytes;
-          mbar_arrive_expect_tx(&full[s], bytes);
+          const uint32_t set = n % kMmScaleSets, scales = ring + S::ScaleOff + set * kMmScaleBytes;
+          const uint32_t at = ring + s * S::StageBytes;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           mbar_arrive_expect_tx(&scaled[set], TILE ? kMmRows * 4 : kMmScaleBytes);
           if (!p.drop_loads) {
-            tma_load_2d(to, &sa_map, w.m0, j, smem_addr(&scaled[set]));
-            if (!TILE) tma_load_2d(to + kMmRows * 4, &sb_map, w.n0, j, smem_addr(&scaled[set]));
-            tma_load_2d(ring + s * kMmStageBytes, &a_map, j * kBlock, w.m0, smem_addr(&full[s]));
-            tma_load_2d(ring + s * kMmStageBytes + kMmABytes, &b_map, j * kBlock, w.n0, smem_addr(&full[s]));
+            const int row0 = w.m0 + (int)rank * kMmRows, col0 = w.n0 + (int)rank * S::BRows;
+            if (kPair) {
+              const uint32_t bar = dsmem_map(&full[s], 0);
+              tma_load_2d_pair(at, &a_map, j * kBlock, row0, bar);
+              tma_load_2d_pair(at + S::ABytes, &b_map, j * kBlock, col0, bar);
+            } else {
+              tma_load_2d(at, &a_map, j * kBlock, row0, smem_addr(&full[s]));
+              tma_load_2d(at + S::ABytes, &b_map, j * kBlock, col0, smem_addr(&full[s]));
+            }
+            tma_load_2d(scales, &sa_map, row0, j, smem_addr(&scaled[set]));
+            if (!TILE) tma_load_2d(scales + kMmRows * 4, &sb_map, w.n0, j, smem_addr(&scaled[set]));
           }
-          if (++s == kMmStages) {
+          if (++s == S::Stages) {
             s = 0;
             turn ^= 1;
           }
         }
       }
-    } else if (warp == kMmWarps + 1 && lane == 0) {
-      constexpr uint32_t idesc = umma_e4m3(kMmRows, kMmCols);
-      for (int item = blockIdx.x; alive && item < p.items; item += gridDim.x) {
-        const MmItem w = mm_item(p, item);
+    } else if (warp == kMmWarps + 1 && lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = umma_e4m3(kMmRows * G, kMmCols);
+      for (int item = first; alive && item < p.items; item += stride) {
+        const MmItem w = mm_item<G>(p, item);
         for (int j = w.j0; j < w.j1; ++j, ++n) {
           const uint32_t b = n & 1;
           if (!wait_alive(&taken[b], ((n >> 1) & 1) ^ 1, dead, p.wait_cycles) ||
@@ -215,11 +241,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
             break;
           }
           tcgen05_fence_after();
-          const uint64_t da = umma_operand(ring + s * kMmStageBytes), db = umma_operand(ring + s * kMmStageBytes + kMmABytes);
+          const uint32_t at = ring + s * S::StageBytes;
+          const uint64_t da = umma_operand(at), db = umma_operand(at + S::ABytes);
 #pragma unroll
-          for (int k = 0; k < kBlock / 32; ++k) umma_f8(tmem + b * kMmCols, da + 2 * k, db + 2 * k, idesc, k > 0);
-          umma_commit(smem_addr(&done[s]));
-          if (++s == kMmStages) {
+          for (int k = 0; k < kBlock / 32; ++k) umma_f8<G>(tmem + b * kMmCols, da + 2 * k, db + 2 * k, idesc, k > 0);
+          umma_commit<G>(smem_addr(&done[s]));
+          if (++s == S::Stages) {
             s = 0;
             turn ^= 1;
           }
@@ -230,38 +257,32 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
     more_registers<kMmSumRegs>();
     const int quarter = warp >> 2;                     // columns 64 quarter .. of the tile
     const uint32_t lanes = (uint32_t)(warp & 3) * 32;  // of tensor memory: rows of the tile
-    unsigned char* box = smem + kMmOutOff + warp * 4096;
-    float* cols = reinterpret_cast<float*>(smem + kMmScaleOff) + warp * 128;
+    unsigned char* box = smem + S::OutOff + warp * 4096;
+    auto release = [&](uint32_t b) {   // one lane
+      if (kPair) mbar_arrive_pair(dsmem_map(&taken[b], 0));
+      else mbar_arrive(smem_addr(&taken[b]));
+    };
     const uint32_t from = tmem + (lanes << 16) + quarter * 64;
     uint32_t s = 0, turn = 0;
-    for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
-      const MmItem w = mm_item(p, item);
-      const int row0 = w.m0 + (int)lanes, col0 = w.n0 + quarter * 64;
+    for (int item = first; item < p.items; item += stride) {
+      const MmItem w = mm_item<G>(p, item);
+      const int row0 = w.m0 + (int)(rank * kMmRows + lanes), col0 = w.n0 + quarter * 64;
       const bool active = row0 < p.M && col0 < p.N;    // otherwise the warp has no results here
       float2 acc[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      // A row's scale is the lane's. The scale of 128 x 128 blocks is one for the warp: a lane holds that of every 32nd
-      // block, fetched 32 blocks ahead; the columns' scales are read from shared memory.
-      const float* sb = p.sb + (TILE ? col0 / kBlock * p.ldsb : 0);
-      auto tile_scales = [&](int j) { return TILE && active && j + lane < w.j1 ? sb[j + lane] : 0.0f; };
-      float now = tile_scales(w.j0), next = tile_scales(w.j0 + 32);
+      // a row's scale is the lane's, that of 128 x 128 blocks one for the warp (32 blocks' lie in a line); the columns'
+      // scales are read from shared memory
+      const float* sb = p.sb + (TILE && active ? col0 / kBlock * p.ldsb : 0);
       for (int j = w.j0; alive && j < w.j1; ++j, ++n) {
         const uint32_t b = n & 1, set = n % kMmScaleSets;
-        const float* scales = reinterpret_cast<const float*>(smem + kMmScaleOff + set * kMmScaleBytes);
+        const float* scales = reinterpret_cast<const float*>(smem + S::ScaleOff + set * kMmScaleBytes);
         const float* cb = scales + kMmRows + quarter * 64;
+        const float tile = TILE ? __ldg(sb + j) : 1.0f;
         bool ok = wait_alive(&scaled[set], (n / kMmScaleSets) & 1, dead, p.wait_cycles);
-        float rs = ok ? scales[lanes + lane] : 0.0f;
-        if (TILE) {
-          const int k = (j - w.j0) & 31;
-          if (k == 0 && j > w.j0) {
-            now = next;
-            next = tile_scales(j + 32);
-          }
-          rs *= __shfl_sync(kFullMask, now, k);
-        }
+        const float rs = ok ? scales[lanes + lane] * tile : 0.0f;
         ok = ok && wait_alive(&done[s], turn, dead, p.wait_cycles);
-        if (++s == kMmStages) {
+        if (++s == S::Stages) {
           s = 0;
           turn ^= 1;
         }
@@ -283,7 +304,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
           tmem_wait(t);
           tcgen05_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&taken[b]));
+          if (lane == 0) release(b);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 v = make_float2(t[2 * i], t[2 * i + 1]);
@@ -291,7 +312,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
                                : __ffma2_rn(__fmul2_rn(v, s2), *reinterpret_cast<const float2*>(cb + 32 + 2 * i), acc[16 + i]);
           }
         } else if (lane == 0) {
-          mbar_arrive(smem_addr(&taken[b]));
+          release(b);
         }
       }
       if (!alive) {
@@ -317,22 +338,24 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
   __syncthreads();
   if (*dead) {
     // copies and products under way end before shared and tensor memory are given up
-    if (threadIdx.x == kMmWarps * 32 && !p.drop_loads)
-      for (uint32_t k = n < kMmStages ? 0 : n - kMmStages; k < n; ++k)
-        (void)mbar_wait_bounded(&full[k % kMmStages], (k / kMmStages) & 1, 4000000000LL);
-    if (threadIdx.x == kMmWarps * 32 && !p.drop_loads)
+    if (threadIdx.x == kMmWarps * 32 && !p.drop_loads) {
+      for (uint32_t k = n < S::Stages ? 0 : n - S::Stages; rank == 0 && k < n; ++k)
+        (void)mbar_wait_bounded(&full[k % S::Stages], (k / S::Stages) & 1, 4000000000LL);
       for (uint32_t k = n < kMmScaleSets ? 0 : n - kMmScaleSets; k < n; ++k)
         (void)mbar_wait_bounded(&scaled[k % kMmScaleSets], (k / kMmScaleSets) & 1, 4000000000LL);
-    if (threadIdx.x == kMmWarps * 32 + 32) {
-      umma_commit(smem_addr(drain));
+    }
+    if (threadIdx.x == kMmWarps * 32 + 32 && rank == 0) {
+      umma_commit<G>(smem_addr(drain));
       (void)mbar_wait_bounded(drain, 0, 4000000000LL);
     }
     __syncthreads();
   }
+  // the other CTA's arrivals and products have ended before this one's shared and tensor memory go
+  if (kPair) cluster_barrier_shared();
   if (warp == kMmWarps + 1) {
     __syncwarp();
     tcgen05_fence_after();
-    tmem_free(tmem, kMmColumns);
+    tmem_free<G>(tmem, kMmColumns);
   }
 }
 
