@@ -144,6 +144,23 @@ __device__ __forceinline__ void mm_store_rows(const float2 (&acc)[32], unsigned 
   }
 }
 
+// W columns of a block, scaled, to the sums.
+template <bool TILE, int W>
+__device__ __forceinline__ void mm_sums(const float (&t)[W], float2 rs, const float* cb, float2 (&acc)[32], int at) {
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i) {
+    const float2 u = make_float2(t[4 * i], t[4 * i + 1]), v = make_float2(t[4 * i + 2], t[4 * i + 3]);
+    if (TILE) {
+      acc[at + 2 * i] = __ffma2_rn(u, rs, acc[at + 2 * i]);
+      acc[at + 2 * i + 1] = __ffma2_rn(v, rs, acc[at + 2 * i + 1]);
+    } else {
+      const float4 c = *reinterpret_cast<const float4*>(cb + 4 * i);
+      acc[at + 2 * i] = __ffma2_rn(__fmul2_rn(u, rs), make_float2(c.x, c.y), acc[at + 2 * i]);
+      acc[at + 2 * i + 1] = __ffma2_rn(__fmul2_rn(v, rs), make_float2(c.z, c.w), acc[at + 2 * i + 1]);
+    }
+  }
+}
+
 template <typename TO, bool TILE, int G>
 __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const BlockMatmulParams p,
                                                                      const __grid_constant__ CUtensorMap a_map,
@@ -197,55 +214,57 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
   if (warp >= kMmWarps) {
     fewer_registers<kMmOtherRegs>();
     uint32_t s = 0, turn = 0;   // stage of block n, and the parity of its phase
-    if (warp == kMmWarps && lane == 0) {
+    if (warp == kMmWarps) {
       const uint32_t bytes = (uint32_t)(p.a_rows * kBlock + S::BBytes) * G;
       for (int item = first; alive && item < p.items; item += stride) {
         const MmItem w = mm_item<G>(p, item);
+        const int row0 = w.m0 + (int)rank * kMmRows, col0 = w.n0 + (int)rank * S::BRows;
         for (int j = w.j0; j < w.j1; ++j, ++n) {
-          if (!wait_alive(&done[s], turn ^ 1, dead, p.wait_cycles)) {
-            alive = false;
-            break;
-          }
-          const uint32_t set = n % kMmScaleSets, scales = ring + S::ScaleOff + set * kMmScaleBytes;
-          const uint32_t at = ring + s * S::StageBytes;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-          mbar_arrive_expect_tx(&scaled[set], TILE ? kMmRows * 4 : kMmScaleBytes);
-          if (!p.drop_loads) {
-            const int row0 = w.m0 + (int)rank * kMmRows, col0 = w.n0 + (int)rank * S::BRows;
-            if (kPair) {
-              const uint32_t bar = dsmem_map(&full[s], 0);
-              tma_load_2d_pair(at, &a_map, j * kBlock, row0, bar);
-              tma_load_2d_pair(at + S::ABytes, &b_map, j * kBlock, col0, bar);
-            } else {
-              tma_load_2d(at, &a_map, j * kBlock, row0, smem_addr(&full[s]));
-              tma_load_2d(at + S::ABytes, &b_map, j * kBlock, col0, smem_addr(&full[s]));
+          alive = __all_sync(kFullMask, wait_alive(&done[s], turn ^ 1, dead, p.wait_cycles));
+          if (!alive) break;
+          if (elect_one()) {
+            const uint32_t set = n % kMmScaleSets, scales = ring + S::ScaleOff + set * kMmScaleBytes;
+            const uint32_t at = ring + s * S::StageBytes;
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+            mbar_arrive_expect_tx(&scaled[set], TILE ? kMmRows * 4 : kMmScaleBytes);
+            if (!p.drop_loads) {
+              if (kPair) {
+                const uint32_t bar = dsmem_map(&full[s], 0);
+                tma_load_2d_pair(at, &a_map, j * kBlock, row0, bar);
+                tma_load_2d_pair(at + S::ABytes, &b_map, j * kBlock, col0, bar);
+              } else {
+                tma_load_2d(at, &a_map, j * kBlock, row0, smem_addr(&full[s]));
+                tma_load_2d(at + S::ABytes, &b_map, j * kBlock, col0, smem_addr(&full[s]));
+              }
+              tma_load_2d(scales, &sa_map, row0, j, smem_addr(&scaled[set]));
+              if (!TILE) tma_load_2d(scales + kMmRows * 4, &sb_map, w.n0, j, smem_addr(&scaled[set]));
             }
-            tma_load_2d(scales, &sa_map, row0, j, smem_addr(&scaled[set]));
-            if (!TILE) tma_load_2d(scales + kMmRows * 4, &sb_map, w.n0, j, smem_addr(&scaled[set]));
           }
+          __syncwarp();
           if (++s == S::Stages) {
             s = 0;
             turn ^= 1;
           }
         }
       }
-    } else if (warp == kMmWarps + 1 && lane == 0 && rank == 0) {
+    } else if (warp == kMmWarps + 1 && rank == 0) {
       constexpr uint32_t idesc = umma_e4m3(kMmRows * G, kMmCols);
       for (int item = first; alive && item < p.items; item += stride) {
         const MmItem w = mm_item<G>(p, item);
         for (int j = w.j0; j < w.j1; ++j, ++n) {
           const uint32_t b = n & 1;
-          if (!wait_alive(&taken[b], ((n >> 1) & 1) ^ 1, dead, p.wait_cycles) ||
-              !wait_alive(&full[s], turn, dead, p.wait_cycles)) {
-            alive = false;
-            break;
-          }
+          alive = __all_sync(kFullMask, wait_alive(&full[s], turn, dead, p.wait_cycles) &&
+                                            wait_alive(&taken[b], ((n >> 1) & 1) ^ 1, dead, p.wait_cycles));
+          if (!alive) break;
           tcgen05_fence_after();
-          const uint32_t at = ring + s * S::StageBytes;
-          const uint64_t da = umma_operand(at), db = umma_operand(at + S::ABytes);
+          if (elect_one()) {
+            const uint32_t at = ring + s * S::StageBytes;
+            const uint64_t da = umma_operand(at), db = umma_operand(at + S::ABytes);
 #pragma unroll
-          for (int k = 0; k < kBlock / 32; ++k) umma_f8<G>(tmem + b * kMmCols, da + 2 * k, db + 2 * k, idesc, k > 0);
-          umma_commit<G>(smem_addr(&done[s]));
+            for (int k = 0; k < kBlock / 32; ++k) umma_f8<G>(tmem + b * kMmCols, da + 2 * k, db + 2 * k, idesc, k > 0);
+            umma_commit<G>(smem_addr(&done[s]));
+          }
+          __syncwarp();
           if (++s == S::Stages) {
             s = 0;
             turn ^= 1;
@@ -289,27 +308,19 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         alive = __all_sync(kFullMask, ok);
         if (!alive) break;
         tcgen05_fence_after();
-        const float2 s2 = make_float2(rs, rs);
         if (active) {
-          float t[32];
-          tmem_load32(from + b * kMmCols, t);
-          tmem_wait(t);
+          constexpr int W = TILE ? 32 : 16;   // columns at a time: with column scales the registers do not hold more
+          const float2 r2 = make_float2(rs, rs);
+          float t[W];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 v = make_float2(t[2 * i], t[2 * i + 1]);
-            acc[i] = TILE ? __ffma2_rn(v, s2, acc[i])
-                          : __ffma2_rn(__fmul2_rn(v, s2), *reinterpret_cast<const float2*>(cb + 2 * i), acc[i]);
-          }
-          tmem_load32(from + b * kMmCols + 32, t);
-          tmem_wait(t);
-          tcgen05_fence_before();
-          __syncwarp();
-          if (lane == 0) release(b);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 v = make_float2(t[2 * i], t[2 * i + 1]);
-            acc[16 + i] = TILE ? __ffma2_rn(v, s2, acc[16 + i])
-                               : __ffma2_rn(__fmul2_rn(v, s2), *reinterpret_cast<const float2*>(cb + 32 + 2 * i), acc[16 + i]);
+          for (int c = 0; c < 64 / W; ++c) {
+            tmem_read(from + b * kMmCols + c * W, t);
+            if (c + 1 == 64 / W) {   // all of the warp's part has been read
+              tcgen05_fence_before();
+              __syncwarp();
+              if (lane == 0) release(b);
+            }
+            mm_sums<TILE, W>(t, r2, cb + c * W, acc, c * W / 2);
           }
         } else if (lane == 0) {
           release(b);
