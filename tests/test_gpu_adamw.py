@@ -306,3 +306,18 @@ def test_binding_refuses(ts, dev):
         ts.vsamp_adamw(state, [g], lr=torch.ones(1, device=dev, dtype=torch.float64), step=1)
     with pytest.raises(ValueError):
         ts.vsamp_adamw(state, [g.cpu()], lr=1e-3, step=1)
+
+
+def test_nothing_is_launched_before_all_is_checked(ts, dev):
+    """A bad gradient of one group of tensors leaves the others as they are; a parameter that got other memory is seen."""
+    a, b = torch.ones(100, device=dev), torch.ones(100, device=dev).bfloat16()
+    state = ts.vsamp_adamw_state([a, b])
+    with pytest.raises(ValueError):
+        ts.vsamp_adamw(state, [torch.ones(100, device=dev), torch.ones(99, device=dev)], lr=1e-1, step=1)
+    assert (a == 1).all() and not state.m[0].any()
+    ts.vsamp_adamw(state, [torch.ones(100, device=dev), None], lr=1e-1, step=1)
+    assert (a < 1).all() and (b == 1).all()
+    a.data = torch.ones(100, device=dev)
+    with pytest.raises(ValueError):
+        ts.vsamp_adamw(state, [torch.ones(100, device=dev), None], lr=1e-1, step=2)
+    assert (a == 1).all()

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from array import array
 from typing import Optional
 
 import torch
@@ -1025,9 +1026,11 @@ _ADAMW_WORDS, _ADAMW_GRAD, _ADAMW_N = 9, 2, 7
 
 
 class AdamWState:
-    """The tensors that an AdamW step updates, checked once: parameters, masters and moments (vsamp_adamw_state)."""
+    """The tensors that an AdamW step updates, checked once: parameters, masters and moments (vsamp_adamw_state). Values
+    are loaded by copying into these tensors; others in their place are not seen."""
 
-    __slots__ = ("params", "masters", "m", "v", "m_scale", "v_scale", "bits", "device", "index", "sizes", "groups")
+    __slots__ = ("params", "masters", "m", "v", "m_scale", "v_scale", "bits", "device", "index", "sizes", "places", "groups",
+                 "held")
 
 
 def _adamw_list(given, n: int, name: str):
@@ -1101,6 +1104,9 @@ def vsamp_adamw_state(params, bits=32, masters=None, m=None, v=None, m_scale=Non
     spans.sort()
     if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
         raise ValueError("tensors that a step writes share memory")
+    s.places = [p.data_ptr() for p in s.params]
+    # the memory stays as long as the state, whatever becomes of the lists above
+    s.held = [t.detach() for t in s.params + s.masters + s.m + s.v + s.m_scale + s.v_scale if t is not None]
     s.groups = []
     for dt in (torch.float32, torch.bfloat16):
         for with_master in (False, True):
@@ -1111,13 +1117,41 @@ def vsamp_adamw_state(params, bits=32, masters=None, m=None, v=None, m_scale=Non
                 words = [[0 if t is None else t.data_ptr() for t in (s.params[i], s.masters[i], None, s.m[i], s.v[i],
                                                                      s.m_scale[i], s.v_scale[i])] + [s.sizes[i], i]
                          for i in at]
-                s.groups.append((_dtype_code(s.params[at[0]]), at, torch.tensor(words, dtype=torch.int64)))
+                s.groups.append((_dtype_code(s.params[at[0]]), at, array("q", [w for row in words for w in row])))
     return s
 
 
 def _device_scalar(v, dtype, index: int, name: str):
     """The address of a device scalar, None for a number of the host."""
     return _at(v, dtype, index, 1, name) if isinstance(v, torch.Tensor) else None
+
+
+_data_ptr, _numel, _is_contiguous, _get_device = (getattr(torch._C.TensorBase, f) for f in
+                                                  ("data_ptr", "numel", "is_contiguous", "get_device"))
+
+
+def _gradients(grads, sizes, index: int):
+    """Checks gradients; a list of (type, addresses, counts) with one entry per type: the counts are 0 for gradients that
+    are missing or of another type, None if there are none. The usual case, all there and of one type, goes without a
+    Python statement per tensor: a step over some hundred tensors is bound by them."""
+    f32, bf16 = torch.float32, torch.bfloat16
+    try:
+        kinds = {g.dtype for g in grads}
+        if (len(kinds) == 1 and kinds <= {f32, bf16} and list(map(_numel, grads)) == sizes and
+                set(map(_get_device, grads)) == {index} and all(map(_is_contiguous, grads))):
+            return [(kinds.pop(), list(map(_data_ptr, grads)), None)]
+    except (AttributeError, TypeError):   # one is None
+        pass
+    found = []
+    for g, n in zip(grads, sizes):
+        if g is None:
+            found.append((0, None))
+            continue
+        if g.numel() != n or (g.dtype is not f32 and g.dtype is not bf16):
+            raise ValueError(f"a gradient must be {n} elements of float32 or bfloat16, got {g.numel()} of {g.dtype}")
+        found.append((_at(g, g.dtype, index, 0, "grads"), g.dtype))
+    return [(kind, [p for p, _ in found], [n if k is kind else 0 for (_, k), n in zip(found, sizes)])
+            for kind in (f32, bf16) if any(k is kind for _, k in found)]
 
 
 def vsamp_adamw(state: AdamWState, grads, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=None,
@@ -1130,32 +1164,26 @@ def vsamp_adamw(state: AdamWState, grads, lr, step, beta1=0.9, beta2=0.999, eps=
     if where is not None:
         with where:
             return vsamp_adamw(state, grads, lr, step, beta1, beta2, eps, weight_decay, grad_scale, seed)
-    at = state.index
-    f32, bf16 = torch.float32, torch.bfloat16
+    at, f32 = state.index, torch.float32
     grads = _adamw_list(grads, len(state.params), "grads")
     on_device = [isinstance(t, torch.Tensor) for t in (lr, step)]
     rule = vsamp_adamw_rule(0.0 if on_device[0] else lr, beta1, beta2, eps, weight_decay, 1 if on_device[1] else step,
                             int(seed) & ((1 << 64) - 1), _device_scalar(lr, f32, at, "lr"),
                             _device_scalar(step, torch.int64, at, "step"), _at(grad_scale, f32, at, 1, "grad_scale"))
-    lib, on = load(), _current(at)
+    if list(map(_data_ptr, state.params)) != state.places:
+        raise ValueError("a parameter's memory is not the one that the state was made for")
+    calls = []   # everything is checked before anything is launched
     for dt, members, words in state.groups:
-        found = []
-        for i in members:
-            g = grads[i]
-            if g is None:
-                found.append((0, None))
-                continue
-            if g.numel() != state.sizes[i] or (g.dtype is not f32 and g.dtype is not bf16):
-                raise ValueError(f"gradient {i} must be {state.sizes[i]} elements of float32 or bfloat16, got {g.numel()} of "
-                                 f"{g.dtype}")
-            found.append((_at(g, g.dtype, at, 0, "grads"), g.dtype))
-        kinds = {k for _, k in found} - {None}
-        for kind in kinds:
-            table = words.clone()
-            table[:, _ADAMW_GRAD] = torch.tensor([p for p, _ in found], dtype=torch.int64)
-            if len(kinds) > 1 or any(k is None for _, k in found):
-                table[:, _ADAMW_N] *= torch.tensor([k is kind for _, k in found])
-            st = lib.vsamp_adamw(table.data_ptr(), len(members), dt, VSAMP_F32 if kind is f32 else VSAMP_BF16, state.bits,
-                                 ctypes.byref(rule), on)
-            if st:
-                _check(st, "vsamp_adamw")
+        mine = grads if len(members) == len(grads) else [grads[i] for i in members]
+        sizes = state.sizes if mine is grads else [state.sizes[i] for i in members]
+        for kind, ptrs, counts in _gradients(mine, sizes, at):
+            table = array("q", words)
+            table[_ADAMW_GRAD::_ADAMW_WORDS] = array("q", ptrs)
+            if counts is not None:
+                table[_ADAMW_N::_ADAMW_WORDS] = array("q", counts)
+            calls.append((table, len(members), dt, VSAMP_F32 if kind is f32 else VSAMP_BF16))
+    lib, on = load(), _current(at)
+    for table, n, dt, kind in calls:
+        st = lib.vsamp_adamw(table.buffer_info()[0], n, dt, kind, state.bits, ctypes.byref(rule), on)
+        if st:
+            _check(st, "vsamp_adamw")
