@@ -7,11 +7,13 @@
 
 namespace vsamp {
 
+static_assert(AdamShape<true>::PerSm == AdamShape<false>::PerSm, "one grid");
+
 static bool at_multiple(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 template <typename TP, typename TG>
 static vsamp_status launch_adamw(const AdamParams& p, bool master, bool bits8, const DeviceInfo& d, cudaStream_t s) {
-  const int64_t most = (int64_t)d.sm_count * kAdamPerSm;
+  const int64_t most = (int64_t)d.sm_count * AdamShape<true>::PerSm;
   const unsigned grid = (unsigned)(p.chunks < most ? p.chunks : most);
   if constexpr (sizeof(TP) == 2) {
     if (master)
@@ -86,7 +88,11 @@ extern "C" vsamp_status vsamp_adamw(const vsamp_adamw_tensor* tensors, int32_t c
   p.lr_dev = r.lr_dev;
   p.step_dev = r.step_dev;
   p.grad_scale = r.grad_scale;
-  constexpr int64_t chunk = (int64_t)kAdamChunk * kBlock;
+  // Long chunks keep the fetches ahead of the arithmetic; short ones spread few elements over the device.
+  int64_t total = 0;
+  for (int32_t k = 0; k < count; ++k) total += tensors[k].n;
+  p.chunk_blocks = total > (int64_t)d.sm_count * AdamShape<true>::PerSm * 4 * 128 * kBlock ? 128 : 32;
+  const int64_t chunk = (int64_t)p.chunk_blocks * kBlock;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int32_t k = 0;
   while (k < count) {

@@ -5,7 +5,8 @@
 //
 // A stream over memory: each element is read and written once. A warp takes 128 consecutive elements of a tensor, four
 // per lane, which is also a block of the 8-bit states: their new scale is one maximum over the warp's registers, and one
-// Philox call gives a lane's four elements their random bits. The tensors' addresses travel in the kernel's parameters
+// Philox call gives a lane's four elements their random bits. The next blocks are on their way while a warp computes, since
+// the 8-bit states' arithmetic (about 80 instructions per element) takes as long as their bytes. The tensors' addresses travel in the kernel's parameters
 // (up to 384 per launch), so a step needs no table in device memory and can be captured as it is.
 #pragma once
 
@@ -14,9 +15,14 @@
 namespace vsamp {
 
 constexpr int kAdamThreads = 256;
-constexpr int kAdamPerSm = 3;        // CTAs per SM
 constexpr int kAdamTensors = 384;    // of 80 bytes: 30,720 of a launch's 32,764 parameter bytes
-constexpr int kAdamChunk = 32;       // blocks of 128 elements that a CTA takes at a time
+// Blocks of 128 elements that a warp fetches at a time, and CTAs per SM. 67M parameters: 8-bit states (fp32 parameters, bf16
+// gradients) 4 blocks and 2 CTAs 211 us, 2 and 3 224, 2 and 2 244, 1 and 4 261; 32-bit ones move with none of it (2 and 2
+// 289 us, 4 and 2 303, their floor is 281).
+template <bool BITS8>
+struct AdamShape {
+  static constexpr int Unroll = BITS8 ? 4 : 2, PerSm = 2;
+};
 
 struct AdamTensor {
   unsigned char* param;
@@ -35,7 +41,7 @@ struct AdamTensor {
 
 struct AdamParams {
   AdamTensor t[kAdamTensors];
-  uint32_t count, chunks;
+  uint32_t count, chunks, chunk_blocks;   // a CTA takes a chunk of blocks of a tensor at a time
   float lr, b1, b2, one_b1, one_b2, eps, wd;
   float ln_b1, ln_b2, c1, c2;      // logarithms of the betas; 1 / (1 - b1^t), 1 / sqrt(1 - b2^t) of the host's step
   uint32_t step, k0[10], k1[10];   // Philox round keys
@@ -65,7 +71,7 @@ __device__ __forceinline__ uint4 adam_words(const AdamParams& p, uint32_t c0, ui
 __device__ __forceinline__ float e4m3_stochastic(float y, uint32_t u) {
   const float base = y < 0x1p-6f ? 0x1p-6f : 0.0f;
   const float q = __uint_as_float((__float_as_uint(y + base) + u) & 0xFFF00000u) - base;
-  return fminf(q, kE4m3Max);
+  return q;   // 480 for a block's largest at most, which the conversion takes for 448
 }
 
 // Two e4m3 codes (the lower 16 bits) as fp32.
@@ -77,11 +83,11 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
   return __half22float2(h);
 }
 
-// A root, a quotient and a reciprocal of about one unit's error each: their errors are far below what the step, lr times
-// the quotient, has of the parameter.
+// A root and a reciprocal of one or two units' error: far below what the step, lr times the quotient, has of the parameter.
+// Numbers below 2^-126 count as 0: a root below 2^-63 adds nothing to an eps above 2^-40.
 __device__ __forceinline__ float sqrt_near(float x) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float rcp_near(float x) {
@@ -99,13 +105,10 @@ __device__ __forceinline__ float moment_scale(uint32_t amax_bits, float& inv) {
 }
 
 template <typename T, bool FULL>
-__device__ __forceinline__ void adam_load(const unsigned char* base, int64_t i, int left, bool aligned, float (&f)[4]) {
-  ElemVec<T, 4> e;
+__device__ __forceinline__ void adam_load(ElemVec<T, 4>& e, const unsigned char* base, int64_t i, int left, bool aligned) {
   const unsigned char* p = base + i * (int64_t)sizeof(T);
   if (FULL) e.load(p, true);
   else e.load_row(p, left, aligned, 0u);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = e.at(j);
 }
 template <typename T, bool FULL>
 __device__ __forceinline__ void adam_store(unsigned char* base, int64_t i, int left, bool aligned, const float (&f)[4]) {
@@ -138,77 +141,100 @@ struct AdamNow {   // the step's numbers, whether they came from the host or the
   uint32_t step;
 };
 
-// Blocks b, b + kAdamThreads / 32, ... (U of them) of a tensor by one warp: all loads first. FULL: whole blocks on aligned
-// addresses.
-template <typename TP, typename TG, bool MASTER, bool BITS8, int U, bool FULL>
-__device__ __forceinline__ void adam_blocks(const AdamParams& p, const AdamTensor& t, const AdamNow& now, int64_t b0, int lane) {
-  constexpr bool kDrawParam = sizeof(TP) == 2 && !MASTER;   // a bf16 parameter without master is rounded at random
-  const bool aligned = t.aligned != 0;
-  float value[U][4], g[U][4], m[U][4], v[U][4], ms[U], vs[U];
+constexpr int kAdamWarps = kAdamThreads / 32;
+
+// A lane's four elements of blocks b, b + kAdamWarps, ... (U of them) as they were read.
+template <typename TP, typename TG, bool MASTER, bool BITS8, int U>
+struct AdamRaw {
+  ElemVec<float, 4> value[MASTER || sizeof(TP) == 4 ? U : 1];
+  ElemVec<__nv_bfloat16, 4> value16[MASTER || sizeof(TP) == 4 ? 1 : U];
+  ElemVec<TG, 4> g[U];
+  ElemVec<float, 4> m[BITS8 ? 1 : U], v[BITS8 ? 1 : U];
   uint32_t mw[U], vw[U];
-  int left[U];
+  float ms[U], vs[U];
+
+  template <bool FULL>
+  __device__ __forceinline__ void load(const AdamTensor& t, int64_t b0, int lane) {
+    const bool aligned = t.aligned != 0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t b = b0 + u * (kAdamThreads / 32), i = b * kBlock + lane * 4;
-    left[u] = FULL ? 4 : (int)(t.n - i < 4 ? (t.n - i > 0 ? t.n - i : 0) : 4);
-    if (MASTER) adam_load<float, FULL>(reinterpret_cast<const unsigned char*>(t.master), i, left[u], aligned, value[u]);
-    else adam_load<TP, FULL>(t.param, i, left[u], aligned, value[u]);
-    adam_load<TG, FULL>(t.grad, i, left[u], aligned, g[u]);
-    if (BITS8) {
-      mw[u] = codes_load<FULL>(t.m, i, left[u], aligned);
-      vw[u] = codes_load<FULL>(t.v, i, left[u], aligned);
-      ms[u] = t.m_scale[b];
-      vs[u] = t.v_scale[b];
-    } else {
-      adam_load<float, FULL>(t.m, i, left[u], aligned, m[u]);
-      adam_load<float, FULL>(t.v, i, left[u], aligned, v[u]);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t b = b0 + u * (kAdamThreads / 32), i = b * kBlock + lane * 4;
-    if (BITS8) {
-#pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        const float2 a = e4m3_values(mw[u] >> (8 * j)), r = e4m3_values(vw[u] >> (8 * j));
-        m[u][j] = a.x * ms[u];
-        m[u][j + 1] = a.y * ms[u];
-        v[u][j] = r.x * vs[u];
-        v[u][j + 1] = r.y * vs[u];
-        v[u][j] *= v[u][j];
-        v[u][j + 1] *= v[u][j + 1];
+    for (int u = 0; u < U; ++u) {
+      const int64_t b = b0 + u * kAdamWarps, i = b * kBlock + lane * 4;
+      const int left = FULL ? 4 : (int)(t.n - i < 4 ? (t.n - i > 0 ? t.n - i : 0) : 4);
+      if constexpr (MASTER)
+        adam_load<float, FULL>(value[u], reinterpret_cast<const unsigned char*>(t.master), i, left, aligned);
+      else if constexpr (sizeof(TP) == 4)
+        adam_load<float, FULL>(value[u], t.param, i, left, aligned);
+      else
+        adam_load<__nv_bfloat16, FULL>(value16[u], t.param, i, left, aligned);
+      adam_load<TG, FULL>(g[u], t.grad, i, left, aligned);
+      if constexpr (BITS8) {
+        mw[u] = codes_load<FULL>(t.m, i, left, aligned);
+        vw[u] = codes_load<FULL>(t.v, i, left, aligned);
+        ms[u] = t.m_scale[b];
+        vs[u] = t.v_scale[b];
+      } else {
+        adam_load<float, FULL>(m[u], t.m, i, left, aligned);
+        adam_load<float, FULL>(v[u], t.v, i, left, aligned);
       }
     }
-    float root[4];
+  }
+};
+
+// The step of those elements. FULL: whole blocks on aligned addresses.
+template <typename TP, typename TG, bool MASTER, bool BITS8, int U, bool FULL>
+__device__ __forceinline__ void adam_step(const AdamParams& p, const AdamTensor& t, const AdamNow& now,
+                                          const AdamRaw<TP, TG, MASTER, BITS8, U>& raw, int64_t b0, int lane) {
+  constexpr bool kDrawParam = sizeof(TP) == 2 && !MASTER;   // a bf16 parameter without master is rounded at random
+  const bool aligned = t.aligned != 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t b = b0 + u * kAdamWarps, i = b * kBlock + lane * 4;
+    const int left = FULL ? 4 : (int)(t.n - i < 4 ? (t.n - i > 0 ? t.n - i : 0) : 4);
+    float value[4], m[4], v[4], root[4];
+    if constexpr (BITS8) {
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        const float2 a = e4m3_values(raw.mw[u] >> (8 * j)), r = e4m3_values(raw.vw[u] >> (8 * j));
+        m[j] = a.x * raw.ms[u];
+        m[j + 1] = a.y * raw.ms[u];
+        v[j] = r.x * raw.vs[u];
+        v[j + 1] = r.y * raw.vs[u];
+        v[j] *= v[j];
+        v[j + 1] *= v[j + 1];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        m[j] = raw.m[u].at(j);
+        v[j] = raw.v[u].at(j);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float gj = g[u][j] * now.gs;
-      m[u][j] = fmaf(p.b1, m[u][j], p.one_b1 * gj);
-      v[u][j] = fmaf(p.b2, v[u][j], p.one_b2 * gj * gj);
-      root[j] = sqrt_near(v[u][j]);
-      const float change = __fdividef(m[u][j] * now.c1, fmaf(root[j], now.c2, p.eps));
-      value[u][j] = fmaf(-now.lr, fmaf(p.wd, value[u][j], change), value[u][j]);
+      if constexpr (MASTER || sizeof(TP) == 4) value[j] = raw.value[u].at(j);
+      else value[j] = raw.value16[u].at(j);
+      const float g = raw.g[u].at(j) * now.gs;
+      m[j] = fmaf(p.b1, m[j], p.one_b1 * g);
+      v[j] = fmaf(p.b2, v[j], p.one_b2 * g * g);
+      root[j] = sqrt_near(v[j]);
+      const float change = m[j] * now.c1 * rcp_near(fmaf(root[j], now.c2, p.eps));
+      value[j] = fmaf(-now.lr, fmaf(p.wd, value[j], change), value[j]);
     }
-    if (MASTER) adam_store<float, FULL>(reinterpret_cast<unsigned char*>(t.master), i, left[u], aligned, value[u]);
+    if (MASTER) adam_store<float, FULL>(reinterpret_cast<unsigned char*>(t.master), i, left, aligned, value);
     if (kDrawParam) {
       const uint4 w = adam_words(p, (uint32_t)(i >> 2), 0x80000000u, now.step, t.index);
       const uint32_t h[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if ((__float_as_uint(value[u][j]) & kInfBits) != kInfBits)
-          value[u][j] = __uint_as_float((__float_as_uint(value[u][j]) + (h[j] & 0xFFFFu)) & 0xFFFF0000u);
+        if ((__float_as_uint(value[j]) & kInfBits) != kInfBits)
+          value[j] = __uint_as_float((__float_as_uint(value[j]) + (h[j] & 0xFFFFu)) & 0xFFFF0000u);
     }
-    adam_store<TP, FULL>(t.param, i, left[u], aligned, value[u]);
-    if (BITS8) {
-      uint32_t ma = 0u, va = 0u;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (FULL || j < left[u]) {
-          ma = max(ma, __float_as_uint(m[u][j]) & 0x7FFFFFFFu);
-          va = max(va, __float_as_uint(root[j]) & 0x7FFFFFFFu);
-        }
-      ma = warp_max_u32(ma);
-      va = warp_max_u32(va);
+    adam_store<TP, FULL>(t.param, i, left, aligned, value);
+    if constexpr (BITS8) {
+      // what lies behind the tensor's end was read as zeros and is one still
+      const uint32_t ma = warp_max_u32(__float_as_uint(
+          max_nan(max_nan(fabsf(m[0]), fabsf(m[1])), max_nan(fabsf(m[2]), fabsf(m[3])))));
+      const uint32_t va = warp_max_u32(__float_as_uint(max_nan(max_nan(root[0], root[1]), max_nan(root[2], root[3]))));
       float mi, vi;
       const float m_new = moment_scale(ma, mi), v_new = moment_scale(va, vi);
       const uint4 w = adam_words(p, (uint32_t)(i >> 2), 0u, now.step, t.index);
@@ -216,28 +242,28 @@ __device__ __forceinline__ void adam_blocks(const AdamParams& p, const AdamTenso
       float y[4], r[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        y[j] = copysignf(e4m3_stochastic(fabsf(m[u][j]) * mi, ((h[j] >> 12) & 0xFFFF0u) | 8u), m[u][j]);
+        y[j] = copysignf(e4m3_stochastic(fabsf(m[j]) * mi, ((h[j] >> 12) & 0xFFFF0u) | 8u), m[j]);
         r[j] = e4m3_stochastic(root[j] * vi, ((h[j] << 4) & 0xFFFF0u) | 8u);
         if (root[j] > 0.0f) r[j] = fmaxf(r[j], 0x1p-9f);
       }
       uint32_t mc = e4m3_quad(y[0], y[1], y[2], y[3]), vc = e4m3_quad(r[0], r[1], r[2], r[3]);
       if (ma >= kInfBits) mc = 0u;
       if (va >= kInfBits) vc = 0u;
-      codes_store<FULL>(t.m, i, left[u], aligned, mc);
-      codes_store<FULL>(t.v, i, left[u], aligned, vc);
+      codes_store<FULL>(t.m, i, left, aligned, mc);
+      codes_store<FULL>(t.v, i, left, aligned, vc);
       if (lane == 0) {
         t.m_scale[b] = m_new;
         t.v_scale[b] = v_new;
       }
     } else {
-      adam_store<float, FULL>(t.m, i, left[u], aligned, m[u]);
-      adam_store<float, FULL>(t.v, i, left[u], aligned, v[u]);
+      adam_store<float, FULL>(t.m, i, left, aligned, m);
+      adam_store<float, FULL>(t.v, i, left, aligned, v);
     }
   }
 }
 
 template <typename TP, typename TG, bool MASTER, bool BITS8>
-__global__ void __launch_bounds__(kAdamThreads, kAdamPerSm) adamw_kernel(const __grid_constant__ AdamParams p) {
+__global__ void __launch_bounds__(kAdamThreads, AdamShape<BITS8>::PerSm) adamw_kernel(const __grid_constant__ AdamParams p) {
   begin_overlapped();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   AdamNow now;
@@ -253,7 +279,7 @@ __global__ void __launch_bounds__(kAdamThreads, kAdamPerSm) adamw_kernel(const _
     now.c1 = 1.0f / -expm1f((float)t * p.ln_b1);
     now.c2 = rsqrtf(-expm1f((float)t * p.ln_b2));
   }
-  constexpr int W = kAdamThreads / 32;
+  constexpr int W = kAdamWarps, U = AdamShape<BITS8>::Unroll;
   for (uint32_t chunk = blockIdx.x; chunk < p.chunks; chunk += gridDim.x) {
     uint32_t lo = 0, hi = p.count;   // the last tensor whose first chunk is not behind this one
     while (hi - lo > 1) {
@@ -262,13 +288,33 @@ __global__ void __launch_bounds__(kAdamThreads, kAdamPerSm) adamw_kernel(const _
       else hi = mid;
     }
     const AdamTensor& t = p.t[lo];
-    const int64_t blocks = (t.n + kBlock - 1) / kBlock, begin = (int64_t)(chunk - t.first_chunk) * kAdamChunk;
-    const int64_t end = begin + kAdamChunk < blocks ? begin + kAdamChunk : blocks;
+    const int64_t blocks = (t.n + kBlock - 1) / kBlock, begin = (int64_t)(chunk - t.first_chunk) * p.chunk_blocks;
+    const int64_t end = begin + p.chunk_blocks < blocks ? begin + p.chunk_blocks : blocks;
     const int64_t whole = t.aligned ? (end < t.n / kBlock ? end : t.n / kBlock) : begin;   // up to here in whole vectors
     int64_t b = begin + warp;
-    for (; b + W < whole; b += 2 * W) adam_blocks<TP, TG, MASTER, BITS8, 2, true>(p, t, now, b, lane);
-    for (; b < whole; b += W) adam_blocks<TP, TG, MASTER, BITS8, 1, true>(p, t, now, b, lane);
-    for (; b < end; b += W) adam_blocks<TP, TG, MASTER, BITS8, 1, false>(p, t, now, b, lane);
+    if (b + (U - 1) * W < whole) {
+      AdamRaw<TP, TG, MASTER, BITS8, U> now_raw, next_raw;
+      now_raw.template load<true>(t, b, lane);
+      for (;;) {
+        const int64_t next = b + U * W;
+        const bool more = next + (U - 1) * W < whole;
+        if (more) next_raw.template load<true>(t, next, lane);
+        adam_step<TP, TG, MASTER, BITS8, U, true>(p, t, now, now_raw, b, lane);
+        b = next;
+        if (!more) break;
+        now_raw = next_raw;
+      }
+    }
+    for (; b < whole; b += W) {
+      AdamRaw<TP, TG, MASTER, BITS8, 1> raw;
+      raw.template load<true>(t, b, lane);
+      adam_step<TP, TG, MASTER, BITS8, 1, true>(p, t, now, raw, b, lane);
+    }
+    for (; b < end; b += W) {
+      AdamRaw<TP, TG, MASTER, BITS8, 1> raw;
+      raw.template load<false>(t, b, lane);
+      adam_step<TP, TG, MASTER, BITS8, 1, false>(p, t, now, raw, b, lane);
+    }
   }
 }
 
