@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::Stages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&done[i], 1);
+      mbar_init(&done[i], 2);   // the products and the scales
     }
     for (int i = 0; i < 2; ++i) mbar_init(&taken[i], kMmWarps * G);
     for (int i = 0; i < kMmScaleSets; ++i) mbar_init(&scaled[i], 1);
@@ -271,6 +271,37 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
           }
         }
       }
+    } else if (warp == kMmWarps + 2) {
+      // The scales of a block's rows, times those of the 128 x 128 blocks, for the warps of sums: its arrival joins the
+      // products', so that they wait once per block and read one number each.
+      for (int item = first; alive && item < p.items; item += stride) {
+        const MmItem w = mm_item<G>(p, item);
+        const float* sb = p.sb + (TILE ? w.n0 / kBlock * p.ldsb : 0);
+        const bool second = w.n0 + kBlock < p.N;
+        for (int j = w.j0; j < w.j1; ++j, ++n) {
+          const uint32_t set = n % kMmScaleSets;
+          float t0 = 0.0f, t1 = 0.0f;
+          if (TILE) {
+            t0 = __ldg(sb + j);
+            if (second) t1 = __ldg(sb + p.ldsb + j);
+          }
+          alive = __all_sync(kFullMask, wait_alive(&scaled[set], (n / kMmScaleSets) & 1, dead, p.wait_cycles));
+          if (!alive) break;
+          if (TILE) {
+            float* scales = reinterpret_cast<float*>(smem + S::ScaleOff + set * kMmScaleBytes);
+            const float4 r = *reinterpret_cast<const float4*>(scales + lane * 4);
+            float* to = scales + kMmRows + lane * 4;
+            *reinterpret_cast<float4*>(to) = make_float4(r.x * t0, r.y * t0, r.z * t0, r.w * t0);
+            *reinterpret_cast<float4*>(to + kMmRows) = make_float4(r.x * t1, r.y * t1, r.z * t1, r.w * t1);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&done[s]));
+          if (++s == S::Stages) {
+            s = 0;
+            turn ^= 1;
+          }
+        }
+      }
     }
   } else {
     more_registers<kMmSumRegs>();
@@ -290,17 +321,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
       float2 acc[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      // a row's scale is the lane's, that of 128 x 128 blocks one for the warp (32 blocks' lie in a line); the columns'
-      // scales are read from shared memory
-      const float* sb = p.sb + (TILE && active ? col0 / kBlock * p.ldsb : 0);
       for (int j = w.j0; alive && j < w.j1; ++j, ++n) {
         const uint32_t b = n & 1, set = n % kMmScaleSets;
         const float* scales = reinterpret_cast<const float*>(smem + S::ScaleOff + set * kMmScaleBytes);
-        const float* cb = scales + kMmRows + quarter * 64;
-        const float tile = TILE ? __ldg(sb + j) : 1.0f;
-        bool ok = wait_alive(&scaled[set], (n / kMmScaleSets) & 1, dead, p.wait_cycles);
-        const float rs = ok ? scales[lanes + lane] * tile : 0.0f;
-        ok = ok && wait_alive(&done[s], turn, dead, p.wait_cycles);
+        const float* cb = scales + kMmRows + quarter * 64;                          // of columns, or
+        const float* row = scales + (TILE ? kMmRows + (quarter >> 1) * kMmRows : 0) + lanes + lane;   // of rows times the block's
+        const bool ok = wait_alive(&done[s], turn, dead, p.wait_cycles);
         if (++s == S::Stages) {
           s = 0;
           turn ^= 1;
@@ -310,6 +336,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         tcgen05_fence_after();
         if (active) {
           constexpr int W = TILE ? 32 : 16;   // columns at a time: with column scales the registers do not hold more
+          const float rs = *row;
           const float2 r2 = make_float2(rs, rs);
           float t[W];
 #pragma unroll
