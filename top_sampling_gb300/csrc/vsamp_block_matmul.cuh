@@ -321,18 +321,18 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
       float2 acc[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[i] = make_float2(0.0f, 0.0f);
-      for (int j = w.j0; alive && j < w.j1; ++j, ++n) {
+      for (int j = w.j0; j < w.j1; ++j, ++n) {
         const uint32_t b = n & 1, set = n % kMmScaleSets;
         const float* scales = reinterpret_cast<const float*>(smem + S::ScaleOff + set * kMmScaleBytes);
         const float* cb = scales + kMmRows + quarter * 64;                          // of columns, or
         const float* row = scales + (TILE ? kMmRows + (quarter >> 1) * kMmRows : 0) + lanes + lane;   // of rows times the block's
-        const bool ok = wait_alive(&done[s], turn, dead, p.wait_cycles);
+        // a wait that gives up marks the CTA, which is looked at once per tile
+        (void)wait_alive(&done[s], turn, dead, p.wait_cycles);
         if (++s == S::Stages) {
           s = 0;
           turn ^= 1;
         }
-        alive = __all_sync(kFullMask, ok);
-        if (!alive) break;
+        __syncwarp();
         tcgen05_fence_after();
         if (active) {
           constexpr int W = TILE ? 32 : 16;   // columns at a time: with column scales the registers do not hold more
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
           release(b);
         }
       }
-      if (!alive) {
+      if (*dead) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[i] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
       }
