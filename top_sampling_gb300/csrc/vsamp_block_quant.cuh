@@ -194,7 +194,7 @@ struct QuantTile<__nv_bfloat16> {   // pairs stay packed: half the registers, tw
 };
 
 template <typename T, bool TILE, bool PLAIN, bool TURNED>
-__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 4 ? 2 : PLAIN && TURNED ? 3 : 4) block_quant_kernel(const BlockQuantParams p) {
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 4 ? 2 : 4) block_quant_kernel(const BlockQuantParams p) {
   begin_overlapped();
   __shared__ __align__(16) unsigned char turned[TURNED ? kBlock * kBlock : 16];
   __shared__ __align__(16) float maxima[8][kBlock];
