@@ -434,7 +434,8 @@ typedef enum vsamp_block_kind {
 } vsamp_block_kind;
 
 /* Quantises x [R, ldx] (fp32 or bf16, C columns) and, in the same pass, x transposed:
- *   scale = max(largest magnitude of the block / 448, 2^-126),  code = e4m3(x * (1 / scale)), to nearest even
+ *   scale = max(largest magnitude of the block / 448, 2^-126),  code = e4m3(x * 448 / that magnitude), to nearest even
+ *   (x * 2^126 with the smallest scale); the quotients are rounded once to fp32
  *   codes [R, ldc], scales       of x, blocks along its columns (both NULL: not written)
  *   codes_t [C, ldt], scales_t   of x^T, blocks along the rows of x (both NULL: not written)
  * Of VSAMP_BLOCK_TILE the two hold the same codes and scales transposed. A block with NaN or an infinity has the scale

@@ -24,14 +24,21 @@ def e4m3(y):
 
 
 def scale_of(amax):
-    """The scale of a block and what its elements are multiplied with, in fp32 as the definition says."""
+    """The scale of a block in fp32, NaN for one that is not finite."""
     s = np.maximum(amax.astype(np.float32) / np.float32(448), np.float32(2.0 ** -126))
-    with np.errstate(invalid="ignore"):
-        return np.where(np.isfinite(amax), s, np.float32(np.nan)), np.float32(1) / s
+    return np.where(np.isfinite(amax), s, np.float32(np.nan))
+
+
+def in_units(v, amax):
+    """Elements in units of their block's scale, the quotient rounded once to fp32 (binary64 before: 29 bits more)."""
+    amax = amax.astype(np.float64)
+    with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
+        y = np.where(amax >= 448 * 2.0 ** -126, v.astype(np.float64) * 448 / amax, v.astype(np.float64) * 2.0 ** 126)
+    return np.where(np.isfinite(amax), y, 0.0).astype(np.float32)
 
 
 def quantise(x, tile):
-    """fp32 values [R, C] -> (code values [R, C], scales in the layout of the kind). Every step is one fp32 operation."""
+    """fp32 values [R, C] -> (code values [R, C], scales in the layout of the kind)."""
     x = np.asarray(x, np.float32)
     R, C = x.shape
     rows = BLOCK if tile else 1
@@ -40,11 +47,8 @@ def quantise(x, tile):
     v = pad.reshape(pad.shape[0] // rows, rows, blocks(C), BLOCK)
     a = np.abs(v)
     amax = np.where(np.isnan(a).any(axis=(1, 3)), np.nan, a.max(axis=(1, 3)))
-    s, inv = scale_of(amax)
-    with np.errstate(invalid="ignore", over="ignore"):
-        y = v * inv[:, None, :, None]
-    y = np.where(np.isnan(s)[:, None, :, None], 0.0, y)
-    y = e4m3(y).reshape(pad.shape)[:R, :C]
+    s = scale_of(amax)
+    y = e4m3(in_units(v, amax[:, None, :, None])).reshape(pad.shape)[:R, :C]
     return y, s if tile else s.T
 
 

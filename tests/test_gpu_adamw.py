@@ -57,8 +57,8 @@ class Model:
             else:
                 for x, codes, scales in ((m, self.m, self.ms), (r, self.v, self.vs)):
                     b = bu.per_block(x)
-                    s, inv = bu.scale_of(np.abs(b).max(axis=1))
-                    codes.append(place(bu.e4m3(b * inv[:, None]).reshape(-1)[:n], F8))
+                    s = bu.scale_of(np.abs(b).max(axis=1))
+                    codes.append(place(bu.e4m3(b / s[:, None]).reshape(-1)[:n], F8))
                     scales.append(place(s, F32))
         more = dict(m_scale=self.ms, v_scale=self.vs) if bits == 8 else {}
         self.state = ts.vsamp_adamw_state(self.params, bits=bits, masters=self.masters if masters else None, m=self.m, v=self.v,

@@ -112,6 +112,28 @@ def test_quantise_error(ts, dev):
         assert (off <= torch.maximum(x.double().abs() * (2.0 ** -4 + 4 * bu.U), s * 2.0 ** -10 * (1 + 4 * bu.U))).all()
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_quantise_ties(ts, dev, dt):
+    """Elements half way between two codes go to the even one: x = max * midpoint / 448 exactly, for maxima whose quotient
+    with 448 has no exact reciprocal."""
+    mids = torch.arange(8, 15, device=dev).float() + 0.5                    # between the codes of a binade, in eighths
+    scale = torch.exp2(torch.arange(-3, 3, device=dev).float())
+    mid = (mids[:, None] * scale).reshape(-1)                              # 42 midpoints, among them 8.5 / 4 ..
+    even = torch.round(mids)[:, None] * scale
+    for top in (7.0, 1.0, 0.75, 1.25, 7 * 2.0 ** 20, 1.75 * 2.0 ** -30):
+        x = torch.zeros((1, 128), dtype=torch.float64, device=dev)
+        x[0, :42] = mid.double() * top / 448
+        x[0, 100] = top
+        if dt == BF16 or not torch.equal(x.float().double(), x):
+            keep = x.to(dt).double() == x
+            x = torch.where(keep, x, torch.zeros_like(x))
+        a, _ = ts.vsamp_block_quantize(x.to(dt))
+        got = a.codes.view(torch.float8_e4m3fn).float()[0, :42]
+        exact = x[0, :42] != 0
+        assert torch.equal(got[exact], even.reshape(-1)[exact]), top
+        assert top not in (7.0, 7 * 2.0 ** 20, 1.75 * 2.0 ** -30) or exact.all()
+
+
 def _operand(ts, rows, cols, tile, dev, seed):
     rng = np.random.default_rng(seed)
     t = ts.BlockTensor.empty(rows, cols, tile, dev)

@@ -1,6 +1,6 @@
 // Quantisation into e4m3 blocks of 128, of a matrix and of its transpose in one pass over it.
 //
-//   scale = max(max |x| / 448, 2^-126) over a block (1 x 128 or 128 x 128), code = e4m3(x * (1 / scale)), nearest even.
+//   scale = max(max |x| / 448, 2^-126) over a block (1 x 128 or 128 x 128), code = e4m3(x * 448 / max |x|), nearest even
 //
 // One CTA takes a tile of 128 x 128 elements, which holds whole blocks of both directions: it is read once, every
 // maximum is formed from registers, and the transpose goes through 16 KB of shared memory so that both outputs are
@@ -32,14 +32,32 @@ struct BlockQuantParams {
   int aligned;      // every row of x begins on the boundary of a thread's vector
 };
 
+// What the elements of a block are multiplied with, 448 / max, in two parts. One fp32 number is off by up to half a unit,
+// and of bf16 values many lie half way between two codes: which side they fell on would be that error's.
+struct BlockInverse {
+  float hi, lo;   // hi below 0: the block is not finite
+};
+
 // The scale of a block from the bits of its largest magnitude (those of NaN are above those of an infinity, and both
-// above every finite value's); inv is what its elements are multiplied with, 0 for a block that is not finite.
-__device__ __forceinline__ float block_scale(uint32_t amax_bits, float& inv) {
-  const float s = fmaxf(__fdiv_rn(__uint_as_float(amax_bits), kE4m3Max), 0x1p-126f);
-  const bool bad = amax_bits >= kInfBits;
-  inv = bad ? 0.0f : __frcp_rn(s);
-  return bad ? __uint_as_float(0x7FC00000u) : s;
+// above every finite value's).
+__device__ __forceinline__ float block_scale(uint32_t amax_bits, BlockInverse& inv) {
+  const float amax = __uint_as_float(amax_bits), s = fmaxf(__fdiv_rn(amax, kE4m3Max), 0x1p-126f);
+  if (amax_bits >= kInfBits) {
+    inv.hi = -1.0f;
+    inv.lo = 0.0f;
+    return __uint_as_float(0x7FC00000u);
+  }
+  inv.hi = 0x1p126f;
+  inv.lo = 0.0f;
+  if (amax >= kE4m3Max * 0x1p-126f) {
+    inv.hi = __fdiv_rn(kE4m3Max, amax);
+    inv.lo = __fdividef(fmaf(-inv.hi, amax, kE4m3Max), amax);
+  }
+  return s;
 }
+
+// x * 448 / max, rounded once, for two elements.
+__device__ __forceinline__ float2 in_units(float2 x, float2 hi, float2 lo) { return __ffma2_rn(x, hi, __fmul2_rn(x, lo)); }
 
 // Two e4m3 codes, a in the low byte; magnitudes above 448 become 448.
 __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
@@ -198,7 +216,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 4 ? 2 : 4) block_q
   begin_overlapped();
   __shared__ __align__(16) unsigned char turned[TURNED ? kBlock * kBlock : 16];
   __shared__ __align__(16) float maxima[8][kBlock];
-  __shared__ __align__(16) float inverse[kBlock];
+  __shared__ __align__(16) float inverse[2][kBlock];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = (lane & 15) * 8, r0 = warp * 16 + (lane >> 4) * 8;   // this thread's 8 x 8 elements
   for (int64_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
@@ -213,8 +231,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 4 ? 2 : 4) block_q
       if (i < rows && left > 0) x.load_row(i, from + i * p.ldx * (int64_t)sizeof(T), left, p.aligned != 0);
       else x.clear_row(i);
     }
-    float tile_inv = 0.0f;
-    bool tile_bad = false;
+    BlockInverse tile_inv = {0.0f, 0.0f};
     if (TILE) {
       uint32_t m = warp_max_u32(__float_as_uint(x.all_max()));
       if (lane == 0) maxima[warp][0] = __uint_as_float(m);
@@ -222,33 +239,35 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 4 ? 2 : 4) block_q
 #pragma unroll
       for (int w = 0; w < 8; ++w) m = max(m, __float_as_uint(maxima[w][0]));
       const float s = block_scale(m, tile_inv);
-      tile_bad = m >= kInfBits;
       if (threadIdx.x == 0) {
         if (PLAIN) p.scales[rt * p.lds + ct] = s;
         if (TURNED) p.scales_t[ct * p.ldst + rt] = s;
       }
     }
     if (PLAIN) {
-      float own_inv = tile_inv;   // of the row lane & 7; below 0 for one that is not finite
+      BlockInverse own = tile_inv;   // of the row lane & 7
       if (!TILE) {
-        const uint32_t m = __float_as_uint(x.row_max(lane));
-        const float s = block_scale(m, own_inv);
-        if (m >= kInfBits) own_inv = -1.0f;
+        const float s = block_scale(__float_as_uint(x.row_max(lane)), own);
         const int64_t r = row + (lane & 7);
         if ((lane & 8) == 0 && r < p.R) p.scales[ct * p.lds + r] = s;
       }
       unsigned char* to = p.codes + row * p.ldc + col;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float inv = TILE ? tile_inv : __shfl_sync(kFullMask, own_inv, (lane & 16) + i);
-        uint2 w;
-        w.x = e4m3_quad(x.at(i, 0) * inv, x.at(i, 1) * inv, x.at(i, 2) * inv, x.at(i, 3) * inv);
-        w.y = e4m3_quad(x.at(i, 4) * inv, x.at(i, 5) * inv, x.at(i, 6) * inv, x.at(i, 7) * inv);
-        if (TILE ? tile_bad : inv < 0.0f) w.x = w.y = 0u;
+        const float hi = TILE ? own.hi : __shfl_sync(kFullMask, own.hi, (lane & 16) + i);
+        const float lo = TILE ? own.lo : __shfl_sync(kFullMask, own.lo, (lane & 16) + i);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 y = in_units(make_float2(x.at(i, 2 * j), x.at(i, 2 * j + 1)), make_float2(hi, hi), make_float2(lo, lo));
+          w[j] = e4m3_pair(y.x, y.y);
+        }
+        uint2 c = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+        if (hi < 0.0f) c.x = c.y = 0u;
         if (i < rows && left > 0) {
-          if (left == 8) *reinterpret_cast<uint2*>(to) = w;
+          if (left == 8) *reinterpret_cast<uint2*>(to) = c;
           else
-            for (int j = 0; j < left; ++j) to[j] = (unsigned char)((j < 4 ? w.x : w.y) >> ((j & 3) * 8));
+            for (int j = 0; j < left; ++j) to[j] = (unsigned char)((j < 4 ? c.x : c.y) >> ((j & 3) * 8));
         }
         to += p.ldc;
       }
@@ -262,24 +281,35 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 4 ? 2 : 4) block_q
           float m = maxima[0][threadIdx.x];
 #pragma unroll
           for (int w = 1; w < 8; ++w) m = max_nan(m, maxima[w][threadIdx.x]);
-          float inv;
+          BlockInverse inv;
           const float s = block_scale(__float_as_uint(m), inv);
-          inverse[threadIdx.x] = __float_as_uint(m) >= kInfBits ? -1.0f : inv;
+          inverse[0][threadIdx.x] = inv.hi;
+          inverse[1][threadIdx.x] = inv.lo;
           const int64_t c = ct * kBlock + threadIdx.x;
           if (c < p.C) p.scales_t[rt * p.ldst + c] = s;
         }
         __syncthreads();
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float inv = TILE ? tile_inv : inverse[c0 + j];
-        uint2 w;
-        w.x = e4m3_quad(x.at(0, j) * inv, x.at(1, j) * inv, x.at(2, j) * inv, x.at(3, j) * inv);
-        w.y = e4m3_quad(x.at(4, j) * inv, x.at(5, j) * inv, x.at(6, j) * inv, x.at(7, j) * inv);
-        if (TILE ? tile_bad : inv < 0.0f) w.x = w.y = 0u;
+      for (int j = 0; j < 8; j += 2) {   // two columns
+        const float2 hi = TILE ? make_float2(tile_inv.hi, tile_inv.hi) : *reinterpret_cast<const float2*>(&inverse[0][c0 + j]);
+        const float2 lo = TILE ? make_float2(tile_inv.lo, tile_inv.lo) : *reinterpret_cast<const float2*>(&inverse[1][c0 + j]);
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = in_units(make_float2(x.at(2 * i, j), x.at(2 * i, j + 1)), hi, lo);
+          const float2 z = in_units(make_float2(x.at(2 * i + 1, j), x.at(2 * i + 1, j + 1)), hi, lo);
+          a[i] = e4m3_pair(y.x, z.x);
+          b[i] = e4m3_pair(y.y, z.y);
+        }
+        uint2 ca = make_uint2(a[0] | (a[1] << 16), a[2] | (a[3] << 16)), cb = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+        if (hi.x < 0.0f) ca.x = ca.y = 0u;
+        if (hi.y < 0.0f) cb.x = cb.y = 0u;
         // 16-byte pieces of a row of 128 are permuted by the column's upper bits: two-way conflicts instead of sixteen
         const int c = c0 + j, piece = (r0 >> 4) ^ ((c >> 3) & 7);
-        *reinterpret_cast<uint2*>(turned + c * kBlock + piece * 16 + (r0 & 8)) = w;
+        unsigned char* to = turned + c * kBlock + piece * 16 + (r0 & 8);
+        *reinterpret_cast<uint2*>(to) = ca;
+        *reinterpret_cast<uint2*>(to + kBlock) = cb;
       }
       __syncthreads();
 #pragma unroll
