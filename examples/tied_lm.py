@@ -5,16 +5,19 @@ ends (tied embeddings). It learns a synthetic chain in which every token has fou
 
 * training: ``vsamp_embed`` -> z, logits (library products) -> ``vsamp_score_tokens`` (loss: minus the mean
   log-probability of the targets minus a small entropy bonus) -> ``vsamp_score_tokens_backward`` into the logits' own
-  buffer -> gradients of W and the table, the lookup's part added by ``vsamp_embed_backward``;
+  buffer -> gradients of W and the table, the lookup's part added by ``vsamp_embed_backward`` -> ``vsamp_adamw``;
+* the same with the vocabulary's three products in 8 bits: ``vsamp_block_quantize`` of the table, the states and the
+  logits' gradient, ``vsamp_block_matmul`` for logits, states' and table's gradient; moments of 8 bits;
 * serving: the table in 4 bits (``vsamp_head_pack``), one decode step captured as a CUDA graph: ``vsamp_embed`` ->
   ``vsamp_head_logits`` -> ``vsamp_sample`` -> ``vsamp_score_tokens`` (log-probability, rank and alternatives of the
   drawn token).
 
-    python -m examples.tied_lm
+    python -m examples.tied_lm [--eight-bit]
 """
 from __future__ import annotations
 
 import math
+import sys
 from typing import NamedTuple
 
 import torch
@@ -46,22 +49,32 @@ class Model(NamedTuple):
     W: torch.Tensor        # [D, D] fp32
 
 
-def gradients(model: Model, tok, target, entropy_bonus: float = 0.0):
-    """Loss and gradients of the mean over the scored positions."""
+def gradients(model: Model, tok, target, entropy_bonus: float = 0.0, eight_bit: bool = False):
+    """Loss and gradients of the mean over the scored positions, the vocabulary's products in bf16 or in 8 bits."""
     table, W = model
     V, D = table.shape
     scored = (target != ts.VSAMP_TOKEN_IGNORE).sum()
     t16, w16 = table.bfloat16(), W.bfloat16()
     h, _ = ts.vsamp_embed(tok, t16, scale=math.sqrt(D))
     z = h @ w16
-    logits = z @ t16.t()
+    if eight_bit:
+        t8, t8_turned = ts.vsamp_block_quantize(table, tile=True, transposed=True)
+        z8, z8_turned = ts.vsamp_block_quantize(z, transposed=True)
+        logits = ts.vsamp_block_matmul(z8, t8)
+    else:
+        logits = z @ t16.t()
     lp, ent, _, _, _, m, logsum, status = ts.vsamp_score_tokens(logits, target)
     loss = -(lp.sum() + entropy_bonus * ent.sum()) / scored
     g = (-1.0 / scored).expand(tok.numel()).contiguous()
     dlogits, _ = ts.vsamp_score_tokens_backward(logits, target, g, m, logsum, entropy=ent, dentropy=entropy_bonus * g,
                                                 dlogits=logits)
-    dz = dlogits @ t16
-    dtable = (dlogits.t() @ z).float()
+    if eight_bit:
+        d8, d8_turned = ts.vsamp_block_quantize(dlogits, transposed=True)
+        dz = ts.vsamp_block_matmul(d8, t8_turned)
+        dtable = ts.vsamp_block_matmul(d8_turned, z8_turned, out_dtype=torch.float32)
+    else:
+        dz = dlogits @ t16
+        dtable = (dlogits.t() @ z).float()
     dW = (h.t() @ dz).float()
     dh = dz @ w16.t()
     ts.vsamp_embed_backward(tok, dh, V, scale=math.sqrt(D), dtable=dtable, accumulate=True)
@@ -69,23 +82,19 @@ def gradients(model: Model, tok, target, entropy_bonus: float = 0.0):
 
 
 def train(chain: Chain, D: int = 256, steps: int = 400, batch: int = 4096, lr: float = 3e-3, seed: int = 1,
-          device="cuda"):
-    """Adam on the model's two matrices. Returns the model and the losses."""
+          device="cuda", eight_bit: bool = False):
+    """Adam on the model's two matrices, with moments of 32 or 8 bits. Returns the model and the losses."""
     dev = torch.device(device)
     gen = torch.Generator().manual_seed(seed)
     model = Model((torch.randn((chain.V, D), generator=gen) * D ** -0.5).to(dev),
                   (torch.eye(D) + torch.randn((D, D), generator=gen) * 0.02).to(dev))
-    first = Model(*(torch.zeros_like(p) for p in model))
-    second = Model(*(torch.zeros_like(p) for p in model))
+    state = ts.vsamp_adamw_state(model, bits=8 if eight_bit else 32)
     losses = []
     for step in range(1, steps + 1):
         tok, target = chain.batch(batch, gen, dev)
-        loss, status, grad = gradients(model, tok, target, entropy_bonus=0.01)
+        loss, status, grad = gradients(model, tok, target, entropy_bonus=0.01, eight_bit=eight_bit)
         losses.append(loss)
-        for p, d, a, b in zip(model, grad, first, second):
-            a.mul_(0.9).add_(d, alpha=0.1)
-            b.mul_(0.99).addcmul_(d, d, value=0.01)
-            p.addcdiv_(a / (1 - 0.9 ** step), (b / (1 - 0.99 ** step)).sqrt_().add_(1e-8), value=-lr)
+        ts.vsamp_adamw(state, grad, lr=lr, step=step, beta2=0.99, seed=seed)
     return model, torch.stack(losses).tolist()
 
 
@@ -150,9 +159,9 @@ class Server:
         return token, lp, rank
 
 
-def main(V: int = 2000, steps: int = 400, n: int = 32, batch: int = 16):
+def main(V: int = 2000, steps: int = 400, n: int = 32, batch: int = 16, eight_bit: bool = False):
     chain = Chain(V)
-    model, losses = train(chain, steps=steps)
+    model, losses = train(chain, steps=steps, eight_bit=eight_bit)
     print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f} (the chain's entropy is {math.log(4):.3f})")
     server = Server(model, batch)
     first = torch.arange(batch, dtype=torch.int32, device=model.table.device)
@@ -165,4 +174,4 @@ def main(V: int = 2000, steps: int = 400, n: int = 32, batch: int = 16):
 
 
 if __name__ == "__main__":
-    main()
+    main(eight_bit="--eight-bit" in sys.argv[1:])
