@@ -166,7 +166,7 @@ def test_product(ts, dev, M, N, K, tile, out):
 
 @pytest.mark.parametrize("tile", [True, False])
 @pytest.mark.parametrize("out", [F32, BF16])
-@pytest.mark.parametrize("pad", [0, 1, 8])
+@pytest.mark.parametrize("pad", [0, 1, 3, 8])
 def test_product_into_rows(ts, dev, tile, out, pad):
     """Padded output rows; adding; what is between the rows stays."""
     M, N, K = 70, 333, 300
@@ -189,6 +189,22 @@ def test_product_long_and_wide(ts, dev, M, N, K, tile):
     y = ts.vsamp_block_matmul(a, b, out_dtype=F32)
     _check_product(y, a, b)
     assert torch.equal(ts.vsamp_block_matmul(a, b, out_dtype=F32), y)
+
+
+@pytest.mark.parametrize("tile", [True, False])
+@pytest.mark.parametrize("out", [F32, BF16])
+@pytest.mark.parametrize("M,N", [(20, 60), (150, 133)])
+def test_product_added_in_parts(ts, dev, tile, out, M, N):
+    """A long inner dimension, divided over CTAs, added to what is there; odd rows and whole ones."""
+    K = 30000
+    assert ts.load().vsamp_block_matmul_workspace_size(M, N, K) > 0
+    a, b = _operand(ts, M, K, False, dev, 7), _operand(ts, N, K, tile, dev, 8)
+    y = torch.full((M, N + 5), 7.0, dtype=out, device=dev)
+    base = torch.randn((M, N), device=dev).to(out)
+    y[:, :N] = base
+    ts.vsamp_block_matmul(a, b, out=y[:, :N], accumulate=True)
+    _check_product(y[:, :N], a, b, bu.f64(base))
+    assert (y[:, N:] == 7.0).all()
 
 
 def test_product_padded_operands(ts, dev):

@@ -224,7 +224,8 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   p.accumulate = accumulate != 0;
   const int es = out_dt == VSAMP_F32 ? 4 : 2;
   // bf16 sums are added and rounded once, by the warps themselves; a stride of a tensor map has 40 bits
-  p.boxes = at_multiple(out, 16) && ldo * es % 16 == 0 && !(p.accumulate && es == 2) && (double)M * ldo * es < 1e12;
+  if (at_multiple(out, 16) && ldo * es % 16 == 0 && !(p.accumulate && es == 2) && (double)M * ldo * es < 1e12)
+    p.boxes = N * es % 16 == 0 ? 2 : 1;
   const long long wc = env_ll("VSAMP_WAIT_CYCLES", 0);
   p.wait_cycles = wc > 0 ? wc : 4000000000LL;   // ~2 s at the maximum SM clock
   p.drop_loads = env_int("VSAMP_TEST_DROP_LOADS", 0) != 0 ? 1 : 0;

@@ -56,7 +56,9 @@ struct BlockMatmulParams {
   int row_tiles, blocks, parts;
   int a_rows;                // rows of a per copy
   int accumulate;
-  int boxes;                 // results leave as boxes of the output's tensor map: its rows begin on 16-byte boundaries
+  // Results leave as boxes of the output's tensor map, whose rows begin on 16-byte boundaries: 2, all of them; 1, those of 64
+  // whole columns (a copy ends at a multiple of 16 bytes, so the rows' end has to be one); 0, none.
+  int boxes;
   int drop_loads;            // test: copies are expected and never made
   long long wait_cycles;
 };
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         const bool add = p.accumulate != 0;
         if (p.parts > 1) {
           mm_store_boxes<float>(acc, box, &o_map, row0, col0, p.N, part, lane, false);
-        } else if (p.boxes) {
+        } else if (p.boxes == 2 || (p.boxes == 1 && col0 + 64 <= p.N)) {
           mm_store_boxes<TO>(acc, box, &o_map, row0, col0, p.N, 0, lane, add);
         } else {
           mm_store_rows<TO>(acc, box, reinterpret_cast<TO*>(p.out), p.ldo, row0, p.M, col0, p.N, lane, add);
