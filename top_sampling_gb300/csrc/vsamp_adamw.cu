@@ -88,10 +88,13 @@ extern "C" vsamp_status vsamp_adamw(const vsamp_adamw_tensor* tensors, int32_t c
   p.lr_dev = r.lr_dev;
   p.step_dev = r.step_dev;
   p.grad_scale = r.grad_scale;
-  // Long chunks keep the fetches ahead of the arithmetic; short ones spread few elements over the device.
+  // With 8-bit states long chunks keep the fetches ahead of the arithmetic (67M elements: 207 us with 128 blocks, 227 with
+  // 32), short ones spread few elements over the device (150 tensors of 20,000: 15.2 us with 32 blocks, 16.3 with 128; one
+  // of 4M: 14.9 and 16.3). Steps with 32-bit states are the better the shorter the chunks (67M: 283 us with 32 blocks, 287
+  // with 128; 150 tensors of 200,000: 128 and 136).
   int64_t total = 0;
   for (int32_t k = 0; k < count; ++k) total += tensors[k].n;
-  p.chunk_blocks = total > (int64_t)d.sm_count * AdamShape<true>::PerSm * 4 * 128 * kBlock ? 128 : 32;
+  p.chunk_blocks = bits8 && total > (int64_t)d.sm_count * AdamShape<true>::PerSm * 4 * 128 * kBlock ? 128 : 32;
   const int64_t chunk = (int64_t)p.chunk_blocks * kBlock;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int32_t k = 0;

@@ -5,9 +5,14 @@
 //
 // A stream over memory: each element is read and written once. A warp takes 128 consecutive elements of a tensor, four
 // per lane, which is also a block of the 8-bit states: their new scale is one maximum over the warp's registers, and one
-// Philox call gives a lane's four elements their random bits. The next blocks are on their way while a warp computes, since
-// the 8-bit states' arithmetic (about 80 instructions per element) takes as long as their bytes. The tensors' addresses travel in the kernel's parameters
-// (up to 384 per launch), so a step needs no table in device memory and can be captured as it is.
+// Philox call gives a lane's four elements their random bits. The next blocks are on their way while a warp computes. The
+// tensors' addresses travel in the kernel's parameters (up to 384 per launch), so a step needs no table in device memory
+// and can be captured as it is.
+//
+// Measured: 32-bit states 95 % of the copy rate (65.5M elements: fp32 283 us, bf16 with masters 281); 8-bit states 69 % (311M
+// fp32 parameters with bf16 gradients 946 us of 657): 75 instructions per element issue in 63 % of the slots, 16 warps per SM
+// wait for each other's results. More warps with fewer blocks each, copies through shared memory and paired arithmetic were
+// measured and are slower. 150 tensors of 13,700 elements: 10 us.
 #pragma once
 
 #include "vsamp_block_quant.cuh"

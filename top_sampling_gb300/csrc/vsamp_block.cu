@@ -89,11 +89,16 @@ static bool mm_fits(int64_t M, int64_t N, int64_t K) {
   return M <= 0x7FFFFE00LL && N <= 0x7FFFFE00LL && K <= 0x7FFFFE00LL && (double)M * N < 3e13;
 }
 
-// Whether pairs of CTAs take tiles of 256 rows.
+// Whether pairs of CTAs take tiles of 256 rows: they need less of the L2 (2048 x 16384 x 4096: 103 us, single CTAs 111;
+// 256 x 151936 x 4096: 136 and 147; 512 x 2048 x 32000: 37 and 40), and lose a little where there are few tiles (400 x 4096 x
+// 4096: 17.3 and 16.6; 129 x 20000 x 2048: 19.2 and 18.8). A tile of 128 rows has nothing to pair.
 static bool mm_pair(int64_t M) { return M > kMmRows; }
 
 // Parts of the inner dimension. A CTA's time goes by the blocks that it walks over and about six blocks' worth for each
-// tile's start and end; parts are written and read again. The fewest blocks of the longest CTA win.
+// tile's start and end; parts are written and read again. The fewest blocks of the longest CTA win. Against all numbers of
+// parts: 64 x 4096 x 151936 105 us with 9 (574 with 1, 156 with 10), 512 x 2048 x 32000 38 with 4 (102, 56 with 5), 16 x 2048
+// x 32000 15 with 16 (97, 22 with 24), 300 x 300 x 100000 32 with 14 (30 with 16, 304 with 1), 2048 x 4096 x 151936 947 with 1
+// (949 with 4, 1011 with 2), 1000 x 4000 x 4000 19 with 1 (28 with 2).
 static int mm_parts(int64_t M, int64_t N, int64_t K) {
   const int64_t g = mm_pair(M) ? 2 : 1, rows = kMmRows * g;
   const int64_t tiles = ((M + rows - 1) / rows) * ((N + kMmCols - 1) / kMmCols), blocks = ceil_blocks(K), at_once = kMmSms / g;

@@ -10,10 +10,16 @@
 // b is the same for a warp's 64 columns, and with one scale per row of b the column scales are read from shared memory as
 // broadcasts.
 //
-// What bounds it with many rows: a CTA alone writes 48 KB per block into shared memory and its tensor core reads them again,
-// 750 cycles at 128 bytes per cycle for products of 512; in a pair each CTA holds half of b, 64 KB both ways. A product
-// waits for its accumulator to have been read, two blocks back: the chain of completion (about 240 cycles), reading and
-// release (190) of both accumulators is what is left.
+// What bounds it with many rows is the sums, not the products (512 cycles per block at the tensor cores' rate, 4.6 PFLOP/s
+// measured): 2048 x 16384 x 32768 takes 750 us (2.9 PFLOP/s), 700 without the multiply-adds, 650 without reading tensor
+// memory, 474 as products alone. Each of the sixteen warps takes every block, one wait, two reads of tensor memory of about
+// 100 cycles and 32 paired multiply-adds; and a product waits until its accumulator has been read, two blocks back, through
+// a completion (235 cycles), that reading and a release (190). So the warp with the scales joins the products' arrival, which
+// leaves one wait (850 -> 754 us), and all operands of copies and products come from uniform registers (894 -> 849). Four
+// accumulators of 128 columns, two issuing warps, deeper reads in smaller steps were measured and are slower. A pair of CTAs
+// holds half of b each: 32 KB per block and CTA instead of 48, which 64 bytes per cycle from the L2 would take 750 cycles for.
+//
+// With few rows it streams b: 64 x 151936 x 4096 takes 100 us (96 % of the copy rate).
 //
 // Every wait is bounded. A CTA one of whose waits gave up lets its copies and products end, frees its tensor memory and
 // leaves NaN in the results that it had not finished.
@@ -31,8 +37,8 @@ constexpr int kMmSumRegs = 112, kMmOtherRegs = 32;  // registers per thread: 512
 constexpr int kMmColumns = 512;                     // of tensor memory: two accumulators
 // A block's scales, 128 of rows and 256 of columns, have a ring of their own: they are read after the block's products are
 // done, when its stage may be written again. Block n is copied once the products of block n - stages are done, whose
-// accumulator had held block n - stages - 2: every warp has read the scales of the block before that one, so eight sets do
-// for up to five stages.
+// accumulator had held block n - stages - 2: every warp had read that one out of it, and used all scales of the block before.
+// So eight sets do for up to five stages.
 constexpr int kMmScaleSets = 8, kMmScaleBytes = (kMmRows + kMmCols) * 4;
 
 template <int G>

@@ -4,7 +4,13 @@
 //
 // One CTA takes a tile of 128 x 128 elements, which holds whole blocks of both directions: it is read once, every
 // maximum is formed from registers, and the transpose goes through 16 KB of shared memory so that both outputs are
-// written in rows of 128 bytes.
+// written in rows of 128 bytes. bf16 pairs stay packed (half the registers, two maxima per instruction), a lane forms the
+// scale of one row and passes it on.
+//
+// Measured: one direction of bf16 99 % of the copy rate (32768 x 8192: 123 us); both directions 84 % (2048 x 151936: 225 us of
+// 189), where the conversions' instructions fill the issue slots; 128 x 128 blocks of fp32 both ways 89 % (32000 x 2048: 66 us).
+// Four CTAs per SM for bf16 (both ways 2048 x 65536: 93 us, three 102, two 128), two for fp32, whose tiles take 64 registers
+// (65536 x 2048 both ways: 134 us, three 149).
 #pragma once
 
 #include "vsamp_device.cuh"
