@@ -183,7 +183,8 @@ def test_product_into_rows(ts, dev, tile, out, pad):
 
 
 @pytest.mark.parametrize("M,N,K,tile", [(4, 40, 151936, True), (33, 500, 30001, True), (130, 260, 40000, False),
-                                        (1, 40961, 512, True), (200, 20000, 256, True), (2100, 1300, 300, False)])
+                                        (1, 40961, 512, True), (200, 20000, 256, True), (2100, 1300, 300, False),
+                                        (40, 40960, 2048, True), (256, 20400, 2048, True), (300, 10001, 2050, False)])
 def test_product_long_and_wide(ts, dev, M, N, K, tile):
     a, b = _operand(ts, M, K, False, dev, 5), _operand(ts, N, K, tile, dev, 6)
     y = ts.vsamp_block_matmul(a, b, out_dtype=F32)

@@ -69,12 +69,12 @@ static bool scales_map(CUtensorMap& map, const float* scales, int64_t ld, int64_
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A map of [parts, rows, cols] results for boxes of 32 rows of 128 bytes.
-static bool results_map(CUtensorMap& map, void* out, bool f32, int64_t ld, int64_t rows, int64_t cols, int parts) {
+// A map of [planes, rows, cols] results for boxes of 32 rows of 128 bytes.
+static bool results_map(CUtensorMap& map, void* out, bool f32, int64_t ld, int64_t rows, int64_t cols, int planes) {
   const EncodeTiled encode = encode_tiled();
   if (!encode) return false;
   const cuuint64_t es = f32 ? 4 : 2;
-  const cuuint64_t size[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+  const cuuint64_t size[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
   const cuuint64_t stride[2] = {(cuuint64_t)ld * es, (cuuint64_t)(rows * ld) * es};
   const cuuint32_t box[3] = {(cuuint32_t)(128 / es), 32, 1}, step[3] = {1, 1, 1};
   return encode(&map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, out, size, stride, box,
@@ -94,29 +94,38 @@ static bool mm_fits(int64_t M, int64_t N, int64_t K) {
 // 4096: 17.3 and 16.6; 129 x 20000 x 2048: 19.2 and 18.8). A tile of 128 rows has nothing to pair.
 static bool mm_pair(int64_t M) { return M > kMmRows; }
 
-// Parts of the inner dimension. A CTA's time goes by the blocks that it walks over and about six blocks' worth for each
-// tile's start and end; parts are written and read again. The fewest blocks of the longest CTA win. Against all numbers of
-// parts: 64 x 4096 x 151936 105 us with 9 (574 with 1, 156 with 10), 512 x 2048 x 32000 38 with 4 (102, 56 with 5), 16 x 2048
-// x 32000 15 with 16 (97, 22 with 24), 300 x 300 x 100000 32 with 14 (30 with 16, 304 with 1), 2048 x 4096 x 151936 947 with 1
-// (949 with 4, 1011 with 2), 1000 x 4000 x 4000 19 with 1 (28 with 2).
-static int mm_parts(int64_t M, int64_t N, int64_t K) {
-  const int64_t g = mm_pair(M) ? 2 : 1, rows = kMmRows * g;
-  const int64_t tiles = ((M + rows - 1) / rows) * ((N + kMmCols - 1) / kMmCols), blocks = ceil_blocks(K), at_once = kMmSms / g;
-  int best = 1;
-  double least = 0;
-  for (int s = 1; s <= 64 && (s == 1 || blocks / s >= 4); ++s) {
-    double t = (double)((tiles * s + at_once - 1) / at_once) * ((double)((blocks + s - 1) / s) + 6);
-    if (s > 1) t += 8 + (double)M * N * s * 8 / 1.5e6;
-    if (s == 1 || t < least * 0.95) {
-      best = s;
+// How the tiles are divided. Whole rounds of tiles over the CTAs (or pairs) go as they are; the tiles that are left over, or
+// all if there are fewer than CTAs, may be cut into parts of the inner dimension. Time goes by the blocks that the longest
+// CTA walks over, and about six blocks' worth for each tile's start and end; parts are written and read again.
+struct MmPlan {
+  int64_t tiles, whole;   // whole: tiles that are not divided
+  int parts, part_rows;
+  size_t bytes() const { return whole < tiles ? (size_t)((tiles - whole) * parts) * (size_t)part_rows * kMmCols * 4 : 0; }
+};
+static MmPlan mm_plan(int64_t M, int64_t N, int64_t K) {
+  const int64_t g = mm_pair(M) ? 2 : 1, rows = kMmRows * g, at_once = kMmSms / g, blocks = ceil_blocks(K);
+  MmPlan p;
+  p.tiles = ((M + rows - 1) / rows) * ((N + kMmCols - 1) / kMmCols);
+  p.whole = p.tiles;
+  p.parts = 1;
+  p.part_rows = (int)(M < rows ? M : rows);
+  const int64_t rest = p.tiles % at_once;
+  const double rounds = (double)((p.tiles - rest) / at_once) * (double)(blocks + 6);
+  double least = rounds + (rest ? (double)(blocks + 6) : 0.0);
+  for (int s = 2; rest && s <= 64 && blocks / s >= 4; ++s) {
+    const double t = rounds + (double)((rest * s + at_once - 1) / at_once) * ((double)((blocks + s - 1) / s) + 6) + 8 +
+                     (double)rest * p.part_rows * kMmCols * s * 8 / 1.5e6;
+    if (t < least * 0.95) {
+      p.whole = p.tiles - rest;
+      p.parts = s;
       least = t;
     }
   }
-  return best;
+  return p;
 }
 
 struct MatmulMaps {
-  CUtensorMap a, b, o, sa, sb;
+  CUtensorMap a, b, o, sa, sb, p;
 };
 
 template <typename TO, bool TILE, int G>
@@ -134,17 +143,18 @@ static vsamp_status launch_matmul_g(const BlockMatmulParams& p, const MatmulMaps
   }
   const int64_t most = d.sm_count / G;
   const unsigned grid = (unsigned)(p.items < most ? p.items : most) * G;
-  if (G == 1) return launch_1d(kern, grid, kMmThreads, smem, s, p, m.a, m.b, m.o, m.sa, m.sb);
-  return launch_clusters(kern, grid, G, kMmThreads, smem, s, p, m.a, m.b, m.o, m.sa, m.sb);
+  if (G == 1) return launch_1d(kern, grid, kMmThreads, smem, s, p, m.a, m.b, m.o, m.sa, m.sb, m.p);
+  return launch_clusters(kern, grid, G, kMmThreads, smem, s, p, m.a, m.b, m.o, m.sa, m.sb, m.p);
 }
 
 template <typename TO, bool TILE>
 static vsamp_status launch_matmul(const BlockMatmulParams& p, const MatmulMaps& m, bool pair, const DeviceInfo& d, int dev,
                                   cudaStream_t s) {
   const vsamp_status st = pair ? launch_matmul_g<TO, TILE, 2>(p, m, d, dev, s) : launch_matmul_g<TO, TILE, 1>(p, m, d, dev, s);
-  if (st != VSAMP_OK || p.parts == 1) return st;
-  const int64_t ctas = ((int64_t)p.M * (p.ldp / 4) + 255) / 256, most = (int64_t)d.sm_count * 8;
-  return launch_1d(block_matmul_join_kernel<TO>, grid_of(ctas < most ? ctas : most), 256, 0, s, p);
+  if (st != VSAMP_OK || p.whole == p.items) return st;
+  const int64_t tiles = (p.items - p.whole) / p.parts;
+  const int64_t ctas = (tiles * p.part_rows * (kMmCols / 4) + 255) / 256, most = (int64_t)d.sm_count * 8;
+  return launch_1d(block_matmul_join_kernel<TO>, grid_of(ctas < most ? ctas : most), 256, 0, s, p, pair ? 2 * kMmRows : kMmRows);
 }
 
 }  // namespace vsamp
@@ -186,8 +196,7 @@ vsamp_status vsamp_block_quantize(const void* x, vsamp_dtype dt, int64_t R, int6
 
 size_t vsamp_block_matmul_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0 || !mm_fits(M, N, K)) return 0;
-  const int parts = mm_parts(M, N, K);
-  return parts > 1 ? (size_t)parts * (size_t)M * (size_t)((N + 3) / 4 * 4) * 4 : 0;
+  return mm_plan(M, N, K).bytes();
 }
 
 vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa, const uint8_t* b,
@@ -199,7 +208,8 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   if (!matrix_ok(a, lda, sa, ldsa, VSAMP_BLOCK_ROW, M, K) || !matrix_ok(b, ldb, sb, ldsb, b_kind, N, K))
     return VSAMP_ERR_INVALID_ARG;
   if (!mm_fits(M, N, K)) return VSAMP_ERR_UNSUPPORTED;
-  const size_t need = vsamp_block_matmul_workspace_size(M, N, K);
+  const MmPlan plan = mm_plan(M, N, K);
+  const size_t need = plan.bytes();
   if (need && (!workspace || !at_multiple(workspace, 16) || workspace_bytes < need)) return VSAMP_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -221,10 +231,11 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   p.out = static_cast<unsigned char*>(out);
   p.blocks = (int)ceil_blocks(K);
   p.row_tiles = (int)((M + tile_rows - 1) / tile_rows);
-  p.parts = mm_parts(M, N, K);
-  p.items = (int)(p.row_tiles * ((N + kMmCols - 1) / kMmCols) * p.parts);
+  p.parts = plan.parts;
+  p.whole = (int)plan.whole;
+  p.items = (int)(plan.whole + (plan.tiles - plan.whole) * plan.parts);
   p.part = static_cast<float*>(workspace);
-  p.ldp = (N + 3) / 4 * 4;
+  p.part_rows = plan.part_rows;
   p.a_rows = (int)(M < kMmRows ? M : kMmRows);
   p.accumulate = accumulate != 0;
   const int es = out_dt == VSAMP_F32 ? 4 : 2;
@@ -239,9 +250,8 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   if (!codes_map(m.a, a, lda, M, K, p.a_rows) || !codes_map(m.b, b, ldb, N, K, pair ? kMmCols / 2 : kMmCols) ||
       !scales_map(m.sa, sa, ldsa, M, K, kMmRows) || (!tile && !scales_map(m.sb, sb, ldsb, N, K, kMmCols)))
     return VSAMP_ERR_CUDA;
-  if (p.parts > 1 ? !results_map(m.o, p.part, true, p.ldp, M, N, p.parts)
-                  : p.boxes && !results_map(m.o, out, es == 4, ldo, M, N, 1))
-    return VSAMP_ERR_CUDA;
+  if (p.boxes && !results_map(m.o, out, es == 4, ldo, M, N, 1)) return VSAMP_ERR_CUDA;
+  if (need && !results_map(m.p, p.part, true, kMmCols, p.part_rows, kMmCols, p.items - p.whole)) return VSAMP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (out_dt == VSAMP_F32) return tile ? launch_matmul<float, true>(p, m, pair, d, dev, s) : launch_matmul<float, false>(p, m, pair, d, dev, s);
   return tile ? launch_matmul<__nv_bfloat16, true>(p, m, pair, d, dev, s) : launch_matmul<__nv_bfloat16, false>(p, m, pair, d, dev, s);

@@ -55,10 +55,11 @@ struct BlockMatmulParams {
   const float* sb;           // of 128 x 128 blocks: the others come by their tensor map
   int64_t ldsb, ldo;
   int M, N;
-  int items;                 // tiles times parts of the inner dimension
+  int items;                 // tiles as a whole, then parts of the inner dimension of the others
+  int whole;                 // tiles as a whole
   unsigned char* out;
-  float* part;               // [parts, M, ldp] sums of a part each, when there are several
-  int64_t ldp;
+  float* part;               // [tile, part, part_rows, 256] sums of the divided tiles
+  int part_rows;             // rows of a tile, or of the matrix if that has fewer
   int row_tiles, blocks, parts;
   int a_rows;                // rows of a per copy
   int accumulate;
@@ -71,15 +72,24 @@ struct BlockMatmulParams {
 
 struct MmItem {
   int m0, n0, j0, j1;
+  int part;   // of all parts, -1 for a tile as a whole
 };
 template <int G>
 __device__ __forceinline__ MmItem mm_item(const BlockMatmulParams& p, int item) {
-  const int tile = item / p.parts, part = item - tile * p.parts, nt = tile / p.row_tiles;
   MmItem w;
+  w.part = item - p.whole;
+  int tile = item;
+  w.j0 = 0;
+  w.j1 = p.blocks;
+  if (w.part >= 0) {
+    const int t = w.part / p.parts, k = w.part - t * p.parts;
+    tile = p.whole + t;
+    w.j0 = (int)((int64_t)p.blocks * k / p.parts);
+    w.j1 = (int)((int64_t)p.blocks * (k + 1) / p.parts);
+  }
+  const int nt = tile / p.row_tiles;
   w.m0 = (tile - nt * p.row_tiles) * (kMmRows * G);
   w.n0 = nt * kMmCols;
-  w.j0 = p.blocks * part / p.parts;
-  w.j1 = p.blocks * (part + 1) / p.parts;
   return w;
 }
 
@@ -175,7 +185,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
                                                                      const __grid_constant__ CUtensorMap b_map,
                                                                      const __grid_constant__ CUtensorMap o_map,
                                                                      const __grid_constant__ CUtensorMap sa_map,
-                                                                     const __grid_constant__ CUtensorMap sb_map) {
+                                                                     const __grid_constant__ CUtensorMap sb_map,
+                                                                     const __grid_constant__ CUtensorMap p_map) {
   using S = MmShape<G>;
   constexpr bool kPair = G == 2;
   extern __shared__ unsigned char smem_raw[];
@@ -321,7 +332,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
       else mbar_arrive(smem_addr(&taken[b]));
     };
     const uint32_t from = tmem + (lanes << 16) + quarter * 64;
-    uint32_t s = 0, turn = 0;
+    uint32_t s = 0, turn = 0;   // with a power of two of stages they are bits of n
     for (int item = first; item < p.items; item += stride) {
       const MmItem w = mm_item<G>(p, item);
       const int row0 = w.m0 + (int)(rank * kMmRows + lanes), col0 = w.n0 + quarter * 64;
@@ -335,8 +346,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         const float* cb = scales + kMmRows + quarter * 64;                          // of columns, or
         const float* row = scales + (TILE ? kMmRows + (quarter >> 1) * kMmRows : 0) + lanes + lane;   // of rows times the block's
         // a wait that gives up marks the CTA, which is looked at once per tile
+        if (S::Stages == 4) {
+          s = n % 4;
+          turn = (n / 4) & 1;
+        }
         (void)wait_alive(&done[s], turn, dead, p.wait_cycles);
-        if (++s == S::Stages) {
+        if (S::Stages != 4 && ++s == S::Stages) {
           s = 0;
           turn ^= 1;
         }
@@ -366,10 +381,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         for (int i = 0; i < 32; ++i) acc[i] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
       }
       if (active) {
-        const int part = item % p.parts;
         const bool add = p.accumulate != 0;
-        if (p.parts > 1) {
-          mm_store_boxes<float>(acc, box, &o_map, row0, col0, p.N, part, lane, false);
+        if (w.part >= 0) {
+          mm_store_boxes<float>(acc, box, &p_map, row0 - w.m0, col0 - w.n0, kMmCols, w.part, lane, false);
         } else if (p.boxes == 2 || (p.boxes == 1 && col0 + 64 <= p.N)) {
           mm_store_boxes<TO>(acc, box, &o_map, row0, col0, p.N, 0, lane, add);
         } else {
@@ -405,17 +419,23 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
   }
 }
 
-// Sums of the parts of the inner dimension, in their order.
+// Sums of the parts of the divided tiles, in their order.
 template <typename TO>
-__global__ void __launch_bounds__(256) block_matmul_join_kernel(const BlockMatmulParams p) {
+__global__ void __launch_bounds__(256) block_matmul_join_kernel(const BlockMatmulParams p, int tile_rows) {
   begin_overlapped();
-  const int64_t quads = p.ldp / 4, total = (int64_t)p.M * quads;
+  constexpr int Q = kMmCols / 4;
+  const int tiles = (p.items - p.whole) / p.parts;
+  const int64_t total = (int64_t)tiles * p.part_rows * Q, one = (int64_t)p.part_rows * kMmCols;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / quads, n = (i - m * quads) * 4;
-    const float* q = p.part + m * p.ldp + n;
+    const int64_t row = i / Q;
+    const int t = (int)(row / p.part_rows), r = (int)(row - (int64_t)t * p.part_rows), c = (int)(i - row * Q) * 4;
+    const int nt = (p.whole + t) / p.row_tiles;
+    const int m = (p.whole + t - nt * p.row_tiles) * tile_rows + r, n = nt * kMmCols + c;
+    if (m >= p.M || n >= p.N) continue;
+    const float* q = p.part + t * p.parts * one + (int64_t)r * kMmCols + c;
     float4 s = *reinterpret_cast<const float4*>(q);
     for (int k = 1; k < p.parts; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(q + k * (int64_t)p.M * p.ldp);
+      const float4 v = *reinterpret_cast<const float4*>(q + k * one);
       s.x += v.x;
       s.y += v.y;
       s.z += v.z;
