@@ -208,6 +208,22 @@ def test_product_added_in_parts(ts, dev, tile, out, M, N):
     assert (y[:, N:] == 7.0).all()
 
 
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_product_tiles_that_leave_differently(ts, dev, out):
+    """A CTA whose first tile leaves as boxes and whose second one, at the rows' odd end, by elements."""
+    M, N, K = 10, 152 * 256 + 130, 100
+    a, b = _operand(ts, M, K, False, dev, 7), _operand(ts, N, K, True, dev, 8)
+    y = torch.full((M, N + 6), 7.0, dtype=out, device=dev)
+    first = None
+    for _ in range(20):
+        ts.vsamp_block_matmul(a, b, out=y[:, :N])
+        if first is None:
+            first = y.clone()
+            _check_product(y[:, :N], a, b)
+        assert torch.equal(y, first)
+    assert (y[:, N:] == 7.0).all()
+
+
 def test_product_padded_operands(ts, dev):
     """Operands inside larger arrays full of NaN codes and scales: only their own rows and columns count."""
     M, N, K = 50, 200, 270

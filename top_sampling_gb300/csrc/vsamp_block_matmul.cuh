@@ -32,7 +32,7 @@ namespace vsamp {
 
 constexpr int kMmRows = 128, kMmCols = 256;         // results of a CTA by itself; of a CTA of a pair as many
 constexpr int kMmWarps = 16;                        // warps of sums: 32 rows x 64 columns each
-constexpr int kMmThreads = kMmWarps * 32 + 128;     // and a warpgroup with the copying and the issuing warp
+constexpr int kMmThreads = kMmWarps * 32 + 128;     // and a warpgroup: the copying, the issuing, the scales' warp, one idle
 constexpr int kMmSumRegs = 112, kMmOtherRegs = 32;  // registers per thread: 512 x 112 + 128 x 32 of the launch's 640 x 96
 constexpr int kMmColumns = 512;                     // of tensor memory: two accumulators
 // A block's scales, 128 of rows and 256 of columns, have a ring of their own: they are read after the block's products are
@@ -141,6 +141,7 @@ __device__ __forceinline__ void mm_store_rows(const float2 (&acc)[32], unsigned 
   for (int c = 0; c < 2; ++c) {
     const int n = n0 + c * 32 + lane;
     if (n0 + c * 32 >= N) break;
+    if (lane == 0) bulk_read_done();   // an earlier tile may have left as a box
     __syncwarp();
     mm_box_row<float>(acc, c, box, lane);
     __syncwarp();
