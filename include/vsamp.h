@@ -438,6 +438,7 @@ typedef enum vsamp_block_kind {
  *   (x * 2^126 with the smallest scale); the quotients are rounded once to fp32
  *   codes [R, ldc], scales       of x, blocks along its columns (both NULL: not written)
  *   codes_t [C, ldt], scales_t   of x^T, blocks along the rows of x (both NULL: not written)
+ * The outputs share no memory with x or with each other.
  * Of VSAMP_BLOCK_TILE the two hold the same codes and scales transposed. A block with NaN or an infinity has the scale
  * NaN and the codes 0: whatever is computed with it is NaN. What lies behind a row's last code is left as it is.
  * One launch on `stream`. */
@@ -451,7 +452,7 @@ vsamp_status vsamp_block_quantize(const void* x, vsamp_dtype dt, int64_t R, int6
  *   b [N, ldb]   codes and scales of b_kind (weights: VSAMP_BLOCK_TILE; the other operand of a weight gradient: _ROW)
  *   K            columns of both
  *   out [M, ldo] fp32 or bf16; accumulate != 0 adds to what it holds
- * Products are exact, a block's sum and the sum over blocks fp32, one rounding at the end. A NaN scale makes its row's
+ * Products are exact, a block's sum, the product of two scales and the sum over blocks fp32, one rounding at the end. A NaN scale makes its row's
  * (or block of columns') results NaN; other results do not depend on it. Sums are formed in an order that depends on
  * the sizes alone: the same call gives the same result.
  *   workspace  vsamp_block_matmul_workspace_size bytes (0 for most sizes: NULL is fine), 16-byte aligned; needs no
@@ -477,7 +478,7 @@ typedef struct vsamp_adamw_tensor {
 } vsamp_adamw_tensor;
 
 typedef struct vsamp_adamw_rule {
-  double lr, beta1, beta2, eps, weight_decay;
+  double lr, beta1, beta2, eps, weight_decay;   /* used as fp32: eps 0 or at least 2^-126, 0 <= beta < 1 */
   int64_t step;             /* 1 for the first step */
   uint64_t seed;            /* key of the random numbers */
   const float* lr_dev;      /* device scalar that replaces lr, or NULL */

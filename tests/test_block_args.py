@@ -100,6 +100,10 @@ def test_adamw_refusals(lib):
                    dict(weight_decay=NAN), dict(step=0), dict(step=-5), dict(lr_dev=4098), dict(step_dev=4100),
                    dict(grad_scale=4097)):
         assert call(**change) == BAD, change
+    for change in (dict(eps=2.0 ** -127), dict(eps=1e-300), dict(eps=1e39), dict(lr=1e39), dict(weight_decay=1e39)):
+        assert call(**change) == BAD, change                              # not as fp32 numbers
+    for change in (dict(eps=0.0), dict(eps=2.0 ** -126)):
+        assert call(tensor=dict(n=0), **change) == 0, change
     for tensor in (dict(n=-1), dict(param=0), dict(grad=0), dict(m=0), dict(v=0), dict(param=4098), dict(grad=8193),
                    dict(m=16386), dict(v=32769), dict(master=65536), dict(master=65538)):
         assert call(tensor=tensor) == BAD, tensor

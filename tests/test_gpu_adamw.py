@@ -128,6 +128,46 @@ def test_step(ts, dev, pdt, gdt, bits, masters, at):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_least_second_moments(ts, dev, bits):
+    """Second moments on both sides of 2^-126 and no eps: a first step of lr 1 moves every parameter by 1. Errors are those
+    of the form's change, and half of the last bit of a second moment, which counts half in its root."""
+    rng = np.random.default_rng(3)
+    n = 1003
+    g = (rng.choice([-1.0, 1.0], size=n) * np.exp2(rng.uniform(-61.5, -58, size=n))).astype(np.float32)
+    p = torch.zeros(n, device=dev)
+    state = ts.vsamp_adamw_state([p], bits=bits)
+    ts.vsamp_adamw(state, [torch.from_numpy(g).to(dev)], lr=1.0, step=1, beta1=0.9, beta2=0.99, eps=0.0)
+    tol = 24 * bu.U + 2.0 ** -149 / (0.01 * g.astype(np.float64) ** 2)
+    assert np.all(np.abs(bu.f64(p) + np.sign(g)) <= tol)
+    assert (state.v[0].float() > 0).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_least_eps(ts, dev, bits):
+    """Nothing moves without a gradient, with the least eps there is."""
+    p = torch.ones(300, device=dev)
+    state = ts.vsamp_adamw_state([p], bits=bits)
+    ts.vsamp_adamw(state, [torch.zeros(300, device=dev)], lr=1.0, step=1, eps=2.0 ** -126)
+    assert (p == 1.0).all()
+
+
+def test_parameters_count_as_changed(ts, dev):
+    """A backward pass through parameters that a step has changed since is refused; without a gradient they are not."""
+    a, b = (torch.nn.Parameter(torch.ones(8, device=dev)) for _ in range(2))
+    state = ts.vsamp_adamw_state([a, b])
+    x = torch.ones(8, device=dev, requires_grad=True)
+    ya, yb = (x * a).sum(), (x * b).sum()
+    ts.vsamp_adamw(state, [torch.ones(8, device=dev), None], lr=0.1, step=1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        ya.backward()
+    yb.backward()
+    with torch.inference_mode():
+        ts.vsamp_adamw(state, [torch.ones(8, device=dev)] * 2, lr=0.1, step=2)
+        own = ts.vsamp_adamw_state([torch.ones(8, device=dev)])
+        ts.vsamp_adamw(own, [torch.ones(8, device=dev)], lr=0.1, step=1)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_many_tensors(ts, dev, bits):
     """More tensors than one launch takes, empty ones and ones without a gradient among them."""
     rng = np.random.default_rng(1)

@@ -365,3 +365,14 @@ def test_binding_refuses(ts, dev):
         ts.vsamp_block_quantize(torch.zeros((256, 8), device=dev).t())
     with pytest.raises(TypeError):
         ts.vsamp_block_quantize(torch.zeros((8, 256), device=dev).half())
+
+
+def test_outputs_that_share_memory(ts, dev):
+    x = torch.randn(128, 128, device=dev)
+    one, two = (ts.BlockTensor.empty(128, 128, False, dev) for _ in range(2))
+    for other in (one, ts.BlockTensor(one.codes, two.scales), ts.BlockTensor(two.codes, one.scales)):
+        with pytest.raises(ValueError, match="share memory"):
+            ts.vsamp_block_quantize(x, transposed=True, out=one, out_t=other)
+    ts.vsamp_block_quantize(x, transposed=True, out=one, out_t=two)
+    _, want = ts.vsamp_block_quantize(x, transposed=True)
+    assert torch.equal(two.codes.view(torch.uint8), want.codes.view(torch.uint8)) and torch.equal(two.scales, want.scales)

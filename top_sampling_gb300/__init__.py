@@ -973,6 +973,9 @@ def vsamp_block_quantize(x, tile=False, plain=True, transposed=False, out=None, 
     dt = _dtype_code(x)
     a = _block_out(out, R, C, tile, at, dev, "out") if plain else None
     b = _block_out(out_t, C, R, tile, at, dev, "out_t") if transposed else None
+    if a is not None and b is not None and (a.codes.data_ptr() == b.codes.data_ptr() or
+                                            a.scales.data_ptr() == b.scales.data_ptr()):
+        raise ValueError("out and out_t share memory")
     st = load().vsamp_block_quantize(
         x.data_ptr(), dt, R, C, ldx, VSAMP_BLOCK_TILE if tile else VSAMP_BLOCK_ROW,
         *((a.codes.data_ptr(), a.ld, a.scales.data_ptr(), a.lds) if a is not None else (None, 0, None, 0)),
@@ -1172,7 +1175,7 @@ def vsamp_adamw(state: AdamWState, grads, lr, step, beta1=0.9, beta2=0.999, eps=
                             _device_scalar(step, torch.int64, at, "step"), _at(grad_scale, f32, at, 1, "grad_scale"))
     if list(map(_data_ptr, state.params)) != state.places:
         raise ValueError("a parameter's memory is not the one that the state was made for")
-    calls = []   # everything is checked before anything is launched
+    calls, usual = [], True   # everything is checked before anything is launched
     for dt, members, words in state.groups:
         mine = grads if len(members) == len(grads) else [grads[i] for i in members]
         sizes = state.sizes if mine is grads else [state.sizes[i] for i in members]
@@ -1181,9 +1184,12 @@ def vsamp_adamw(state: AdamWState, grads, lr, step, beta1=0.9, beta2=0.999, eps=
             table[_ADAMW_GRAD::_ADAMW_WORDS] = array("q", ptrs)
             if counts is not None:
                 table[_ADAMW_N::_ADAMW_WORDS] = array("q", counts)
+                usual = False
             calls.append((table, len(members), dt, VSAMP_F32 if kind is f32 else VSAMP_BF16))
     lib, on = load(), _current(at)
     for table, n, dt, kind in calls:
         st = lib.vsamp_adamw(table.buffer_info()[0], n, dt, kind, state.bits, ctypes.byref(rule), on)
         if st:
             _check(st, "vsamp_adamw")
+    torch.autograd.graph.increment_version(
+        state.params if usual else [p for p, g in zip(state.params, grads) if g is not None])

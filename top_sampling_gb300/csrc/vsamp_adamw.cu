@@ -36,9 +36,9 @@ extern "C" vsamp_status vsamp_adamw(const vsamp_adamw_tensor* tensors, int32_t c
   if (state_bits != 32 && state_bits != 8) return VSAMP_ERR_INVALID_ARG;
   const vsamp_adamw_rule& r = *rule;
   if (!(r.beta1 >= 0 && r.beta1 < 1 && r.beta2 >= 0 && r.beta2 < 1 && r.eps >= 0 && r.weight_decay >= 0) ||
-      !std::isfinite(r.eps) || !std::isfinite(r.weight_decay))
+      !std::isfinite((float)r.eps) || !std::isfinite((float)r.weight_decay) || (r.eps > 0 && r.eps < 0x1p-126))
     return VSAMP_ERR_INVALID_ARG;
-  if (!r.lr_dev && !(r.lr >= 0 && std::isfinite(r.lr))) return VSAMP_ERR_INVALID_ARG;
+  if (!r.lr_dev && !(r.lr >= 0 && std::isfinite((float)r.lr))) return VSAMP_ERR_INVALID_ARG;
   if (!r.step_dev && r.step < 1) return VSAMP_ERR_INVALID_ARG;
   if (!at_multiple(r.lr_dev, 4) || !at_multiple(r.step_dev, 8) || !at_multiple(r.grad_scale, 4)) return VSAMP_ERR_INVALID_ARG;
   const bool bits8 = state_bits == 8;
@@ -88,9 +88,9 @@ extern "C" vsamp_status vsamp_adamw(const vsamp_adamw_tensor* tensors, int32_t c
   p.lr_dev = r.lr_dev;
   p.step_dev = r.step_dev;
   p.grad_scale = r.grad_scale;
-  // With 8-bit states long chunks keep the fetches ahead of the arithmetic (67M elements: 207 us with 128 blocks, 227 with
-  // 32), short ones spread few elements over the device (150 tensors of 20,000: 15.2 us with 32 blocks, 16.3 with 128; one
-  // of 4M: 14.9 and 16.3). Steps with 32-bit states are the better the shorter the chunks (67M: 283 us with 32 blocks, 287
+  // With 8-bit states long chunks keep the fetches ahead of the arithmetic (67M elements: 212 us with 128 blocks, 233 with
+  // 32), short ones spread few elements over the device (150 tensors of 20,000: 15.6 us with 32 blocks, 16.7 with 128; one
+  // of 4M: 14.7 and 16.2). Steps with 32-bit states are the better the shorter the chunks (67M: 283 us with 32 blocks, 287
   // with 128; 150 tensors of 200,000: 128 and 136).
   int64_t total = 0;
   for (int32_t k = 0; k < count; ++k) total += tensors[k].n;

@@ -9,8 +9,8 @@
 // tensors' addresses travel in the kernel's parameters (up to 384 per launch), so a step needs no table in device memory
 // and can be captured as it is.
 //
-// Measured: 32-bit states 95 % of the copy rate (65.5M elements: fp32 283 us, bf16 with masters 281); 8-bit states 69 % (311M
-// fp32 parameters with bf16 gradients 946 us of 657): 75 instructions per element issue in 63 % of the slots, 16 warps per SM
+// Measured: 32-bit states 95 % of the copy rate (65.5M elements: fp32 283 us, bf16 with masters 281); 8-bit states 68 % (311M
+// fp32 parameters with bf16 gradients 961 us of 657): 78 instructions per element issue in 63 % of the slots, 16 warps per SM
 // wait for each other's results. More warps with fewer blocks each, copies through shared memory and paired arithmetic were
 // measured and are slower. 150 tensors of 13,700 elements: 10 us.
 #pragma once
@@ -22,7 +22,7 @@ namespace vsamp {
 constexpr int kAdamThreads = 256;
 constexpr int kAdamTensors = 384;    // of 80 bytes: 30,720 of a launch's 32,764 parameter bytes
 // Blocks of 128 elements that a warp fetches at a time, and CTAs per SM. 67M parameters: 8-bit states (fp32 parameters, bf16
-// gradients) 4 blocks and 2 CTAs 211 us, 2 and 3 224, 2 and 2 244, 1 and 4 261; 32-bit ones move with none of it (2 and 2
+// gradients) 4 blocks and 2 CTAs 212 us, 2 and 3 242, 2 and 2 246, 1 and 4 261; 32-bit ones move with none of it (2 and 2
 // 289 us, 4 and 2 303, their floor is 281).
 template <bool BITS8>
 struct AdamShape {
@@ -89,10 +89,11 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
 }
 
 // A root and a reciprocal of one or two units' error: far below what the step, lr times the quotient, has of the parameter.
-// Numbers below 2^-126 count as 0: a root below 2^-63 adds nothing to an eps above 2^-40.
+// The root holds for second moments below 2^-126 too, those of gradients near 10^-18: with a small eps they count. The
+// reciprocal need not: 2^-75 is the least root, and an eps between 0 and 2^-126 is refused.
 __device__ __forceinline__ float sqrt_near(float x) {
   float r;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float rcp_near(float x) {
