@@ -134,6 +134,24 @@ def test_quantise_ties(ts, dev, dt):
         assert top not in (7.0, 7 * 2.0 ** 20, 1.75 * 2.0 ** -30) or exact.all()
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("exponent", [-110, -1, 126, 127])
+def test_quantise_ties_at_the_ends(ts, dev, dt, exponent):
+    """10.5 / 448 of any largest magnitude t is 1.5 t / 64, half way between the codes 10 and 11: it goes to the even one,
+    whatever 448 / t rounds to, near the type's ends too."""
+    t = torch.ldexp(torch.arange(128, 256, dtype=torch.float64), torch.tensor(exponent - 7.0, dtype=torch.float64))
+    x = torch.zeros((128, 128), dtype=torch.float64)
+    x[:, 0], x[:, 1], x[:, 2] = t, 1.5 * t / 64, -1.5 * t / 512
+    x = x.to(dt).to(dev)
+    exact = x[:, 1].double().cpu() == 1.5 * t / 64
+    assert exact.sum() >= 40
+    a, _ = ts.vsamp_block_quantize(x)
+    _, b = ts.vsamp_block_quantize(x.t().contiguous(), plain=False, transposed=True)
+    for q in (a, b):
+        codes = q.codes.view(torch.float8_e4m3fn).float().cpu()
+        assert (codes[:, 0] == 448).all() and (codes[exact, 1] == 10).all() and (codes[exact, 2] == -1.25).all()
+
+
 def _operand(ts, rows, cols, tile, dev, seed):
     rng = np.random.default_rng(seed)
     t = ts.BlockTensor.empty(rows, cols, tile, dev)

@@ -57,7 +57,7 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits, BlockInverse& i
   inv.lo = 0.0f;
   if (amax >= kE4m3Max * 0x1p-126f) {
     inv.hi = __fdiv_rn(kE4m3Max, amax);
-    inv.lo = __fdividef(fmaf(-inv.hi, amax, kE4m3Max), amax);
+    inv.lo = fmaf(-inv.hi, amax, kE4m3Max) * inv.hi * (1.0f / kE4m3Max);
   }
   return s;
 }
