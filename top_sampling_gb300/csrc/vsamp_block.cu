@@ -234,7 +234,11 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   p.ldo = ldo;
   p.out = static_cast<unsigned char*>(out);
   p.blocks = (int)ceil_blocks(K);
-  p.row_tiles = (int)((M + tile_rows - 1) / tile_rows);
+  // The matrix with fewer rows stays in the L2 while the other one is walked through once. With more rows of a, along rows of
+  // results and down columns: 32003 x 2050 x 1501 167 and 175 us, 151936 x 2048 x 2048 772 and 799; with more rows of b,
+  // 2048 x 151936 x 4096, 1,028 and 876.
+  p.across = M > N;
+  p.inner_tiles = (int)(p.across ? (N + kMmCols - 1) / kMmCols : (M + tile_rows - 1) / tile_rows);
   p.parts = plan.parts;
   p.whole = (int)plan.whole;
   p.items = (int)(plan.whole + (plan.tiles - plan.whole) * plan.parts);
@@ -246,6 +250,7 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   // bf16 sums are added and rounded once, by the warps themselves; a stride of a tensor map has 40 bits
   if (at_multiple(out, 16) && ldo * es % 16 == 0 && !(p.accumulate && es == 2) && (double)M * ldo * es < 1e12)
     p.boxes = N * es % 16 == 0 ? 2 : 1;
+  p.pairs = at_multiple(out, 2 * es) && ldo % 2 == 0;
   const long long wc = env_ll("VSAMP_WAIT_CYCLES", 0);
   p.wait_cycles = wc > 0 ? wc : 4000000000LL;   // ~2 s at the maximum SM clock
   p.drop_loads = env_int("VSAMP_TEST_DROP_LOADS", 0) != 0 ? 1 : 0;

@@ -6,9 +6,8 @@
 // both operands into a ring in shared memory (tensor copies with the 128-byte swizzle the tensor cores read), another issues
 // four products of 32 inner elements per block into one of two accumulators in tensor memory, and sixteen warps take each
 // finished block out of tensor memory and add it, scaled, to fp32 sums in registers: the sum of a block's 128 products is
-// the only one that the tensor core forms. A row of a is a lane, so its scale is one register; a 128 x 128 block's scale of
-// b is the same for a warp's 64 columns, and with one scale per row of b the column scales are read from shared memory as
-// broadcasts.
+// the only one that the tensor core forms. With 128 x 128 blocks of b, whose scale is the same for a warp's 64 columns, a row
+// of a is a lane, and its scale one register; with one scale per row of b a lane takes 4 rows and 16 columns.
 //
 // What bounds it with many rows is the sums, not the products (512 cycles per block at the tensor cores' rate, 4.6 PFLOP/s
 // measured): 2048 x 16384 x 32768 takes 750 us (2.9 PFLOP/s), 700 without the multiply-adds, 650 without reading tensor
@@ -60,15 +59,24 @@ struct BlockMatmulParams {
   unsigned char* out;
   float* part;               // [tile, part, part_rows, 256] sums of the divided tiles
   int part_rows;             // rows of a tile, or of the matrix if that has fewer
-  int row_tiles, blocks, parts;
+  int across, inner_tiles;   // tiles follow each other along a row of results, or down a column; tiles of one
+  int blocks, parts;
   int a_rows;                // rows of a per copy
   int accumulate;
   // Results leave as boxes of the output's tensor map, whose rows begin on 16-byte boundaries: 2, all of them; 1, those of 64
   // whole columns (a copy ends at a multiple of 16 bytes, so the rows' end has to be one); 0, none.
   int boxes;
+  int pairs;                 // rows of results begin on the boundary of two elements
   int drop_loads;            // test: copies are expected and never made
   long long wait_cycles;
 };
+
+// Where a tile begins.
+__device__ __forceinline__ void mm_origin(const BlockMatmulParams& p, int tile, int tile_rows, int& m0, int& n0) {
+  const int u = tile / p.inner_tiles, v = tile - u * p.inner_tiles;
+  m0 = (p.across ? u : v) * tile_rows;
+  n0 = (p.across ? v : u) * kMmCols;
+}
 
 struct MmItem {
   int m0, n0, j0, j1;
@@ -87,37 +95,63 @@ __device__ __forceinline__ MmItem mm_item(const BlockMatmulParams& p, int item) 
     w.j0 = (int)((int64_t)p.blocks * k / p.parts);
     w.j1 = (int)((int64_t)p.blocks * (k + 1) / p.parts);
   }
-  const int nt = tile / p.row_tiles;
-  w.m0 = (tile - nt * p.row_tiles) * (kMmRows * G);
-  w.n0 = nt * kMmCols;
+  mm_origin(p, tile, kMmRows * G, w.m0, w.n0);
   return w;
 }
 
-// A row's 128 bytes of results, 32 fp32 or 64 bf16 columns, to the lane's row of the warp's box. Its 16-byte pieces are
-// permuted by the row (the 128-byte swizzle): no bank conflicts on either side.
-template <typename T>
-__device__ __forceinline__ void mm_box_row(const float2 (&acc)[32], int c, unsigned char* box, int lane) {
+// Columns of a tile that are computed: whole 64 of a warp, fewer at the matrix' end (19456 x 64 x 15000: 54 us, with all 256
+// columns 57). A pair's halves of b are halves of them.
+__device__ __forceinline__ int mm_columns(const BlockMatmulParams& p, int n0) {
+  return p.N - n0 < kMmCols ? (p.N - n0 + 63) & ~63 : kMmCols;
+}
+
+// Sums of a warp's 32 rows x 64 columns. TILE: a lane has a row, its columns 2 i and 2 i + 1 in acc[i]. Otherwise acc[4 k + 2 h
+// + i] holds the columns 8 k + 2 (lane % 4) and the next of row 16 h + 8 i + lane / 4: 16 columns' scales per lane instead of
+// 64, which took more of the registers and of shared memory's reads (151936 x 2048 x 2048, added: 750 us, 772 with a row per
+// lane; 32003 x 2302 x 1501 added to bf16: 364 and 378).
+//
+// 32 rows x 128 bytes of results, 32 fp32 or 64 bf16 columns, to the warp's box. A row's 16-byte pieces are permuted by the
+// row (the 128-byte swizzle): no bank conflicts.
+template <typename T, bool TILE>
+__device__ __forceinline__ void mm_box(const float2 (&acc)[32], int c, unsigned char* box, int lane) {
+  if constexpr (TILE) {
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    uint4 w;
-    if constexpr (sizeof(T) == 4) {
-      const float2 a = acc[c * 16 + q * 2], b = acc[c * 16 + q * 2 + 1];
-      w = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
-    } else {
-      uint32_t u[4];
+    for (int q = 0; q < 8; ++q) {
+      uint4 w;
+      if constexpr (sizeof(T) == 4) {
+        const float2 a = acc[c * 16 + q * 2], b = acc[c * 16 + q * 2 + 1];
+        w = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+      } else {
+        uint32_t u[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __float22bfloat162_rn(acc[q * 4 + i]);
-        memcpy(&u[i], &h, 4);
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 h = __float22bfloat162_rn(acc[q * 4 + i]);
+          memcpy(&u[i], &h, 4);
+        }
+        w = make_uint4(u[0], u[1], u[2], u[3]);
       }
-      w = make_uint4(u[0], u[1], u[2], u[3]);
+      *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
     }
-    *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
+  } else {
+    const int r = lane >> 2, e = lane & 3;
+#pragma unroll
+    for (int hi = 0; hi < 4; ++hi) {
+      unsigned char* to = box + (8 * hi + r) * 128;
+      if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<float2*>(to + (((2 * k + (e >> 1)) ^ r) << 4) + (e & 1) * 8) = acc[(c * 4 + k) * 4 + hi];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<__nv_bfloat162*>(to + ((k ^ r) << 4) + e * 4) = __float22bfloat162_rn(acc[k * 4 + hi]);
+      }
+    }
   }
 }
 
 // A warp's 32 rows x 64 columns to boxes of the map; the copies run on while the warp goes on.
-template <typename T>
+template <typename T, bool TILE>
 __device__ __forceinline__ void mm_store_boxes(const float2 (&acc)[32], unsigned char* box, const CUtensorMap* map, int m0,
                                                int n0, int N, int part, int lane, bool add) {
   constexpr int C = 128 / sizeof(T);   // columns of a box
@@ -126,58 +160,98 @@ __device__ __forceinline__ void mm_store_boxes(const float2 (&acc)[32], unsigned
     if (n0 + c * C >= N) break;
     if (lane == 0) bulk_read_done();   // of the box's last use
     __syncwarp();
-    mm_box_row<T>(acc, c, box, lane);
+    mm_box<T, TILE>(acc, c, box, lane);
     fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) tma_store_3d(map, n0 + c * C, m0, part, smem_addr(box), add);
   }
 }
 
-// The same to rows at any address: a lane per column, fp32 in the box.
-template <typename T>
+// The same to rows at any address, fp32 in the box, 16 rows of 64 columns at a time: a lane takes two neighbours (`pairs`:
+// every row begins on their boundary) or two columns 32 apart: 32003 x 2050 x 1501 added to fp32 171 us and 180, 32003 x 2302 x
+// 1501 added to bf16 378 and 539.
+template <typename T, bool TILE>
 __device__ __forceinline__ void mm_store_rows(const float2 (&acc)[32], unsigned char* box, T* out, int64_t ldo, int m0, int M,
-                                              int n0, int N, int lane, bool add) {
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int n = n0 + c * 32 + lane;
-    if (n0 + c * 32 >= N) break;
+                                              int n0, int N, int lane, bool add, bool pairs) {
+#pragma unroll 1
+  for (int h = 0; h < 32 && m0 + h < M; h += 16) {
     if (lane == 0) bulk_read_done();   // an earlier tile may have left as a box
     __syncwarp();
-    mm_box_row<float>(acc, c, box, lane);
+    if constexpr (TILE) {
+      if ((lane & 16) == h) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const float2 a = acc[q * 2], b = acc[q * 2 + 1];
+          *reinterpret_cast<float4*>(box + (lane & 15) * 256 + ((q ^ (lane & 7)) << 4)) = make_float4(a.x, a.y, b.x, b.y);
+        }
+      }
+    } else {
+      const int r = lane >> 2, e = lane & 3;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<float2*>(box + (8 * i + r) * 256 + (((2 * k + (e >> 1)) ^ r) << 4) + (e & 1) * 8) =
+              h ? acc[k * 4 + 2 + i] : acc[k * 4 + i];
+    }
     __syncwarp();
-    if (n < N) {
-      const int rows = M - m0 < 32 ? M - m0 : 32;
-      T* to = out + m0 * ldo + n;
+    const int rows = M - m0 - h < 16 ? M - m0 - h : 16, c = pairs ? 2 * lane : lane;
+    T* to = out + (m0 + h) * ldo + n0 + c;
+    if (pairs && n0 + c + 1 < N) {
 #pragma unroll 8
       for (int r = 0; r < rows; ++r, to += ldo) {
-        const float v = *reinterpret_cast<const float*>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+        float2 v = *reinterpret_cast<const float2*>(box + r * 256 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8);
         if constexpr (sizeof(T) == 4) {
           // one addition per element and call: the same result every time
-          if (add) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(to), "f"(v) : "memory");
-          else *to = v;
+          if (add) asm volatile("red.relaxed.gpu.global.add.v2.f32 [%0], {%1, %2};" ::"l"(to), "f"(v.x), "f"(v.y) : "memory");
+          else *reinterpret_cast<float2*>(to) = v;
         } else {
-          *to = (T)(add ? v + (float)*to : v);
+          __nv_bfloat162* at = reinterpret_cast<__nv_bfloat162*>(to);
+          if (add) {
+            const float2 w = __bfloat1622float2(*at);
+            v = make_float2(v.x + w.x, v.y + w.y);
+          }
+          *at = __float22bfloat162_rn(v);
+        }
+      }
+    } else {
+      const int step = pairs ? 64 : 32;   // of pairs only the last column is left
+#pragma unroll 1
+      for (int k = 0; k < 64 && n0 + c + k < N; k += step, to += step) {
+        T* at = to;
+        const int piece = (c + k) >> 2;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r, at += ldo) {
+          const float v = *reinterpret_cast<const float*>(box + r * 256 + ((piece ^ (r & 7)) << 4) + (c & 3) * 4);
+          if constexpr (sizeof(T) == 4) {
+            if (add) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(at), "f"(v) : "memory");
+            else *at = v;
+          } else {
+            *at = (T)(add ? v + (float)*at : v);
+          }
         }
       }
     }
   }
 }
 
-// W columns of a block, scaled, to the sums.
-template <bool TILE, int W>
-__device__ __forceinline__ void mm_sums(const float (&t)[W], float2 rs, const float* cb, float2 (&acc)[32], int at) {
+// 32 columns of a block, times the row's scale (and the 128 x 128 block's of b), to the sums.
+__device__ __forceinline__ void mm_sums(const float (&t)[32], float2 rs, float2 (&acc)[32], int at) {
 #pragma unroll
-  for (int i = 0; i < W / 4; ++i) {
-    const float2 u = make_float2(t[4 * i], t[4 * i + 1]), v = make_float2(t[4 * i + 2], t[4 * i + 3]);
-    if (TILE) {
-      acc[at + 2 * i] = __ffma2_rn(u, rs, acc[at + 2 * i]);
-      acc[at + 2 * i + 1] = __ffma2_rn(v, rs, acc[at + 2 * i + 1]);
-    } else {
-      const float4 c = *reinterpret_cast<const float4*>(cb + 4 * i);
-      acc[at + 2 * i] = __ffma2_rn(__fmul2_rn(u, rs), make_float2(c.x, c.y), acc[at + 2 * i]);
-      acc[at + 2 * i + 1] = __ffma2_rn(__fmul2_rn(v, rs), make_float2(c.z, c.w), acc[at + 2 * i + 1]);
+  for (int i = 0; i < 16; ++i) acc[at + i] = __ffma2_rn(make_float2(t[2 * i], t[2 * i + 1]), rs, acc[at + i]);
+}
+
+// 16 rows and 32 columns of a block, times the scales of both.
+__device__ __forceinline__ void mm_sums(const float (&t)[16], const float (&rs)[4], const float2 (&cs)[4], float2 (&acc)[32],
+                                        int c, int h) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float r = rs[2 * h + i];
+      float2& a = acc[(c * 4 + k) * 4 + 2 * h + i];
+      a = __ffma2_rn(__fmul2_rn(make_float2(t[4 * k + 2 * i], t[4 * k + 2 * i + 1]), make_float2(r, r)), cs[k], a);
     }
-  }
 }
 
 template <typename TO, bool TILE, int G>
@@ -238,7 +312,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
       const uint32_t bytes = (uint32_t)(p.a_rows * kBlock + S::BBytes) * G;
       for (int item = first; alive && item < p.items; item += stride) {
         const MmItem w = mm_item<G>(p, item);
-        const int row0 = w.m0 + (int)rank * kMmRows, col0 = w.n0 + (int)rank * S::BRows;
+        const int row0 = w.m0 + (int)rank * kMmRows, col0 = w.n0 + (int)rank * (mm_columns(p, w.n0) / G);
         for (int j = w.j0; j < w.j1; ++j, ++n) {
           alive = __all_sync(kFullMask, wait_alive(&done[s], turn ^ 1, dead, p.wait_cycles));
           if (!alive) break;
@@ -268,9 +342,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         }
       }
     } else if (warp == kMmWarps + 1 && rank == 0) {
-      constexpr uint32_t idesc = umma_e4m3(kMmRows * G, kMmCols);
       for (int item = first; alive && item < p.items; item += stride) {
         const MmItem w = mm_item<G>(p, item);
+        const uint32_t idesc = umma_e4m3(kMmRows * G, mm_columns(p, w.n0));
         for (int j = w.j0; j < w.j1; ++j, ++n) {
           const uint32_t b = n & 1;
           alive = __all_sync(kFullMask, wait_alive(&full[s], turn, dead, p.wait_cycles) &&
@@ -345,7 +419,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         const uint32_t b = n & 1, set = n % kMmScaleSets;
         const float* scales = reinterpret_cast<const float*>(smem + S::ScaleOff + set * kMmScaleBytes);
         const float* cb = scales + kMmRows + quarter * 64;                          // of columns, or
-        const float* row = scales + (TILE ? kMmRows + (quarter >> 1) * kMmRows : 0) + lanes + lane;   // of rows times the block's
+        const float* row = scales + (TILE ? kMmRows + (quarter >> 1) * kMmRows : 0) + lanes;   // of rows times the block's
         // a wait that gives up marks the CTA, which is looked at once per tile
         if (S::Stages == 4) {
           s = n % 4;
@@ -359,19 +433,37 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         __syncwarp();
         tcgen05_fence_after();
         if (active) {
-          constexpr int W = TILE ? 32 : 16;   // columns at a time: with column scales the registers do not hold more
-          const float rs = *row;
-          const float2 r2 = make_float2(rs, rs);
-          float t[W];
+          auto read = [&] {   // all of the warp's part has been read
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0) release(b);
+          };
+          if constexpr (TILE) {
+            const float rs = row[lane];
+            const float2 r2 = make_float2(rs, rs);
+            float t[32];
 #pragma unroll
-          for (int c = 0; c < 64 / W; ++c) {
-            tmem_read(from + b * kMmCols + c * W, t);
-            if (c + 1 == 64 / W) {   // all of the warp's part has been read
-              tcgen05_fence_before();
-              __syncwarp();
-              if (lane == 0) release(b);
+            for (int c = 0; c < 2; ++c) {
+              tmem_read(from + b * kMmCols + c * 32, t);
+              if (c == 1) read();
+              mm_sums(t, r2, acc, c * 16);
             }
-            mm_sums<TILE, W>(t, r2, cb + c * W, acc, c * W / 2);
+          } else {
+            float rs[4], t[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rs[i] = row[8 * i + (lane >> 2)];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float2 cs[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) cs[k] = *reinterpret_cast<const float2*>(cb + c * 32 + 8 * k + 2 * (lane & 3));
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                tmem_read_16(from + b * kMmCols + c * 32 + (h << 20), t);
+                if (c == 1 && h == 1) read();
+                mm_sums(t, rs, cs, acc, c, h);
+              }
+            }
           }
         } else if (lane == 0) {
           release(b);
@@ -384,11 +476,11 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
       if (active) {
         const bool add = p.accumulate != 0;
         if (w.part >= 0) {
-          mm_store_boxes<float>(acc, box, &p_map, row0 - w.m0, col0 - w.n0, kMmCols, w.part, lane, false);
+          mm_store_boxes<float, TILE>(acc, box, &p_map, row0 - w.m0, col0 - w.n0, kMmCols, w.part, lane, false);
         } else if (p.boxes == 2 || (p.boxes == 1 && col0 + 64 <= p.N)) {
-          mm_store_boxes<TO>(acc, box, &o_map, row0, col0, p.N, 0, lane, add);
+          mm_store_boxes<TO, TILE>(acc, box, &o_map, row0, col0, p.N, 0, lane, add);
         } else {
-          mm_store_rows<TO>(acc, box, reinterpret_cast<TO*>(p.out), p.ldo, row0, p.M, col0, p.N, lane, add);
+          mm_store_rows<TO, TILE>(acc, box, reinterpret_cast<TO*>(p.out), p.ldo, row0, p.M, col0, p.N, lane, add, p.pairs != 0);
         }
       }
     }
@@ -430,8 +522,10 @@ __global__ void __launch_bounds__(256) block_matmul_join_kernel(const BlockMatmu
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / Q;
     const int t = (int)(row / p.part_rows), r = (int)(row - (int64_t)t * p.part_rows), c = (int)(i - row * Q) * 4;
-    const int nt = (p.whole + t) / p.row_tiles;
-    const int m = (p.whole + t - nt * p.row_tiles) * tile_rows + r, n = nt * kMmCols + c;
+    int m, n;
+    mm_origin(p, p.whole + t, tile_rows, m, n);
+    m += r;
+    n += c;
     if (m >= p.M || n >= p.N) continue;
     const float* q = p.part + t * p.parts * one + (int64_t)r * kMmCols + c;
     float4 s = *reinterpret_cast<const float4*>(q);
