@@ -132,10 +132,10 @@ struct MatmulMaps {
   CUtensorMap a, b, o, sa, sb, p;
 };
 
-template <typename TO, bool TILE, int G>
+template <typename TO, bool TILE, int G, bool ADD16>
 static vsamp_status launch_matmul_g(const BlockMatmulParams& p, const MatmulMaps& m, const DeviceInfo& d, int dev,
                                     cudaStream_t s) {
-  auto kern = block_matmul_kernel<TO, TILE, G>;
+  auto kern = block_matmul_kernel<TO, TILE, G, ADD16>;
   constexpr int smem = MmShape<G>::Smem;
   static std::atomic<bool> raised[64];
   if (dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
@@ -151,10 +151,11 @@ static vsamp_status launch_matmul_g(const BlockMatmulParams& p, const MatmulMaps
   return launch_clusters(kern, grid, G, kMmThreads, smem, s, p, m.a, m.b, m.o, m.sa, m.sb, m.p);
 }
 
-template <typename TO, bool TILE>
+template <typename TO, bool TILE, bool ADD16 = false>
 static vsamp_status launch_matmul(const BlockMatmulParams& p, const MatmulMaps& m, bool pair, const DeviceInfo& d, int dev,
                                   cudaStream_t s) {
-  const vsamp_status st = pair ? launch_matmul_g<TO, TILE, 2>(p, m, d, dev, s) : launch_matmul_g<TO, TILE, 1>(p, m, d, dev, s);
+  const vsamp_status st = pair ? launch_matmul_g<TO, TILE, 2, ADD16>(p, m, d, dev, s)
+                               : launch_matmul_g<TO, TILE, 1, ADD16>(p, m, d, dev, s);
   if (st != VSAMP_OK || p.whole == p.items) return st;
   const int64_t tiles = (p.items - p.whole) / p.parts;
   const int64_t ctas = (tiles * p.part_rows * (kMmCols / 4) + 255) / 256, most = (int64_t)d.sm_count * 8;
@@ -262,8 +263,12 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   if (p.boxes && !results_map(m.o, out, es == 4, ldo, M, N, 1)) return VSAMP_ERR_CUDA;
   if (need && !results_map(m.p, p.part, true, kMmCols, p.part_rows, kMmCols, p.items - p.whole)) return VSAMP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (out_dt == VSAMP_F32) return tile ? launch_matmul<float, true>(p, m, pair, d, dev, s) : launch_matmul<float, false>(p, m, pair, d, dev, s);
-  return tile ? launch_matmul<__nv_bfloat16, true>(p, m, pair, d, dev, s) : launch_matmul<__nv_bfloat16, false>(p, m, pair, d, dev, s);
+  if (out_dt == VSAMP_F32)
+    return tile ? launch_matmul<float, true>(p, m, pair, d, dev, s) : launch_matmul<float, false>(p, m, pair, d, dev, s);
+  using B = __nv_bfloat16;
+  if (accumulate)
+    return tile ? launch_matmul<B, true, true>(p, m, pair, d, dev, s) : launch_matmul<B, false, true>(p, m, pair, d, dev, s);
+  return tile ? launch_matmul<B, true>(p, m, pair, d, dev, s) : launch_matmul<B, false>(p, m, pair, d, dev, s);
 }
 
 }  // extern "C"

@@ -108,7 +108,7 @@ __device__ __forceinline__ int mm_columns(const BlockMatmulParams& p, int n0) {
 // Sums of a warp's 32 rows x 64 columns. TILE: a lane has a row, its columns 2 i and 2 i + 1 in acc[i]. Otherwise acc[4 k + 2 h
 // + i] holds the columns 8 k + 2 (lane % 4) and the next of row 16 h + 8 i + lane / 4: 16 columns' scales per lane instead of
 // 64, which took more of the registers and of shared memory's reads (151936 x 2048 x 2048, added: 750 us, 772 with a row per
-// lane; 32003 x 2302 x 1501 added to bf16: 364 and 378).
+// lane).
 //
 // 32 rows x 128 bytes of results, 32 fp32 or 64 bf16 columns, to the warp's box. A row's 16-byte pieces are permuted by the
 // row (the 128-byte swizzle): no bank conflicts.
@@ -169,8 +169,8 @@ __device__ __forceinline__ void mm_store_boxes(const float2 (&acc)[32], unsigned
 
 // The same to rows at any address, fp32 in the box, 16 rows of 64 columns at a time: a lane takes two neighbours (`pairs`:
 // every row begins on their boundary) or two columns 32 apart: 32003 x 2050 x 1501 added to fp32 171 us and 180, 32003 x 2302 x
-// 1501 added to bf16 378 and 539.
-template <typename T, bool TILE>
+// 1501 added to bf16 219 and 539 (of pairs, eight rows are read at once; one after another they take 364).
+template <typename T, bool TILE, bool ADD16>
 __device__ __forceinline__ void mm_store_rows(const float2 (&acc)[32], unsigned char* box, T* out, int64_t ldo, int m0, int M,
                                               int n0, int N, int lane, bool add, bool pairs) {
 #pragma unroll 1
@@ -198,20 +198,33 @@ __device__ __forceinline__ void mm_store_rows(const float2 (&acc)[32], unsigned 
     const int rows = M - m0 - h < 16 ? M - m0 - h : 16, c = pairs ? 2 * lane : lane;
     T* to = out + (m0 + h) * ldo + n0 + c;
     if (pairs && n0 + c + 1 < N) {
-#pragma unroll 8
-      for (int r = 0; r < rows; ++r, to += ldo) {
-        float2 v = *reinterpret_cast<const float2*>(box + r * 256 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8);
-        if constexpr (sizeof(T) == 4) {
-          // one addition per element and call: the same result every time
-          if (add) asm volatile("red.relaxed.gpu.global.add.v2.f32 [%0], {%1, %2};" ::"l"(to), "f"(v.x), "f"(v.y) : "memory");
-          else *reinterpret_cast<float2*>(to) = v;
-        } else {
-          __nv_bfloat162* at = reinterpret_cast<__nv_bfloat162*>(to);
-          if (add) {
-            const float2 w = __bfloat1622float2(*at);
-            v = make_float2(v.x + w.x, v.y + w.y);
+      auto value = [&](int r) {
+        return *reinterpret_cast<const float2*>(box + r * 256 + (((lane >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8);
+      };
+      if constexpr (ADD16) {   // the sums are added before the rounding; what they are added to is read eight rows at once
+        constexpr int kAhead = 8;
+#pragma unroll 1
+        for (int r = 0; r < rows; r += kAhead, to += kAhead * ldo) {
+          __nv_bfloat162 w[kAhead];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k)
+            if (r + k < rows) w[k] = *reinterpret_cast<const __nv_bfloat162*>(to + k * ldo);
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const float2 v = value(r + k), u = __bfloat1622float2(w[k]);
+            if (r + k < rows) *reinterpret_cast<__nv_bfloat162*>(to + k * ldo) = __float22bfloat162_rn(make_float2(v.x + u.x, v.y + u.y));
           }
-          *at = __float22bfloat162_rn(v);
+        }
+      } else {
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r, to += ldo) {
+          const float2 v = value(r);
+          if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<__nv_bfloat162*>(to) = __float22bfloat162_rn(v);
+          else if (add)   // one addition per element and call: the same result every time
+            asm volatile("red.relaxed.gpu.global.add.v2.f32 [%0], {%1, %2};" ::"l"(to), "f"(v.x), "f"(v.y) : "memory");
+          else
+            *reinterpret_cast<float2*>(to) = v;
         }
       }
     } else {
@@ -227,7 +240,7 @@ __device__ __forceinline__ void mm_store_rows(const float2 (&acc)[32], unsigned 
             if (add) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(at), "f"(v) : "memory");
             else *at = v;
           } else {
-            *at = (T)(add ? v + (float)*at : v);
+            *at = (T)(ADD16 ? v + (float)*at : v);
           }
         }
       }
@@ -254,7 +267,9 @@ __device__ __forceinline__ void mm_sums(const float (&t)[16], const float (&rs)[
     }
 }
 
-template <typename TO, bool TILE, int G>
+// ADD16: bf16 results are added to what is there. A kernel of its own, since those reads take registers that the others miss
+// (16384 x 8192 x 2048 written as bf16: 263 us, 270 in one kernel with it).
+template <typename TO, bool TILE, int G, bool ADD16>
 __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const BlockMatmulParams p,
                                                                      const __grid_constant__ CUtensorMap a_map,
                                                                      const __grid_constant__ CUtensorMap b_map,
@@ -477,10 +492,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         const bool add = p.accumulate != 0;
         if (w.part >= 0) {
           mm_store_boxes<float, TILE>(acc, box, &p_map, row0 - w.m0, col0 - w.n0, kMmCols, w.part, lane, false);
-        } else if (p.boxes == 2 || (p.boxes == 1 && col0 + 64 <= p.N)) {
+        } else if (!ADD16 && (p.boxes == 2 || (p.boxes == 1 && col0 + 64 <= p.N))) {
           mm_store_boxes<TO, TILE>(acc, box, &o_map, row0, col0, p.N, 0, lane, add);
         } else {
-          mm_store_rows<TO, TILE>(acc, box, reinterpret_cast<TO*>(p.out), p.ldo, row0, p.M, col0, p.N, lane, add, p.pairs != 0);
+          mm_store_rows<TO, TILE, ADD16>(acc, box, reinterpret_cast<TO*>(p.out), p.ldo, row0, p.M, col0, p.N, lane, add, p.pairs != 0);
         }
       }
     }
