@@ -242,6 +242,32 @@ def test_product_tiles_that_leave_differently(ts, dev, out):
     assert (y[:, N:] == 7.0).all()
 
 
+@pytest.mark.parametrize("tile", [True, False])
+@pytest.mark.parametrize("M", [100, 300])
+@pytest.mark.parametrize("N", [1, 63, 65, 257, 320, 385, 450, 512])
+def test_product_narrow_last_tiles(ts, dev, tile, M, N):
+    """Last tiles of one to four warps' columns, one CTA's and a pair's, into rows at odd and even strides, written and
+    added to."""
+    a, b = _operand(ts, M, 300, False, dev, N), _operand(ts, N, 300, tile, dev, N + 1)
+    for out in (F32, BF16):
+        for pad in (0, 1, 2):
+            base = torch.randn((M, N + pad), dtype=torch.float64).to(out).to(dev)
+            for add in (False, True):
+                y = base.clone()
+                ts.vsamp_block_matmul(a, b, out=y[:, :N], accumulate=add)
+                _check_product(y[:, :N], a, b, bu.f64(base[:, :N]) if add else None)
+                assert torch.equal(y[:, N:], base[:, N:])
+
+
+@pytest.mark.parametrize("tile", [True, False])
+@pytest.mark.parametrize("M,N", [(700, 600), (600, 700), (250, 1000), (1000, 250)])
+def test_product_order_of_tiles(ts, dev, tile, M, N):
+    """Several tiles that are divided, along rows and down columns of results."""
+    a, b = _operand(ts, M, 20000, False, dev, M), _operand(ts, N, 20000, tile, dev, N)
+    assert ts.load().vsamp_block_matmul_workspace_size(M, N, 20000) > 0
+    _check_product(ts.vsamp_block_matmul(a, b, out_dtype=F32), a, b)
+
+
 def test_product_padded_operands(ts, dev):
     """Operands inside larger arrays full of NaN codes and scales: only their own rows and columns count."""
     M, N, K = 50, 200, 270
