@@ -142,6 +142,21 @@ def test_least_second_moments(ts, dev, bits):
     assert (state.v[0].float() > 0).all()
 
 
+def test_first_moments_bit_for_bit(ts, dev):
+    """Codes of first moments are those of fp32 operations rounded one by one: m, the scale's reciprocal, their product (the
+    sum with the random bits and its floor are exact in binary64). Tensors long enough for every way through the kernel."""
+    for n in (1 << 20, 4097):
+        model = Model(ts, [n], F32, BF16, 8, False, dev, seed=n)
+        m = model.m[0].float() * model.ms[0].repeat_interleave(128)[:n]
+        m = m * 0.9 + model.grads[0].float() * (1 - 0.9)
+        ts.vsamp_adamw(model.state, model.grads, lr=1e-3, step=7, beta1=0.9, beta2=0.99, seed=11)
+        inv = torch.reciprocal(model.ms[0]).repeat_interleave(128)[:n]
+        y = bu.f64((m * inv).abs())
+        step = np.ldexp(1.0, np.maximum(np.frexp(y)[1] - 1, -6) - 3)
+        want = np.minimum(np.floor(y / step + ((bu.words(n, 0, 7, 0, 11) >> 16) + 0.5) / 65536) * step, 448.0)
+        assert np.array_equal(np.abs(bu.f64(model.m[0].float())), want)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_least_eps(ts, dev, bits):
     """Nothing moves without a gradient, with the least eps there is."""

@@ -9,8 +9,8 @@
 // tensors' addresses travel in the kernel's parameters (up to 384 per launch), so a step needs no table in device memory
 // and can be captured as it is.
 //
-// Measured: 32-bit states 95 % of the copy rate (65.5M elements: fp32 283 us, bf16 with masters 281); 8-bit states 68 % (311M
-// fp32 parameters with bf16 gradients 961 us of 657): 78 instructions per element issue in 63 % of the slots, 16 warps per SM
+// Measured: 32-bit states 95 % of the copy rate (65.5M elements: fp32 283 us, bf16 with masters 281); 8-bit states 67 % (311M
+// fp32 parameters with bf16 gradients 979 us of 657): 80 instructions per element issue in 63 % of the slots, 16 warps per SM
 // wait for each other's results. More warps with fewer blocks each, copies through shared memory and paired arithmetic were
 // measured and are slower. 150 tensors of 13,700 elements: 10 us.
 #pragma once
@@ -22,7 +22,7 @@ namespace vsamp {
 constexpr int kAdamThreads = 256;
 constexpr int kAdamTensors = 384;    // of 80 bytes: 30,720 of a launch's 32,764 parameter bytes
 // Blocks of 128 elements that a warp fetches at a time, and CTAs per SM. 67M parameters: 8-bit states (fp32 parameters, bf16
-// gradients) 4 blocks and 2 CTAs 212 us, 2 and 3 242, 2 and 2 246, 1 and 4 261; 32-bit ones move with none of it (2 and 2
+// gradients) 4 blocks and 2 CTAs 217 us, 2 and 3 233, 2 and 2 248, 1 and 4 260; 32-bit ones move with none of it (2 and 2
 // 289 us, 4 and 2 303, their floor is 281).
 template <bool BITS8>
 struct AdamShape {
@@ -102,11 +102,15 @@ __device__ __forceinline__ float rcp_near(float x) {
   return r;
 }
 
-// The scale of a block of moments; inv is what they are multiplied with, 0 for a block that is not finite.
+// The scale of a block of moments; inv is what they are multiplied with, 0 for a block that is not finite. It is the scale's
+// reciprocal after a Newton step, rounded as a division's, and the first moments are formed in separately rounded operations:
+// their codes are those of elementary fp32 operations, which a random rounding else leaves by a whole code where the
+// last bit decides (one element of 10^6), and the next steps' scales with them. 1.5 % of the 8-bit step.
 __device__ __forceinline__ float moment_scale(uint32_t amax_bits, float& inv) {
   const float s = fmaxf(__uint_as_float(amax_bits) * (1.0f / kE4m3Max), 0x1p-126f);
   const bool bad = amax_bits >= kInfBits;
-  inv = bad ? 0.0f : rcp_near(s);
+  const float near = rcp_near(s);
+  inv = bad ? 0.0f : fmaf(near, fmaf(-s, near, 1.0f), near);
   return bad ? __uint_as_float(0x7FC00000u) : s;
 }
 
@@ -220,7 +224,7 @@ __device__ __forceinline__ void adam_step(const AdamParams& p, const AdamTensor&
       if constexpr (MASTER || sizeof(TP) == 4) value[j] = raw.value[u].at(j);
       else value[j] = raw.value16[u].at(j);
       const float g = raw.g[u].at(j) * now.gs;
-      m[j] = fmaf(p.b1, m[j], p.one_b1 * g);
+      m[j] = __fadd_rn(__fmul_rn(p.b1, m[j]), __fmul_rn(p.one_b1, g));
       v[j] = fmaf(p.b2, v[j], p.one_b2 * g * g);
       root[j] = sqrt_near(v[j]);
       const float change = m[j] * now.c1 * rcp_near(fmaf(root[j], now.c2, p.eps));
