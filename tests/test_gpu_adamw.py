@@ -142,19 +142,24 @@ def test_least_second_moments(ts, dev, bits):
     assert (state.v[0].float() > 0).all()
 
 
-def test_first_moments_bit_for_bit(ts, dev):
-    """Codes of first moments are those of fp32 operations rounded one by one: m, the scale's reciprocal, their product (the
+def test_codes_bit_for_bit(ts, dev):
+    """Codes are those of fp32 operations rounded one by one: the moments, the root, the scale's reciprocal, their product (the
     sum with the random bits and its floor are exact in binary64). Tensors long enough for every way through the kernel."""
     for n in (1 << 20, 4097):
         model = Model(ts, [n], F32, BF16, 8, False, dev, seed=n)
         m = model.m[0].float() * model.ms[0].repeat_interleave(128)[:n]
-        m = m * 0.9 + model.grads[0].float() * (1 - 0.9)
+        g = model.grads[0].float()
+        m = m * 0.9 + g * (1 - 0.9)
+        v = (model.v[0].float() * model.vs[0].repeat_interleave(128)[:n]).square() * 0.99 + (1 - 0.99) * g * g
         ts.vsamp_adamw(model.state, model.grads, lr=1e-3, step=7, beta1=0.9, beta2=0.99, seed=11)
-        inv = torch.reciprocal(model.ms[0]).repeat_interleave(128)[:n]
-        y = bu.f64((m * inv).abs())
-        step = np.ldexp(1.0, np.maximum(np.frexp(y)[1] - 1, -6) - 3)
-        want = np.minimum(np.floor(y / step + ((bu.words(n, 0, 7, 0, 11) >> 16) + 0.5) / 65536) * step, 448.0)
-        assert np.array_equal(np.abs(bu.f64(model.m[0].float())), want)
+        w = bu.words(n, 0, 7, 0, 11)
+        for x, codes, scales, h, least in ((m, model.m, model.ms, w >> 16, 0.0),
+                                           (torch.sqrt(v), model.v, model.vs, w & 0xFFFF, 2.0 ** -9)):
+            y = bu.f64((x * torch.reciprocal(scales[0]).repeat_interleave(128)[:n]).abs())
+            step = np.ldexp(1.0, np.maximum(np.frexp(y)[1] - 1, -6) - 3)
+            want = np.minimum(np.floor(y / step + (h + 0.5) / 65536) * step, 448.0)
+            want = np.where(y > 0, np.maximum(want, least), want)
+            assert np.array_equal(np.abs(bu.f64(codes[0].float())), want)
 
 
 @pytest.mark.parametrize("bits", [32, 8])

@@ -88,9 +88,9 @@ extern "C" vsamp_status vsamp_adamw(const vsamp_adamw_tensor* tensors, int32_t c
   p.lr_dev = r.lr_dev;
   p.step_dev = r.step_dev;
   p.grad_scale = r.grad_scale;
-  // With 8-bit states long chunks keep the fetches ahead of the arithmetic (67M elements: 217 us with 128 blocks, 237 with
-  // 32), short ones spread few elements over the device (150 tensors of 20,000: 15.8 us with 32 blocks, 17.1 with 128; one
-  // of 4M: 14.9 and 16.6). Steps with 32-bit states are the better the shorter the chunks (67M: 283 us with 32 blocks, 287
+  // With 8-bit states long chunks keep the fetches ahead of the arithmetic (67M elements: 203 us with 128 blocks, 238 with
+  // 32), short ones spread few elements over the device (150 tensors of 20,000: 16.8 us with 32 blocks, 17.1 with 128; one
+  // of 4M: 15.4 and 16.6). Steps with 32-bit states are the better the shorter the chunks (67M: 283 us with 32 blocks, 287
   // with 128; 150 tensors of 200,000: 128 and 136).
   int64_t total = 0;
   for (int32_t k = 0; k < count; ++k) total += tensors[k].n;

@@ -9,8 +9,8 @@
 // tensors' addresses travel in the kernel's parameters (up to 384 per launch), so a step needs no table in device memory
 // and can be captured as it is.
 //
-// Measured: 32-bit states 95 % of the copy rate (65.5M elements: fp32 283 us, bf16 with masters 281); 8-bit states 67 % (311M
-// fp32 parameters with bf16 gradients 979 us of 657): 80 instructions per element issue in 63 % of the slots, 16 warps per SM
+// Measured: 32-bit states 95 % of the copy rate (65.5M elements: fp32 283 us, bf16 with masters 281); 8-bit states 71 % (311M
+// fp32 parameters with bf16 gradients 925 us of 657): 85 instructions per element issue in 72 % of the slots, 16 warps per SM
 // wait for each other's results. More warps with fewer blocks each, copies through shared memory and paired arithmetic were
 // measured and are slower. 150 tensors of 13,700 elements: 10 us.
 #pragma once
@@ -22,7 +22,7 @@ namespace vsamp {
 constexpr int kAdamThreads = 256;
 constexpr int kAdamTensors = 384;    // of 80 bytes: 30,720 of a launch's 32,764 parameter bytes
 // Blocks of 128 elements that a warp fetches at a time, and CTAs per SM. 67M parameters: 8-bit states (fp32 parameters, bf16
-// gradients) 4 blocks and 2 CTAs 217 us, 2 and 3 233, 2 and 2 248, 1 and 4 260; 32-bit ones move with none of it (2 and 2
+// gradients) 4 blocks and 2 CTAs 203 us, 2 and 3 221, 2 and 2 243, 1 and 4 258; 32-bit ones move with none of it (2 and 2
 // 289 us, 4 and 2 303, their floor is 281).
 template <bool BITS8>
 struct AdamShape {
@@ -88,14 +88,8 @@ __device__ __forceinline__ float2 e4m3_values(uint32_t codes) {
   return __half22float2(h);
 }
 
-// A root and a reciprocal of one or two units' error: far below what the step, lr times the quotient, has of the parameter.
-// The root holds for second moments below 2^-126 too, those of gradients near 10^-18: with a small eps they count. The
-// reciprocal need not: 2^-75 is the least root, and an eps between 0 and 2^-126 is refused.
-__device__ __forceinline__ float sqrt_near(float x) {
-  float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
+// A reciprocal of one unit's error: far below what the step, lr times the quotient, has of the parameter. Its divisor is 0 or
+// at least 2^-126, since an eps between them is refused and 2^-75 is the least root.
 __device__ __forceinline__ float rcp_near(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -103,9 +97,9 @@ __device__ __forceinline__ float rcp_near(float x) {
 }
 
 // The scale of a block of moments; inv is what they are multiplied with, 0 for a block that is not finite. It is the scale's
-// reciprocal after a Newton step, rounded as a division's, and the first moments are formed in separately rounded operations:
-// their codes are those of elementary fp32 operations, which a random rounding else leaves by a whole code where the
-// last bit decides (one element of 10^6), and the next steps' scales with them. 1.5 % of the 8-bit step.
+// reciprocal after a Newton step, rounded as a division's, and moments and roots are formed in separately rounded operations:
+// the codes are those of elementary fp32 operations, which a random rounding else leaves by a whole code where the last bit
+// decides (one element of 10^6), and the next steps' scales with them.
 __device__ __forceinline__ float moment_scale(uint32_t amax_bits, float& inv) {
   const float s = fmaxf(__uint_as_float(amax_bits) * (1.0f / kE4m3Max), 0x1p-126f);
   const bool bad = amax_bits >= kInfBits;
@@ -225,8 +219,8 @@ __device__ __forceinline__ void adam_step(const AdamParams& p, const AdamTensor&
       else value[j] = raw.value16[u].at(j);
       const float g = raw.g[u].at(j) * now.gs;
       m[j] = __fadd_rn(__fmul_rn(p.b1, m[j]), __fmul_rn(p.one_b1, g));
-      v[j] = fmaf(p.b2, v[j], p.one_b2 * g * g);
-      root[j] = sqrt_near(v[j]);
+      v[j] = __fadd_rn(__fmul_rn(p.b2, v[j]), __fmul_rn(__fmul_rn(p.one_b2, g), g));
+      root[j] = __fsqrt_rn(v[j]);
       const float change = m[j] * now.c1 * rcp_near(fmaf(root[j], now.c2, p.eps));
       value[j] = fmaf(-now.lr, fmaf(p.wd, value[j], change), value[j]);
     }
