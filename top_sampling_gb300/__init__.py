@@ -1179,13 +1179,17 @@ def vsamp_adamw(state: AdamWState, grads, lr, step, beta1=0.9, beta2=0.999, eps=
     for dt, members, words in state.groups:
         mine = grads if len(members) == len(grads) else [grads[i] for i in members]
         sizes = state.sizes if mine is grads else [state.sizes[i] for i in members]
-        for kind, ptrs, counts in _gradients(mine, sizes, at):
+        kinds = _gradients(mine, sizes, at)
+        usual = usual and bool(kinds)
+        for kind, ptrs, counts in kinds:
             table = array("q", words)
             table[_ADAMW_GRAD::_ADAMW_WORDS] = array("q", ptrs)
             if counts is not None:
                 table[_ADAMW_N::_ADAMW_WORDS] = array("q", counts)
                 usual = False
             calls.append((table, len(members), dt, VSAMP_F32 if kind is f32 else VSAMP_BF16))
+    if not calls:   # no gradient at all: the rule is checked on an empty tensor
+        calls.append((array("q", [0] * _ADAMW_WORDS), 1, VSAMP_F32, VSAMP_F32))
     lib, on = load(), _current(at)
     for table, n, dt, kind in calls:
         st = lib.vsamp_adamw(table.buffer_info()[0], n, dt, kind, state.bits, ctypes.byref(rule), on)
