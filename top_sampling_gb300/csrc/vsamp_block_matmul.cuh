@@ -391,8 +391,9 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
           const uint32_t set = n % kMmScaleSets;
           float t0 = 0.0f, t1 = 0.0f;
           if (TILE) {
-            t0 = __ldg(sb + j);
-            if (second) t1 = __ldg(sb + p.ldsb + j);
+            // plain loads: the kernel may have begun while the one that writes these scales still ran
+            t0 = sb[j];
+            if (second) t1 = sb[p.ldsb + j];
           }
           alive = __all_sync(kFullMask, wait_alive(&scaled[set], (n / kMmScaleSets) & 1, dead, p.wait_cycles));
           if (!alive) break;
