@@ -1,5 +1,6 @@
 // vsamp_block_quantize and vsamp_block_matmul: argument checks and launches.
 #include <atomic>
+#include <climits>
 
 #include "vsamp_block_matmul.cuh"
 #include "vsamp_block_quant.cuh"
@@ -255,6 +256,9 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   const long long wc = env_ll("VSAMP_WAIT_CYCLES", 0);
   p.wait_cycles = wc > 0 ? wc : 4000000000LL;   // ~2 s at the maximum SM clock
   p.drop_loads = env_int("VSAMP_TEST_DROP_LOADS", 0) != 0 ? 1 : 0;
+  const int stop0 = env_int("VSAMP_TEST_STOP_LOADS_0", 0), stop1 = env_int("VSAMP_TEST_STOP_LOADS_1", 0);
+  p.stop0 = stop0 > 0 ? stop0 : INT_MAX;
+  p.stop1 = stop1 > 0 ? stop1 : INT_MAX;
   const bool tile = b_kind == VSAMP_BLOCK_TILE;
   MatmulMaps m{};
   if (!codes_map(m.a, a, lda, M, K, p.a_rows) || !codes_map(m.b, b, ldb, N, K, pair ? kMmCols / 2 : kMmCols) ||

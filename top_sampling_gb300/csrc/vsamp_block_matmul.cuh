@@ -21,7 +21,8 @@
 // With few rows it streams b: 64 x 151936 x 4096 takes 100 us (96 % of the copy rate).
 //
 // Every wait is bounded. A CTA one of whose waits gave up lets its copies and products end, frees its tensor memory and
-// leaves NaN in the results that it had not finished.
+// leaves NaN in the results that it had not finished. A pair's CTAs tell each other how many blocks they copied, since one
+// may have given up before the other: rank 0, on whose barriers the copies of both are counted, waits for those of both.
 #pragma once
 
 #include "vsamp_block_quant.cuh"
@@ -68,6 +69,7 @@ struct BlockMatmulParams {
   int boxes;
   int pairs;                 // rows of results begin on the boundary of two elements
   int drop_loads;            // test: copies are expected and never made
+  int stop0, stop1;          // test: blocks after which the copying warp of a CTA of rank 0, 1 ends
   long long wait_cycles;
 };
 
@@ -289,6 +291,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
   uint64_t* scaled = drain + 1;                                     // a set of scales has landed
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(scaled + kMmScaleSets);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
+  volatile uint32_t* other = tmem_at + 2;   // of the pair's other CTA, at the end: blocks copied, and whether it gave up
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = kPair ? blockIdx.x & 1 : 0;
   const int first = blockIdx.x / G, stride = gridDim.x / G;
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         const MmItem w = mm_item<G>(p, item);
         const int row0 = w.m0 + (int)rank * kMmRows, col0 = w.n0 + (int)rank * (mm_columns(p, w.n0) / G);
         for (int j = w.j0; j < w.j1; ++j, ++n) {
-          alive = __all_sync(kFullMask, wait_alive(&done[s], turn ^ 1, dead, p.wait_cycles));
+          alive = __all_sync(kFullMask, wait_alive(&done[s], turn ^ 1, dead, p.wait_cycles)) && n < (uint32_t)(rank ? p.stop1 : p.stop0);
           if (!alive) break;
           if (elect_one()) {
             const uint32_t set = n % kMmScaleSets, scales = ring + S::ScaleOff + set * kMmScaleBytes;
@@ -505,22 +508,38 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
   __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
-  if (*dead) {
+  bool gave_up = *dead != 0;
+  uint32_t copied = n;   // by the other CTA; counts of the copying warps alone are used
+  if (kPair) {
+    if (threadIdx.x == kMmWarps * 32) dsmem_store_u32(dsmem_map(const_cast<uint32_t*>(other), rank ^ 1), n * 2 + (gave_up ? 1 : 0));
+    __syncwarp();
+    // the other CTA's arrivals and, if neither gave up, its products have ended before this one's shared and tensor memory go
+    cluster_barrier_shared();
+    gave_up |= (*other & 1) != 0;
+    copied = *other >> 1;
+  }
+  if (gave_up) {
     // copies and products under way end before shared and tensor memory are given up
     if (threadIdx.x == kMmWarps * 32 && !p.drop_loads) {
-      for (uint32_t k = n < S::Stages ? 0 : n - S::Stages; rank == 0 && k < n; ++k)
+      // neither CTA is more than the stages ahead of the products; before that all copies have been waited for
+      const uint32_t most = n > copied ? n : copied, half = (uint32_t)(p.a_rows * kBlock + S::BBytes);
+      for (uint32_t k = most < S::Stages ? 0 : most - S::Stages; rank == 0 && k < most; ++k) {
+        if (k >= n) mbar_arrive_expect_tx(&full[k % S::Stages], half);   // copied by the other CTA alone
+        else if (k >= copied) mbar_complete_tx(&full[k % S::Stages], half);   // expected of it and not copied
         (void)mbar_wait_bounded(&full[k % S::Stages], (k / S::Stages) & 1, 4000000000LL);
+      }
       for (uint32_t k = n < kMmScaleSets ? 0 : n - kMmScaleSets; k < n; ++k)
         (void)mbar_wait_bounded(&scaled[k % kMmScaleSets], (k / kMmScaleSets) & 1, 4000000000LL);
     }
-    if (threadIdx.x == kMmWarps * 32 + 32 && rank == 0) {
-      umma_commit<G>(smem_addr(drain));
+    if (warp == kMmWarps + 1) {
+      if (rank == 0 && elect_one()) umma_commit<G>(smem_addr(drain));   // by the thread that issued the products
+      __syncwarp();
       (void)mbar_wait_bounded(drain, 0, 4000000000LL);
+      __syncwarp();
     }
     __syncthreads();
+    if (kPair) cluster_barrier_shared();
   }
-  // the other CTA's arrivals and products have ended before this one's shared and tensor memory go
-  if (kPair) cluster_barrier_shared();
   if (warp == kMmWarps + 1) {
     __syncwarp();
     tcgen05_fence_after();
