@@ -1,6 +1,6 @@
 """Waits of the block product that run out with copies made and products under way: the copying warps of a pair's two CTAs end
-after different numbers of blocks (`VSAMP_TEST_STOP_LOADS_0`, `_1`). Every result
-is right or NaN, and the context and the next call are sound. In a child process, as the other tests of waits."""
+after different numbers of blocks (`VSAMP_TEST_STOP_LOADS_0`, `_1`), or all waits are short (`VSAMP_WAIT_CYCLES`). Every
+result is right or NaN, and the context and the next call are sound. In a child process, as the other tests of waits."""
 import json
 import os
 import subprocess
@@ -78,3 +78,10 @@ def test_pairs_that_end_apart(tile, M, N, K, stops, some):
 def test_single_ctas(tile):
     for wrong, nan, total, after in _run(100, 50000, 300, tile, [_stop(n, 0) for n in (3, 4, 5)]):
         assert wrong == 0 and after == 0 and 0 < nan < total
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(2100, 5000, 300), (100, 50000, 300), (600, 1000, 20000)])
+def test_short_waits(M, N, K):
+    """Waits of a cycle and more, none of whose copies is left out: whoever gives up leaves nothing wrong."""
+    for wrong, _, _, after in _run(M, N, K, True, [{"VSAMP_WAIT_CYCLES": str(c)} for c in (1, 500, 2000, 8000)]):
+        assert wrong == 0 and after == 0

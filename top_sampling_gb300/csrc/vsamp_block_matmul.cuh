@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         const MmItem w = mm_item<G>(p, item);
         const int row0 = w.m0 + (int)rank * kMmRows, col0 = w.n0 + (int)rank * (mm_columns(p, w.n0) / G);
         for (int j = w.j0; j < w.j1; ++j, ++n) {
-          alive = __all_sync(kFullMask, wait_alive(&done[s], turn ^ 1, dead, p.wait_cycles)) && n < (uint32_t)(rank ? p.stop1 : p.stop0);
+          alive = __all_sync(kFullMask, wait_alive<G>(&done[s], turn ^ 1, dead, p.wait_cycles)) && n < (uint32_t)(rank ? p.stop1 : p.stop0);
           if (!alive) break;
           if (elect_one()) {
             const uint32_t set = n % kMmScaleSets, scales = ring + S::ScaleOff + set * kMmScaleBytes;
@@ -365,8 +365,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         const uint32_t idesc = umma_e4m3(kMmRows * G, mm_columns(p, w.n0));
         for (int j = w.j0; j < w.j1; ++j, ++n) {
           const uint32_t b = n & 1;
-          alive = __all_sync(kFullMask, wait_alive(&full[s], turn, dead, p.wait_cycles) &&
-                                            wait_alive(&taken[b], ((n >> 1) & 1) ^ 1, dead, p.wait_cycles));
+          alive = __all_sync(kFullMask, wait_alive<G>(&full[s], turn, dead, p.wait_cycles) &&
+                                            wait_alive<G>(&taken[b], ((n >> 1) & 1) ^ 1, dead, p.wait_cycles));
           if (!alive) break;
           tcgen05_fence_after();
           if (elect_one()) {
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
             t0 = sb[j];
             if (second) t1 = sb[p.ldsb + j];
           }
-          alive = __all_sync(kFullMask, wait_alive(&scaled[set], (n / kMmScaleSets) & 1, dead, p.wait_cycles));
+          alive = __all_sync(kFullMask, wait_alive<G>(&scaled[set], (n / kMmScaleSets) & 1, dead, p.wait_cycles));
           if (!alive) break;
           if (TILE) {
             float* scales = reinterpret_cast<float*>(smem + S::ScaleOff + set * kMmScaleBytes);
@@ -439,12 +439,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         const float* scales = reinterpret_cast<const float*>(smem + S::ScaleOff + set * kMmScaleBytes);
         const float* cb = scales + kMmRows + quarter * 64;                          // of columns, or
         const float* row = scales + (TILE ? kMmRows + (quarter >> 1) * kMmRows : 0) + lanes;   // of rows times the block's
-        // a wait that gives up marks the CTA, which is looked at once per tile
+        // A wait that gives up marks the CTA, and the pair's other one, which is looked at once per tile. Its warp goes on and
+        // passes accumulators on that were not waited for: the next products in them reach marked CTAs alone.
         if (S::Stages == 4) {
           s = n % 4;
           turn = (n / 4) & 1;
         }
-        (void)wait_alive(&done[s], turn, dead, p.wait_cycles);
+        (void)wait_alive<G>(&done[s], turn, dead, p.wait_cycles);
         if (S::Stages != 4 && ++s == S::Stages) {
           s = 0;
           turn ^= 1;

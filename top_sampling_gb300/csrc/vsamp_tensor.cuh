@@ -168,17 +168,30 @@ __device__ __forceinline__ void tmem_read_16(uint32_t at, float (&r)[16]) {
       : "memory");
 }
 
-// Waits for a phase of `bar`, until `limit` clock cycles have passed or another thread of the CTA has given up; then
-// *dead is set and the answer is false.
+// Marks this CTA, and in a pair the other one too, as one of whose waits gave up. The marks are in place before anything that
+// the thread does next: what it passes on without having waited for it is passed on to CTAs that are marked.
+template <int G>
+__device__ __forceinline__ void mark_dead(volatile int* dead) {
+  if constexpr (G == 2) {
+    uint32_t rank;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    dsmem_store_u32(dsmem_map(const_cast<int*>(dead), rank ^ 1), 1u);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  }
+  *dead = 1;
+}
+
+// Waits for a phase of `bar`, until `limit` clock cycles have passed or the CTA is marked; then it, and a pair's other CTA, are
+// marked and the answer is false.
+template <int G>
 __device__ __forceinline__ bool wait_alive(void* bar, uint32_t parity, volatile int* dead, long long limit) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(bar, parity)) return true;
-    if (*dead) return false;
-    if (clock64() - t0 > limit) {
-      *dead = 1;
+    if (*dead || clock64() - t0 > limit) {
+      mark_dead<G>(dead);
       return false;
     }
   }
