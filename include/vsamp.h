@@ -438,7 +438,8 @@ typedef enum vsamp_block_kind {
  *   (x * 2^126 with the smallest scale); the quotients are rounded once to fp32
  *   codes [R, ldc], scales       of x, blocks along its columns (both NULL: not written)
  *   codes_t [C, ldt], scales_t   of x^T, blocks along the rows of x (both NULL: not written)
- * The outputs share no memory with x or with each other.
+ * The outputs share no memory with x or with each other (columns of one array may be divided among them): such a call is
+ * refused.
  * Of VSAMP_BLOCK_TILE the two hold the same codes and scales transposed. A block with NaN or an infinity has the scale
  * NaN and the codes 0: whatever is computed with it is NaN. What lies behind a row's last code is left as it is.
  * One launch on `stream`. */
@@ -455,8 +456,9 @@ vsamp_status vsamp_block_quantize(const void* x, vsamp_dtype dt, int64_t R, int6
  * Products are exact, a block's sum, the product of two scales and the sum over blocks fp32, one rounding at the end. A NaN scale makes its row's
  * (or block of columns') results NaN; other results do not depend on it. Sums are formed in an order that depends on
  * the sizes alone: the same call gives the same result.
- *   workspace  vsamp_block_matmul_workspace_size bytes (0 for most sizes: NULL is fine), 16-byte aligned; needs no
- *              initialisation, not shared by calls that may overlap. */
+ *   workspace  vsamp_block_matmul_workspace_size bytes (0 where no tile is divided along K: NULL is fine), 16-byte aligned;
+ *              needs no initialisation, not shared by calls that may overlap.
+ * out and workspace share no memory with each other or with the operands: such a call is refused. */
 size_t vsamp_block_matmul_workspace_size(int64_t M, int64_t N, int64_t K);
 vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa, const uint8_t* b,
                                 int64_t ldb, const float* sb, int64_t ldsb, vsamp_block_kind b_kind, int64_t M,

@@ -21,6 +21,28 @@ static bool matrix_ok(const void* codes, int64_t ld, const float* scales, int64_
   return at_multiple(scales, 16) && lds >= rows && lds % 4 == 0;
 }
 
+// Rows of `width` bytes, `stride` apart.
+struct Region {
+  __int128 at, stride, width, rows;
+  Region(const void* p, int64_t n, int64_t ld, int64_t cols, int elem)
+      : at(p ? (__int128)reinterpret_cast<uintptr_t>(p) : 0), stride((__int128)ld * elem), width(p ? (__int128)cols * elem : 0), rows(n) {}
+  __int128 end() const { return at + (rows - 1) * stride + width; }
+};
+static Region codes_region(const void* p, int64_t ld, int64_t rows, int64_t cols) { return Region(p, rows, ld, cols, 1); }
+static Region scales_region(const void* p, int64_t ld, vsamp_block_kind kind, int64_t rows, int64_t cols) {
+  if (kind == VSAMP_BLOCK_TILE) return Region(p, ceil_blocks(rows), ld, ceil_blocks(cols), 4);
+  return Region(p, ceil_blocks(cols), ld, rows, 4);
+}
+// Whether two regions have memory in common. Ranges of columns of one array, whose rows are equally far apart, do not; other
+// regions are taken from their first byte to their last.
+static bool share(const Region& a, const Region& b) {
+  if (!a.width || !b.width || a.end() <= b.at || b.end() <= a.at) return false;
+  const __int128 stride = a.rows > 1 ? a.stride : b.stride;   // that of a single row says nothing
+  if (stride <= 0 || (a.rows > 1 && b.rows > 1 && a.stride != b.stride)) return true;
+  const __int128 off = ((b.at - a.at) % stride + stride) % stride;   // of b's rows behind those of a
+  return off < a.width || off + b.width > stride;
+}
+
 template <typename T, bool TILE>
 static vsamp_status launch_quant(const BlockQuantParams& p, cudaStream_t s) {
   const unsigned grid = grid_of(p.tiles);
@@ -178,6 +200,12 @@ vsamp_status vsamp_block_quantize(const void* x, vsamp_dtype dt, int64_t R, int6
   if (codes && !matrix_ok(codes, ldc, scales, lds, kind, R, C)) return VSAMP_ERR_INVALID_ARG;
   if (codes_t && !matrix_ok(codes_t, ldt, scales_t, ldst, kind, C, R)) return VSAMP_ERR_INVALID_ARG;
   if (R > 0x7FFFFF00LL || C > 0x7FFFFF00LL) return VSAMP_ERR_UNSUPPORTED;
+  const Region all[5] = {Region(x, R, ldx, C, dt == VSAMP_F32 ? 4 : 2), codes_region(codes, ldc, R, C),
+                         scales_region(scales, lds, kind, R, C), codes_region(codes_t, ldt, C, R),
+                         scales_region(scales_t, ldst, kind, C, R)};
+  for (int i = 0; i < 5; ++i)
+    for (int j = i + 1; j < 5; ++j)
+      if (share(all[i], all[j])) return VSAMP_ERR_INVALID_ARG;
   BlockQuantParams p{};
   p.x = static_cast<const unsigned char*>(x);
   p.R = R;
@@ -217,6 +245,13 @@ vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, 
   const MmPlan plan = mm_plan(M, N, K);
   const size_t need = plan.bytes();
   if (need && (!workspace || !at_multiple(workspace, 16) || workspace_bytes < need)) return VSAMP_ERR_INVALID_ARG;
+  // what is written shares no memory with what is read
+  const Region read[4] = {codes_region(a, lda, M, K), scales_region(sa, ldsa, VSAMP_BLOCK_ROW, M, K), codes_region(b, ldb, N, K),
+                          scales_region(sb, ldsb, b_kind, N, K)};
+  const Region result(out, M, ldo, N, out_dt == VSAMP_F32 ? 4 : 2), room(need ? workspace : nullptr, 1, 0, (int64_t)need, 1);
+  for (const Region& r : read)
+    if (share(r, result) || share(r, room)) return VSAMP_ERR_INVALID_ARG;
+  if (share(result, room)) return VSAMP_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
