@@ -453,9 +453,11 @@ vsamp_status vsamp_block_quantize(const void* x, vsamp_dtype dt, int64_t R, int6
  *   b [N, ldb]   codes and scales of b_kind (weights: VSAMP_BLOCK_TILE; the other operand of a weight gradient: _ROW)
  *   K            columns of both
  *   out [M, ldo] fp32 or bf16; accumulate != 0 adds to what it holds
- * Products are exact, a block's sum, the product of two scales and the sum over blocks fp32, one rounding at the end. A NaN scale makes its row's
- * (or block of columns') results NaN; other results do not depend on it. Sums are formed in an order that depends on
- * the sizes alone: the same call gives the same result.
+ * Products are exact, a block's sum, the product of two scales and the sum over blocks fp32, one rounding at the end. A NaN
+ * scale makes its row's (or block of columns') results NaN; other results do not depend on it. Sums are formed in an order
+ * that depends on the sizes alone: the same call gives the same result. An addition to fp32 results may take what is added,
+ * what it is added to and the sum for zeros where they are below 2^-126: rows of whole 16 bytes on such boundaries keep such
+ * values, others lose them in the memory's own additions.
  *   workspace  vsamp_block_matmul_workspace_size bytes (0 where no tile is divided along K: NULL is fine), 16-byte aligned;
  *              needs no initialisation, not shared by calls that may overlap.
  * out and workspace share no memory with each other or with the operands: such a call is refused. */

@@ -223,7 +223,7 @@ __device__ __forceinline__ void mm_store_rows(const float2 (&acc)[32], unsigned 
           const float2 v = value(r);
           if constexpr (sizeof(T) == 2)
             *reinterpret_cast<__nv_bfloat162*>(to) = __float22bfloat162_rn(v);
-          else if (add)   // one addition per element and call: the same result every time
+          else if (add)   // one addition per element and call: the same result every time; below 2^-126 this one counts zeros
             asm volatile("red.relaxed.gpu.global.add.v2.f32 [%0], {%1, %2};" ::"l"(to), "f"(v.x), "f"(v.y) : "memory");
           else
             *reinterpret_cast<float2*>(to) = v;

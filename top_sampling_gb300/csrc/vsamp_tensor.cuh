@@ -29,8 +29,9 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
 }
 
 // A box of shared memory (128-byte swizzle as the map says) to a 3-D tensor at element (x, y, z), none negative, x * element
-// size a multiple of 16 bytes; what lies outside the tensor is not written. add: fp32 values are added in memory. The box
-// may be written again after bulk_read_done, and is in memory after bulk_done (both by the storing thread).
+// size a multiple of 16 bytes; what lies outside the tensor is not written. add: fp32 values are added in memory (those
+// below 2^-126 too, as measured; red.global takes them for zeros). The box may be written again after bulk_read_done, and is in
+// memory after bulk_done (both by the storing thread).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t src, bool add) {
   if (add)
     asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
