@@ -460,7 +460,10 @@ vsamp_status vsamp_block_quantize(const void* x, vsamp_dtype dt, int64_t R, int6
  * values, others lose them in the memory's own additions.
  *   workspace  vsamp_block_matmul_workspace_size bytes (0 where no tile is divided along K: NULL is fine), 16-byte aligned;
  *              needs no initialisation, not shared by calls that may overlap.
- * out and workspace share no memory with each other or with the operands: such a call is refused. */
+ * out and workspace share no memory with each other or with the operands: such a call is refused.
+ * Every wait on the device is bounded (about 2 s). If one runs out, which nothing but a fault of the device or a kernel that
+ * keeps it from running is known to cause, the results of its tile and those not begun are NaN, added to or not: there is no
+ * status, so that a NaN is the only sign, and what out held there is lost. */
 size_t vsamp_block_matmul_workspace_size(int64_t M, int64_t N, int64_t K);
 vsamp_status vsamp_block_matmul(const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa, const uint8_t* b,
                                 int64_t ldb, const float* sb, int64_t ldsb, vsamp_block_kind b_kind, int64_t M,

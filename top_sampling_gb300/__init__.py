@@ -989,7 +989,7 @@ def vsamp_block_matmul(a: BlockTensor, b: BlockTensor, out=None, out_dtype=torch
                        workspace=None, stream=None):
     """a [M, K] times b [N, K] transposed: [M, N] in fp32 or bf16. a has blocks of 1 x 128 (activations, gradients), b of
     128 x 128 (weights) or of 1 x 128. ``out`` (rows may be padded) or a new tensor of out_dtype is returned;
-    accumulate adds to what ``out`` holds."""
+    accumulate adds to what ``out`` holds. Results are NaN where a wait on the device ran out (vsamp.h)."""
     where = _elsewhere(a.codes, stream)
     if where is not None:
         with where:
