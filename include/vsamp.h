@@ -499,8 +499,9 @@ typedef struct vsamp_adamw_rule {
  * `tensors` and `rule` are HOST pointers, read before the call returns. One launch per 384 tensors.
  *   param_dt    fp32, or bf16: with a master that one is updated and param gets its rounding; without, param is rounded
  *               stochastically (16 random bits are added below the kept ones), so that small steps are not lost
- *   state_bits  32, or 8: e4m3 codes with a scale (largest magnitude / 448, at least 2^-126) per 128 elements from the
- *               tensor's first, of m and of r = sqrt(v). Values between two codes go to one of them at random, to the
+ *   state_bits  32, or 8: e4m3 codes with a scale (largest magnitude times fp32 1/448, rounded, at least 2^-126: its last bits
+ *               may differ from vsamp_block_quantize's quotient) per 128 elements from the tensor's first, of m and of
+ *               r = sqrt(v). Values between two codes go to one of them at random, to the
  *               nearer with more probability, so that moments follow changes below a code's step; r > 0 is never
  *               rounded to 0. p is computed from the moments before that rounding. A block with NaN or an infinity gets
  *               the scale NaN.
