@@ -85,3 +85,26 @@ def test_short_waits(M, N, K):
     """Waits of a cycle and more, none of whose copies is left out: whoever gives up leaves nothing wrong."""
     for wrong, _, _, after in _run(M, N, K, True, [{"VSAMP_WAIT_CYCLES": str(c)} for c in (1, 500, 2000, 8000)]):
         assert wrong == 0 and after == 0
+
+
+@pytest.mark.gpu
+def test_pairs_between_other_kernels():
+    """Pairs' products one behind the other and between kernels that leave something else in shared memory: no CTA takes what
+    was there for the other one's word that it gave up."""
+    torch = pytest.importorskip("torch")
+    import __graft_entry__ as g
+
+    g.build()
+    import top_sampling_gb300 as ts
+
+    dev = torch.device("cuda:0")
+    gen = torch.Generator(device=dev).manual_seed(1)
+    p, q = (torch.randn((4096, 4096), generator=gen, device=dev) for _ in range(2))
+    a, _ = ts.vsamp_block_quantize(torch.randn((20000, 1024), generator=gen, device=dev))
+    for tile in (True, False):
+        b, _ = ts.vsamp_block_quantize(torch.randn((2048, 1024), generator=gen, device=dev), tile=tile)
+        ref = ts.vsamp_block_matmul(a, b, out_dtype=torch.float32)
+        for k in range(40):
+            p @ q if k % 2 else p.bfloat16() @ q.bfloat16()
+            outs = [ts.vsamp_block_matmul(a, b, out_dtype=torch.float32) for _ in range(3)]
+            assert all(torch.equal(y, ref) for y in outs)

@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
     for (int i = 0; i < kMmScaleSets; ++i) mbar_init(&scaled[i], 1);
     mbar_init(drain, 1);
     *dead = 0;
+    *other = 0;
     fence_mbar_init();
   }
   if (warp == kMmWarps + 1) tmem_alloc<G>(smem_addr(tmem_at), kMmColumns);
@@ -512,7 +513,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
   bool gave_up = *dead != 0;
   uint32_t copied = n;   // by the other CTA; counts of the copying warps alone are used
   if (kPair) {
-    if (threadIdx.x == kMmWarps * 32) dsmem_store_u32(dsmem_map(const_cast<uint32_t*>(other), rank ^ 1), n * 2 + (gave_up ? 1 : 0));
+    // both CTAs have to come to the same answer: what follows, the freeing of tensor memory too, they do together
+    if (threadIdx.x == kMmWarps * 32) dsmem_publish_u32(dsmem_map(const_cast<uint32_t*>(other), rank ^ 1), n * 2 + (gave_up ? 1 : 0));
     __syncwarp();
     // the other CTA's arrivals and, if neither gave up, its products have ended before this one's shared and tensor memory go
     cluster_barrier_shared();

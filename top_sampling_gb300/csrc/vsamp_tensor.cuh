@@ -169,6 +169,13 @@ __device__ __forceinline__ void tmem_read_16(uint32_t at, float (&r)[16]) {
       : "memory");
 }
 
+// A word into the other CTA's shared memory, in place before anything that the thread does next (cluster_barrier_shared by
+// itself publishes a thread's writes to its own CTA's shared memory alone).
+__device__ __forceinline__ void dsmem_publish_u32(uint32_t addr, uint32_t v) {
+  dsmem_store_u32(addr, v);
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
 // Marks this CTA, and in a pair the other one too, as one of whose waits gave up. The marks are in place before anything that
 // the thread does next: what it passes on without having waited for it is passed on to CTAs that are marked.
 template <int G>
@@ -176,8 +183,7 @@ __device__ __forceinline__ void mark_dead(volatile int* dead) {
   if constexpr (G == 2) {
     uint32_t rank;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    dsmem_store_u32(dsmem_map(const_cast<int*>(dead), rank ^ 1), 1u);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    dsmem_publish_u32(dsmem_map(const_cast<int*>(dead), rank ^ 1), 1u);
   }
   *dead = 1;
 }
