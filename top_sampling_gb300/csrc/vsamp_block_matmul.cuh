@@ -505,7 +505,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         }
       }
     }
-    if (lane == 0) bulk_done();
+    if (lane == 0) {
+      bulk_done();
+      if (kPair) fence_cluster();   // its last arrivals have reached the other CTA, whose shared memory goes behind the barrier
+    }
   }
   __syncwarp();
   tcgen05_fence_before();

@@ -169,11 +169,13 @@ __device__ __forceinline__ void tmem_read_16(uint32_t at, float (&r)[16]) {
       : "memory");
 }
 
-// A word into the other CTA's shared memory, in place before anything that the thread does next (cluster_barrier_shared by
-// itself publishes a thread's writes to its own CTA's shared memory alone).
+// What this thread wrote to the other CTA's shared memory, and its arrivals there, are in place before anything that it does next
+// (cluster_barrier_shared by itself publishes a thread's writes to its own CTA's shared memory alone).
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
 __device__ __forceinline__ void dsmem_publish_u32(uint32_t addr, uint32_t v) {
   dsmem_store_u32(addr, v);
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  fence_cluster();
 }
 
 // Marks this CTA, and in a pair the other one too, as one of whose waits gave up. The marks are in place before anything that
