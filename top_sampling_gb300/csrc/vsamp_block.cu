@@ -25,7 +25,7 @@ static bool matrix_ok(const void* codes, int64_t ld, const float* scales, int64_
 struct Region {
   __int128 at, stride, width, rows;
   Region(const void* p, int64_t n, int64_t ld, int64_t cols, int elem)
-      : at(p ? (__int128)reinterpret_cast<uintptr_t>(p) : 0), stride((__int128)ld * elem), width(p ? (__int128)cols * elem : 0), rows(n) {}
+      : at(reinterpret_cast<uintptr_t>(p)), stride((__int128)ld * elem), width(p ? (__int128)cols * elem : 0), rows(n) {}
   __int128 end() const { return at + (rows - 1) * stride + width; }
 };
 static Region codes_region(const void* p, int64_t ld, int64_t rows, int64_t cols) { return Region(p, rows, ld, cols, 1); }

@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) block_matmul_kernel(const Block
         const MmItem w = mm_item<G>(p, item);
         const int row0 = w.m0 + (int)rank * kMmRows, col0 = w.n0 + (int)rank * (mm_columns(p, w.n0) / G);
         for (int j = w.j0; j < w.j1; ++j, ++n) {
-          alive = __all_sync(kFullMask, wait_alive<G>(&done[s], turn ^ 1, dead, p.wait_cycles)) && n < (uint32_t)(rank ? p.stop1 : p.stop0);
+          alive = __all_sync(kFullMask, wait_alive<G>(&done[s], turn ^ 1, dead, p.wait_cycles)) &&
+                  n < (uint32_t)(rank ? p.stop1 : p.stop0);
           if (!alive) break;
           if (elect_one()) {
             const uint32_t set = n % kMmScaleSets, scales = ring + S::ScaleOff + set * kMmScaleBytes;
